@@ -1,0 +1,230 @@
+"""Binding of the paged-cache attention in libcoli_moe.so (include/coli_attn.h).
+
+    eng = attn.PagedAttention(n_q=48, n_kv=8, head_dim=128, page=64, max_tokens=512, max_seqs=64)
+    cache = eng.bind_cache(k_cache, v_cache)           # [pages, n_kv, page, head_dim], any strides
+    batch = attn.Batch(q_start, kv_len, table, n_tokens=T, max_q=1)
+    q = eng.append(cache, batch, k, v, q)              # rotate, store, return the rotated queries
+    o = eng.window(cache, batch, q, window=4096, sinks=4)
+    o = eng.prefix(cache, batch, prefix_table, prefix_len, q)
+
+Argument marshalling only; every step runs in the library's CUDA kernels.
+"""
+import ctypes
+import math
+import sys
+
+import torch
+
+from . import coli
+
+_i, _f, _vp, _i64, _d = ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_int64, ctypes.c_double
+
+DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+
+
+class AttnConfig(ctypes.Structure):
+    _fields_ = [("n_q", _i), ("n_kv", _i), ("head_dim", _i), ("page", _i), ("dtype", _i),
+                ("max_tokens", _i), ("max_seqs", _i), ("rot_dim", _i), ("rot_interleaved", _i),
+                ("rope_base", _d), ("inv_freq", ctypes.POINTER(_d))]
+
+
+class AttnCache(ctypes.Structure):
+    _fields_ = [("k", _vp), ("v", _vp), ("n_pages", _i64), ("k_page_stride", _i64), ("k_head_stride", _i64),
+                ("k_slot_stride", _i64), ("v_page_stride", _i64), ("v_head_stride", _i64),
+                ("v_slot_stride", _i64)]
+
+
+class AttnBatch(ctypes.Structure):
+    _fields_ = [("q_start", _vp), ("kv_len", _vp), ("table", _vp), ("table_stride", _i64), ("n_seqs", _i),
+                ("max_pages", _i), ("n_tokens", _i), ("max_q", _i)]
+
+
+_lib = None
+
+
+def lib():
+    global _lib
+    L = coli.lib()
+    if _lib is not L:
+        L.coli_attn_create.argtypes = [ctypes.POINTER(AttnConfig), ctypes.POINTER(_vp)]
+        L.coli_attn_destroy.argtypes = [_vp]
+        L.coli_attn_destroy.restype = None
+        L.coli_attn_cache_bind.argtypes = [_vp, ctypes.POINTER(AttnCache), ctypes.POINTER(_vp)]
+        L.coli_attn_cache_release.argtypes = [_vp]
+        L.coli_attn_cache_release.restype = None
+        L.coli_attn_append.argtypes = [_vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp]
+        L.coli_attn_window.argtypes = [_vp, _vp, _vp, _vp, _i64, _i, _i, _f, _vp, _i64, _vp, _vp]
+        L.coli_attn_prefix.argtypes = [_vp, _vp, _vp, _vp, _i, _vp, _vp, _i64, _f, _vp, _i64, _vp, _vp]
+        L.coli_attn_status.argtypes = [_vp, _vp]
+        L.coli_attn_launches.argtypes = [_vp, _i, _i]
+        _lib = L
+    return L
+
+
+def _int32(t, dims, what):
+    if t.dtype is not torch.int32 or t.dim() != dims or (t.numel() and t.stride(-1) != 1) or not t.is_cuda:
+        raise ValueError(f"{what}: a {dims}-dimensional int32 tensor on the device, rows contiguous")
+    return t
+
+
+class Batch:
+    """The ragged batch of a call: sequence b has the query tokens q_start[b] .. q_start[b+1]-1, the last
+    of its kv_len[b] cached tokens, whose pages are table[b].  The three int32 tensors stay the
+    caller's (they may be updated in place between calls and are read on the device); n_tokens is the
+    number of query tokens, max_q at least the new tokens of any sequence."""
+
+    def __init__(self, q_start, kv_len, table, n_tokens, max_q):
+        _int32(q_start, 1, "q_start"), _int32(kv_len, 1, "kv_len"), _int32(table, 2, "table")
+        n = kv_len.shape[0]
+        if q_start.shape[0] != n + 1 or table.shape[0] != n:
+            raise ValueError("q_start has one entry more than kv_len, table one row for each sequence")
+        self.q_start, self.kv_len, self.table = q_start, kv_len, table
+        self.n_tokens, self.max_q, self.n_seqs = int(n_tokens), int(max_q), n
+        self.c = AttnBatch(q_start.data_ptr(), kv_len.data_ptr(), table.data_ptr(),
+                           max(table.stride(0), table.shape[1]), n, table.shape[1], self.n_tokens, self.max_q)
+        self.ref = ctypes.addressof(self.c)
+
+
+class KvCache:
+    """A cache bound to an engine (coli_attn_cache_bind); keeps the two tensors alive."""
+
+    def __init__(self, engine, k, v):
+        dims = (engine.n_kv, engine.page, engine.head_dim)
+        for t in (k, v):
+            if t.dim() != 4 or tuple(t.shape[1:]) != dims or t.dtype is not engine.dtype or not t.is_cuda:
+                raise ValueError(f"the cache is [pages, {dims[0]}, {dims[1]}, {dims[2]}] of {engine.dtype} on the device")
+            if t.stride(3) != 1:
+                raise ValueError("a head's values are contiguous")
+        if k.shape[0] != v.shape[0]:
+            raise ValueError("K and V have the same number of pages")
+        self.k, self.v = k, v
+
+        def strides(t):  # a dimension of one has no stride of its own
+            return [t.stride(i) if t.shape[i] > 1 else max(t.stride(i), engine.head_dim) // 8 * 8 for i in range(3)]
+
+        c = AttnCache(k.data_ptr(), v.data_ptr(), k.shape[0], *strides(k), *strides(v))
+        h = _vp()
+        coli._check(lib().coli_attn_cache_bind(engine.h, ctypes.byref(c), ctypes.byref(h)), "coli_attn_cache_bind")
+        self.h = h
+
+    def close(self):
+        if getattr(self, "h", None) is not None and self.h.value:
+            lib().coli_attn_cache_release(self.h)
+            self.h = _vp()
+
+    def __del__(self):
+        if sys.is_finalizing():  # the process is exiting: no native calls during teardown
+            return
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class PagedAttention:
+    """Shapes, rotation and workspace of the attention over a paged cache on the current device.
+    rot_dim None rotates the whole head, 0 none of it; inv_freq (rot_dim/2 radians per position) takes
+    the place of rope_base."""
+
+    def __init__(self, n_q, n_kv, head_dim, page, max_tokens, max_seqs, dtype=torch.bfloat16, rot_dim=None,
+                 interleaved=False, rope_base=10000.0, inv_freq=None):
+        if dtype not in DTYPES:
+            raise ValueError(f"{dtype}: the attention kernels take bfloat16 or float16")
+        rot = head_dim if rot_dim is None else rot_dim
+        freq = None
+        if inv_freq is not None:
+            freq = (_d * len(inv_freq))(*[float(x) for x in inv_freq])
+            if len(inv_freq) != rot // 2:
+                raise ValueError(f"inv_freq has rot_dim/2 = {rot // 2} entries")
+        cfg = AttnConfig(n_q, n_kv, head_dim, page, DTYPES[dtype], max_tokens, max_seqs, rot, int(interleaved),
+                         rope_base, freq)
+        h = _vp()
+        coli._check(lib().coli_attn_create(ctypes.byref(cfg), ctypes.byref(h)), "coli_attn_create")
+        self.h = h
+        self.n_q, self.n_kv, self.head_dim, self.page, self.dtype = n_q, n_kv, head_dim, page, dtype
+        self.max_tokens, self.max_seqs, self.rot_dim = max_tokens, max_seqs, rot
+        self.scale = 1.0 / math.sqrt(head_dim)
+
+    def close(self):
+        if getattr(self, "h", None) is not None and self.h.value:
+            lib().coli_attn_destroy(self.h)
+            self.h = _vp()
+
+    __del__ = KvCache.__del__
+
+    def bind_cache(self, k_cache, v_cache):
+        return KvCache(self, k_cache, v_cache)
+
+    def _heads(self, t, heads, batch, what):
+        """the token stride of t [n_tokens, heads, head_dim]"""
+        D = self.head_dim
+        if (t.dtype is not self.dtype or t.shape != (batch.n_tokens, heads, D) or not t.is_cuda
+                or t.stride(2) != 1 or (heads > 1 and t.stride(1) != D)):
+            raise ValueError(f"{what}: [{batch.n_tokens}, {heads}, {D}] of {self.dtype} on the device, heads contiguous")
+        return t.stride(0) if batch.n_tokens > 1 else heads * D
+
+    def _out(self, out, batch, stream, like):
+        if out is None:
+            out = torch.empty((batch.n_tokens, self.n_q, self.head_dim), dtype=self.dtype, device=like.device)
+            if stream is not None and isinstance(stream, torch.cuda.Stream):
+                out.record_stream(stream)
+        return out
+
+    def append(self, cache, batch, k, v, q=None, q_out=None, pos_base=None, stream=None):
+        """Stores the batch's new keys (rotated) and values in the cache; rotates q into q_out (new by
+        default, q itself for in place) and returns it.  pos_base: int32 [1] on the device, added to the
+        positions for the rotation (the length of a shared prefix).  coli_attn_append"""
+        ks, vs = self._heads(k, self.n_kv, batch, "k"), self._heads(v, self.n_kv, batch, "v")
+        qp = op = None
+        qs = os = 0
+        if q is not None:
+            qs = self._heads(q, self.n_q, batch, "q")
+            q_out = self._out(q_out, batch, stream, q)
+            os = self._heads(q_out, self.n_q, batch, "q_out")
+            qp, op = q.data_ptr(), q_out.data_ptr()
+        base = None if pos_base is None else _int32(pos_base, 1, "pos_base").data_ptr()
+        coli._check(lib().coli_attn_append(self.h, cache.h, batch.ref, qp, qs, k.data_ptr(), ks, v.data_ptr(), vs,
+                                           op, os, base, coli._stream(stream)), "coli_attn_append")
+        return q_out
+
+    def window(self, cache, batch, q, window=-1, sinks=0, scale=None, out=None, lse=None, stream=None):
+        """Causal attention over the last `window` keys (all with -1) and the first `sinks` ones ->
+        [n_tokens, n_q, head_dim]; lse: float32 [n_tokens, n_q] to fill, or None.  coli_attn_window"""
+        qs = self._heads(q, self.n_q, batch, "q")
+        out = self._out(out, batch, stream, q)
+        coli._check(lib().coli_attn_window(self.h, cache.h, batch.ref, q.data_ptr(), qs, window, sinks,
+                                           self.scale if scale is None else scale, out.data_ptr(),
+                                           self._heads(out, self.n_q, batch, "out"), self._lse(lse, batch),
+                                           coli._stream(stream)), "coli_attn_window")
+        return out
+
+    def prefix(self, cache, batch, prefix_table, prefix_len, q, scale=None, out=None, lse=None, stream=None):
+        """Attention of a batch behind a shared prefix: prefix_len (int32 [1] on the device) tokens in the
+        pages prefix_table (int32 [pages]), then each sequence's own cache.  coli_attn_prefix"""
+        qs = self._heads(q, self.n_q, batch, "q")
+        out = self._out(out, batch, stream, q)
+        _int32(prefix_table, 1, "prefix_table"), _int32(prefix_len, 1, "prefix_len")
+        coli._check(lib().coli_attn_prefix(self.h, cache.h, batch.ref, prefix_table.data_ptr(),
+                                           prefix_table.shape[0], prefix_len.data_ptr(), q.data_ptr(), qs,
+                                           self.scale if scale is None else scale, out.data_ptr(),
+                                           self._heads(out, self.n_q, batch, "out"), self._lse(lse, batch),
+                                           coli._stream(stream)), "coli_attn_prefix")
+        return out
+
+    def _lse(self, lse, batch):
+        if lse is None:
+            return None
+        if lse.dtype is not torch.float32 or lse.shape != (batch.n_tokens, self.n_q) or not lse.is_contiguous():
+            raise ValueError(f"lse: contiguous float32 [{batch.n_tokens}, {self.n_q}]")
+        return lse.data_ptr()
+
+    def status(self, stream=None):
+        """device status of earlier calls (coli_attn_status); 0 when all went well"""
+        return int(lib().coli_attn_status(self.h, coli._stream(stream)))
+
+    def launches(self, op, max_q):
+        """kernels one call launches; op "append", "window" or "prefix" (coli_attn_launches)"""
+        n = int(lib().coli_attn_launches(self.h, ("append", "window", "prefix").index(op), max_q))
+        if n < 0:
+            raise coli.ColiError(n, "coli_attn_launches")
+        return n

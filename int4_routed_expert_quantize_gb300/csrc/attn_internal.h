@@ -1,0 +1,95 @@
+// Internal types of the paged-cache attention (coli_attn.h): what the kernels get, the workspace
+// and the launchers.  Not part of the C ABI.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "coli_attn.h"
+
+namespace coli {
+
+constexpr int kAttnMaxSeqs = 4096;
+constexpr int kAttnMaxGroup = 64;     // query heads per key head
+constexpr int kAttnPrefixRows = 8;    // tokens per sequence the prefix workspace is sized for
+constexpr int kAttnNoWindow = 1 << 30;
+constexpr int kSplitKeys = 64;        // keys per tile of the split kernel
+constexpr int kTileKeys = 128;        // keys per tile of the tensor-memory kernel
+constexpr int kTileRows = 256;        // query rows per block of the tensor-memory kernel (2 x 128)
+
+// A unit of attention work is one block of query tokens of one sequence with one key head; its
+// key tiles are a contiguous stretch of one long list over all units, and each CTA takes an equal
+// stretch of that list.  A unit cut by a stretch's end leaves one partial result per CTA in
+// the workspace; Rec (one per CTA, written by the CTA that holds the unit's second part) tells the
+// combine kernel where they are.
+struct AttnRec {
+  int first_cta, last_cta;  // CTAs with a part of the unit; first_cta < 0: no record
+  int first_slot;           // partial slot (0 or 1) of first_cta; all others have theirs in slot 0
+  int token0, tokens;       // the unit's query tokens
+  int head;                 // key head
+  int pad[2];
+};
+
+struct AttnParams {
+  const void* q;
+  int64_t q_stride;
+  void* out;
+  int64_t out_stride;
+  float* lse;
+  const int32_t* q_start;  // nullptr: one sequence of all n_tokens tokens (the shared prefix)
+  const int32_t* kv_len;
+  const int32_t* table;
+  int64_t table_stride;
+  int n_seqs, n_tokens, max_pages;
+  int n_q, n_kv, group, head_dim;
+  int page_shift, n_pages;
+  int window, sinks;  // window >= kAttnNoWindow: none (and sinks 0)
+  int causal;         // 0: every query sees all kv_len keys
+  float scale_log2;   // scale * log2(e)
+  int block_tokens;   // query tokens per block
+  int64_t rows_lo, rows_hi;  // only sequences with rows_lo < new tokens * group <= rows_hi
+  // workspace
+  float* part_o;     // [2 * CTAs][rows per block][head_dim] unnormalised partial outputs
+  float2* part_ml;   // [2 * CTAs][rows per block] their maximum (log2 units) and sum
+  AttnRec* rec;      // [CTAs]
+  int64_t* seq_pos;  // [n_seqs + 2] first list position of each sequence, the total, the stretch
+  float* dense_o;    // prefix only: rows of uncut units go here, unnormalised, by (token, head)
+  float2* dense_ml;
+  int* status;
+};
+
+struct AttnKvMaps {  // boxes of 64 values x min(page, box) slots, 128-byte swizzle
+  CUtensorMap k64, v64;    // box 64 slots: split kernel
+  CUtensorMap k128, v128;  // box 128 slots: tensor-memory kernel
+};
+
+struct AttnAppend {
+  const void *q, *k, *v;
+  void *q_out, *kc, *vc;
+  int64_t q_stride, k_stride, v_stride, q_out_stride;
+  int64_t kp, kh, ks, vp, vh, vs;  // cache strides in elements
+  const int32_t *q_start, *kv_len, *table;
+  int64_t table_stride;
+  int n_seqs, n_tokens, max_pages, n_pages, page_shift;
+  int n_q, n_kv, head_dim, rot, interleaved;
+  const int32_t* pos_base;  // added to every position for the rotation, or nullptr
+  const uint64_t* turn;  // [rot/2] turns per position as a fraction of 2^64
+  int* status;
+};
+
+int split_rows(int rows);  // rows per block the split kernel takes for units of `rows` rows
+int split_grid(int rows, int num_sms);
+cudaError_t configure_attn_split();
+cudaError_t launch_attn_split(const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v,
+                              int rows, int dtype, int num_sms, cudaStream_t stream);
+// merges the partials of cut units into out / lse
+cudaError_t launch_attn_combine(const AttnParams& p, int rows, int ctas, int dtype,
+                                cudaStream_t stream);
+// merges, for every row, the prefix's and the sequence's own results into out / lse
+cudaError_t launch_attn_join(const AttnParams& own, int own_rows, const AttnParams& shared,
+                             int shared_rows, int own_tile, int shared_tile, int dtype,
+                             cudaStream_t stream);
+cudaError_t launch_attn_append(const AttnAppend& a, int dtype, int num_sms, cudaStream_t stream);
+
+}  // namespace coli

@@ -1,0 +1,373 @@
+// Host side of the paged-cache attention (coli_attn.h): argument checks, the workspace, the tensor maps
+// of a bound cache and the launch sequences.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <cmath>
+#include <mutex>
+#include <new>
+#include <vector>
+
+#include "attn_internal.h"
+
+using namespace coli;
+
+struct coli_attn {
+  coli_attn_config cfg{};
+  int device = 0, num_sms = 0, page_shift = 0, prefix_tokens = 0;
+  std::vector<void*> allocs;
+  float* part_o = nullptr;
+  float2* part_ml = nullptr;
+  AttnRec* rec = nullptr;
+  int64_t* seq_pos = nullptr;
+  // the shared half of a prefix call
+  float* part_o2 = nullptr;
+  float2* part_ml2 = nullptr;
+  AttnRec* rec2 = nullptr;
+  int64_t* seq_pos2 = nullptr;
+  float *dense_o = nullptr, *dense_o2 = nullptr;
+  float2 *dense_ml = nullptr, *dense_ml2 = nullptr;
+  uint64_t* turn = nullptr;
+  int32_t* status = nullptr;
+};
+
+struct coli_attn_kv {
+  coli_attn_cache c{};
+  int n_kv = 0, head_dim = 0, page = 0, dtype = 0, device = 0;
+  AttnKvMaps maps;
+};
+
+namespace {
+
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                                CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                                CUtensorMapFloatOOBfill);
+
+// the driver's tensor-map encoder, looked up through the runtime (no link against libcuda)
+EncodeTiled encoder() {
+  static EncodeTiled fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      p = nullptr;
+    }
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  return fn;
+}
+
+// cache memory as [page][head][slot][value], boxes of 64 values x `slots` slots
+bool cache_map(CUtensorMap* map, const void* base, const coli_attn_kv& kv, int64_t ps, int64_t hs,
+               int64_t ss, int slots) {
+  EncodeTiled fn = encoder();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)kv.head_dim, (cuuint64_t)kv.page, (cuuint64_t)kv.n_kv,
+                              (cuuint64_t)kv.c.n_pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)ss * 2, (cuuint64_t)hs * 2, (cuuint64_t)ps * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)(kv.page < slots ? kv.page : slots), 1, 1};
+  const cuuint32_t unit[4] = {1, 1, 1, 1};
+  return fn(map, kv.dtype == COLI_ATTN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+            4, const_cast<void*>(base), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class T>
+int dalloc(coli_attn* h, T** p, size_t count) {
+  void* q = nullptr;
+  if (cudaMalloc(&q, (count ? count : 1) * sizeof(T)) != cudaSuccess) {
+    cudaGetLastError();
+    return COLI_ENOMEM;
+  }
+  h->allocs.push_back(q);
+  *p = static_cast<T*>(q);
+  return COLI_OK;
+}
+
+void free_all(coli_attn* h) {
+  for (void* p : h->allocs) cudaFree(p);
+  h->allocs.clear();
+}
+
+constexpr int kMaxDevices = 64;
+bool g_configured[kMaxDevices] = {};
+std::mutex g_mutex;
+
+// shared-memory attributes, once per device
+cudaError_t configure_device(int dev) {
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(g_mutex);
+  if (g_configured[dev]) return cudaSuccess;
+  const cudaError_t e = configure_attn_split();
+  if (e == cudaSuccess) g_configured[dev] = true;
+  return e;
+}
+
+bool misaligned(const void* p, int64_t stride) { return ((uintptr_t)p & 15u) || (stride & 7); }
+
+int check_device(int device) {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return COLI_ECUDA;
+  return dev == device ? COLI_OK : COLI_ESTATE;
+}
+
+int check_call(const coli_attn* h, const coli_attn_kv* kv, const coli_attn_batch* b) {
+  if (!h || !kv || !b) return COLI_EINVAL;
+  const coli_attn_config& c = h->cfg;
+  if (kv->n_kv != c.n_kv || kv->head_dim != c.head_dim || kv->page != c.page || kv->dtype != c.dtype ||
+      kv->device != h->device)
+    return COLI_EINVAL;
+  if (b->n_tokens < 0 || b->n_tokens > c.max_tokens || b->n_seqs < 0 || b->n_seqs > c.max_seqs) return COLI_EINVAL;
+  if (b->n_tokens == 0) return COLI_OK;
+  if (b->n_seqs == 0 || !b->q_start || !b->kv_len || b->max_pages < 0 || b->table_stride < b->max_pages ||
+      b->max_q < 1 || (b->max_pages > 0 && !b->table) ||
+      ((int64_t)b->max_pages << h->page_shift) > kAttnNoWindow)
+    return COLI_EINVAL;
+  return check_device(h->device);
+}
+
+AttnParams params(const coli_attn* h, const coli_attn_kv* kv, const coli_attn_batch* b, const void* q,
+                  int64_t q_stride, void* out, int64_t out_stride, float* lse, float scale) {
+  AttnParams p = {};
+  p.q = q, p.q_stride = q_stride, p.out = out, p.out_stride = out_stride, p.lse = lse;
+  p.q_start = b->q_start, p.kv_len = b->kv_len, p.table = b->table, p.table_stride = b->table_stride;
+  p.n_seqs = b->n_seqs, p.n_tokens = b->n_tokens, p.max_pages = b->max_pages;
+  p.n_q = h->cfg.n_q, p.n_kv = h->cfg.n_kv, p.group = h->cfg.n_q / h->cfg.n_kv, p.head_dim = h->cfg.head_dim;
+  p.page_shift = h->page_shift, p.n_pages = (int)kv->c.n_pages;
+  p.window = kAttnNoWindow, p.sinks = 0, p.causal = 1;
+  p.scale_log2 = scale * 1.44269504088896340736f;
+  p.rows_lo = 0, p.rows_hi = INT64_MAX;
+  p.part_o = h->part_o, p.part_ml = h->part_ml, p.rec = h->rec, p.seq_pos = h->seq_pos;
+  p.status = h->status;
+  return p;
+}
+
+int rows_of(const coli_attn* h, int64_t tokens) {
+  const int64_t rows = tokens * (h->cfg.n_q / h->cfg.n_kv);
+  return split_rows((int)(rows < 64 ? rows : 64));
+}
+
+int query_args(const coli_attn* h, int64_t n_tokens, const void* q, int64_t q_stride, const void* out,
+               int64_t out_stride, float scale) {
+  const int64_t width = (int64_t)h->cfg.n_q * h->cfg.head_dim;
+  if (!q || !out || misaligned(q, q_stride) || misaligned(out, out_stride) || q_stride < width ||
+      out_stride < width || !(scale > 0.f) || !std::isfinite(scale))
+    return COLI_EINVAL;
+  const char *qa = static_cast<const char*>(q), *oa = static_cast<const char*>(out);
+  // rows may interleave (slices of one buffer); the same start cannot be meant
+  (void)n_tokens;
+  return qa == oa ? COLI_EINVAL : COLI_OK;
+}
+
+}  // namespace
+
+extern "C" int coli_attn_create(const coli_attn_config* cfg, coli_attn** out) {
+  if (out) *out = nullptr;
+  if (!cfg || !out) return COLI_EINVAL;
+  const coli_attn_config& c = *cfg;
+  if (c.n_kv < 1 || c.n_kv > 256 || c.n_q < 1 || c.n_q % c.n_kv || c.max_tokens < 1 || c.max_tokens > 4194304 ||
+      c.max_seqs < 1 || c.max_seqs > kAttnMaxSeqs || c.rot_dim < 0 || c.page < 1 || c.head_dim < 1)
+    return COLI_EINVAL;
+  if (c.rot_interleaved != 0 && c.rot_interleaved != 1) return COLI_EINVAL;
+  if (c.rot_dim > 0 && !c.inv_freq && !(c.rope_base > 0.0 && std::isfinite(c.rope_base))) return COLI_EINVAL;
+  if ((c.head_dim != 64 && c.head_dim != 128) || (c.dtype != COLI_ATTN_BF16 && c.dtype != COLI_ATTN_FP16) ||
+      c.n_q / c.n_kv > kAttnMaxGroup || c.rot_dim > c.head_dim || c.rot_dim % 16)
+    return COLI_EUNSUPPORTED;
+  int shift = 0;
+  while ((1 << shift) < c.page) ++shift;
+  if ((1 << shift) != c.page || c.page < 16 || c.page > 256) return COLI_EUNSUPPORTED;
+  std::vector<uint64_t> turn;
+  for (int i = 0; i < c.rot_dim / 2; ++i) {
+    const long double f = c.inv_freq ? (long double)c.inv_freq[i]
+                                     : powl((long double)c.rope_base, -2.0L * i / c.rot_dim);
+    if (!std::isfinite((double)f)) return COLI_EINVAL;
+    long double t = f / 6.283185307179586476925286766559005768L;
+    t -= floorl(t);  // whole turns do not count
+    long double v = floorl(t * 18446744073709551616.0L + 0.5L);
+    turn.push_back(v >= 18446744073709551616.0L ? 0 : (uint64_t)v);
+  }
+
+  coli_attn* h = new (std::nothrow) coli_attn();
+  if (!h) return COLI_ENOMEM;
+  h->cfg = c;
+  h->cfg.inv_freq = nullptr;  // read above; not kept
+  h->page_shift = shift;
+  cudaDeviceProp prop;
+  int rc = COLI_OK;
+  if (cudaGetDevice(&h->device) != cudaSuccess || cudaGetDeviceProperties(&prop, h->device) != cudaSuccess ||
+      configure_device(h->device) != cudaSuccess) {
+    cudaGetLastError();
+    rc = COLI_ECUDA;
+  }
+  if (!rc) {
+    h->num_sms = prop.multiProcessorCount;
+    const size_t D = c.head_dim, ctas = (size_t)2 * h->num_sms;
+    // partials: two per CTA of the split kernel, 2 CTAs an SM of 16 rows or one of up to 64
+    const size_t rows = 2 * (size_t)h->num_sms * 64;
+    // the prefix call keeps every row twice: up to kAttnPrefixRows tokens a sequence
+    const int64_t pt = (int64_t)kAttnPrefixRows * c.max_seqs;
+    h->prefix_tokens = (int)(pt < c.max_tokens ? pt : c.max_tokens);
+    const size_t dense = (size_t)h->prefix_tokens * c.n_q;
+    if (!rc) rc = dalloc(h, &h->part_o, rows * D);
+    if (!rc) rc = dalloc(h, &h->part_ml, rows);
+    if (!rc) rc = dalloc(h, &h->rec, ctas);
+    if (!rc) rc = dalloc(h, &h->seq_pos, c.max_seqs + 2);
+    if (!rc) rc = dalloc(h, &h->part_o2, rows * D);
+    if (!rc) rc = dalloc(h, &h->part_ml2, rows);
+    if (!rc) rc = dalloc(h, &h->rec2, ctas);
+    if (!rc) rc = dalloc(h, &h->seq_pos2, 3);
+    if (!rc) rc = dalloc(h, &h->dense_o, dense * D);
+    if (!rc) rc = dalloc(h, &h->dense_ml, dense);
+    if (!rc) rc = dalloc(h, &h->dense_o2, dense * D);
+    if (!rc) rc = dalloc(h, &h->dense_ml2, dense);
+    if (!rc) rc = dalloc(h, &h->turn, turn.size());
+    if (!rc) rc = dalloc(h, &h->status, 4);
+    if (!rc && ((!turn.empty() && cudaMemcpy(h->turn, turn.data(), turn.size() * 8, cudaMemcpyHostToDevice) != cudaSuccess) ||
+                cudaMemset(h->status, 0, 16) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess))
+      rc = COLI_ECUDA;
+  }
+  if (rc) {
+    free_all(h);
+    delete h;
+    return rc;
+  }
+  *out = h;
+  return COLI_OK;
+}
+
+extern "C" void coli_attn_destroy(coli_attn* h) {
+  if (!h) return;
+  cudaDeviceSynchronize();
+  free_all(h);
+  delete h;
+}
+
+extern "C" int coli_attn_cache_bind(coli_attn* h, const coli_attn_cache* cache, coli_attn_kv** out) {
+  if (out) *out = nullptr;
+  if (!h || !cache || !out) return COLI_EINVAL;
+  const coli_attn_cache& c = *cache;
+  if (!c.k || !c.v || c.n_pages < 1 || c.n_pages > 0x7FFFFFFE) return COLI_EINVAL;
+  const int64_t D = h->cfg.head_dim;
+  const int64_t strides[6] = {c.k_page_stride, c.k_head_stride, c.k_slot_stride,
+                              c.v_page_stride, c.v_head_stride, c.v_slot_stride};
+  for (int64_t s : strides)
+    if (s < D || (s & 7) || s >= (1LL << 38)) return COLI_EINVAL;
+  if (((uintptr_t)c.k & 15u) || ((uintptr_t)c.v & 15u)) return COLI_EINVAL;
+  int rc = check_device(h->device);
+  if (rc) return rc;
+  coli_attn_kv* kv = new (std::nothrow) coli_attn_kv();
+  if (!kv) return COLI_ENOMEM;
+  kv->c = c;
+  kv->n_kv = h->cfg.n_kv, kv->head_dim = h->cfg.head_dim, kv->page = h->cfg.page;
+  kv->dtype = h->cfg.dtype, kv->device = h->device;
+  if (!cache_map(&kv->maps.k64, c.k, *kv, c.k_page_stride, c.k_head_stride, c.k_slot_stride, kSplitKeys) ||
+      !cache_map(&kv->maps.v64, c.v, *kv, c.v_page_stride, c.v_head_stride, c.v_slot_stride, kSplitKeys) ||
+      !cache_map(&kv->maps.k128, c.k, *kv, c.k_page_stride, c.k_head_stride, c.k_slot_stride, kTileKeys) ||
+      !cache_map(&kv->maps.v128, c.v, *kv, c.v_page_stride, c.v_head_stride, c.v_slot_stride, kTileKeys)) {
+    delete kv;
+    return COLI_ECUDA;
+  }
+  *out = kv;
+  return COLI_OK;
+}
+
+extern "C" void coli_attn_cache_release(coli_attn_kv* kv) { delete kv; }
+
+extern "C" int coli_attn_append(coli_attn* h, const coli_attn_kv* kv, const coli_attn_batch* b,
+                                const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                const void* v, int64_t v_stride, void* q_out, int64_t q_out_stride,
+                                const int32_t* pos_base, void* stream) {
+  const int rc = check_call(h, kv, b);
+  if (rc) return rc;
+  if (b->n_tokens == 0) return COLI_OK;
+  const int64_t kvw = (int64_t)h->cfg.n_kv * h->cfg.head_dim, qw = (int64_t)h->cfg.n_q * h->cfg.head_dim;
+  if (!k || !v || misaligned(k, k_stride) || misaligned(v, v_stride) || k_stride < kvw || v_stride < kvw)
+    return COLI_EINVAL;
+  if ((q == nullptr) != (q_out == nullptr)) return COLI_EINVAL;
+  if (q && (misaligned(q, q_stride) || misaligned(q_out, q_out_stride) || q_stride < qw || q_out_stride < qw ||
+            (q == q_out && q_stride != q_out_stride)))
+    return COLI_EINVAL;
+  AttnAppend a = {};
+  a.q = q, a.k = k, a.v = v, a.q_out = q_out, a.kc = kv->c.k, a.vc = kv->c.v;
+  a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride, a.q_out_stride = q_out_stride;
+  a.kp = kv->c.k_page_stride, a.kh = kv->c.k_head_stride, a.ks = kv->c.k_slot_stride;
+  a.vp = kv->c.v_page_stride, a.vh = kv->c.v_head_stride, a.vs = kv->c.v_slot_stride;
+  a.q_start = b->q_start, a.kv_len = b->kv_len, a.table = b->table, a.table_stride = b->table_stride;
+  a.n_seqs = b->n_seqs, a.n_tokens = b->n_tokens, a.max_pages = b->max_pages;
+  a.n_pages = (int)kv->c.n_pages, a.page_shift = h->page_shift;
+  a.n_q = h->cfg.n_q, a.n_kv = h->cfg.n_kv, a.head_dim = h->cfg.head_dim;
+  a.rot = h->cfg.rot_dim, a.interleaved = h->cfg.rot_interleaved;
+  a.pos_base = pos_base, a.turn = h->turn, a.status = h->status;
+  return launch_attn_append(a, h->cfg.dtype, h->num_sms, (cudaStream_t)stream) == cudaSuccess ? COLI_OK
+                                                                                               : COLI_ECUDA;
+}
+
+extern "C" int coli_attn_window(coli_attn* h, const coli_attn_kv* kv, const coli_attn_batch* b, const void* q,
+                                int64_t q_stride, int window, int sinks, float scale, void* out,
+                                int64_t out_stride, float* lse, void* stream) {
+  int rc = check_call(h, kv, b);
+  if (rc) return rc;
+  if (sinks < 0) return COLI_EINVAL;
+  if (b->n_tokens == 0) return COLI_OK;
+  rc = query_args(h, b->n_tokens, q, q_stride, out, out_stride, scale);
+  if (rc) return rc;
+  cudaStream_t st = (cudaStream_t)stream;
+  AttnParams p = params(h, kv, b, q, q_stride, out, out_stride, lse, scale);
+  if (window >= 0 && window < kAttnNoWindow) p.window = window, p.sinks = sinks;
+  const int rows = rows_of(h, b->max_q);
+  p.block_tokens = rows / p.group;
+  cudaError_t e = launch_attn_split(p, kv->maps.k64, kv->maps.v64, rows, h->cfg.dtype, h->num_sms, st);
+  if (e == cudaSuccess) e = launch_attn_combine(p, rows, split_grid(rows, h->num_sms), h->cfg.dtype, st);
+  return e == cudaSuccess ? COLI_OK : COLI_ECUDA;
+}
+
+extern "C" int coli_attn_prefix(coli_attn* h, const coli_attn_kv* kv, const coli_attn_batch* b,
+                                const int32_t* prefix_table, int prefix_pages, const int32_t* prefix_len,
+                                const void* q, int64_t q_stride, float scale, void* out, int64_t out_stride,
+                                float* lse, void* stream) {
+  int rc = check_call(h, kv, b);
+  if (rc) return rc;
+  if (prefix_pages < 0 || (prefix_pages > 0 && !prefix_table) || !prefix_len ||
+      ((int64_t)prefix_pages << h->page_shift) > kAttnNoWindow || b->n_tokens > h->prefix_tokens)
+    return COLI_EINVAL;
+  if (b->n_tokens == 0) return COLI_OK;
+  rc = query_args(h, b->n_tokens, q, q_stride, out, out_stride, scale);
+  if (rc) return rc;
+  cudaStream_t st = (cudaStream_t)stream;
+  AttnParams own = params(h, kv, b, q, q_stride, out, out_stride, lse, scale);
+  own.dense_o = h->dense_o, own.dense_ml = h->dense_ml;
+  AttnParams pre = own;
+  pre.q_start = nullptr, pre.kv_len = prefix_len, pre.table = prefix_table, pre.table_stride = prefix_pages;
+  pre.n_seqs = 1, pre.max_pages = prefix_pages, pre.causal = 0;
+  pre.part_o = h->part_o2, pre.part_ml = h->part_ml2, pre.rec = h->rec2, pre.seq_pos = h->seq_pos2;
+  pre.dense_o = h->dense_o2, pre.dense_ml = h->dense_ml2;
+  const int own_rows = rows_of(h, b->max_q), pre_rows = rows_of(h, b->n_tokens);
+  own.block_tokens = own_rows / own.group;
+  pre.block_tokens = pre_rows / own.group;
+  cudaError_t e = launch_attn_split(own, kv->maps.k64, kv->maps.v64, own_rows, h->cfg.dtype, h->num_sms, st);
+  if (e == cudaSuccess)
+    e = launch_attn_split(pre, kv->maps.k64, kv->maps.v64, pre_rows, h->cfg.dtype, h->num_sms, st);
+  if (e == cudaSuccess)
+    e = launch_attn_join(own, own_rows, pre, pre_rows, kSplitKeys, kSplitKeys, h->cfg.dtype, st);
+  return e == cudaSuccess ? COLI_OK : COLI_ECUDA;
+}
+
+extern "C" int coli_attn_status(coli_attn* h, void* stream) {
+  if (!h) return COLI_EINVAL;
+  const int rc = check_device(h->device);
+  if (rc) return rc;
+  cudaStream_t st = (cudaStream_t)stream;
+  int32_t v = 0;
+  if (cudaMemcpyAsync(&v, h->status, sizeof(v), cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+      cudaMemsetAsync(h->status, 0, sizeof(v), st) != cudaSuccess || cudaStreamSynchronize(st) != cudaSuccess)
+    return COLI_ECUDA;
+  return v;
+}
+
+extern "C" int coli_attn_launches(const coli_attn* h, int op, int max_q) {
+  if (!h || op < 0 || op > 2 || max_q < 1) return COLI_EINVAL;
+  return op == 0 ? 1 : op == 1 ? 2 : 3;
+}

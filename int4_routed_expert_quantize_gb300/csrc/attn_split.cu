@@ -1,0 +1,394 @@
+// Attention of few query rows over a paged cache: o = softmax(scale q K^T) V with a running
+// maximum and sum, one pass over the keys.
+//
+// A block is up to 16, 32 or 64 rows: the query heads of one key head times the tokens of
+// one sequence.  At such sizes every key and value byte is used by few rows, so the kernel is bound
+// by HBM and is built around the copies: one warp keeps a ring of key tiles (64 keys, K and
+// V) full with tensor copies straight from the pages, and the other warps each take 16 or 32
+// keys of a tile for 16 rows with mma.sync and a running softmax of their own, joined once
+// at the end of the unit, so nothing but the ring synchronises them.  Legacy mma.sync suffices: its rate
+// is several times what the copies can feed at these row counts, and its fragments keep P in
+// registers.  The list of all units' key tiles is cut into equal stretches, one per CTA, so a
+// single long sequence and many short ones fill the GPU alike.
+#include "attn_device.cuh"
+
+namespace coli {
+
+namespace {
+
+static_assert(sizeof(Stretch) + 4 <= 80, "tail of the shared memory");
+
+template <int D, int RG>
+struct SplitCfg {
+  static constexpr int KG = RG == 4 ? 2 : 4;  // key groups: warps that share 16 rows
+  static constexpr int warps = RG * KG;
+  static constexpr int threads = (warps + 1) * 32;
+  static constexpr int rows = RG * 16;
+  static constexpr int kw = kSplitKeys / KG;  // keys per warp and tile
+  static constexpr int ctas = RG == 1 ? 2 : 1;  // per SM
+  static constexpr int tile_bytes = kSplitKeys * D * 2;
+  static constexpr int stages = (RG == 1 ? 98304 : 163840) / (2 * tile_bytes);
+  static constexpr int merge_floats = 16 * D + 32;
+  static constexpr int merge_bytes = RG * (KG / 2) * merge_floats * 4;
+  static constexpr int smem = stages * 2 * tile_bytes + merge_bytes + 2 * stages * 8 + 80;
+};
+
+// 16 rows x kw keys of one tile for one warp
+template <class T, int D, int RG, bool Masked>
+__device__ __forceinline__ void tile_step(const AttnParams& p, uint32_t ks, uint32_t vs, int key0,
+                                          int p0, int p1, const int (&pos)[2], int tok_lo, int tok_hi,
+                                          const uint32_t (&qf)[D / 16][4], float (&o)[D / 8][4],
+                                          float (&mx)[2], float (&sum)[2], int lane, int row0) {
+  using C = SplitCfg<D, RG>;
+  constexpr int NT = C::kw / 8;
+  const int c2 = (lane & 3) * 2;
+  float s[NT][4];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[n][i] = 0.f;
+  const int kloc = key0 & (kSplitKeys - 1);  // the warp's first key within the tile
+#pragma unroll
+  for (int n = 0; n < NT; n += 2) {
+    const int row = kloc + n * 8 + ((lane >> 4) << 3) + (lane & 7);
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      const int ch = (k * 2 + ((lane >> 3) & 1));
+      uint32_t b[4];
+      ldsm4(ks + (ch >> 3) * kSplitKeys * 128 + row * 128 + (((ch & 7) ^ (row & 7)) << 4), b);
+      mma16816<T>(s[n], qf[k], b[0], b[1]);
+      mma16816<T>(s[n + 1], qf[k], b[2], b[3]);
+    }
+  }
+  if (Masked) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (!sees(p, pos[i >> 1], key0 + n * 8 + c2 + (i & 1))) s[n][i] = -INFINITY;
+  }
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    float m = mx[r];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) m = fmaxf(m, fmaxf(s[n][2 * r], s[n][2 * r + 1]));
+    m = fmaxf(m, __shfl_xor_sync(FULL, m, 1));
+    m = fmaxf(m, __shfl_xor_sync(FULL, m, 2));
+    const float base = m == -INFINITY ? 0.f : m * p.scale_log2;
+    const float fix = ex2(mx[r] * p.scale_log2 - base);  // mx = -inf: 0, and o, sum are 0
+    mx[r] = m;
+    float a = 0.f;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float e = ex2(fmaf(s[n][2 * r + i], p.scale_log2, -base));
+        s[n][2 * r + i] = e;
+        a += e;
+      }
+    sum[r] = fmaf(sum[r], fix, a);  // this thread's share of the row; joined at the end
+#pragma unroll
+    for (int d = 0; d < D / 8; ++d) {
+      o[d][2 * r] *= fix;
+      o[d][2 * r + 1] *= fix;
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < NT; n += 2) {
+    const uint32_t pf[4] = {T::pack(s[n][0], s[n][1]), T::pack(s[n][2], s[n][3]),
+                            T::pack(s[n + 1][0], s[n + 1][1]), T::pack(s[n + 1][2], s[n + 1][3])};
+    const int row = kloc + n * 8 + (lane & 15);
+    const int kk = key0 + n * 8 + c2;
+    uint32_t z0 = 0xFFFFFFFFu, z1 = 0xFFFFFFFFu;  // values of keys that no row sees become 0
+    if (Masked) {
+      z0 = (some_sees(p, p0, p1, kk) ? 0xFFFFu : 0u) | (some_sees(p, p0, p1, kk + 1) ? 0xFFFF0000u : 0u);
+      z1 = (some_sees(p, p0, p1, kk + 8) ? 0xFFFFu : 0u) |
+           (some_sees(p, p0, p1, kk + 9) ? 0xFFFF0000u : 0u);
+    }
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d) {
+      const int ch = d * 2 + (lane >> 4);
+      uint32_t b[4];
+      ldsm4t(vs + (ch >> 3) * kSplitKeys * 128 + row * 128 + (((ch & 7) ^ (row & 7)) << 4), b);
+      if (Masked) {
+        b[0] &= z0, b[2] &= z0;
+        b[1] &= z1, b[3] &= z1;
+        // A non-finite value that only some rows see must not reach the others (0 * inf = NaN):
+        // then each token's rows are multiplied on their own, with only the values they see.
+        uint32_t bad = 0;
+        if (tok_hi > tok_lo)
+          bad = nonfinite2<T>(b[0]) | nonfinite2<T>(b[1]) | nonfinite2<T>(b[2]) | nonfinite2<T>(b[3]);
+        if (__any_sync(FULL, bad != 0)) {
+          for (int t = tok_lo; t <= tok_hi; ++t) {
+            const int pt = p.causal ? p0 + t : p0;
+            const uint32_t y0 = (sees(p, pt, kk) ? 0xFFFFu : 0u) | (sees(p, pt, kk + 1) ? 0xFFFF0000u : 0u);
+            const uint32_t y1 =
+                (sees(p, pt, kk + 8) ? 0xFFFFu : 0u) | (sees(p, pt, kk + 9) ? 0xFFFF0000u : 0u);
+            float u[2][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) u[0][i] = o[2 * d][i], u[1][i] = o[2 * d + 1][i];
+            mma16816<T>(u[0], pf, b[0] & y0, b[1] & y1);
+            mma16816<T>(u[1], pf, b[2] & y0, b[3] & y1);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if ((row0 + (lane >> 2) + (i >> 1) * 8) / p.group == t) {
+                o[2 * d][i] = u[0][i];
+                o[2 * d + 1][i] = u[1][i];
+              }
+          }
+          continue;
+        }
+      }
+      mma16816<T>(o[2 * d], pf, b[0], b[1]);
+      mma16816<T>(o[2 * d + 1], pf, b[2], b[3]);
+    }
+  }
+}
+
+template <class T, int D, int RG>
+__global__ void __launch_bounds__(SplitCfg<D, RG>::threads, SplitCfg<D, RG>::ctas)
+    attn_split_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap,
+                      const __grid_constant__ CUtensorMap vmap) {
+  using C = SplitCfg<D, RG>;
+  constexpr int NST = C::stages;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  float* merge = reinterpret_cast<float*>(smem + NST * 2 * C::tile_bytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + NST * 2 * C::tile_bytes + C::merge_bytes);
+  uint64_t* empty = full + NST;
+  // (no static shared memory: with it, two CTAs of 16 rows would no longer fit one SM)
+  Stretch* stretch = reinterpret_cast<Stretch*>(empty + NST);
+  int* abort_flag = reinterpret_cast<int*>(stretch + 1);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    *abort_flag = 0;
+    for (int i = 0; i < NST; ++i) mbar_init(full + i, 1), mbar_init(empty + i, C::warps);
+    fence_barrier_init();
+    prefetch_map(&kmap);
+    prefetch_map(&vmap);
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+  const Stretch st = schedule<kSplitKeys>(p, reinterpret_cast<int64_t*>(smem), stretch);
+  if (warp == 0 && lane == 0) write_record<kSplitKeys>(p, st);
+  // the copies below overwrite what schedule() kept in the ring's memory
+  fence_proxy_async_smem();
+  __syncthreads();
+
+  Cursor<kSplitKeys> cur;
+  cur.start(p, st);
+  if (warp == C::warps) {  // ---- copies
+    int it = 0;
+    for (; cur.valid(); cur.next(p)) {
+      const int64_t row = (int64_t)cur.b * p.table_stride;
+      for (int i = cur.i0; i < cur.i1; ++i, ++it) {
+        const int sgi = it % NST;
+        if (it >= NST && !mbar_wait_bounded(empty + sgi, ((it / NST) + 1) & 1, abort_flag, p.status)) {
+          drain_fills(full, NST, it);
+          return;
+        }
+        uint8_t* dst = smem + sgi * 2 * C::tile_bytes;
+        const int j0 = cur.t.tile(i) * kSplitKeys;
+        const uint32_t bytes = fill_bytes<kSplitKeys, D>(p, cur.t.p0, cur.t.p1, j0, lane);
+        if (lane == 0) mbar_expect_tx(full + sgi, 2 * bytes);
+        __syncwarp();
+        fill_boxes<kSplitKeys, D>(p, &kmap, dst, full + sgi, row, cur.t.p0, cur.t.p1, j0, cur.head, lane);
+        fill_boxes<kSplitKeys, D>(p, &vmap, dst + C::tile_bytes, full + sgi, row, cur.t.p0, cur.t.p1, j0,
+                                  cur.head, lane);
+      }
+    }
+    return;
+  }
+
+  // ---- products
+  const int rg = warp % RG, kg = warp / RG;
+  const int row0 = rg * 16;  // this warp's rows of the block
+  int it = 0;
+  for (; cur.valid(); cur.next(p)) {
+    const int tok0 = cur.s.start + cur.blk * p.block_tokens;
+    const int nt = min(p.block_tokens, cur.s.n - cur.blk * p.block_tokens);
+    const int p0 = cur.t.p0, p1 = cur.t.p1;
+    int pos[2], tok[2];
+    bool live[2];
+    uint32_t qf[D / 16][4];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = row0 + (lane >> 2) + r * 8;
+      tok[r] = row / p.group;
+      live[r] = tok[r] < nt;
+      pos[r] = p.causal ? p0 + tok[r] : p0;
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(
+          static_cast<const uint16_t*>(p.q) + (int64_t)(tok0 + tok[r]) * p.q_stride +
+          (int64_t)(cur.head * p.group + row - tok[r] * p.group) * D);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        qf[k][r] = live[r] ? __ldg(src + k * 8 + (lane & 3)) : 0u;
+        qf[k][r + 2] = live[r] ? __ldg(src + k * 8 + 4 + (lane & 3)) : 0u;
+      }
+    }
+    const int tok_lo = row0 / p.group, tok_hi = min(nt - 1, (row0 + 15) / p.group);
+    float o[D / 8][4], mx[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+#pragma unroll
+    for (int d = 0; d < D / 8; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[d][i] = 0.f;
+
+    for (int i = cur.i0; i < cur.i1; ++i, ++it) {
+      const int sgi = it % NST;
+      if (!mbar_wait_bounded(full + sgi, (it / NST) & 1, abort_flag, p.status)) goto out;
+      {
+        const uint32_t ks = smem_addr(smem + sgi * 2 * C::tile_bytes), vs = ks + C::tile_bytes;
+        const int key0 = cur.t.tile(i) * kSplitKeys + kg * C::kw;
+        if (all_see(p, p0, p1, key0, key0 + C::kw - 1))
+          tile_step<T, D, RG, false>(p, ks, vs, key0, p0, p1, pos, tok_lo, tok_hi, qf, o, mx, sum, lane, row0);
+        else
+          tile_step<T, D, RG, true>(p, ks, vs, key0, p0, p1, pos, tok_lo, tok_hi, qf, o, mx, sum, lane, row0);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty + sgi);
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      sum[r] += __shfl_xor_sync(FULL, sum[r], 1);
+      sum[r] += __shfl_xor_sync(FULL, sum[r], 2);
+    }
+    // join the warps that share these rows: the upper half hands over to the lower half
+#pragma unroll
+    for (int half = C::KG / 2; half >= 1; half >>= 1) {
+      const int slot = (kg % half) * RG + rg;
+      float4* buf = reinterpret_cast<float4*>(merge + slot * C::merge_floats);
+      float2* ml = reinterpret_cast<float2*>(merge + slot * C::merge_floats + 16 * D);
+      named_bar_sync(1, C::warps * 32);
+      if (kg >= half && kg < 2 * half) {
+#pragma unroll
+        for (int d = 0; d < D / 8; ++d) buf[d * 32 + lane] = make_float4(o[d][0], o[d][1], o[d][2], o[d][3]);
+        if ((lane & 3) == 0) {
+          ml[lane >> 2] = make_float2(mx[0], sum[0]);
+          ml[(lane >> 2) + 8] = make_float2(mx[1], sum[1]);
+        }
+      }
+      named_bar_sync(1, C::warps * 32);
+      if (kg < half) {
+        float fa[2], fb[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float2 other = ml[(lane >> 2) + r * 8];
+          const float m = fmaxf(mx[r], other.x);
+          const float base = m == -INFINITY ? 0.f : m * p.scale_log2;
+          fa[r] = ex2(mx[r] * p.scale_log2 - base);
+          fb[r] = ex2(other.x * p.scale_log2 - base);
+          mx[r] = m;
+          sum[r] = sum[r] * fa[r] + other.y * fb[r];
+        }
+#pragma unroll
+        for (int d = 0; d < D / 8; ++d) {
+          const float4 v = buf[d * 32 + lane];
+          o[d][0] = o[d][0] * fa[0] + v.x * fb[0];
+          o[d][1] = o[d][1] * fa[0] + v.y * fb[0];
+          o[d][2] = o[d][2] * fa[1] + v.z * fb[1];
+          o[d][3] = o[d][3] * fa[1] + v.w * fb[1];
+        }
+      }
+    }
+    if (kg == 0) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = row0 + (lane >> 2) + r * 8;
+        const float m2 = mx[r] * p.scale_log2;  // -inf stays -inf
+        if (cur.whole() && !p.dense_o) {
+          if (!live[r]) continue;
+          const int hq = cur.head * p.group + row - tok[r] * p.group;
+          const float inv = sum[r] == 0.f ? 0.f : 1.f / sum[r];
+          uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) +
+                                                      (int64_t)(tok0 + tok[r]) * p.out_stride + (int64_t)hq * D);
+#pragma unroll
+          for (int d = 0; d < D / 8; ++d)
+            dst[d * 4 + (lane & 3)] = T::pack(o[d][2 * r] * inv, o[d][2 * r + 1] * inv);
+          if (p.lse && (lane & 3) == 0)
+            p.lse[(int64_t)(tok0 + tok[r]) * p.n_q + hq] =
+                sum[r] == 0.f ? -INFINITY : (m2 + log2f(sum[r])) * 0.69314718055994530942f;
+        } else {
+          int64_t at;
+          float* dst;
+          float2* ml;
+          if (cur.whole()) {
+            if (!live[r]) continue;
+            at = (int64_t)(tok0 + tok[r]) * p.n_q + cur.head * p.group + row - tok[r] * p.group;
+            dst = p.dense_o, ml = p.dense_ml;
+          } else {
+            at = ((int64_t)blockIdx.x * 2 + (cur.first ? 0 : 1)) * C::rows + row;
+            dst = p.part_o, ml = p.part_ml;
+          }
+#pragma unroll
+          for (int d = 0; d < D / 8; ++d)
+            *reinterpret_cast<float2*>(dst + at * D + d * 8 + (lane & 3) * 2) =
+                make_float2(o[d][2 * r], o[d][2 * r + 1]);
+          if ((lane & 3) == 0) ml[at] = make_float2(m2, sum[r]);
+        }
+      }
+    }
+  }
+out:
+  return;
+}
+
+typedef void (*SplitKernel)(const AttnParams, const CUtensorMap, const CUtensorMap);
+
+template <class T, int D, int RG>
+cudaError_t configure() {
+  return cudaFuncSetAttribute(attn_split_kernel<T, D, RG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              SplitCfg<D, RG>::smem);
+}
+
+template <class T, int D, int RG>
+cudaError_t launch(const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v, int grid,
+                   cudaStream_t stream) {
+  using C = SplitCfg<D, RG>;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(C::threads);
+  cfg.dynamicSmemBytes = C::smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_split_kernel<T, D, RG>, p, k, v);
+}
+
+template <class T, int D>
+cudaError_t launch_rows(const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v, int rows,
+                        int grid, cudaStream_t stream) {
+  if (rows == 16) return launch<T, D, 1>(p, k, v, grid, stream);
+  if (rows == 32) return launch<T, D, 2>(p, k, v, grid, stream);
+  return launch<T, D, 4>(p, k, v, grid, stream);
+}
+
+}  // namespace
+
+int split_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+int split_grid(int rows, int num_sms) { return split_rows(rows) == 16 ? 2 * num_sms : num_sms; }
+
+cudaError_t configure_attn_split() {
+  cudaError_t e = cudaSuccess;
+#define COLI_CFG(T, D)                                  \
+  if (e == cudaSuccess) e = configure<T, D, 1>();       \
+  if (e == cudaSuccess) e = configure<T, D, 2>();       \
+  if (e == cudaSuccess) e = configure<T, D, 4>();
+  COLI_CFG(Bf16, 64) COLI_CFG(Bf16, 128) COLI_CFG(Fp16, 64) COLI_CFG(Fp16, 128)
+#undef COLI_CFG
+  return e;
+}
+
+cudaError_t launch_attn_split(const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v,
+                              int rows, int dtype, int num_sms, cudaStream_t stream) {
+  const int r = split_rows(rows), grid = split_grid(rows, num_sms);
+  if (dtype == COLI_ATTN_BF16)
+    return p.head_dim == 64 ? launch_rows<Bf16, 64>(p, k, v, r, grid, stream)
+                            : launch_rows<Bf16, 128>(p, k, v, r, grid, stream);
+  return p.head_dim == 64 ? launch_rows<Fp16, 64>(p, k, v, r, grid, stream)
+                          : launch_rows<Fp16, 128>(p, k, v, r, grid, stream);
+}
+
+}  // namespace coli
