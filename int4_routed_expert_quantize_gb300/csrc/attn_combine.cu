@@ -71,14 +71,69 @@ struct Join {
   }
 };
 
+// One query row from its definition, by one warp: for the rare blocks that hold values which are not
+// finite and which only some of the block's rows see.  qf: D floats of shared memory.
 template <class T, int D>
-__global__ void __launch_bounds__(kWarps * 32)
-    attn_combine_kernel(const AttnParams p, int rows, int rows_per_block) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const AttnRec r = p.rec[blockIdx.x];
-  if (r.first_cta < 0) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__device__ void redo_row(const AttnParams& p, const SeqInfo& s, int b, int i, int hq, float* qf, int lane) {
+  constexpr int V = D / 32;
+  const int pos = s.len - s.n + i, head = hq / p.group;
+  const uint16_t* q = static_cast<const uint16_t*>(p.q) + (int64_t)(s.start + i) * p.q_stride + (int64_t)hq * D;
+  __syncwarp();
+  for (int d = lane * 2; d < D; d += 64) {
+    const uint32_t v = *reinterpret_cast<const uint32_t*>(q + d);
+    qf[d] = T::lo(v), qf[d + 1] = T::hi(v);
+  }
+  __syncwarp();
+  const int lo = p.window >= kAttnNoWindow ? 0 : max(0, pos - p.window + 1);
+  const auto slot = [&](const void* base, int64_t sp, int64_t sh, int64_t ss, int j) -> const uint16_t* {
+    const int id = __ldg(p.table + (int64_t)b * p.table_stride + (j >> p.page_shift));
+    if (id < 0 || id >= p.n_pages) return nullptr;  // reads as zeros
+    return static_cast<const uint16_t*>(base) + id * sp + head * sh + (j & ((1 << p.page_shift) - 1)) * ss;
+  };
+  Join<D> r;
+  for (int j0 = 0; j0 <= pos; j0 += 32) {
+    if (j0 >= p.sinks && j0 + 31 < lo) {
+      j0 = (lo & ~31) - 32;
+      continue;
+    }
+    const int j = j0 + lane;
+    float x = -INFINITY;
+    if (sees(p, pos, j)) {
+      const uint16_t* k = slot(p.kc, p.k_page, p.k_head, p.k_slot, j);
+      x = 0.f;
+      for (int d = 0; k && d < D; d += 2) {
+        const uint32_t v = *reinterpret_cast<const uint32_t*>(k + d);
+        x = fmaf(qf[d], T::lo(v), fmaf(qf[d + 1], T::hi(v), x));
+      }
+      x *= p.scale_log2;
+    }
+    const float top = fmaxf(r.m, warp_max(x)), base = top == -INFINITY ? 0.f : top;
+    const float keep = ex2(r.m - base), w = ex2(x - base);
+    float sum = w;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+    r.l = r.l * keep + sum;
+    r.m = top;
+#pragma unroll
+    for (int e = 0; e < V; ++e) r.o[e] *= keep;
+    for (int n = 0; n < 32; ++n) {
+      if (!sees(p, pos, j0 + n)) continue;
+      const float wn = __shfl_sync(FULL, w, n);
+      const uint16_t* v = slot(p.vc, p.v_page, p.v_head, p.v_slot, j0 + n);
+      if (!v) continue;
+#pragma unroll
+      for (int e = 0; e < V; e += 2) {
+        const uint32_t y = *reinterpret_cast<const uint32_t*>(v + lane * V + e);
+        r.o[e] = fmaf(wn, T::lo(y), r.o[e]), r.o[e + 1] = fmaf(wn, T::hi(y), r.o[e + 1]);
+      }
+    }
+  }
+  r.template write<T>(p, s.start + i, hq, lane);
+}
+
+template <class T, int D>
+__device__ __forceinline__ void join_parts(const AttnParams& p, const AttnRec& r, int rows, int rows_per_block,
+                                           int warp, int lane) {
   for (int i = warp; i < rows_per_block; i += kWarps) {
     const int row = blockIdx.y * rows_per_block + i;
     const int tok = row / p.group;
@@ -88,6 +143,37 @@ __global__ void __launch_bounds__(kWarps * 32)
       return ((int64_t)(r.first_cta + c) * 2 + (c == 0 ? r.first_slot : 0)) * rows + row;
     });
     j.template write<T>(p, r.token0 + tok, r.head * p.group + row - tok * p.group, lane);
+  }
+}
+
+template <class T, int D>
+__global__ void __launch_bounds__(kWarps * 32)
+    attn_combine_kernel(const AttnParams p, int rows, int rows_per_block) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const AttnRec r = p.rec[blockIdx.x];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int redo = p.redo ? min(__ldcg(p.redo_count), p.redo_cap) : 0;
+  bool mine = r.first_cta >= 0;
+  for (int k = 0; k < redo && mine; ++k) {
+    const int4 u = __ldcg(p.redo + k);
+    mine = u.x != r.seq || u.y != r.blk || u.z != r.head;
+  }
+  if (mine) join_parts<T, D>(p, r, rows, rows_per_block, warp, lane);
+  if (redo == 0) return;
+  __shared__ float qf[kWarps][D];
+  const int blocks = gridDim.x * gridDim.y, unit_rows = p.block_tokens * p.group;
+  for (int64_t k = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kWarps + warp; k < (int64_t)redo * unit_rows;
+       k += (int64_t)blocks * kWarps) {
+    const int4 u = __ldcg(p.redo + k / unit_rows);
+    const int row = (int)(k % unit_rows), i = u.y * p.block_tokens + row / p.group;
+    const SeqInfo s = seq_info(p, u.x);
+    if (i < s.n) redo_row<T, D>(p, s, u.x, i, u.z * p.group + row % p.group, qf[warp], lane);
+  }
+  __syncthreads();  // this block has read the list; the last block empties it for the next call
+  if (threadIdx.x == 0 && atomicAdd(p.redo_count + 1, 1) == blocks - 1) {
+    p.redo_count[0] = 0;
+    p.redo_count[1] = 0;
   }
 }
 
@@ -187,6 +273,8 @@ cudaError_t join(const AttnParams& own, int own_rows, const AttnParams& shared, 
   const dim3 grid((unsigned)(((int64_t)own.n_tokens * own.n_q + kWarps - 1) / kWarps));
   if (ot == kSplitKeys && st == kSplitKeys)
     return go(attn_join_kernel<T, D, kSplitKeys, kSplitKeys>, grid, stream, own, own_rows, shared, shared_rows);
+  if (ot == kSplitKeys && st == kTileKeys)
+    return go(attn_join_kernel<T, D, kSplitKeys, kTileKeys>, grid, stream, own, own_rows, shared, shared_rows);
   return cudaErrorInvalidValue;
 }
 

@@ -14,6 +14,7 @@ constexpr int kAttnMaxSeqs = 4096;
 constexpr int kAttnMaxGroup = 64;     // query heads per key head
 constexpr int kAttnPrefixRows = 8;    // tokens per sequence the prefix workspace is sized for
 constexpr int kAttnNoWindow = 1 << 30;
+constexpr int kSplitMaxRows = 64;     // rows of a sequence up to which the split kernel takes it
 constexpr int kSplitKeys = 64;        // keys per tile of the split kernel
 constexpr int kTileKeys = 128;        // keys per tile of the tensor-memory kernel
 constexpr int kTileRows = 256;        // query rows per block of the tensor-memory kernel (2 x 128)
@@ -28,7 +29,7 @@ struct AttnRec {
   int first_slot;           // partial slot (0 or 1) of first_cta; all others have theirs in slot 0
   int token0, tokens;       // the unit's query tokens
   int head;                 // key head
-  int pad[2];
+  int seq, blk;
 };
 
 struct AttnParams {
@@ -56,6 +57,11 @@ struct AttnParams {
   int64_t* seq_pos;  // [n_seqs + 2] first list position of each sequence, the total, the stretch
   float* dense_o;    // prefix only: rows of uncut units go here, unnormalised, by (token, head)
   float2* dense_ml;
+  int4* redo;        // units (sequence, block, key head) that the tensor-memory kernel leaves to the
+  int* redo_count;   // kernel after it; [0] how many, [1] blocks of that kernel that are done
+  int redo_cap;
+  int64_t k_page, k_head, k_slot, v_page, v_head, v_slot;  // cache strides, for those units
+  const void *kc, *vc;
   int* status;
 };
 
@@ -83,6 +89,10 @@ int split_grid(int rows, int num_sms);
 cudaError_t configure_attn_split();
 cudaError_t launch_attn_split(const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v,
                               int rows, int dtype, int num_sms, cudaStream_t stream);
+int tile_block_tokens(int group);  // tokens per block of the tensor-memory kernel
+cudaError_t configure_attn_tile();
+cudaError_t launch_attn_tile(const AttnParams& p, const CUtensorMap& q, const CUtensorMap& k,
+                             const CUtensorMap& v, int dtype, int num_sms, cudaStream_t stream);
 // merges the partials of cut units into out / lse
 cudaError_t launch_attn_combine(const AttnParams& p, int rows, int ctas, int dtype,
                                 cudaStream_t stream);

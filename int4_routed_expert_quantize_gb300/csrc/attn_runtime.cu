@@ -20,13 +20,16 @@ struct coli_attn {
   float2* part_ml = nullptr;
   AttnRec* rec = nullptr;
   int64_t* seq_pos = nullptr;
-  // the shared half of a prefix call
+  // the tensor-memory kernel's (beside the split kernel's: one call may run both)
   float* part_o2 = nullptr;
   float2* part_ml2 = nullptr;
   AttnRec* rec2 = nullptr;
   int64_t* seq_pos2 = nullptr;
   float *dense_o = nullptr, *dense_o2 = nullptr;
   float2 *dense_ml = nullptr, *dense_ml2 = nullptr;
+  int4* redo = nullptr;
+  int* redo_count = nullptr;
+  int redo_cap = 0;
   uint64_t* turn = nullptr;
   int32_t* status = nullptr;
 };
@@ -101,7 +104,8 @@ cudaError_t configure_device(int dev) {
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> lock(g_mutex);
   if (g_configured[dev]) return cudaSuccess;
-  const cudaError_t e = configure_attn_split();
+  cudaError_t e = configure_attn_split();
+  if (e == cudaSuccess) e = configure_attn_tile();
   if (e == cudaSuccess) g_configured[dev] = true;
   return e;
 }
@@ -141,8 +145,33 @@ AttnParams params(const coli_attn* h, const coli_attn_kv* kv, const coli_attn_ba
   p.scale_log2 = scale * 1.44269504088896340736f;
   p.rows_lo = 0, p.rows_hi = INT64_MAX;
   p.part_o = h->part_o, p.part_ml = h->part_ml, p.rec = h->rec, p.seq_pos = h->seq_pos;
+  p.k_page = kv->c.k_page_stride, p.k_head = kv->c.k_head_stride, p.k_slot = kv->c.k_slot_stride;
+  p.v_page = kv->c.v_page_stride, p.v_head = kv->c.v_head_stride, p.v_slot = kv->c.v_slot_stride;
+  p.kc = kv->c.k, p.vc = kv->c.v;
   p.status = h->status;
   return p;
+}
+
+// queries as [token][head][value], boxes of 64 values x the heads of a key head x half a block's tokens
+bool query_map(CUtensorMap* map, const coli_attn* h, const void* q, int64_t q_stride, int n_tokens) {
+  EncodeTiled fn = encoder();
+  if (!fn) return false;
+  const int G = h->cfg.n_q / h->cfg.n_kv;
+  const cuuint64_t dims[3] = {(cuuint64_t)h->cfg.head_dim, (cuuint64_t)h->cfg.n_q, (cuuint64_t)n_tokens};
+  const cuuint64_t strides[2] = {(cuuint64_t)h->cfg.head_dim * 2, (cuuint64_t)q_stride * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)(tile_block_tokens(G) / 2)};
+  const cuuint32_t unit[3] = {1, 1, 1};
+  return fn(map, h->cfg.dtype == COLI_ATTN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+            3, const_cast<void*>(q), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// switches a launch's parameters to the tensor-memory kernel's workspace and blocks
+void use_tile(const coli_attn* h, AttnParams* p) {
+  p->part_o = h->part_o2, p->part_ml = h->part_ml2, p->rec = h->rec2, p->seq_pos = h->seq_pos2;
+  p->redo = h->redo, p->redo_count = h->redo_count, p->redo_cap = h->redo_cap;
+  p->block_tokens = tile_block_tokens(p->group);
 }
 
 int rows_of(const coli_attn* h, int64_t tokens) {
@@ -205,8 +234,10 @@ extern "C" int coli_attn_create(const coli_attn_config* cfg, coli_attn** out) {
   if (!rc) {
     h->num_sms = prop.multiProcessorCount;
     const size_t D = c.head_dim, ctas = (size_t)2 * h->num_sms;
-    // partials: two per CTA of the split kernel, 2 CTAs an SM of 16 rows or one of up to 64
-    const size_t rows = 2 * (size_t)h->num_sms * 64;
+    // partials: two per CTA of the split kernel (2 CTAs an SM of 16 rows or one of up to 64) and of the
+    // tensor-memory kernel
+    const size_t rows = 2 * (size_t)h->num_sms * 64, rows2 = 2 * (size_t)h->num_sms * kTileRows;
+    h->redo_cap = (int)(((size_t)c.max_tokens / tile_block_tokens(c.n_q / c.n_kv) + c.max_seqs) * c.n_kv) + 8 * h->num_sms;
     // the prefix call keeps every row twice: up to kAttnPrefixRows tokens a sequence
     const int64_t pt = (int64_t)kAttnPrefixRows * c.max_seqs;
     h->prefix_tokens = (int)(pt < c.max_tokens ? pt : c.max_tokens);
@@ -215,18 +246,20 @@ extern "C" int coli_attn_create(const coli_attn_config* cfg, coli_attn** out) {
     if (!rc) rc = dalloc(h, &h->part_ml, rows);
     if (!rc) rc = dalloc(h, &h->rec, ctas);
     if (!rc) rc = dalloc(h, &h->seq_pos, c.max_seqs + 2);
-    if (!rc) rc = dalloc(h, &h->part_o2, rows * D);
-    if (!rc) rc = dalloc(h, &h->part_ml2, rows);
+    if (!rc) rc = dalloc(h, &h->part_o2, rows2 * D);
+    if (!rc) rc = dalloc(h, &h->part_ml2, rows2);
     if (!rc) rc = dalloc(h, &h->rec2, ctas);
-    if (!rc) rc = dalloc(h, &h->seq_pos2, 3);
+    if (!rc) rc = dalloc(h, &h->seq_pos2, c.max_seqs + 2);
     if (!rc) rc = dalloc(h, &h->dense_o, dense * D);
     if (!rc) rc = dalloc(h, &h->dense_ml, dense);
     if (!rc) rc = dalloc(h, &h->dense_o2, dense * D);
     if (!rc) rc = dalloc(h, &h->dense_ml2, dense);
+    if (!rc) rc = dalloc(h, &h->redo, h->redo_cap);
+    if (!rc) rc = dalloc(h, &h->redo_count, 2);
     if (!rc) rc = dalloc(h, &h->turn, turn.size());
     if (!rc) rc = dalloc(h, &h->status, 4);
     if (!rc && ((!turn.empty() && cudaMemcpy(h->turn, turn.data(), turn.size() * 8, cudaMemcpyHostToDevice) != cudaSuccess) ||
-                cudaMemset(h->status, 0, 16) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess))
+                cudaMemset(h->status, 0, 16) != cudaSuccess || cudaMemset(h->redo_count, 0, 8) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess))
       rc = COLI_ECUDA;
   }
   if (rc) {
@@ -317,10 +350,25 @@ extern "C" int coli_attn_window(coli_attn* h, const coli_attn_kv* kv, const coli
   cudaStream_t st = (cudaStream_t)stream;
   AttnParams p = params(h, kv, b, q, q_stride, out, out_stride, lse, scale);
   if (window >= 0 && window < kAttnNoWindow) p.window = window, p.sinks = sinks;
-  const int rows = rows_of(h, b->max_q);
-  p.block_tokens = rows / p.group;
-  cudaError_t e = launch_attn_split(p, kv->maps.k64, kv->maps.v64, rows, h->cfg.dtype, h->num_sms, st);
-  if (e == cudaSuccess) e = launch_attn_combine(p, rows, split_grid(rows, h->num_sms), h->cfg.dtype, st);
+  // sequences of up to kSplitMaxRows rows go to the split kernel, longer ones to the tensor-memory kernel
+  const bool many = (int64_t)b->max_q * p.group > kSplitMaxRows;
+  cudaError_t e = cudaSuccess;
+  if (many) {
+    AttnParams t = p;
+    use_tile(h, &t);
+    t.rows_lo = kSplitMaxRows;
+    CUtensorMap qm;
+    if (!query_map(&qm, h, q, q_stride, b->n_tokens)) return COLI_ECUDA;
+    e = launch_attn_tile(t, qm, kv->maps.k128, kv->maps.v128, h->cfg.dtype, h->num_sms, st);
+    if (e == cudaSuccess) e = launch_attn_combine(t, kTileRows, h->num_sms, h->cfg.dtype, st);
+    p.rows_hi = kSplitMaxRows;
+  }
+  if (e == cudaSuccess && (!many || b->n_seqs > 1)) {
+    const int rows = rows_of(h, b->max_q);
+    p.block_tokens = rows / p.group;
+    e = launch_attn_split(p, kv->maps.k64, kv->maps.v64, rows, h->cfg.dtype, h->num_sms, st);
+    if (e == cudaSuccess) e = launch_attn_combine(p, rows, split_grid(rows, h->num_sms), h->cfg.dtype, st);
+  }
   return e == cudaSuccess ? COLI_OK : COLI_ECUDA;
 }
 
@@ -340,18 +388,20 @@ extern "C" int coli_attn_prefix(coli_attn* h, const coli_attn_kv* kv, const coli
   AttnParams own = params(h, kv, b, q, q_stride, out, out_stride, lse, scale);
   own.dense_o = h->dense_o, own.dense_ml = h->dense_ml;
   AttnParams pre = own;
+  use_tile(h, &pre);
+  pre.redo = nullptr;  // every row sees every key of the prefix
   pre.q_start = nullptr, pre.kv_len = prefix_len, pre.table = prefix_table, pre.table_stride = prefix_pages;
   pre.n_seqs = 1, pre.max_pages = prefix_pages, pre.causal = 0;
-  pre.part_o = h->part_o2, pre.part_ml = h->part_ml2, pre.rec = h->rec2, pre.seq_pos = h->seq_pos2;
   pre.dense_o = h->dense_o2, pre.dense_ml = h->dense_ml2;
-  const int own_rows = rows_of(h, b->max_q), pre_rows = rows_of(h, b->n_tokens);
+  const int own_rows = rows_of(h, b->max_q);
   own.block_tokens = own_rows / own.group;
-  pre.block_tokens = pre_rows / own.group;
+  CUtensorMap qm;
+  if (!query_map(&qm, h, q, q_stride, b->n_tokens)) return COLI_ECUDA;
   cudaError_t e = launch_attn_split(own, kv->maps.k64, kv->maps.v64, own_rows, h->cfg.dtype, h->num_sms, st);
   if (e == cudaSuccess)
-    e = launch_attn_split(pre, kv->maps.k64, kv->maps.v64, pre_rows, h->cfg.dtype, h->num_sms, st);
+    e = launch_attn_tile(pre, qm, kv->maps.k128, kv->maps.v128, h->cfg.dtype, h->num_sms, st);
   if (e == cudaSuccess)
-    e = launch_attn_join(own, own_rows, pre, pre_rows, kSplitKeys, kSplitKeys, h->cfg.dtype, st);
+    e = launch_attn_join(own, own_rows, pre, kTileRows, kSplitKeys, kTileKeys, h->cfg.dtype, st);
   return e == cudaSuccess ? COLI_OK : COLI_ECUDA;
 }
 
@@ -369,5 +419,6 @@ extern "C" int coli_attn_status(coli_attn* h, void* stream) {
 
 extern "C" int coli_attn_launches(const coli_attn* h, int op, int max_q) {
   if (!h || op < 0 || op > 2 || max_q < 1) return COLI_EINVAL;
-  return op == 0 ? 1 : op == 1 ? 2 : 3;
+  const bool many = (int64_t)max_q * (h->cfg.n_q / h->cfg.n_kv) > kSplitMaxRows;
+  return op == 0 ? 1 : op == 1 ? (many ? 4 : 2) : 3;
 }

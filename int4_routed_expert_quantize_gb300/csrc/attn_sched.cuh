@@ -242,7 +242,7 @@ __device__ __forceinline__ void write_record(const AttnParams& p, const Stretch&
   AttnRec r;
   r.first_cta = -1;
   r.last_cta = r.first_slot = r.token0 = r.tokens = r.head = 0;
-  r.pad[0] = r.pad[1] = 0;
+  r.seq = r.blk = 0;
   if (st.begin < st.end && st.off > 0 && st.off <= st.per) {
     Cursor<KT> c;
     c.start(p, st);
@@ -252,7 +252,7 @@ __device__ __forceinline__ void write_record(const AttnParams& p, const Stretch&
     r.last_cta = (int)((unit + c.t.count - 1) / st.per);
     r.token0 = c.s.start + c.blk * p.block_tokens;
     r.tokens = min(p.block_tokens, c.s.n - c.blk * p.block_tokens);
-    r.head = c.head;
+    r.head = c.head, r.seq = c.b, r.blk = c.blk;
   }
   p.rec[blockIdx.x] = r;
 }
