@@ -35,6 +35,12 @@ struct Fp16 {
   static constexpr uint32_t kExp = 0x7C007C00u, kExpInc = 0x04000400u;
 };
 
+// A bounded wait by a whole warp: every lane sees the phase, and the lanes are together afterwards
+// (the instructions that follow are warp-wide).
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  return __all_sync(FULL, mbar_wait_bounded(bar, parity, abort_flag, status));
+}
+
 // nonzero when one of the two 16-bit values is infinite or NaN (all exponent bits set: adding
 // one to the exponent field carries into the sign bit, which the mask had cleared)
 template <class T>

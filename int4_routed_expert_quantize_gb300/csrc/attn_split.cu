@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(SplitCfg<D, RG>::threads, SplitCfg<D, RG>::cta
       const int64_t row = (int64_t)cur.b * p.table_stride;
       for (int i = cur.i0; i < cur.i1; ++i, ++it) {
         const int sgi = it % NST;
-        if (it >= NST && !mbar_wait_bounded(empty + sgi, ((it / NST) + 1) & 1, abort_flag, p.status)) {
+        if (it >= NST && !warp_wait(empty + sgi, ((it / NST) + 1) & 1, abort_flag, p.status)) {
           drain_fills(full, NST, it);
           return;
         }
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(SplitCfg<D, RG>::threads, SplitCfg<D, RG>::cta
 
     for (int i = cur.i0; i < cur.i1; ++i, ++it) {
       const int sgi = it % NST;
-      if (!mbar_wait_bounded(full + sgi, (it / NST) & 1, abort_flag, p.status)) goto out;
+      if (!warp_wait(full + sgi, (it / NST) & 1, abort_flag, p.status)) goto out;
       {
         const uint32_t ks = smem_addr(smem + sgi * 2 * C::tile_bytes), vs = ks + C::tile_bytes;
         const int key0 = cur.t.tile(i) * kSplitKeys + kg * C::kw;

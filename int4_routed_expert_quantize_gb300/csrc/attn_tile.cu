@@ -7,7 +7,7 @@
 // scores are in the softmax the other's products run, and the matrix unit is meant never to wait.
 //
 //   tensor memory (512 columns)   S0/P0 | S1/P1 | O0 | O1
-//   shared memory                 Q0, Q1 and a ring of key/value tiles, 128-byte swizzled boxes
+//   shared memory                 Q0, Q1, a ring of key and a ring of value tiles, 128-byte swizzled boxes
 //   warps 0-3, 4-7   softmax, rescaling and the epilogue of row tile 0, 1
 //   warp 8           issues every product; warp 9 every copy
 //   warps 10, 11     look at value tiles with keys that not every row sees
@@ -33,10 +33,14 @@ constexpr int kTileSmemRing = 163840;
 template <int D>
 struct TileCfg {
   static constexpr int tile_bytes = kTileKeys * D * 2;  // K or V of one stage; Q of one row tile
-  static constexpr int stages = kTileSmemRing / tile_bytes;
+  // Two rings, each with waiters that see every one of its tiles in order: with one ring for both, a
+  // waiter for value tiles alone could meet a stage whose previous (key) tile is still on its way and take
+  // the barrier's older phase for the one it wants.
+  static constexpr int k_stages = 2 * (kTileSmemRing / 5 / tile_bytes);
+  static constexpr int v_stages = 3 * (kTileSmemRing / 5 / tile_bytes);
   static constexpr int q_bytes = 2 * tile_bytes;
-  // barriers: ring full/empty/checked, q full/empty, scores, weights, output, drain
-  static constexpr int bars = 3 * stages + 4 + 6 + 1;
+  // barriers: keys full/empty, values full/empty/checked, q full/empty, scores, weights, output, drain
+  static constexpr int bars = 2 * k_stages + 3 * v_stages + 4 + 6 + 1;
   static constexpr int smem = kTileSmemRing + q_bytes + bars * 8 + 128;
   static constexpr uint32_t o_col = 256;  // first column of O0; O1 follows after D columns
 };
@@ -138,12 +142,13 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
     attn_tile_kernel(const AttnParams p, const __grid_constant__ CUtensorMap qmap,
                      const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using C = TileCfg<D>;
-  constexpr int NST = C::stages;
+  constexpr int KST = C::k_stages, VST = C::v_stages;
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* ring = smem;
+  uint8_t *kring = smem, *vring = smem + KST * C::tile_bytes;
   uint8_t* qs = smem + kTileSmemRing;
-  uint64_t* full = reinterpret_cast<uint64_t*>(qs + C::q_bytes);
-  uint64_t *empty = full + NST, *checked = empty + NST, *q_full = checked + NST, *q_empty = q_full + 2,
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(qs + C::q_bytes);
+  uint64_t *k_empty = k_full + KST, *v_full = k_empty + KST, *v_empty = v_full + VST, *checked = v_empty + VST,
+           *q_full = checked + VST, *q_empty = q_full + 2,
            *s_full = q_empty + 2, *p_full = s_full + 2, *o_full = p_full + 2, *drain = o_full + 2;
   Stretch* stretch = reinterpret_cast<Stretch*>(drain + 1);
   int* abort_flag = reinterpret_cast<int*>(stretch + 1);
@@ -152,7 +157,8 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
 
   if (tid == 0) {
     *abort_flag = 0;
-    for (int i = 0; i < NST; ++i) mbar_init(full + i, 1), mbar_init(empty + i, 1), mbar_init(checked + i, 2);
+    for (int i = 0; i < KST; ++i) mbar_init(k_full + i, 1), mbar_init(k_empty + i, 1);
+    for (int i = 0; i < VST; ++i) mbar_init(v_full + i, 1), mbar_init(v_empty + i, 1), mbar_init(checked + i, 2);
     for (int s = 0; s < 2; ++s) {
       mbar_init(q_full + s, 1), mbar_init(q_empty + s, 1), mbar_init(s_full + s, 1);
       mbar_init(p_full + s, 4), mbar_init(o_full + s, 1);
@@ -164,9 +170,9 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
   if (warp == 8) tmem_alloc(tmem_slot, 512);
   griddep_wait();
   griddep_launch_dependents();
-  const Stretch st = schedule<kTileKeys>(p, reinterpret_cast<int64_t*>(ring), stretch);
+  const Stretch st = schedule<kTileKeys>(p, reinterpret_cast<int64_t*>(smem), stretch);
   if (warp == 9 && lane == 0) write_record<kTileKeys>(p, st);
-  fence_proxy_async_smem();  // the copies overwrite what schedule() kept in the ring
+  fence_proxy_async_smem();  // the copies overwrite what schedule() kept in the rings
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -181,7 +187,7 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
   };
 
   if (warp == 9) {  // ---- copies
-    int it = 0, qn[2] = {0, 0};
+    int it = 0, kt = 0, qn[2] = {0, 0};  // value, key and query tiles asked for
     bool ok = true;
     for (; cur.valid() && ok; cur.next(p)) {
       const int64_t row = (int64_t)cur.b * p.table_stride;
@@ -189,7 +195,7 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
       const uint32_t qb = (uint32_t)(p.group * half_tokens) * D * 2;
       for (int s = 0; s < 2 && ok; ++s) {
         if (tokens(cur, s) == 0) continue;
-        if (qn[s] > 0) ok = mbar_wait_bounded(q_empty + s, (qn[s] - 1) & 1, abort_flag, p.status);
+        if (qn[s] > 0) ok = warp_wait(q_empty + s, (qn[s] - 1) & 1, abort_flag, p.status);
         if (!ok) break;
         ++qn[s];
         if (lane == 0) {
@@ -200,22 +206,28 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
         }
         __syncwarp();
       }
-      for (int i = cur.i0; i < cur.i1 && ok; ++i) {
+      for (int i = cur.i0; i < cur.i1 && ok; ++i, ++it) {
         const int j0 = cur.t.tile(i) * kTileKeys;
         const uint32_t bytes = fill_bytes<kTileKeys, D>(p, cur.t.p0, cur.t.p1, j0, lane);
-        for (int kv = 0; kv < 2; ++kv, ++it) {
-          const int sg = it % NST;
-          if (it >= NST) ok = mbar_wait_bounded(empty + sg, ((it / NST) + 1) & 1, abort_flag, p.status);
-          if (!ok) break;
-          if (lane == 0) mbar_expect_tx(full + sg, bytes);
-          __syncwarp();
-          fill_boxes<kTileKeys, D>(p, kv ? &vmap : &kmap, ring + sg * C::tile_bytes, full + sg, row, cur.t.p0,
-                                   cur.t.p1, j0, cur.head, lane);
-        }
+        const int ks = it % KST, vs = it % VST;
+        if (it >= KST) ok = warp_wait(k_empty + ks, ((it / KST) + 1) & 1, abort_flag, p.status);
+        if (!ok) break;
+        if (lane == 0) mbar_expect_tx(k_full + ks, bytes);
+        __syncwarp();
+        fill_boxes<kTileKeys, D>(p, &kmap, kring + ks * C::tile_bytes, k_full + ks, row, cur.t.p0, cur.t.p1, j0,
+                                 cur.head, lane);
+        ++kt;
+        if (it >= VST) ok = warp_wait(v_empty + vs, ((it / VST) + 1) & 1, abort_flag, p.status);
+        if (!ok) break;
+        if (lane == 0) mbar_expect_tx(v_full + vs, bytes);
+        __syncwarp();
+        fill_boxes<kTileKeys, D>(p, &vmap, vring + vs * C::tile_bytes, v_full + vs, row, cur.t.p0, cur.t.p1, j0,
+                                 cur.head, lane);
       }
     }
     if (!ok) {
-      drain_fills(full, NST, it);
+      drain_fills(k_full, KST, kt);
+      drain_fills(v_full, VST, it);
       for (int s = 0; s < 2; ++s)
         if (qn[s] > 0) drain_fills(q_full + s, 1, qn[s]);
     }
@@ -227,11 +239,11 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
     const auto scores = [&](int s) {  // S_s of tile ni of nxt; nit: its number
       if (tokens(nxt, s) == 0) return;
       if (ni == nxt.i0) {
-        ok = ok && mbar_wait_bounded(q_full + s, qn[s] & 1, abort_flag, p.status);
+        ok = ok && warp_wait(q_full + s, qn[s] & 1, abort_flag, p.status);
         ++qn[s];
       }
-      const int sg = (2 * nit) % NST;
-      ok = ok && mbar_wait_bounded(full + sg, ((2 * nit) / NST) & 1, abort_flag, p.status);
+      const int sg = nit % KST;
+      ok = ok && warp_wait(k_full + sg, (nit / KST) & 1, abort_flag, p.status);
       if (!ok) return;
       tc_fence_after();
       if (lane == 0) {
@@ -239,7 +251,7 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
         for (int k = 0; k < D / 16; ++k) {
           const int off = (k >> 2) * kTileKeys * 128 + (k & 3) * 32;
           tc_mma_bf16(tmem + s * 128, smem_desc_sw128(qs + s * C::tile_bytes + off),
-                      smem_desc_sw128(ring + sg * C::tile_bytes + off), qk_desc, k > 0);
+                      smem_desc_sw128(kring + sg * C::tile_bytes + off), qk_desc, k > 0);
         }
         tc_commit(s_full + s);
         if (ni == nxt.i1 - 1) tc_commit(q_empty + s);
@@ -247,7 +259,7 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
       __syncwarp();
     };
     const auto step = [&]() {  // nxt's key tile is done with
-      if (lane == 0) tc_commit(empty + (2 * nit) % NST);
+      if (lane == 0) tc_commit(k_empty + nit % KST);
       __syncwarp();
       ++nit;
       if (++ni == nxt.i1) {
@@ -263,11 +275,11 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
     int it = 0;
     for (; cur.valid() && ok; cur.next(p))
       for (int i = cur.i0; i < cur.i1 && ok; ++i, ++it) {
-        const int sg = (2 * it + 1) % NST;
+        const int sg = it % VST;
         for (int s = 0; s < 2 && ok; ++s) {
           if (tokens(cur, s) > 0) {
-            ok = mbar_wait_bounded(checked + it % NST, (it / NST) & 1, abort_flag, p.status) &&
-                 mbar_wait_bounded(p_full + s, pn[s] & 1, abort_flag, p.status);
+            ok = warp_wait(checked + sg, (it / VST) & 1, abort_flag, p.status) &&
+                 warp_wait(p_full + s, pn[s] & 1, abort_flag, p.status);
             ++pn[s];
             if (!ok) break;
             tc_fence_after();
@@ -275,7 +287,7 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
 #pragma unroll 1
               for (int k = 0; k < kTileKeys / 16; ++k)
                 tc_mma_ts(tmem + C::o_col + s * D, tmem + s * 128 + k * 8,
-                          smem_desc_values(ring + sg * C::tile_bytes + k * 2048), pv_desc, i > cur.i0 || k > 0);
+                          smem_desc_values(vring + sg * C::tile_bytes + k * 2048), pv_desc, i > cur.i0 || k > 0);
               if (i == cur.i1 - 1) tc_commit(o_full + s);
             }
             __syncwarp();
@@ -283,7 +295,7 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
           if (more) scores(s);
         }
         if (!ok) break;
-        if (lane == 0) tc_commit(empty + sg);
+        if (lane == 0) tc_commit(v_empty + sg);
         __syncwarp();
         if (more) step();
       }
@@ -297,8 +309,8 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
     for (; cur.valid() && ok; cur.next(p)) {
       bool listed = false;
       for (int i = cur.i0; i < cur.i1; ++i, ++it) {
-        const int sg = (2 * it + 1) % NST;
-        ok = mbar_wait_bounded(full + sg, ((2 * it + 1) / NST) & 1, abort_flag, p.status);
+        const int sg = it % VST;
+        ok = warp_wait(v_full + sg, (it / VST) & 1, abort_flag, p.status);
         if (!ok) break;
         const int j0 = cur.t.tile(i) * kTileKeys;
         if (!all_see(p, cur.t.p0, cur.t.p1, j0, j0 + kTileKeys - 1)) {
@@ -310,7 +322,7 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
             if (all) continue;
 #pragma unroll
             for (int sl = 0; sl < D / 64; ++sl) {
-              uint4* v = reinterpret_cast<uint4*>(ring + sg * C::tile_bytes + sl * kTileKeys * 128 + r * 128) + (lane & 7);
+              uint4* v = reinterpret_cast<uint4*>(vring + sg * C::tile_bytes + sl * kTileKeys * 128 + r * 128) + (lane & 7);
               if (some) {
                 const uint4 x = *v;
                 bad |= nonfinite2<T>(x.x) | nonfinite2<T>(x.y) | nonfinite2<T>(x.z) | nonfinite2<T>(x.w);
@@ -329,7 +341,7 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(checked + it % NST);  // one phase a value tile
+        if (lane == 0) mbar_arrive(checked + sg);
       }
     }
   } else {  // ---- softmax of row tile s; thread = row
@@ -348,7 +360,7 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
       const int pos = p.causal ? pa + tok : pa;
       float ref = -INFINITY, sum0 = 0.f, sum1 = 0.f;
       for (int i = cur.i0; i < cur.i1; ++i) {
-        ok = mbar_wait_bounded(s_full + s, sn & 1, abort_flag, p.status);
+        ok = warp_wait(s_full + s, sn & 1, abort_flag, p.status);
         ++sn;
         if (!ok) break;
         tc_fence_after();
@@ -432,7 +444,7 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
         if (lane == 0) mbar_arrive(p_full + s);
       }
       if (!ok) break;
-      ok = mbar_wait_bounded(o_full + s, on & 1, abort_flag, p.status);
+      ok = warp_wait(o_full + s, on & 1, abort_flag, p.status);
       ++on;
       if (!ok) break;
       tc_fence_after();

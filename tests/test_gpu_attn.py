@@ -236,6 +236,15 @@ def test_window_repeats_bit_for_bit():
         assert torch.equal(s.eng.window(s.cache, s.batch, s.q, window=2000, sinks=4), a)
 
 
+def test_window_many_calls_in_a_row():
+    """hundreds of long-row calls that nothing waits between: none of their bounded waits gives up"""
+    s = Setup([1500], [2600], 8, 2, 128, 64, BF)
+    a = s.window(window=-1)
+    for _ in range(300):
+        b = s.eng.window(s.cache, s.batch, s.q, window=-1)
+    assert torch.equal(a, b) and s.eng.status() == 0
+
+
 # ---- prefix ----
 
 @pytest.mark.parametrize("n_q,n_kv,D,page,dt,layout", [
