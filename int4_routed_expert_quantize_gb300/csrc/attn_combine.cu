@@ -71,10 +71,11 @@ struct Join {
   }
 };
 
-// One query row from its definition, by one warp: for the rare blocks that hold values which are not
-// finite and which only some of the block's rows see.  qf: D floats of shared memory.
+// Adds one query row's attention to its own cache, from the definition, by one warp: for the rare blocks with
+// values that are not finite and that only some of the block's rows see.  qf: D floats of shared memory.
 template <class T, int D>
-__device__ void redo_row(const AttnParams& p, const SeqInfo& s, int b, int i, int hq, float* qf, int lane) {
+__device__ __noinline__ void add_direct(Join<D>& r, const AttnParams& p, const SeqInfo& s, int b, int i, int hq,
+                                        float* qf, int lane) {
   constexpr int V = D / 32;
   const int pos = s.len - s.n + i, head = hq / p.group;
   const uint16_t* q = static_cast<const uint16_t*>(p.q) + (int64_t)(s.start + i) * p.q_stride + (int64_t)hq * D;
@@ -90,7 +91,6 @@ __device__ void redo_row(const AttnParams& p, const SeqInfo& s, int b, int i, in
     if (id < 0 || id >= p.n_pages) return nullptr;  // reads as zeros
     return static_cast<const uint16_t*>(base) + id * sp + head * sh + (j & ((1 << p.page_shift) - 1)) * ss;
   };
-  Join<D> r;
   for (int j0 = 0; j0 <= pos; j0 += 32) {
     if (j0 >= p.sinks && j0 + 31 < lo) {
       j0 = (lo & ~31) - 32;
@@ -128,7 +128,29 @@ __device__ void redo_row(const AttnParams& p, const SeqInfo& s, int b, int i, in
       }
     }
   }
-  r.template write<T>(p, s.start + i, hq, lane);
+}
+
+// the sequence of a token: the first one that ends after it (n_seqs: none)
+__device__ __forceinline__ int seq_of(const AttnParams& p, int token, int lane) {
+  int b = 0;
+  for (int b0 = 0; b0 < p.n_seqs; b0 += 32) {
+    const bool before = b0 + lane < p.n_seqs && __ldg(p.q_start + b0 + lane + 1) <= token;
+    const int n = __popc(__ballot_sync(FULL, before));
+    b += n;
+    if (n < 32) break;
+  }
+  return b;
+}
+
+// the last block to get here clears the flags for the next call
+__device__ __noinline__ void clear_flags(const AttnParams& p) {
+  __shared__ int last;
+  __syncthreads();  // this block has read what it needs
+  if (threadIdx.x == 0) last = atomicAdd(p.redo_any + 1, 1) == (int)(gridDim.x * gridDim.y) - 1;
+  __syncthreads();
+  if (!last) return;
+  for (int64_t k = threadIdx.x; k < (int64_t)p.n_tokens * p.n_kv; k += blockDim.x) p.redo[k] = 0;
+  if (threadIdx.x == 0) p.redo_any[0] = p.redo_any[1] = 0;
 }
 
 template <class T, int D>
@@ -140,7 +162,7 @@ __device__ __forceinline__ void join_parts(const AttnParams& p, const AttnRec& r
     if (tok >= r.tokens) break;
     Join<D> j;
     j.add(p.part_o, p.part_ml, r.last_cta - r.first_cta + 1, lane, [&](int c) {
-      return ((int64_t)(r.first_cta + c) * 2 + (c == 0 ? r.first_slot : 0)) * rows + row;
+      return ((int64_t)(r.first_cta + c) * 2 + (c == 0 ? 1 : 0)) * rows + row;
     });
     j.template write<T>(p, r.token0 + tok, r.head * p.group + row - tok * p.group, lane);
   }
@@ -153,64 +175,61 @@ __global__ void __launch_bounds__(kWarps * 32)
   griddep_launch_dependents();
   const AttnRec r = p.rec[blockIdx.x];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int redo = p.redo ? min(__ldcg(p.redo_count), p.redo_cap) : 0;
-  bool mine = r.first_cta >= 0;
-  for (int k = 0; k < redo && mine; ++k) {
-    const int4 u = __ldcg(p.redo + k);
-    mine = u.x != r.seq || u.y != r.blk || u.z != r.head;
-  }
-  if (mine) join_parts<T, D>(p, r, rows, rows_per_block, warp, lane);
-  if (redo == 0) return;
+  const bool redo = __ldcg(p.redo_any) != 0;
+  if (r.first_cta >= 0 && !(redo && __ldcg(p.redo + (int64_t)r.token0 * p.n_kv + r.head)))
+    join_parts<T, D>(p, r, rows, rows_per_block, warp, lane);
+  if (!redo) return;
   __shared__ float qf[kWarps][D];
-  const int blocks = gridDim.x * gridDim.y, unit_rows = p.block_tokens * p.group;
-  for (int64_t k = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kWarps + warp; k < (int64_t)redo * unit_rows;
-       k += (int64_t)blocks * kWarps) {
-    const int4 u = __ldcg(p.redo + k / unit_rows);
-    const int row = (int)(k % unit_rows), i = u.y * p.block_tokens + row / p.group;
-    const SeqInfo s = seq_info(p, u.x);
-    if (i < s.n) redo_row<T, D>(p, s, u.x, i, u.z * p.group + row % p.group, qf[warp], lane);
+  const int64_t stride = (int64_t)gridDim.x * gridDim.y * kWarps;
+  for (int64_t k = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kWarps + warp; k < (int64_t)p.n_tokens * p.n_kv;
+       k += stride) {
+    if (!__ldcg(p.redo + k)) continue;
+    const int token = (int)(k / p.n_kv), b = seq_of(p, token, lane);
+    const SeqInfo s = seq_info(p, b);
+    for (int g = 0; g < p.group; ++g) {
+      Join<D> j;
+      const int hq = (int)(k % p.n_kv) * p.group + g;
+      add_direct<T, D>(j, p, s, b, token - s.start, hq, qf[warp], lane);
+      j.template write<T>(p, token, hq, lane);
+    }
   }
-  __syncthreads();  // this block has read the list; the last block empties it for the next call
-  if (threadIdx.x == 0 && atomicAdd(p.redo_count + 1, 1) == blocks - 1) {
-    p.redo_count[0] = 0;
-    p.redo_count[1] = 0;
-  }
+  clear_flags(p);
 }
 
 // where one row's results of one source are
 struct Parts {
   int n;        // parts; 1 with dense: the row sits in the dense buffer
   bool dense;
-  int first_cta, first_slot, rows, row;
+  int first_cta, rows, row;
 };
 
 template <int KT>
 __device__ __forceinline__ Parts find_parts(const AttnParams& p, int rows, int b, int i, int head, int g) {
   // token i of sequence b
   const SeqInfo s = seq_info(p, b);
-  const int64_t per = __ldcg(p.seq_pos + p.n_seqs + 1);
+  const uint32_t per = __ldcg(p.seq_pos + p.n_seqs + 1);
   const int blk = i / p.block_tokens;
-  int64_t at = __ldcg(p.seq_pos + b);
+  uint32_t at = __ldcg(p.seq_pos + b);
   Tiles<KT> t;
   if (p.causal) {
+#pragma unroll 1
     for (int k = 0; k < blk; ++k) {
       t.set(p, s, k);
-      at += (int64_t)t.count * p.n_kv;
+      at += (t.count + p.unit_cost) * p.n_kv;
     }
     t.set(p, s, blk);
   } else {  // every block has the same tiles
     t.set(p, s, blk);
-    at += (int64_t)blk * t.count * p.n_kv;
+    at += blk * (t.count + p.unit_cost) * p.n_kv;
   }
-  at += (int64_t)head * t.count;
+  at += head * (t.count + p.unit_cost) + p.unit_cost;
   Parts r;
   r.row = (i - blk * p.block_tokens) * p.group + g;
   r.rows = rows;
-  const int64_t c0 = at / per, c1 = (at + t.count - 1) / per;
+  const int c0 = at / per, c1 = (at + t.count - 1) / per;
   r.dense = c0 == c1;
-  r.n = (int)(c1 - c0) + 1;
-  r.first_cta = (int)c0;
-  r.first_slot = at == c0 * per ? 0 : 1;
+  r.n = c1 - c0 + 1;
+  r.first_cta = c0;
   return r;
 }
 
@@ -221,8 +240,31 @@ __device__ __forceinline__ void add_parts(Join<D>& j, const AttnParams& p, const
     j.add(p.dense_o, p.dense_ml, 1, lane, [&](int) { return dense_row; });
   else
     j.add(p.part_o, p.part_ml, r.n, lane, [&](int c) {
-      return ((int64_t)(r.first_cta + c) * 2 + (c == 0 ? r.first_slot : 0)) * r.rows + r.row;
+      return ((int64_t)(r.first_cta + c) * 2 + (c == 0 ? 1 : 0)) * r.rows + r.row;
     });
+}
+
+template <class T, int D, int OWN, int SHARED>
+__device__ __forceinline__ void join_row(const AttnParams& own, int own_rows, const AttnParams& shared, int shared_rows,
+                                         int64_t row, int lane, bool redo) {
+  const int token = (int)(row / own.n_q), hq = (int)(row - (int64_t)token * own.n_q);
+  const int head = hq / own.group, g = hq - head * own.group;
+  Join<D> j;
+  add_parts(j, shared, find_parts<SHARED>(shared, shared_rows, 0, token, head, g), row, lane);
+  const int b = seq_of(own, token, lane);
+  if (b < own.n_seqs) {
+    const SeqInfo s = seq_info(own, b);
+    const int i = token - s.start;
+    if (i >= 0 && i < s.n) {
+      if (redo && __ldcg(own.redo + (int64_t)token * own.n_kv + head)) {
+        __shared__ float qf[kWarps][D];
+        add_direct<T, D>(j, own, s, b, i, hq, qf[threadIdx.x >> 5], lane);
+      } else {
+        add_parts(j, own, find_parts<OWN>(own, own_rows, b, i, head, g), row, lane);
+      }
+    }
+  }
+  j.template write<T>(own, token, hq, lane);
 }
 
 template <class T, int D, int OWN, int SHARED>
@@ -232,25 +274,9 @@ __global__ void __launch_bounds__(kWarps * 32)
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (row >= (int64_t)own.n_tokens * own.n_q) return;
-  const int token = (int)(row / own.n_q), hq = (int)(row - (int64_t)token * own.n_q);
-  const int head = hq / own.group, g = hq - head * own.group;
-  Join<D> j;
-  add_parts(j, shared, find_parts<SHARED>(shared, shared_rows, 0, token, head, g), row, lane);
-  int b = 0;  // the first sequence that ends after the token
-  for (int b0 = 0; b0 < own.n_seqs; b0 += 32) {
-    const bool before = b0 + lane < own.n_seqs && __ldg(own.q_start + b0 + lane + 1) <= token;
-    const int n = __popc(__ballot_sync(FULL, before));
-    b += n;
-    if (n < 32) break;
-  }
-  if (b < own.n_seqs) {
-    const SeqInfo s = seq_info(own, b);
-    const int i = token - s.start;
-    if (i >= 0 && i < s.n)
-      add_parts(j, own, find_parts<OWN>(own, own_rows, b, i, head, g), row, lane);
-  }
-  j.template write<T>(own, token, hq, lane);
+  const bool redo = __ldcg(own.redo_any) != 0;
+  if (row < (int64_t)own.n_tokens * own.n_q) join_row<T, D, OWN, SHARED>(own, own_rows, shared, shared_rows, row, lane, redo);
+  if (redo) clear_flags(own);
 }
 
 template <class K, class... A>

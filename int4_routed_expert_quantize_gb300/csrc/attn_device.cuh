@@ -36,9 +36,36 @@ struct Fp16 {
 };
 
 // A bounded wait by a whole warp: every lane sees the phase, and the lanes are together afterwards
-// (the instructions that follow are warp-wide).
+// (the instructions that follow are warp-wide).  The rules of mbar_wait_bounded, but inline: a call would
+// tie the kernels that split their registers by role to one count.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
-  return __all_sync(FULL, mbar_wait_bounded(bar, parity, abort_flag, status));
+  bool ok = mbar_try_wait(bar, parity);
+  if (!ok) {
+    const uint64_t t0 = global_ns();
+#pragma unroll 1
+    for (uint32_t it = 1; !*abort_flag; ++it) {
+      if (mbar_try_wait(bar, parity)) {
+        ok = true;
+        break;
+      }
+      if ((it & 63u) == 0 && global_ns() - t0 > kWaitLimitNs) {
+        *abort_flag = 1;
+        atomicExch(status, COLI_ETIMEOUT);
+      }
+    }
+  }
+  return __all_sync(FULL, ok);
+}
+
+// drain_fills, inline for the same reason
+__device__ __forceinline__ void drain_ring(uint64_t* full, int stages, int issued) {
+#pragma unroll 1
+  for (int it = max(0, issued - stages); it < issued; ++it) {
+    const uint64_t t0 = global_ns();
+#pragma unroll 1
+    while (!mbar_try_wait(full + it % stages, (uint32_t)((it / stages) & 1)))
+      if (global_ns() - t0 > kWaitLimitNs / 8) break;
+  }
 }
 
 // nonzero when one of the two 16-bit values is infinite or NaN (all exponent bits set: adding
@@ -102,47 +129,45 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
-// One warp fills one stage: the boxes of a KT-key tile of K (and of V after it) that hold keys
-// some row of the block sees.  Pages whose id is out of range read as zeros (page coordinate
-// past the end) and are reported.
-template <int KT, int D>
-__device__ __forceinline__ void fill_boxes(const AttnParams& p, const CUtensorMap* map, uint8_t* dst,
-                                           uint64_t* bar, int64_t table_row, int p0, int p1, int j0,
-                                           int head, int lane) {
-  constexpr int kSlabs = D / 64;
+// One warp fills the stage of a KT-key tile of K and of V: the boxes that hold keys some row of the block
+// sees.  Lane i takes box i: K's, and (N = 2) V's at v_offset; N = 1 takes one map.  Pages whose id is out of
+// range read as zeros (page coordinate past the end) and are reported.
+template <int KT, int D, int N>
+__device__ __forceinline__ void fill_boxes(const AttnParams& p, const CUtensorMap* kmap, const CUtensorMap* vmap,
+                                           uint8_t* dst, uint64_t* kbar, uint64_t* vbar, int v_offset,
+                                           int64_t table_row, int p0, int p1, int j0, int head, int lane) {
   const int page = 1 << p.page_shift;
   const int rows = min(page, KT);  // slots per box
-  const int boxes = KT / rows;     // per slab
-  bool need = false;
-  int id = p.n_pages;
-  if (lane < boxes) {
-    const int a = j0 + lane * rows, e = a + rows - 1;  // the box's keys
-    // some_sees of some key in [a, e]
-    if (a <= p1 && p1 >= 0 && (e > p0 - p.window || a < p.sinks)) {
-      need = true;
-      id = __ldg(p.table + table_row + (a >> p.page_shift));
-      if (id < 0 || id >= p.n_pages) {
-        id = p.n_pages;
-        atomicExch(p.status, COLI_EINVAL);
-      }
+  const int boxes = KT / rows;     // per 64 values
+  const int a = j0 + lane * rows, e = a + rows - 1;  // the lane's keys
+  const bool need = lane < boxes && a <= p1 && (e > p0 - p.window || a < p.sinks);
+  int id = 0;
+  if (need) id = __ldg(p.table + table_row + (a >> p.page_shift));
+  const uint32_t bytes = (uint32_t)__popc(__ballot_sync(FULL, need)) * (uint32_t)rows * D * 2;
+  if (lane == 0) {
+    if (N == 2 && kbar == vbar) {
+      mbar_expect_tx(kbar, 2 * bytes);
+    } else {
+      mbar_expect_tx(kbar, bytes);
+      if (N == 2) mbar_expect_tx(vbar, bytes);
     }
   }
+  __syncwarp();
   if (need) {
-    const int slot = (j0 + lane * rows) & (page - 1);
+    if (id < 0 || id >= p.n_pages) {
+      id = p.n_pages;
+      atomicExch(p.status, COLI_EINVAL);
+    }
+    const int slot = a & (page - 1);
+    dst += lane * rows * 128;
 #pragma unroll
-    for (int s = 0; s < kSlabs; ++s)
-      tma_load_4d(dst + s * KT * 128 + lane * rows * 128, map, s * 64, slot, head, id, bar);
+    for (int s = 0; s < D / 64; ++s) tma_load_4d(dst + s * KT * 128, kmap, s * 64, slot, head, id, kbar);
+    if (N == 2)
+#pragma unroll
+      for (int s = 0; s < D / 64; ++s)
+        tma_load_4d(dst + v_offset + s * KT * 128, vmap, s * 64, slot, head, id, vbar);
   }
-}
-
-// bytes fill_boxes will copy for this tile
-template <int KT, int D>
-__device__ __forceinline__ uint32_t fill_bytes(const AttnParams& p, int p0, int p1, int j0, int lane) {
-  const int rows = min(1 << p.page_shift, KT);
-  const int boxes = KT / rows;
-  const int a = j0 + lane * rows, e = a + rows - 1;
-  const bool need = lane < boxes && a <= p1 && p1 >= 0 && (e > p0 - p.window || a < p.sinks);
-  return (uint32_t)__popc(__ballot_sync(FULL, need)) * (uint32_t)rows * D * 2;
+  __syncwarp();
 }
 
 }  // namespace coli

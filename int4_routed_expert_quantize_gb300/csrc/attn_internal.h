@@ -14,22 +14,22 @@ constexpr int kAttnMaxSeqs = 4096;
 constexpr int kAttnMaxGroup = 64;     // query heads per key head
 constexpr int kAttnPrefixRows = 8;    // tokens per sequence the prefix workspace is sized for
 constexpr int kAttnNoWindow = 1 << 30;
+constexpr int kSplitUnitCost = 1;     // AttnParams::unit_cost of the two kernels
+constexpr int kTileUnitCost = 3;
 constexpr int kSplitMaxRows = 64;     // rows of a sequence up to which the split kernel takes it
 constexpr int kSplitKeys = 64;        // keys per tile of the split kernel
 constexpr int kTileKeys = 128;        // keys per tile of the tensor-memory kernel
 constexpr int kTileRows = 256;        // query rows per block of the tensor-memory kernel (2 x 128)
 
-// A unit of attention work is one block of query tokens of one sequence with one key head; its
-// key tiles are a contiguous stretch of one long list over all units, and each CTA takes an equal
-// stretch of that list.  A unit cut by a stretch's end leaves one partial result per CTA in
-// the workspace; Rec (one per CTA, written by the CTA that holds the unit's second part) tells the
-// combine kernel where they are.
+// A unit of attention work is one block of query tokens of one sequence with one key head; a list of all
+// units' key tiles is cut into equal stretches, one per CTA.  A unit cut by a stretch's end leaves
+// one partial result per CTA in the workspace: the first part in slot 1 of its CTA, the others in slot 0
+// of theirs.  Its record, at the index of the CTA with the second part, tells the combine kernel.
 struct AttnRec {
   int first_cta, last_cta;  // CTAs with a part of the unit; first_cta < 0: no record
-  int first_slot;           // partial slot (0 or 1) of first_cta; all others have theirs in slot 0
   int token0, tokens;       // the unit's query tokens
   int head;                 // key head
-  int seq, blk;
+  int seq, blk, pad;
 };
 
 struct AttnParams {
@@ -49,17 +49,17 @@ struct AttnParams {
   int causal;         // 0: every query sees all kv_len keys
   float scale_log2;   // scale * log2(e)
   int block_tokens;   // query tokens per block
+  int unit_cost;      // list positions of a unit besides its tiles
   int64_t rows_lo, rows_hi;  // only sequences with rows_lo < new tokens * group <= rows_hi
   // workspace
   float* part_o;     // [2 * CTAs][rows per block][head_dim] unnormalised partial outputs
   float2* part_ml;   // [2 * CTAs][rows per block] their maximum (log2 units) and sum
   AttnRec* rec;      // [CTAs]
-  int64_t* seq_pos;  // [n_seqs + 2] first list position of each sequence, the total, the stretch
+  uint32_t* seq_pos;  // [n_seqs + 2] first list position of each sequence, the total, the stretch; or nullptr
   float* dense_o;    // prefix only: rows of uncut units go here, unnormalised, by (token, head)
   float2* dense_ml;
-  int4* redo;        // units (sequence, block, key head) that the tensor-memory kernel leaves to the
-  int* redo_count;   // kernel after it; [0] how many, [1] blocks of that kernel that are done
-  int redo_cap;
+  uint8_t* redo;   // [max_tokens][n_kv] rows the joining kernel computes again (flag_unit), zero otherwise
+  int* redo_any;   // [0] some are; [1] blocks of that kernel that are done
   int64_t k_page, k_head, k_slot, v_page, v_head, v_slot;  // cache strides, for those units
   const void *kc, *vc;
   int* status;

@@ -19,17 +19,16 @@ struct coli_attn {
   float* part_o = nullptr;
   float2* part_ml = nullptr;
   AttnRec* rec = nullptr;
-  int64_t* seq_pos = nullptr;
+  uint32_t* seq_pos = nullptr;
   // the tensor-memory kernel's (beside the split kernel's: one call may run both)
   float* part_o2 = nullptr;
   float2* part_ml2 = nullptr;
   AttnRec* rec2 = nullptr;
-  int64_t* seq_pos2 = nullptr;
+  uint32_t* seq_pos2 = nullptr;
   float *dense_o = nullptr, *dense_o2 = nullptr;
   float2 *dense_ml = nullptr, *dense_ml2 = nullptr;
-  int4* redo = nullptr;
-  int* redo_count = nullptr;
-  int redo_cap = 0;
+  uint8_t* redo = nullptr;
+  int* redo_any = nullptr;
   uint64_t* turn = nullptr;
   int32_t* status = nullptr;
 };
@@ -148,6 +147,7 @@ AttnParams params(const coli_attn* h, const coli_attn_kv* kv, const coli_attn_ba
   p.k_page = kv->c.k_page_stride, p.k_head = kv->c.k_head_stride, p.k_slot = kv->c.k_slot_stride;
   p.v_page = kv->c.v_page_stride, p.v_head = kv->c.v_head_stride, p.v_slot = kv->c.v_slot_stride;
   p.kc = kv->c.k, p.vc = kv->c.v;
+  p.redo = h->redo, p.redo_any = h->redo_any, p.unit_cost = kSplitUnitCost;
   p.status = h->status;
   return p;
 }
@@ -170,7 +170,7 @@ bool query_map(CUtensorMap* map, const coli_attn* h, const void* q, int64_t q_st
 // switches a launch's parameters to the tensor-memory kernel's workspace and blocks
 void use_tile(const coli_attn* h, AttnParams* p) {
   p->part_o = h->part_o2, p->part_ml = h->part_ml2, p->rec = h->rec2, p->seq_pos = h->seq_pos2;
-  p->redo = h->redo, p->redo_count = h->redo_count, p->redo_cap = h->redo_cap;
+  p->unit_cost = kTileUnitCost;
   p->block_tokens = tile_block_tokens(p->group);
 }
 
@@ -237,7 +237,6 @@ extern "C" int coli_attn_create(const coli_attn_config* cfg, coli_attn** out) {
     // partials: two per CTA of the split kernel (2 CTAs an SM of 16 rows or one of up to 64) and of the
     // tensor-memory kernel
     const size_t rows = 2 * (size_t)h->num_sms * 64, rows2 = 2 * (size_t)h->num_sms * kTileRows;
-    h->redo_cap = (int)(((size_t)c.max_tokens / tile_block_tokens(c.n_q / c.n_kv) + c.max_seqs) * c.n_kv) + 8 * h->num_sms;
     // the prefix call keeps every row twice: up to kAttnPrefixRows tokens a sequence
     const int64_t pt = (int64_t)kAttnPrefixRows * c.max_seqs;
     h->prefix_tokens = (int)(pt < c.max_tokens ? pt : c.max_tokens);
@@ -254,12 +253,13 @@ extern "C" int coli_attn_create(const coli_attn_config* cfg, coli_attn** out) {
     if (!rc) rc = dalloc(h, &h->dense_ml, dense);
     if (!rc) rc = dalloc(h, &h->dense_o2, dense * D);
     if (!rc) rc = dalloc(h, &h->dense_ml2, dense);
-    if (!rc) rc = dalloc(h, &h->redo, h->redo_cap);
-    if (!rc) rc = dalloc(h, &h->redo_count, 2);
+    if (!rc) rc = dalloc(h, &h->redo, (size_t)c.max_tokens * c.n_kv);
+    if (!rc) rc = dalloc(h, &h->redo_any, 2);
     if (!rc) rc = dalloc(h, &h->turn, turn.size());
     if (!rc) rc = dalloc(h, &h->status, 4);
     if (!rc && ((!turn.empty() && cudaMemcpy(h->turn, turn.data(), turn.size() * 8, cudaMemcpyHostToDevice) != cudaSuccess) ||
-                cudaMemset(h->status, 0, 16) != cudaSuccess || cudaMemset(h->redo_count, 0, 8) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess))
+                cudaMemset(h->status, 0, 16) != cudaSuccess || cudaMemset(h->redo_any, 0, 8) != cudaSuccess ||
+                cudaMemset(h->redo, 0, (size_t)c.max_tokens * c.n_kv) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess))
       rc = COLI_ECUDA;
   }
   if (rc) {
@@ -389,7 +389,6 @@ extern "C" int coli_attn_prefix(coli_attn* h, const coli_attn_kv* kv, const coli
   own.dense_o = h->dense_o, own.dense_ml = h->dense_ml;
   AttnParams pre = own;
   use_tile(h, &pre);
-  pre.redo = nullptr;  // every row sees every key of the prefix
   pre.q_start = nullptr, pre.kv_len = prefix_len, pre.table = prefix_table, pre.table_stride = prefix_pages;
   pre.n_seqs = 1, pre.max_pages = prefix_pages, pre.causal = 0;
   pre.dense_o = h->dense_o2, pre.dense_ml = h->dense_ml2;

@@ -77,184 +77,223 @@ __device__ __forceinline__ bool all_see(const AttnParams& p, int p0, int p1, int
   return j1 <= p0 && (j0 > p1 - p.window || j1 < p.sinks);
 }
 
-// list positions of one sequence: blocks in order, each block's key heads in order
-template <int KT>
-__device__ __forceinline__ int64_t seq_weight_serial(const AttnParams& p, const SeqInfo& s) {
-  int64_t w = 0;
-  const int nb = (s.n + p.block_tokens - 1) / p.block_tokens;
-  for (int blk = 0; blk < nb; ++blk) {
-    Tiles<KT> t;
-    t.set(p, s, blk);
-    w += t.count;
-  }
-  return w * p.n_kv;
-}
+// ---- the list ----
+// A unit is one block with one key head.  On the list it takes unit_cost positions (what it costs besides
+// its tiles: queries in, results out) and then one position a tile; a CTA's stretch is `per` positions,
+// and a tile belongs to the CTA whose stretch holds its position.  Order: sequences, blocks, key heads.
 
-struct Stretch {
-  int64_t begin, end, per, total;
-  int b, blk, head, off;  // the unit at `begin` and the tile within it
+// One unit's tiles i0..i1-1, for the roles of a CTA.
+struct alignas(16) Unit {
+  int tok0, nt;      // first query token (of all), tokens
+  int p0, p1;        // Tiles
+  int sink, base;
+  int i0, i1;        // i1 = 0: the end
+  int head, b, blk;
+  int whole;         // 1: all of its tiles; otherwise a part goes to slot (i0 > 0 ? 0 : 1) of the workspace
+  __device__ __forceinline__ int tile(int i) const { return i < sink ? i : base + i - sink; }
+};
+static_assert(sizeof(Unit) == 48, "three 16-byte words");
+
+constexpr int kUnitSlots = 4;
+struct UnitRing {  // one warp fills it, every warp of the other roles reads it
+  Unit u[kUnitSlots];
+  uint64_t full[kUnitSlots], empty[kUnitSlots];
+  __device__ __forceinline__ void init(int readers) {
+    for (int i = 0; i < kUnitSlots; ++i) mbar_init(full + i, 1), mbar_init(empty + i, readers);
+  }
 };
 
-constexpr int kSchedSerialBlocks = 4;
+constexpr int kSerialBlocks = 4;
 
-// All threads of the CTA take part.  pos: shared, [n_seqs + 1] (may overlay memory that is used
-// only afterwards).  Returns this CTA's stretch; CTA 0 also writes the list positions to
-// the workspace (p.seq_pos).
+// Positions of each sequence into pos[b + 1] (shared memory; may overlay memory that is used only
+// afterwards), by all threads of the CTA; the caller synchronises.
 template <int KT>
-__device__ Stretch schedule(const AttnParams& p, int64_t* pos, Stretch* shared_out) {
-  const int nthreads = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int nwarps = nthreads >> 5;
-  for (int b = tid; b < p.n_seqs; b += nthreads) {
+__device__ __forceinline__ void weigh(const AttnParams& p, uint32_t* pos) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarps = blockDim.x >> 5;
+  bool any_long = false;
+#pragma unroll 1
+  for (int b = tid; b < p.n_seqs; b += blockDim.x) {
     const SeqInfo s = seq_info(p, b);
     if (blockIdx.x == 0) seq_check(p, b);
+    uint32_t w = 0;
     const int nb = (s.n + p.block_tokens - 1) / p.block_tokens;
-    pos[b + 1] = nb <= kSchedSerialBlocks ? seq_weight_serial<KT>(p, s) : -1;
+#pragma unroll 1
+    for (int blk = 0; blk < nb && nb <= kSerialBlocks; ++blk) {
+      Tiles<KT> t;
+      t.set(p, s, blk);
+      w += t.count + p.unit_cost;
+    }
+    any_long |= nb > kSerialBlocks;
+    pos[b + 1] = nb > kSerialBlocks ? 0xFFFFFFFFu : w * p.n_kv;
   }
-  __syncthreads();
+  if (!__syncthreads_or(any_long)) return;
+#pragma unroll 1
   for (int b = warp; b < p.n_seqs; b += nwarps) {  // long sequences: one warp over the blocks
-    if (pos[b + 1] >= 0) continue;
+    const uint32_t have = pos[b + 1];
+    __syncwarp();
+    if (have != 0xFFFFFFFFu) continue;
     const SeqInfo s = seq_info(p, b);
     const int nb = (s.n + p.block_tokens - 1) / p.block_tokens;
-    int64_t w = 0;
+    uint32_t w = 0;
+#pragma unroll 1
     for (int blk = lane; blk < nb; blk += 32) {
       Tiles<KT> t;
       t.set(p, s, blk);
-      w += t.count;
+      w += t.count + p.unit_cost;
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) w += __shfl_xor_sync(FULL, w, o);
-    __syncwarp();
+    w = __reduce_add_sync(FULL, w);
     if (lane == 0) pos[b + 1] = w * p.n_kv;
   }
   __syncthreads();
-  if (warp == 0) {
-    int64_t run = 0;
+}
+
+// Walks a CTA's stretch; one warp, all lanes alike.
+template <int KT>
+struct Walk {
+  SeqInfo s;
+  Tiles<KT> t;
+  uint32_t begin, end, per, at;  // at: the current unit's first position
+  int b, blk, head;
+  // pos as weigh() left it; becomes the sequences' first positions
+  __device__ __forceinline__ void start(const AttnParams& p, uint32_t* pos, int lane) {
+    uint32_t run = 0;
+    if (lane == 0) pos[0] = 0;
+#pragma unroll 1
     for (int b0 = 0; b0 < p.n_seqs; b0 += 32) {
-      int64_t v = b0 + lane < p.n_seqs ? pos[b0 + lane + 1] : 0;
+      uint32_t v = b0 + lane < p.n_seqs ? pos[b0 + lane + 1] : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int64_t u = __shfl_up_sync(FULL, v, o);
+        const uint32_t u = __shfl_up_sync(FULL, v, o);
         if (lane >= o) v += u;
       }
       if (b0 + lane < p.n_seqs) pos[b0 + lane + 1] = run + v;
       run += __shfl_sync(FULL, v, 31);
     }
-    if (lane == 0) pos[0] = 0;
     __syncwarp();
-    Stretch st;
-    st.total = run;
-    st.per = max((int64_t)1, (run + gridDim.x - 1) / gridDim.x);
-    st.begin = min((int64_t)blockIdx.x * st.per, run);
-    st.end = min(st.begin + st.per, run);
-    st.b = st.blk = st.head = st.off = 0;
-    if (st.begin < st.end) {
-      int lo = 0, hi = p.n_seqs - 1;  // the sequence with pos[b] <= begin < pos[b+1]
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (pos[mid] <= st.begin) lo = mid;
-        else hi = mid - 1;
+    per = max(1u, (run + gridDim.x - 1) / gridDim.x);
+    begin = min(blockIdx.x * per, run);
+    end = min(begin + per, run);
+    b = blk = head = 0;
+    at = end;  // nothing to do
+    if (blockIdx.x == 0 && p.seq_pos) {
+#pragma unroll 1
+      for (int i = lane; i <= p.n_seqs; i += 32) p.seq_pos[i] = pos[i];
+      if (lane == 0) p.seq_pos[p.n_seqs + 1] = per;
+    }
+    if (begin >= end) return;
+    int hi = p.n_seqs - 1;  // the sequence with pos[b] <= begin < pos[b+1]
+#pragma unroll 1
+    while (b < hi) {
+      const int mid = (b + hi + 1) >> 1;
+      if (pos[mid] <= begin) b = mid;
+      else hi = mid - 1;
+    }
+    at = pos[b];
+    s = seq_info(p, b);
+    const int nb = (s.n + p.block_tokens - 1) / p.block_tokens;
+#pragma unroll 1
+    for (int blk0 = 0; blk0 < nb; blk0 += 32) {
+      uint32_t w = 0;
+      if (blk0 + lane < nb) {
+        t.set(p, s, blk0 + lane);
+        w = (t.count + p.unit_cost) * p.n_kv;
       }
-      st.b = lo;
-      int64_t x = st.begin - pos[lo];
-      const SeqInfo s = seq_info(p, lo);
-      const int nb = (s.n + p.block_tokens - 1) / p.block_tokens;
-      for (int blk0 = 0; blk0 < nb; blk0 += 32) {
-        Tiles<KT> t;
-        int64_t w = 0;
-        if (blk0 + lane < nb) {
-          t.set(p, s, blk0 + lane);
-          w = (int64_t)t.count * p.n_kv;
-        }
-        int64_t v = w;
+      uint32_t v = w;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t u = __shfl_up_sync(FULL, v, o);
-          if (lane >= o) v += u;
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(FULL, v, o);
+        if (lane >= o) v += u;
+      }
+      const unsigned in = __ballot_sync(FULL, begin < at + v);
+      if (in) {
+        const int l = __ffs(in) - 1;
+        blk = blk0 + l;
+        at += __shfl_sync(FULL, v - w, l);
+        break;
+      }
+      at += __shfl_sync(FULL, v, 31);
+    }
+    t.set(p, s, blk);
+    const uint32_t cost = t.count + p.unit_cost;
+    head = (begin - at) / cost;
+    at += head * cost;
+  }
+  // the next unit of which a tile belongs to this CTA; false at the end
+  __device__ __forceinline__ bool next(const AttnParams& p, Unit& u) {
+    while (at < end) {
+      const int first = at + p.unit_cost;  // the first tile's position
+      u.i0 = max(0, (int)begin - first);
+      u.i1 = min(t.count, (int)end - first);
+      u.head = head, u.b = b, u.blk = blk;
+      u.p0 = t.p0, u.p1 = t.p1, u.sink = t.sink, u.base = t.base;
+      u.tok0 = s.start + blk * p.block_tokens;
+      u.nt = min(p.block_tokens, s.n - blk * p.block_tokens);
+      u.whole = u.i0 == 0 && u.i1 == t.count;
+      const uint32_t here = at;
+      at += t.count + p.unit_cost;
+      if (++head == p.n_kv && at < end) {
+        head = 0;
+        if (++blk * p.block_tokens >= s.n) {
+          blk = 0;
+#pragma unroll 1
+          do {
+            ++b;
+            s = seq_info(p, b);
+          } while (s.n == 0);  // a later sequence has tokens: the stretch ends inside the list
         }
-        const unsigned in = __ballot_sync(FULL, x < v);
-        if (in) {
-          const int l = __ffs(in) - 1;
-          st.blk = blk0 + l;
-          x -= __shfl_sync(FULL, v - w, l);
-          const int cnt = __shfl_sync(FULL, (int)(w / p.n_kv), l);
-          st.head = (int)(x / cnt);
-          st.off = (int)(x % cnt);
-          break;
-        }
-        x -= __shfl_sync(FULL, v, 31);
+        t.set(p, s, blk);
+      }
+      if (u.i1 > u.i0) {
+        if (u.i0 > 0) record(p, u, here + p.unit_cost, at - here - p.unit_cost);
+        return true;
       }
     }
-    if (lane == 0) *shared_out = st;
-    if (blockIdx.x == 0) {
-      for (int b = lane; b <= p.n_seqs; b += 32) p.seq_pos[b] = pos[b];
-      if (lane == 0) p.seq_pos[p.n_seqs + 1] = st.per;
-    }
+    return false;
   }
-  __syncthreads();
-  return *shared_out;
-}
-
-// Walks the units of a stretch; every role of a CTA runs its own copy.
-template <int KT>
-struct Cursor {
-  SeqInfo s;
-  Tiles<KT> t;
-  int b, blk, head, i0, i1;  // tiles i0..i1-1 of the unit are this CTA's
-  int64_t pos, end;
-  bool first;
-  __device__ __forceinline__ void start(const AttnParams& p, const Stretch& st) {
-    b = st.b, blk = st.blk, head = st.head, i0 = st.off;
-    pos = st.begin, end = st.end;
-    first = true;
-    if (pos < end) {
-      s = seq_info(p, b);
-      t.set(p, s, blk);
-      i1 = (int)min((int64_t)t.count, i0 + (end - pos));
-    }
-  }
-  __device__ __forceinline__ bool valid() const { return pos < end; }
-  __device__ __forceinline__ bool whole() const { return i0 == 0 && i1 == t.count; }
-  __device__ __forceinline__ void next(const AttnParams& p) {
-    pos += i1 - i0;
-    first = false;
-    if (pos >= end) return;
-    i0 = 0;
-    if (++head == p.n_kv) {
-      head = 0;
-      const int nb = (s.n + p.block_tokens - 1) / p.block_tokens;
-      if (++blk >= nb) {
-        blk = 0;
-        do {
-          ++b;
-          s = seq_info(p, b);
-        } while (s.n == 0);  // a later sequence has tokens: the stretch ends inside the list
-      }
-      t.set(p, s, blk);
-    }
-    i1 = (int)min((int64_t)t.count, end - pos);
+  // a unit whose first part is the previous CTA's: the combine kernel learns of it from here
+  __device__ __forceinline__ void record(const AttnParams& p, const Unit& u, uint32_t first, uint32_t count) const {
+    const int c0 = first / per;
+    if (c0 + 1 != (int)blockIdx.x || (threadIdx.x & 31) != 0) return;
+    AttnRec r;
+    r.first_cta = c0, r.last_cta = (first + count - 1) / per;
+    r.token0 = u.tok0, r.tokens = u.nt, r.head = u.head, r.seq = u.b, r.blk = u.blk, r.pad = 0;
+    p.rec[blockIdx.x] = r;
   }
 };
 
-// The record of a CTA: filled when its stretch starts inside a unit whose first part lies in
-// the previous CTA's stretch.
-template <int KT>
-__device__ __forceinline__ void write_record(const AttnParams& p, const Stretch& st) {
-  AttnRec r;
-  r.first_cta = -1;
-  r.last_cta = r.first_slot = r.token0 = r.tokens = r.head = 0;
-  r.seq = r.blk = 0;
-  if (st.begin < st.end && st.off > 0 && st.off <= st.per) {
-    Cursor<KT> c;
-    c.start(p, st);
-    const int64_t unit = st.begin - st.off;
-    r.first_cta = blockIdx.x - 1;
-    r.first_slot = unit == st.begin - st.per ? 0 : 1;
-    r.last_cta = (int)((unit + c.t.count - 1) / st.per);
-    r.token0 = c.s.start + c.blk * p.block_tokens;
-    r.tokens = min(p.block_tokens, c.s.n - c.blk * p.block_tokens);
-    r.head = c.head, r.seq = c.b, r.blk = c.blk;
+// A block in which a value that is not finite met rows that do not see it: its rows are computed again, one by one,
+// by the kernel that joins the parts (0 * inf = NaN has spoilt them here).
+__device__ __forceinline__ void flag_unit(const AttnParams& p, const Unit& u, int lane) {
+#pragma unroll 1
+  for (int i = lane; i < u.nt; i += 32) p.redo[(int64_t)(u.tok0 + i) * p.n_kv + u.head] = 1;
+  if (lane == 0) atomicExch(p.redo_any, 1);
+}
+
+// The copying warp hands unit u (number n of the CTA) to the other roles; false: a wait gave up.
+template <class Wait>
+__device__ __forceinline__ bool give_unit(UnitRing* r, const Unit& u, int n, int lane, Wait wait) {
+  const int slot = n % kUnitSlots;
+  if (n >= kUnitSlots && !wait(r->empty + slot, (n / kUnitSlots + 1) & 1)) return false;
+  if (lane == 0) {
+    const int4* src = reinterpret_cast<const int4*>(&u);
+    int4* dst = reinterpret_cast<int4*>(r->u + slot);
+    dst[0] = src[0], dst[1] = src[1], dst[2] = src[2];
+    mbar_arrive(r->full + slot);
   }
-  p.rec[blockIdx.x] = r;
+  __syncwarp();
+  return true;
+}
+// A warp of another role takes its n-th unit; false: the end, or a wait gave up.
+template <class Wait>
+__device__ __forceinline__ bool take_unit(UnitRing* r, Unit& u, int n, int lane, Wait wait) {
+  const int slot = n % kUnitSlots;
+  if (!wait(r->full + slot, (n / kUnitSlots) & 1)) return false;
+  int4* dst = reinterpret_cast<int4*>(&u);
+  const int4* src = reinterpret_cast<const int4*>(r->u + slot);
+  dst[0] = src[0], dst[1] = src[1], dst[2] = src[2];
+  __syncwarp();
+  if (lane == 0) mbar_arrive(r->empty + slot);
+  return u.i1 > 0;
 }
 
 }  // namespace coli

@@ -16,8 +16,6 @@ namespace coli {
 
 namespace {
 
-static_assert(sizeof(Stretch) + 4 <= 80, "tail of the shared memory");
-
 template <int D, int RG>
 struct SplitCfg {
   static constexpr int KG = RG == 4 ? 2 : 4;  // key groups: warps that share 16 rows
@@ -30,15 +28,16 @@ struct SplitCfg {
   static constexpr int stages = (RG == 1 ? 98304 : 163840) / (2 * tile_bytes);
   static constexpr int merge_floats = 16 * D + 32;
   static constexpr int merge_bytes = RG * (KG / 2) * merge_floats * 4;
-  static constexpr int smem = stages * 2 * tile_bytes + merge_bytes + 2 * stages * 8 + 80;
+  static constexpr int smem = stages * 2 * tile_bytes + merge_bytes + 2 * stages * 8 + (int)sizeof(UnitRing) + 24;
 };
 
-// 16 rows x kw keys of one tile for one warp
+// 16 rows, at positions p0..p1, x kw keys of one tile for one warp.  bad: a value that is not finite and that
+// only some of the rows see has gone into products with the others' zero weights.
 template <class T, int D, int RG, bool Masked>
 __device__ __forceinline__ void tile_step(const AttnParams& p, uint32_t ks, uint32_t vs, int key0,
-                                          int p0, int p1, const int (&pos)[2], int tok_lo, int tok_hi,
+                                          int p0, int p1, const int (&pos)[2],
                                           const uint32_t (&qf)[D / 16][4], float (&o)[D / 8][4],
-                                          float (&mx)[2], float (&sum)[2], int lane, int row0) {
+                                          float (&mx)[2], float (&sum)[2], uint32_t& bad, int lane) {
   using C = SplitCfg<D, RG>;
   constexpr int NT = C::kw / 8;
   const int c2 = (lane & 3) * 2;
@@ -113,31 +112,7 @@ __device__ __forceinline__ void tile_step(const AttnParams& p, uint32_t ks, uint
       if (Masked) {
         b[0] &= z0, b[2] &= z0;
         b[1] &= z1, b[3] &= z1;
-        // A non-finite value that only some rows see must not reach the others (0 * inf = NaN):
-        // then each token's rows are multiplied on their own, with only the values they see.
-        uint32_t bad = 0;
-        if (tok_hi > tok_lo)
-          bad = nonfinite2<T>(b[0]) | nonfinite2<T>(b[1]) | nonfinite2<T>(b[2]) | nonfinite2<T>(b[3]);
-        if (__any_sync(FULL, bad != 0)) {
-          for (int t = tok_lo; t <= tok_hi; ++t) {
-            const int pt = p.causal ? p0 + t : p0;
-            const uint32_t y0 = (sees(p, pt, kk) ? 0xFFFFu : 0u) | (sees(p, pt, kk + 1) ? 0xFFFF0000u : 0u);
-            const uint32_t y1 =
-                (sees(p, pt, kk + 8) ? 0xFFFFu : 0u) | (sees(p, pt, kk + 9) ? 0xFFFF0000u : 0u);
-            float u[2][4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) u[0][i] = o[2 * d][i], u[1][i] = o[2 * d + 1][i];
-            mma16816<T>(u[0], pf, b[0] & y0, b[1] & y1);
-            mma16816<T>(u[1], pf, b[2] & y0, b[3] & y1);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if ((row0 + (lane >> 2) + (i >> 1) * 8) / p.group == t) {
-                o[2 * d][i] = u[0][i];
-                o[2 * d + 1][i] = u[1][i];
-              }
-          }
-          continue;
-        }
+        bad |= nonfinite2<T>(b[0]) | nonfinite2<T>(b[1]) | nonfinite2<T>(b[2]) | nonfinite2<T>(b[3]);
       }
       mma16816<T>(o[2 * d], pf, b[0], b[1]);
       mma16816<T>(o[2 * d + 1], pf, b[2], b[3]);
@@ -153,61 +128,70 @@ __global__ void __launch_bounds__(SplitCfg<D, RG>::threads, SplitCfg<D, RG>::cta
   constexpr int NST = C::stages;
   extern __shared__ __align__(1024) uint8_t smem[];
   float* merge = reinterpret_cast<float*>(smem + NST * 2 * C::tile_bytes);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + NST * 2 * C::tile_bytes + C::merge_bytes);
-  uint64_t* empty = full + NST;
+  UnitRing* units = reinterpret_cast<UnitRing*>(smem + NST * 2 * C::tile_bytes + C::merge_bytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(units + 1);
+  uint64_t *empty = full + NST, *met = empty + NST;
   // (no static shared memory: with it, two CTAs of 16 rows would no longer fit one SM)
-  Stretch* stretch = reinterpret_cast<Stretch*>(empty + NST);
-  int* abort_flag = reinterpret_cast<int*>(stretch + 1);
+  int* abort_flag = reinterpret_cast<int*>(met + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const auto wait = [&](uint64_t* bar, uint32_t parity) { return warp_wait(bar, parity, abort_flag, p.status); };
 
   if (tid == 0) {
     *abort_flag = 0;
+    units->init(C::warps);
     for (int i = 0; i < NST; ++i) mbar_init(full + i, 1), mbar_init(empty + i, C::warps);
+    mbar_init(met, C::warps);
     fence_barrier_init();
     prefetch_map(&kmap);
     prefetch_map(&vmap);
   }
   griddep_wait();
   griddep_launch_dependents();
-  const Stretch st = schedule<kSplitKeys>(p, reinterpret_cast<int64_t*>(smem), stretch);
-  if (warp == 0 && lane == 0) write_record<kSplitKeys>(p, st);
-  // the copies below overwrite what schedule() kept in the ring's memory
-  fence_proxy_async_smem();
-  __syncthreads();
+  uint32_t* weights = reinterpret_cast<uint32_t*>(smem);  // in the ring, before the first copy
+  weigh<kSplitKeys>(p, weights);
 
-  Cursor<kSplitKeys> cur;
-  cur.start(p, st);
   if (warp == C::warps) {  // ---- copies
-    int it = 0;
-    for (; cur.valid(); cur.next(p)) {
-      const int64_t row = (int64_t)cur.b * p.table_stride;
-      for (int i = cur.i0; i < cur.i1; ++i, ++it) {
+    Walk<kSplitKeys> walk;
+    walk.start(p, weights, lane);
+    if (lane == 0) p.rec[blockIdx.x].first_cta = -1;
+    __syncwarp();
+    fence_proxy_async_smem();
+    int it = 0, n = 0;
+    Unit u;
+    bool ok = true;
+    while (ok && walk.next(p, u)) {
+      ok = give_unit(units, u, n++, lane, wait);
+      const int64_t row = (int64_t)u.b * p.table_stride;
+#pragma unroll 1
+      for (int i = u.i0; i < u.i1 && ok; ++i, ++it) {
         const int sgi = it % NST;
-        if (it >= NST && !warp_wait(empty + sgi, ((it / NST) + 1) & 1, abort_flag, p.status)) {
-          drain_fills(full, NST, it);
-          return;
-        }
+        if (it >= NST) ok = wait(empty + sgi, ((it / NST) + 1) & 1);
+        if (!ok) break;
         uint8_t* dst = smem + sgi * 2 * C::tile_bytes;
-        const int j0 = cur.t.tile(i) * kSplitKeys;
-        const uint32_t bytes = fill_bytes<kSplitKeys, D>(p, cur.t.p0, cur.t.p1, j0, lane);
-        if (lane == 0) mbar_expect_tx(full + sgi, 2 * bytes);
-        __syncwarp();
-        fill_boxes<kSplitKeys, D>(p, &kmap, dst, full + sgi, row, cur.t.p0, cur.t.p1, j0, cur.head, lane);
-        fill_boxes<kSplitKeys, D>(p, &vmap, dst + C::tile_bytes, full + sgi, row, cur.t.p0, cur.t.p1, j0,
-                                  cur.head, lane);
+        fill_boxes<kSplitKeys, D, 2>(p, &kmap, &vmap, dst, full + sgi, full + sgi, C::tile_bytes, row, u.p0, u.p1,
+                                     u.tile(i) * kSplitKeys, u.head, lane);
       }
     }
+    u.i1 = 0;
+    if (ok) ok = give_unit(units, u, n, lane, wait);
+    if (!ok) drain_ring(full, NST, it);
     return;
   }
 
   // ---- products
   const int rg = warp % RG, kg = warp / RG;
   const int row0 = rg * 16;  // this warp's rows of the block
+  uint32_t meetings = 0;
+  // the product warps wait for one another (bounded: one that gave up must not leave the others behind)
+  const auto meet = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(met);
+    return wait(met, meetings++ & 1);
+  };
   int it = 0;
-  for (; cur.valid(); cur.next(p)) {
-    const int tok0 = cur.s.start + cur.blk * p.block_tokens;
-    const int nt = min(p.block_tokens, cur.s.n - cur.blk * p.block_tokens);
-    const int p0 = cur.t.p0, p1 = cur.t.p1;
+  Unit u;
+  for (int n = 0; take_unit(units, u, n, lane, wait); ++n) {
+    const int tok0 = u.tok0, nt = u.nt, p0 = u.p0;
     int pos[2], tok[2];
     bool live[2];
     uint32_t qf[D / 16][4];
@@ -219,34 +203,41 @@ __global__ void __launch_bounds__(SplitCfg<D, RG>::threads, SplitCfg<D, RG>::cta
       pos[r] = p.causal ? p0 + tok[r] : p0;
       const uint32_t* src = reinterpret_cast<const uint32_t*>(
           static_cast<const uint16_t*>(p.q) + (int64_t)(tok0 + tok[r]) * p.q_stride +
-          (int64_t)(cur.head * p.group + row - tok[r] * p.group) * D);
+          (int64_t)(u.head * p.group + row - tok[r] * p.group) * D);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         qf[k][r] = live[r] ? __ldg(src + k * 8 + (lane & 3)) : 0u;
         qf[k][r + 2] = live[r] ? __ldg(src + k * 8 + 4 + (lane & 3)) : 0u;
       }
     }
+    // the warp's own tokens and their positions
     const int tok_lo = row0 / p.group, tok_hi = min(nt - 1, (row0 + 15) / p.group);
+    const int w0 = p.causal ? p0 + tok_lo : p0, w1 = p.causal ? p0 + tok_hi : p0;
+    uint32_t bad = 0;
     float o[D / 8][4], mx[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
 #pragma unroll
     for (int d = 0; d < D / 8; ++d)
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[d][i] = 0.f;
 
-    for (int i = cur.i0; i < cur.i1; ++i, ++it) {
+#pragma unroll 1
+    for (int i = u.i0; i < u.i1; ++i, ++it) {
       const int sgi = it % NST;
-      if (!warp_wait(full + sgi, (it / NST) & 1, abort_flag, p.status)) goto out;
+      if (!wait(full + sgi, (it / NST) & 1)) return;
       {
         const uint32_t ks = smem_addr(smem + sgi * 2 * C::tile_bytes), vs = ks + C::tile_bytes;
-        const int key0 = cur.t.tile(i) * kSplitKeys + kg * C::kw;
-        if (all_see(p, p0, p1, key0, key0 + C::kw - 1))
-          tile_step<T, D, RG, false>(p, ks, vs, key0, p0, p1, pos, tok_lo, tok_hi, qf, o, mx, sum, lane, row0);
-        else
-          tile_step<T, D, RG, true>(p, ks, vs, key0, p0, p1, pos, tok_lo, tok_hi, qf, o, mx, sum, lane, row0);
+        const int key0 = u.tile(i) * kSplitKeys + kg * C::kw;
+        if (tok_lo >= nt) {
+        } else if (all_see(p, w0, w1, key0, key0 + C::kw - 1)) {
+          tile_step<T, D, RG, false>(p, ks, vs, key0, w0, w1, pos, qf, o, mx, sum, bad, lane);
+        } else {
+          tile_step<T, D, RG, true>(p, ks, vs, key0, w0, w1, pos, qf, o, mx, sum, bad, lane);
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(empty + sgi);
     }
+    if (tok_hi > tok_lo && __any_sync(FULL, bad != 0)) flag_unit(p, u, lane);
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       sum[r] += __shfl_xor_sync(FULL, sum[r], 1);
@@ -258,7 +249,7 @@ __global__ void __launch_bounds__(SplitCfg<D, RG>::threads, SplitCfg<D, RG>::cta
       const int slot = (kg % half) * RG + rg;
       float4* buf = reinterpret_cast<float4*>(merge + slot * C::merge_floats);
       float2* ml = reinterpret_cast<float2*>(merge + slot * C::merge_floats + 16 * D);
-      named_bar_sync(1, C::warps * 32);
+      if (!meet()) return;
       if (kg >= half && kg < 2 * half) {
 #pragma unroll
         for (int d = 0; d < D / 8; ++d) buf[d * 32 + lane] = make_float4(o[d][0], o[d][1], o[d][2], o[d][3]);
@@ -267,7 +258,7 @@ __global__ void __launch_bounds__(SplitCfg<D, RG>::threads, SplitCfg<D, RG>::cta
           ml[(lane >> 2) + 8] = make_float2(mx[1], sum[1]);
         }
       }
-      named_bar_sync(1, C::warps * 32);
+      if (!meet()) return;
       if (kg < half) {
         float fa[2], fb[2];
 #pragma unroll
@@ -295,9 +286,9 @@ __global__ void __launch_bounds__(SplitCfg<D, RG>::threads, SplitCfg<D, RG>::cta
       for (int r = 0; r < 2; ++r) {
         const int row = row0 + (lane >> 2) + r * 8;
         const float m2 = mx[r] * p.scale_log2;  // -inf stays -inf
-        if (cur.whole() && !p.dense_o) {
+        if (u.whole && !p.dense_o) {
           if (!live[r]) continue;
-          const int hq = cur.head * p.group + row - tok[r] * p.group;
+          const int hq = u.head * p.group + row - tok[r] * p.group;
           const float inv = sum[r] == 0.f ? 0.f : 1.f / sum[r];
           uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) +
                                                       (int64_t)(tok0 + tok[r]) * p.out_stride + (int64_t)hq * D);
@@ -311,12 +302,12 @@ __global__ void __launch_bounds__(SplitCfg<D, RG>::threads, SplitCfg<D, RG>::cta
           int64_t at;
           float* dst;
           float2* ml;
-          if (cur.whole()) {
+          if (u.whole) {
             if (!live[r]) continue;
-            at = (int64_t)(tok0 + tok[r]) * p.n_q + cur.head * p.group + row - tok[r] * p.group;
+            at = (int64_t)(tok0 + tok[r]) * p.n_q + u.head * p.group + row - tok[r] * p.group;
             dst = p.dense_o, ml = p.dense_ml;
           } else {
-            at = ((int64_t)blockIdx.x * 2 + (cur.first ? 0 : 1)) * C::rows + row;
+            at = ((int64_t)blockIdx.x * 2 + (u.i0 > 0 ? 0 : 1)) * C::rows + row;
             dst = p.part_o, ml = p.part_ml;
           }
 #pragma unroll
@@ -328,8 +319,6 @@ __global__ void __launch_bounds__(SplitCfg<D, RG>::threads, SplitCfg<D, RG>::cta
       }
     }
   }
-out:
-  return;
 }
 
 typedef void (*SplitKernel)(const AttnParams, const CUtensorMap, const CUtensorMap);

@@ -41,7 +41,7 @@ struct TileCfg {
   static constexpr int q_bytes = 2 * tile_bytes;
   // barriers: keys full/empty, values full/empty/checked, q full/empty, scores, weights, output, drain
   static constexpr int bars = 2 * k_stages + 3 * v_stages + 4 + 6 + 1;
-  static constexpr int smem = kTileSmemRing + q_bytes + bars * 8 + 128;
+  static constexpr int smem = kTileSmemRing + q_bytes + (int)sizeof(UnitRing) + bars * 8 + 16;
   static constexpr uint32_t o_col = 256;  // first column of O0; O1 follows after D columns
 };
 
@@ -130,6 +130,17 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// the n lowest bits (n may be out of 0..32)
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u;
+}
+
 // 32 bytes of a thread's row at once: a full sector per thread
 __device__ __forceinline__ void st_sector(void* p, const uint32_t (&v)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
@@ -146,19 +157,24 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t *kring = smem, *vring = smem + KST * C::tile_bytes;
   uint8_t* qs = smem + kTileSmemRing;
-  uint64_t* k_full = reinterpret_cast<uint64_t*>(qs + C::q_bytes);
+  UnitRing* units = reinterpret_cast<UnitRing*>(qs + C::q_bytes);
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(units + 1);
   uint64_t *k_empty = k_full + KST, *v_full = k_empty + KST, *v_empty = v_full + VST, *checked = v_empty + VST,
-           *q_full = checked + VST, *q_empty = q_full + 2,
-           *s_full = q_empty + 2, *p_full = s_full + 2, *o_full = p_full + 2, *drain = o_full + 2;
-  Stretch* stretch = reinterpret_cast<Stretch*>(drain + 1);
-  int* abort_flag = reinterpret_cast<int*>(stretch + 1);
+           *q_full = checked + VST, *q_empty = q_full + 2, *s_full = q_empty + 2, *p_full = s_full + 2,
+           *o_full = p_full + 2, *drain = o_full + 2;
+  int* abort_flag = reinterpret_cast<int*>(drain + 1);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(abort_flag + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const auto wait = [&](uint64_t* bar, uint32_t parity) { return warp_wait(bar, parity, abort_flag, p.status); };
 
   if (tid == 0) {
     *abort_flag = 0;
+    units->init(11);  // every warp but the copying one
+#pragma unroll 1
     for (int i = 0; i < KST; ++i) mbar_init(k_full + i, 1), mbar_init(k_empty + i, 1);
+#pragma unroll 1
     for (int i = 0; i < VST; ++i) mbar_init(v_full + i, 1), mbar_init(v_empty + i, 1), mbar_init(checked + i, 2);
+#pragma unroll 1
     for (int s = 0; s < 2; ++s) {
       mbar_init(q_full + s, 1), mbar_init(q_empty + s, 1), mbar_init(s_full + s, 1);
       mbar_init(p_full + s, 4), mbar_init(o_full + s, 1);
@@ -170,226 +186,229 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
   if (warp == 8) tmem_alloc(tmem_slot, 512);
   griddep_wait();
   griddep_launch_dependents();
-  const Stretch st = schedule<kTileKeys>(p, reinterpret_cast<int64_t*>(smem), stretch);
-  if (warp == 9 && lane == 0) write_record<kTileKeys>(p, st);
-  fence_proxy_async_smem();  // the copies overwrite what schedule() kept in the rings
+  uint32_t* weights = reinterpret_cast<uint32_t*>(smem);  // in the rings, before the first copy
   tc_fence_before();
-  __syncthreads();
+  weigh<kTileKeys>(p, weights);
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int half_tokens = p.block_tokens / 2;  // tokens of one row tile
 
-  Cursor<kTileKeys> cur;
-  cur.start(p, st);
-  // tokens of row tile s of the current unit
-  const auto tokens = [&](const Cursor<kTileKeys>& c, int s) {
-    return max(0, min(half_tokens, c.s.n - c.blk * p.block_tokens - s * half_tokens));
-  };
-
-  if (warp == 9) {  // ---- copies
-    int it = 0, kt = 0, qn[2] = {0, 0};  // value, key and query tiles asked for
+  // registers: 200 for each of the 256 softmax threads, 104 for the others: the 384 x 168 of the launch
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    Unit u;
     bool ok = true;
-    for (; cur.valid() && ok; cur.next(p)) {
-      const int64_t row = (int64_t)cur.b * p.table_stride;
-      const int tok0 = cur.s.start + cur.blk * p.block_tokens;
+    if (warp == 9) {  // ---- copies
+      Walk<kTileKeys> walk;
+      walk.start(p, weights, lane);
+      if (lane == 0) p.rec[blockIdx.x].first_cta = -1;
+      __syncwarp();
+      fence_proxy_async_smem();
+      int it = 0, kt = 0, n = 0, qn0 = 0, qn1 = 0;  // value, key tiles, units, queries of either row tile
       const uint32_t qb = (uint32_t)(p.group * half_tokens) * D * 2;
-      for (int s = 0; s < 2 && ok; ++s) {
-        if (tokens(cur, s) == 0) continue;
-        if (qn[s] > 0) ok = warp_wait(q_empty + s, (qn[s] - 1) & 1, abort_flag, p.status);
-        if (!ok) break;
-        ++qn[s];
-        if (lane == 0) {
-          mbar_expect_tx(q_full + s, qb);
-          for (int sl = 0; sl < D / 64; ++sl)
-            tma_load_3d(qs + s * C::tile_bytes + sl * kTileKeys * 128, &qmap, sl * 64, cur.head * p.group,
-                        tok0 + s * half_tokens, q_full + s);
-        }
-        __syncwarp();
-      }
-      for (int i = cur.i0; i < cur.i1 && ok; ++i, ++it) {
-        const int j0 = cur.t.tile(i) * kTileKeys;
-        const uint32_t bytes = fill_bytes<kTileKeys, D>(p, cur.t.p0, cur.t.p1, j0, lane);
-        const int ks = it % KST, vs = it % VST;
-        if (it >= KST) ok = warp_wait(k_empty + ks, ((it / KST) + 1) & 1, abort_flag, p.status);
-        if (!ok) break;
-        if (lane == 0) mbar_expect_tx(k_full + ks, bytes);
-        __syncwarp();
-        fill_boxes<kTileKeys, D>(p, &kmap, kring + ks * C::tile_bytes, k_full + ks, row, cur.t.p0, cur.t.p1, j0,
-                                 cur.head, lane);
-        ++kt;
-        if (it >= VST) ok = warp_wait(v_empty + vs, ((it / VST) + 1) & 1, abort_flag, p.status);
-        if (!ok) break;
-        if (lane == 0) mbar_expect_tx(v_full + vs, bytes);
-        __syncwarp();
-        fill_boxes<kTileKeys, D>(p, &vmap, vring + vs * C::tile_bytes, v_full + vs, row, cur.t.p0, cur.t.p1, j0,
-                                 cur.head, lane);
-      }
-    }
-    if (!ok) {
-      drain_fills(k_full, KST, kt);
-      drain_fills(v_full, VST, it);
-      for (int s = 0; s < 2; ++s)
-        if (qn[s] > 0) drain_fills(q_full + s, 1, qn[s]);
-    }
-  } else if (warp == 8) {  // ---- products (lane 0 issues; the warp waits together)
-    constexpr uint32_t qk_desc = mma_desc<T>(kTileKeys, false), pv_desc = mma_desc<T>(D, true);
-    Cursor<kTileKeys> nxt = cur;  // the unit and tile whose scores come next
-    int ni = nxt.i0, nit = 0, qn[2] = {0, 0}, pn[2] = {0, 0};
-    bool ok = true, more = nxt.valid();
-    const auto scores = [&](int s) {  // S_s of tile ni of nxt; nit: its number
-      if (tokens(nxt, s) == 0) return;
-      if (ni == nxt.i0) {
-        ok = ok && warp_wait(q_full + s, qn[s] & 1, abort_flag, p.status);
-        ++qn[s];
-      }
-      const int sg = nit % KST;
-      ok = ok && warp_wait(k_full + sg, (nit / KST) & 1, abort_flag, p.status);
-      if (!ok) return;
-      tc_fence_after();
-      if (lane == 0) {
 #pragma unroll 1
-        for (int k = 0; k < D / 16; ++k) {
-          const int off = (k >> 2) * kTileKeys * 128 + (k & 3) * 32;
-          tc_mma_bf16(tmem + s * 128, smem_desc_sw128(qs + s * C::tile_bytes + off),
-                      smem_desc_sw128(kring + sg * C::tile_bytes + off), qk_desc, k > 0);
+      while (ok && walk.next(p, u)) {
+        ok = give_unit(units, u, n++, lane, wait);
+#pragma unroll 1
+        for (int s = 0; s < 2 && ok && u.nt > s * half_tokens; ++s) {
+          const int qn = s ? qn1 : qn0;
+          if (qn > 0) ok = wait(q_empty + s, (qn - 1) & 1);
+          if (!ok) break;
+          s ? ++qn1 : ++qn0;
+          if (lane == 0) {
+            mbar_expect_tx(q_full + s, qb);
+#pragma unroll
+            for (int sl = 0; sl < D / 64; ++sl)
+              tma_load_3d(qs + s * C::tile_bytes + sl * kTileKeys * 128, &qmap, sl * 64, u.head * p.group,
+                          u.tok0 + s * half_tokens, q_full + s);
+          }
+          __syncwarp();
         }
-        tc_commit(s_full + s);
-        if (ni == nxt.i1 - 1) tc_commit(q_empty + s);
+        const int64_t row = (int64_t)u.b * p.table_stride;
+#pragma unroll 1
+        for (int i = u.i0; i < u.i1 && ok; ++i, ++it) {
+          const int j0 = u.tile(i) * kTileKeys, ks = it % KST, vs = it % VST;
+          if (it >= KST) ok = wait(k_empty + ks, ((it / KST) + 1) & 1);
+          if (!ok) break;
+          fill_boxes<kTileKeys, D, 1>(p, &kmap, nullptr, kring + ks * C::tile_bytes, k_full + ks, nullptr, 0, row, u.p0,
+                                      u.p1, j0, u.head, lane);
+          ++kt;
+          if (it >= VST) ok = wait(v_empty + vs, ((it / VST) + 1) & 1);
+          if (!ok) break;
+          fill_boxes<kTileKeys, D, 1>(p, &vmap, nullptr, vring + vs * C::tile_bytes, v_full + vs, nullptr, 0, row, u.p0,
+                                      u.p1, j0, u.head, lane);
+        }
       }
-      __syncwarp();
-    };
-    const auto step = [&]() {  // nxt's key tile is done with
-      if (lane == 0) tc_commit(k_empty + nit % KST);
-      __syncwarp();
-      ++nit;
-      if (++ni == nxt.i1) {
-        nxt.next(p);
-        more = nxt.valid();
-        ni = more ? nxt.i0 : 0;
+      u.i1 = 0;
+      if (ok) ok = give_unit(units, u, n, lane, wait);
+      if (!ok) {
+        drain_ring(k_full, KST, kt);
+        drain_ring(v_full, VST, it);
+        drain_ring(q_full, 1, qn0);
+        drain_ring(q_full + 1, 1, qn1);
       }
-    };
-    if (more) {
-      scores(0), scores(1);
-      if (ok) step();
-    }
-    int it = 0;
-    for (; cur.valid() && ok; cur.next(p))
-      for (int i = cur.i0; i < cur.i1 && ok; ++i, ++it) {
-        const int sg = it % VST;
+    } else if (warp == 8) {  // ---- products (lane 0 issues; the warp waits together)
+      constexpr uint32_t qk_idesc = mma_desc<T>(kTileKeys, false), pv_idesc = mma_desc<T>(D, true);
+      // descriptors of the first tiles; others are a whole number of 16-byte units further (no carry out of
+      // the 14-bit address field: shared memory ends below 2^18 bytes)
+      const uint64_t q_desc = smem_desc_sw128(qs), k_desc = smem_desc_sw128(kring), v_desc = smem_desc_values(vring);
+      // Scores run one key tile ahead of values: a_* is the unit they are in (a_left tiles to go, a_first: none
+      // yet), b_* the values' one.  Each round issues, for either row tile, values of tile it and scores of it + 1.
+      int units_taken = 0, it = -1;
+      uint32_t qn0 = 0, qn1 = 0, pn0 = 0, pn1 = 0;
+      int a_left = 0, b_left = 0;
+      bool a_two = false, b_two = false, a_first = false, b_first = false;
+      const auto take = [&]() {
+        if (!take_unit(units, u, units_taken++, lane, wait)) return false;
+        a_left = u.i1 - u.i0, a_two = u.nt > half_tokens, a_first = true;
+        return true;
+      };
+      bool more = take();
+#pragma unroll 1
+      while (ok && (more || b_left > 0)) {
+        const bool s_last = a_left == 1;
+#pragma unroll 1
         for (int s = 0; s < 2 && ok; ++s) {
-          if (tokens(cur, s) > 0) {
-            ok = warp_wait(checked + sg, (it / VST) & 1, abort_flag, p.status) &&
-                 warp_wait(p_full + s, pn[s] & 1, abort_flag, p.status);
-            ++pn[s];
+          if (b_left > 0 && (s == 0 || b_two)) {
+            const int sg = it % VST;
+            ok = wait(checked + sg, (it / VST) & 1) && wait(p_full + s, (s ? pn1 : pn0) & 1);
             if (!ok) break;
+            s ? ++pn1 : ++pn0;
             tc_fence_after();
             if (lane == 0) {
-#pragma unroll 1
-              for (int k = 0; k < kTileKeys / 16; ++k)
-                tc_mma_ts(tmem + C::o_col + s * D, tmem + s * 128 + k * 8,
-                          smem_desc_values(vring + sg * C::tile_bytes + k * 2048), pv_desc, i > cur.i0 || k > 0);
-              if (i == cur.i1 - 1) tc_commit(o_full + s);
+              const uint64_t b = v_desc + sg * (C::tile_bytes >> 4);
+              const uint32_t d = tmem + C::o_col + s * D, a = tmem + s * 128;
+              tc_mma_ts(d, a, b, pv_idesc, !b_first);
+#pragma unroll
+              for (int k = 1; k < kTileKeys / 16; ++k) tc_mma_ts(d, a + k * 8, b + k * (2048 >> 4), pv_idesc, true);
+              if (b_left == 1) tc_commit(o_full + s);
             }
             __syncwarp();
           }
-          if (more) scores(s);
+          if (more && (s == 0 || a_two)) {
+            if (a_first) {
+              ok = wait(q_full + s, (s ? qn1 : qn0) & 1);
+              s ? ++qn1 : ++qn0;
+            }
+            const int nit = it + 1, sg = nit % KST;
+            ok = ok && wait(k_full + sg, (nit / KST) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) {
+              const uint64_t a = q_desc + s * (C::tile_bytes >> 4), b = k_desc + sg * (C::tile_bytes >> 4);
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k) {
+                const int off = ((k >> 2) * kTileKeys * 128 + (k & 3) * 32) >> 4;
+                tc_mma_bf16(tmem + s * 128, a + off, b + off, qk_idesc, k > 0);
+              }
+              tc_commit(s_full + s);
+              if (s_last) tc_commit(q_empty + s);
+            }
+            __syncwarp();
+          }
         }
         if (!ok) break;
-        if (lane == 0) tc_commit(v_empty + sg);
+        if (lane == 0) {
+          if (b_left > 0) tc_commit(v_empty + it % VST);
+          if (more) tc_commit(k_empty + (it + 1) % KST);
+        }
         __syncwarp();
-        if (more) step();
+        ++it;
+        if (b_left > 0) --b_left, b_first = false;
+        if (b_left == 0 && more) b_left = a_left, b_two = a_two, b_first = true;  // the scores of its first tile are out
+        if (more) {
+          a_first = false;
+          if (--a_left == 0) more = take();
+        }
       }
-    if (!ok) {  // wait, with a limit of its own, for the products in flight
-      if (lane == 0) tc_commit(drain);
-      drain_fills(drain, 1, 1);
-    }
-  } else if (warp >= 10) {  // ---- values that not every row sees
-    int it = 0;
-    bool ok = true;
-    for (; cur.valid() && ok; cur.next(p)) {
-      bool listed = false;
-      for (int i = cur.i0; i < cur.i1; ++i, ++it) {
-        const int sg = it % VST;
-        ok = warp_wait(v_full + sg, (it / VST) & 1, abort_flag, p.status);
-        if (!ok) break;
-        const int j0 = cur.t.tile(i) * kTileKeys;
-        if (!all_see(p, cur.t.p0, cur.t.p1, j0, j0 + kTileKeys - 1)) {
-          uint32_t bad = 0;
-          // warp 10 takes the even keys, 11 the odd ones; 8 lanes a 128-byte row
-          for (int r = (warp - 10) + (lane >> 3) * 2; r < kTileKeys; r += 8) {
-            const bool some = some_sees(p, cur.t.p0, cur.t.p1, j0 + r);
-            const bool all = all_see(p, cur.t.p0, cur.t.p1, j0 + r, j0 + r);
-            if (all) continue;
+      if (*reinterpret_cast<volatile int*>(abort_flag)) {  // wait, with a limit of its own, for the products in flight
+        if (lane == 0) tc_commit(drain);
+        drain_ring(drain, 1, 1);
+      }
+    } else {  // ---- values that not every row sees
+      int it = 0;
+#pragma unroll 1
+      for (int n = 0; ok && take_unit(units, u, n, lane, wait); ++n) {
+        uint32_t bad = 0;
+#pragma unroll 1
+        for (int i = u.i0; i < u.i1; ++i, ++it) {
+          const int sg = it % VST;
+          ok = wait(v_full + sg, (it / VST) & 1);
+          if (!ok) break;
+          const int j0 = u.tile(i) * kTileKeys;
+          if (!all_see(p, u.p0, u.p1, j0, j0 + kTileKeys - 1)) {
+            // warp 10 takes the even keys, 11 the odd ones; 8 lanes a 128-byte row
+#pragma unroll 1
+            for (int r = (warp - 10) + (lane >> 3) * 2; r < kTileKeys; r += 8) {
+              if (all_see(p, u.p0, u.p1, j0 + r, j0 + r)) continue;
+              const bool some = some_sees(p, u.p0, u.p1, j0 + r);
 #pragma unroll
-            for (int sl = 0; sl < D / 64; ++sl) {
-              uint4* v = reinterpret_cast<uint4*>(vring + sg * C::tile_bytes + sl * kTileKeys * 128 + r * 128) + (lane & 7);
-              if (some) {
-                const uint4 x = *v;
-                bad |= nonfinite2<T>(x.x) | nonfinite2<T>(x.y) | nonfinite2<T>(x.z) | nonfinite2<T>(x.w);
-              } else {
-                *v = make_uint4(0, 0, 0, 0);
+              for (int sl = 0; sl < D / 64; ++sl) {
+                uint4* v = reinterpret_cast<uint4*>(vring + sg * C::tile_bytes + sl * kTileKeys * 128 + r * 128) + (lane & 7);
+                if (some) {
+                  const uint4 x = *v;
+                  bad |= nonfinite2<T>(x.x) | nonfinite2<T>(x.y) | nonfinite2<T>(x.z) | nonfinite2<T>(x.w);
+                } else {
+                  *v = make_uint4(0, 0, 0, 0);
+                }
               }
             }
+            fence_proxy_async_smem();
           }
-          fence_proxy_async_smem();
-          if (__any_sync(FULL, bad != 0) && !listed) {
-            listed = true;
-            if (lane == 0 && p.redo) {
-              const int at = atomicAdd(p.redo_count, 1);
-              if (at < p.redo_cap) p.redo[at] = make_int4(cur.b, cur.blk, cur.head, 0);
-            }
-          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(checked + sg);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(checked + sg);
+        if (__any_sync(FULL, bad != 0)) flag_unit(p, u, lane);
       }
     }
   } else {  // ---- softmax of row tile s; thread = row
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     const int s = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t st_addr = tmem + lane_base + s * 128, ot_addr = tmem + lane_base + C::o_col + s * D;
     const int tok = row / p.group;
     const float slack = 8.f / p.scale_log2;
-    int sn = 0, on = 0;
-    bool ok = true;
-    for (; cur.valid() && ok; cur.next(p)) {
-      const int nt = tokens(cur, s);
-      if (nt == 0) continue;
-      const int pa = p.causal ? cur.t.p0 + s * half_tokens : cur.t.p0;  // the row tile's positions
+    uint32_t sn = 0, on = 0;
+    Unit u;
+#pragma unroll 1
+    for (int n = 0; take_unit(units, u, n, lane, wait); ++n) {
+      const int nt = min(half_tokens, u.nt - s * half_tokens);
+      if (nt <= 0) continue;
+      const int pa = p.causal ? u.p0 + s * half_tokens : u.p0;  // the row tile's positions
       const int pb = p.causal ? pa + nt - 1 : pa;
       const int pos = p.causal ? pa + tok : pa;
       float ref = -INFINITY, sum0 = 0.f, sum1 = 0.f;
-      for (int i = cur.i0; i < cur.i1; ++i) {
-        ok = warp_wait(s_full + s, sn & 1, abort_flag, p.status);
+      bool ok = true;
+#pragma unroll 1
+      for (int i = u.i0; i < u.i1; ++i) {
+        ok = wait(s_full + s, sn & 1);
         ++sn;
         if (!ok) break;
         tc_fence_after();
-        const int j0 = cur.t.tile(i) * kTileKeys;
+        const int j0 = u.tile(i) * kTileKeys;
+        float x[128];
+        COLI_LD32(st_addr, x);
+        COLI_LD32(st_addr + 32, x + 32);
+        COLI_LD32(st_addr + 64, x + 64);
+        COLI_LD32(st_addr + 96, x + 96);
+        float m0 = -INFINITY, m1 = m0, m2 = m0, m3 = m0;
         const bool masked = !all_see(p, pa, pb, j0, j0 + kTileKeys - 1);
         const int hi = pos - j0, lo = pos - p.window - j0, sk = p.sinks - j0;
-        // Scores are read twice, for the maximum and for the weights: holding all 128 would spill.
-        float m0 = -INFINITY, m1 = m0, m2 = m0, m3 = m0;
-        {
-          float x[128];
-          COLI_LD32(st_addr, x);
-          COLI_LD32(st_addr + 32, x + 32);
-          COLI_LD32(st_addr + 64, x + 64);
-          COLI_LD32(st_addr + 96, x + 96);
-          COLI_LDWAIT32(x);
-          COLI_LDWAIT32(x + 32);
-          COLI_LDWAIT32(x + 64);
-          COLI_LDWAIT32(x + 96);
-          if (masked) {
 #pragma unroll
-            for (int c = 0; c < 128; ++c)
-              if (c > hi || (c <= lo && c >= sk)) x[c] = -INFINITY;
+        for (int c = 0; c < 128; c += 32) {
+          COLI_LDWAIT32(x + c);
+          if (masked) {  // bit k: the row sees key c + k
+            const uint32_t see = low_bits(hi + 1 - c) & (~low_bits(lo + 1 - c) | low_bits(sk - c));
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (!(see & (1u << k))) x[c + k] = -INFINITY;
           }
 #pragma unroll
-          for (int c = 0; c < 128; c += 8) {
-            m0 = fmaxf(m0, fmaxf(x[c], x[c + 1]));
-            m1 = fmaxf(m1, fmaxf(x[c + 2], x[c + 3]));
-            m2 = fmaxf(m2, fmaxf(x[c + 4], x[c + 5]));
-            m3 = fmaxf(m3, fmaxf(x[c + 6], x[c + 7]));
+          for (int k = 0; k < 32; k += 8) {
+            m0 = max3(m0, x[c + k], x[c + k + 1]);
+            m1 = max3(m1, x[c + k + 2], x[c + k + 3]);
+            m2 = max3(m2, x[c + k + 4], x[c + k + 5]);
+            m3 = max3(m3, x[c + k + 6], x[c + k + 7]);
           }
         }
         const float top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
@@ -402,8 +421,8 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
             sum0 *= fix, sum1 *= fix;
           }
           // the scores' commit also covers the products before them: O is complete
-          if (i > cur.i0 && __any_sync(FULL, fix != 1.f)) {
-#pragma unroll
+          if (i > u.i0 && __any_sync(FULL, fix != 1.f)) {
+#pragma unroll 1
             for (int c = 0; c < D; c += 32) {
               float o[32];
               COLI_LD32(ot_addr + c, o);
@@ -415,47 +434,43 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
           }
         }
         const float base = ref == -INFINITY ? 0.f : -ref * p.scale_log2;
-        float y[2][32];
-        COLI_LD32(st_addr, y[0]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float* x = y[c & 1];
-          COLI_LDWAIT32(x);
-          if (c < 3) COLI_LD32(st_addr + 32 * (c + 1), y[(c + 1) & 1]);
-          if (masked) {
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (c * 32 + k > hi || (c * 32 + k <= lo && c * 32 + k >= sk)) x[k] = -INFINITY;
-          }
+        for (int c = 0; c < 128; c += 32) {
           uint32_t w[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             float e = base, f = base;
-            fma2_rn(x[2 * k], x[2 * k + 1], p.scale_log2, p.scale_log2, e, f);
+            fma2_rn(x[c + 2 * k], x[c + 2 * k + 1], p.scale_log2, p.scale_log2, e, f);
             e = ex2(e), f = ex2(f);
-            add2_rn(e, f, sum0, sum1);
+            x[c + 2 * k] = e, x[c + 2 * k + 1] = f;
             w[k] = T::pack(e, f);
           }
-          tmem_st16u(st_addr + 16 * c, w);  // over scores that have been read
+          tmem_st16u(st_addr + c / 2, w);
         }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full + s);
+        float s2 = 0.f, s3 = 0.f;  // the sum is not needed before the end of the unit
+#pragma unroll
+        for (int c = 0; c < 128; c += 4) {
+          add2_rn(x[c], x[c + 1], sum0, sum1);
+          add2_rn(x[c + 2], x[c + 3], s2, s3);
+        }
+        sum0 += s2, sum1 += s3;
       }
       if (!ok) break;
-      ok = warp_wait(o_full + s, on & 1, abort_flag, p.status);
+      ok = wait(o_full + s, on & 1);
       ++on;
       if (!ok) break;
       tc_fence_after();
       const float sum = sum0 + sum1, m2 = ref * p.scale_log2;
-      const int tok0 = cur.s.start + cur.blk * p.block_tokens + s * half_tokens;
-      const int hq = cur.head * p.group + row - tok * p.group;
+      const int token = u.tok0 + s * half_tokens + tok, hq = u.head * p.group + row - tok * p.group;
       const bool live = tok < nt;
-      if (cur.whole() && !p.dense_o) {
+      if (u.whole && !p.dense_o) {
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        uint16_t* dst = static_cast<uint16_t*>(p.out) + (int64_t)(tok0 + tok) * p.out_stride + (int64_t)hq * D;
-#pragma unroll
+        uint16_t* dst = static_cast<uint16_t*>(p.out) + (int64_t)token * p.out_stride + (int64_t)hq * D;
+#pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           float o[32];
           COLI_LD32(ot_addr + c, o);
@@ -471,16 +486,14 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
           }
         }
         if (live && p.lse)
-          p.lse[(int64_t)(tok0 + tok) * p.n_q + hq] =
-              sum == 0.f ? -INFINITY : (m2 + log2f(sum)) * 0.69314718055994530942f;
+          p.lse[(int64_t)token * p.n_q + hq] = sum == 0.f ? -INFINITY : (m2 + log2f(sum)) * 0.69314718055994530942f;
       } else {
-        const bool dense = cur.whole();
-        // a cut unit's rows, numbered over both row tiles: row tile 1 starts at half_tokens * group
-        const int64_t at = dense ? (int64_t)(tok0 + tok) * p.n_q + hq
-                                 : ((int64_t)blockIdx.x * 2 + (cur.first ? 0 : 1)) * kTileRows +
-                                       s * half_tokens * p.group + row;
-        float* dst = (dense ? p.dense_o : p.part_o) + at * D;
-#pragma unroll
+        // a cut unit's rows are numbered over both row tiles: row tile 1 starts at half_tokens * group
+        const int64_t at = u.whole ? (int64_t)token * p.n_q + hq
+                                   : ((int64_t)blockIdx.x * 2 + (u.i0 > 0 ? 0 : 1)) * kTileRows +
+                                         s * half_tokens * p.group + row;
+        float* dst = (u.whole ? p.dense_o : p.part_o) + at * D;
+#pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           float o[32];
           COLI_LD32(ot_addr + c, o);
@@ -495,7 +508,7 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
             }
           }
         }
-        if (live) (dense ? p.dense_ml : p.part_ml)[at] = make_float2(m2, sum);
+        if (live) (u.whole ? p.dense_ml : p.part_ml)[at] = make_float2(m2, sum);
       }
       tc_fence_before();  // the next unit's products overwrite O after this row tile's next arrival
     }
