@@ -7,7 +7,7 @@
 // scores are in the softmax the other's products run, and the matrix unit is meant never to wait.
 //
 //   tensor memory (512 columns)   S0/P0 | S1/P1 | O0 | O1
-//   shared memory                 Q0, Q1, a ring of key and a ring of value tiles, 128-byte swizzled boxes
+//   shared memory                 Q0, Q1 and a ring of key and value tiles, 128-byte swizzled boxes
 //   warps 0-3, 4-7   softmax, rescaling and the epilogue of row tile 0, 1
 //   warp 8           issues every product; warp 9 every copy
 //   warps 10, 11     look at value tiles with keys that not every row sees
@@ -33,14 +33,10 @@ constexpr int kTileSmemRing = 163840;
 template <int D>
 struct TileCfg {
   static constexpr int tile_bytes = kTileKeys * D * 2;  // K or V of one stage; Q of one row tile
-  // Two rings, each with waiters that see every one of its tiles in order: with one ring for both, a
-  // waiter for value tiles alone could meet a stage whose previous (key) tile is still on its way and take
-  // the barrier's older phase for the one it wants.
-  static constexpr int k_stages = 2 * (kTileSmemRing / 5 / tile_bytes);
-  static constexpr int v_stages = 3 * (kTileSmemRing / 5 / tile_bytes);
+  static constexpr int stages = kTileSmemRing / tile_bytes;
   static constexpr int q_bytes = 2 * tile_bytes;
-  // barriers: keys full/empty, values full/empty/checked, q full/empty, scores, weights, output, drain
-  static constexpr int bars = 2 * k_stages + 3 * v_stages + 4 + 6 + 1;
+  // barriers: ring full/empty/checked, q full/empty, scores, weights (first half, all), output, drain
+  static constexpr int bars = 3 * stages + 4 + 2 + 4 + 2 + 1;
   static constexpr int smem = kTileSmemRing + q_bytes + (int)sizeof(UnitRing) + bars * 8 + 16;
   static constexpr uint32_t o_col = 256;  // first column of O0; O1 follows after D columns
 };
@@ -130,6 +126,13 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
+// true in one lane of a converged warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -153,31 +156,29 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
     attn_tile_kernel(const AttnParams p, const __grid_constant__ CUtensorMap qmap,
                      const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using C = TileCfg<D>;
-  constexpr int KST = C::k_stages, VST = C::v_stages;
+  constexpr int NST = C::stages;
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t *kring = smem, *vring = smem + KST * C::tile_bytes;
+  uint8_t* ring = smem;  // key tile i is item 2i, value tile i item 2i + 1
   uint8_t* qs = smem + kTileSmemRing;
   UnitRing* units = reinterpret_cast<UnitRing*>(qs + C::q_bytes);
-  uint64_t* k_full = reinterpret_cast<uint64_t*>(units + 1);
-  uint64_t *k_empty = k_full + KST, *v_full = k_empty + KST, *v_empty = v_full + VST, *checked = v_empty + VST,
-           *q_full = checked + VST, *q_empty = q_full + 2, *s_full = q_empty + 2, *p_full = s_full + 2,
-           *o_full = p_full + 2, *drain = o_full + 2;
+  uint64_t* full = reinterpret_cast<uint64_t*>(units + 1);
+  uint64_t *empty = full + NST, *checked = empty + NST, *q_full = checked + NST, *q_empty = q_full + 2,
+           *s_full = q_empty + 2, *p_half = s_full + 2, *p_full = p_half + 2, *o_full = p_full + 2, *drain = o_full + 2;
   int* abort_flag = reinterpret_cast<int*>(drain + 1);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(abort_flag + 1);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // (the shuffle tells the compiler that a warp's number, and with it every role's control flow, is uniform)
+  const int tid = threadIdx.x, warp = __shfl_sync(FULL, tid >> 5, 0), lane = tid & 31;
   const auto wait = [&](uint64_t* bar, uint32_t parity) { return warp_wait(bar, parity, abort_flag, p.status); };
 
   if (tid == 0) {
     *abort_flag = 0;
     units->init(11);  // every warp but the copying one
 #pragma unroll 1
-    for (int i = 0; i < KST; ++i) mbar_init(k_full + i, 1), mbar_init(k_empty + i, 1);
-#pragma unroll 1
-    for (int i = 0; i < VST; ++i) mbar_init(v_full + i, 1), mbar_init(v_empty + i, 1), mbar_init(checked + i, 2);
+    for (int i = 0; i < NST; ++i) mbar_init(full + i, 1), mbar_init(empty + i, 1), mbar_init(checked + i, 2);
 #pragma unroll 1
     for (int s = 0; s < 2; ++s) {
       mbar_init(q_full + s, 1), mbar_init(q_empty + s, 1), mbar_init(s_full + s, 1);
-      mbar_init(p_full + s, 4), mbar_init(o_full + s, 1);
+      mbar_init(p_half + s, 4), mbar_init(p_full + s, 4), mbar_init(o_full + s, 1);
     }
     mbar_init(drain, 1);
     fence_barrier_init();
@@ -186,7 +187,7 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
   if (warp == 8) tmem_alloc(tmem_slot, 512);
   griddep_wait();
   griddep_launch_dependents();
-  uint32_t* weights = reinterpret_cast<uint32_t*>(smem);  // in the rings, before the first copy
+  uint32_t* weights = reinterpret_cast<uint32_t*>(smem);  // in the ring, before the first copy
   tc_fence_before();
   weigh<kTileKeys>(p, weights);
   tc_fence_after();
@@ -204,7 +205,7 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
       if (lane == 0) p.rec[blockIdx.x].first_cta = -1;
       __syncwarp();
       fence_proxy_async_smem();
-      int it = 0, kt = 0, n = 0, qn0 = 0, qn1 = 0;  // value, key tiles, units, queries of either row tile
+      int it = 0, n = 0, qn0 = 0, qn1 = 0;  // items, units, queries of either row tile
       const uint32_t qb = (uint32_t)(p.group * half_tokens) * D * 2;
 #pragma unroll 1
       while (ok && walk.next(p, u)) {
@@ -226,32 +227,26 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
         }
         const int64_t row = (int64_t)u.b * p.table_stride;
 #pragma unroll 1
-        for (int i = u.i0; i < u.i1 && ok; ++i, ++it) {
-          const int j0 = u.tile(i) * kTileKeys, ks = it % KST, vs = it % VST;
-          if (it >= KST) ok = wait(k_empty + ks, ((it / KST) + 1) & 1);
+        for (int i = 2 * u.i0; i < 2 * u.i1 && ok; ++i, ++it) {
+          const int j0 = u.tile(i >> 1) * kTileKeys, sg = it % NST;
+          if (it >= NST) ok = wait(empty + sg, ((it / NST) + 1) & 1);
           if (!ok) break;
-          fill_boxes<kTileKeys, D, 1>(p, &kmap, nullptr, kring + ks * C::tile_bytes, k_full + ks, nullptr, 0, row, u.p0,
-                                      u.p1, j0, u.head, lane);
-          ++kt;
-          if (it >= VST) ok = wait(v_empty + vs, ((it / VST) + 1) & 1);
-          if (!ok) break;
-          fill_boxes<kTileKeys, D, 1>(p, &vmap, nullptr, vring + vs * C::tile_bytes, v_full + vs, nullptr, 0, row, u.p0,
-                                      u.p1, j0, u.head, lane);
+          fill_boxes<kTileKeys, D, 1>(p, i & 1 ? &vmap : &kmap, nullptr, ring + sg * C::tile_bytes, full + sg, nullptr, 0,
+                                      row, u.p0, u.p1, j0, u.head, lane);
         }
       }
       u.i1 = 0;
       if (ok) ok = give_unit(units, u, n, lane, wait);
       if (!ok) {
-        drain_ring(k_full, KST, kt);
-        drain_ring(v_full, VST, it);
+        drain_ring(full, NST, it);
         drain_ring(q_full, 1, qn0);
         drain_ring(q_full + 1, 1, qn1);
       }
-    } else if (warp == 8) {  // ---- products (lane 0 issues; the warp waits together)
+    } else if (warp == 8) {  // ---- products (one lane issues; the warp waits together)
       constexpr uint32_t qk_idesc = mma_desc<T>(kTileKeys, false), pv_idesc = mma_desc<T>(D, true);
       // descriptors of the first tiles; others are a whole number of 16-byte units further (no carry out of
       // the 14-bit address field: shared memory ends below 2^18 bytes)
-      const uint64_t q_desc = smem_desc_sw128(qs), k_desc = smem_desc_sw128(kring), v_desc = smem_desc_values(vring);
+      const uint64_t q_desc = smem_desc_sw128(qs), k_desc = smem_desc_sw128(ring), v_desc = smem_desc_values(ring);
       // Scores run one key tile ahead of values: a_* is the unit they are in (a_left tiles to go, a_first: none
       // yet), b_* the values' one.  Each round issues, for either row tile, values of tile it and scores of it + 1.
       int units_taken = 0, it = -1;
@@ -270,17 +265,25 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
 #pragma unroll 1
         for (int s = 0; s < 2 && ok; ++s) {
           if (b_left > 0 && (s == 0 || b_two)) {
-            const int sg = it % VST;
-            ok = wait(checked + sg, (it / VST) & 1) && wait(p_full + s, (s ? pn1 : pn0) & 1);
+            const int item = 2 * it + 1, sg = item % NST;
+            const uint32_t phase = (s ? pn1++ : pn0++) & 1;
+            ok = wait(checked + sg, (item / NST) & 1) && wait(p_half + s, phase);
             if (!ok) break;
-            s ? ++pn1 : ++pn0;
             tc_fence_after();
-            if (lane == 0) {
-              const uint64_t b = v_desc + sg * (C::tile_bytes >> 4);
-              const uint32_t d = tmem + C::o_col + s * D, a = tmem + s * 128;
+            const uint64_t b = v_desc + sg * (C::tile_bytes >> 4);
+            const uint32_t d = tmem + C::o_col + s * D, a = tmem + s * 128;
+            if (elect_one()) {  // the first 64 keys' weights are there
               tc_mma_ts(d, a, b, pv_idesc, !b_first);
 #pragma unroll
-              for (int k = 1; k < kTileKeys / 16; ++k) tc_mma_ts(d, a + k * 8, b + k * (2048 >> 4), pv_idesc, true);
+              for (int k = 1; k < 4; ++k) tc_mma_ts(d, a + k * 8, b + k * (2048 >> 4), pv_idesc, true);
+            }
+            __syncwarp();
+            ok = wait(p_full + s, phase);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 4; k < 8; ++k) tc_mma_ts(d, a + k * 8, b + k * (2048 >> 4), pv_idesc, true);
               if (b_left == 1) tc_commit(o_full + s);
             }
             __syncwarp();
@@ -290,11 +293,11 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
               ok = wait(q_full + s, (s ? qn1 : qn0) & 1);
               s ? ++qn1 : ++qn0;
             }
-            const int nit = it + 1, sg = nit % KST;
-            ok = ok && wait(k_full + sg, (nit / KST) & 1);
+            const int item = 2 * it + 2, sg = item % NST;
+            ok = ok && wait(checked + sg, (item / NST) & 1);
             if (!ok) break;
             tc_fence_after();
-            if (lane == 0) {
+            if (elect_one()) {
               const uint64_t a = q_desc + s * (C::tile_bytes >> 4), b = k_desc + sg * (C::tile_bytes >> 4);
 #pragma unroll
               for (int k = 0; k < D / 16; ++k) {
@@ -308,9 +311,9 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
           }
         }
         if (!ok) break;
-        if (lane == 0) {
-          if (b_left > 0) tc_commit(v_empty + it % VST);
-          if (more) tc_commit(k_empty + (it + 1) % KST);
+        if (elect_one()) {
+          if (b_left > 0) tc_commit(empty + (2 * it + 1) % NST);
+          if (more) tc_commit(empty + (2 * it + 2) % NST);
         }
         __syncwarp();
         ++it;
@@ -322,21 +325,25 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
         }
       }
       if (*reinterpret_cast<volatile int*>(abort_flag)) {  // wait, with a limit of its own, for the products in flight
-        if (lane == 0) tc_commit(drain);
+        if (elect_one()) tc_commit(drain);
+        __syncwarp();
         drain_ring(drain, 1, 1);
       }
-    } else {  // ---- values that not every row sees
+    } else {
+      // ---- values that not every row sees.  These warps pass every item of the ring on to the products' warp, key
+      // tiles too: a waiter that skipped items could meet a stage whose previous item is still on its way
+      // and take the barrier's older phase for the one it wants.
       int it = 0;
 #pragma unroll 1
       for (int n = 0; ok && take_unit(units, u, n, lane, wait); ++n) {
         uint32_t bad = 0;
 #pragma unroll 1
-        for (int i = u.i0; i < u.i1; ++i, ++it) {
-          const int sg = it % VST;
-          ok = wait(v_full + sg, (it / VST) & 1);
+        for (int i = 2 * u.i0; i < 2 * u.i1; ++i, ++it) {
+          const int sg = it % NST;
+          ok = wait(full + sg, (it / NST) & 1);
           if (!ok) break;
-          const int j0 = u.tile(i) * kTileKeys;
-          if (!all_see(p, u.p0, u.p1, j0, j0 + kTileKeys - 1)) {
+          const int j0 = u.tile(i >> 1) * kTileKeys;
+          if ((i & 1) && !all_see(p, u.p0, u.p1, j0, j0 + kTileKeys - 1)) {
             // warp 10 takes the even keys, 11 the odd ones; 8 lanes a 128-byte row
 #pragma unroll 1
             for (int r = (warp - 10) + (lane >> 3) * 2; r < kTileKeys; r += 8) {
@@ -344,7 +351,7 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
               const bool some = some_sees(p, u.p0, u.p1, j0 + r);
 #pragma unroll
               for (int sl = 0; sl < D / 64; ++sl) {
-                uint4* v = reinterpret_cast<uint4*>(vring + sg * C::tile_bytes + sl * kTileKeys * 128 + r * 128) + (lane & 7);
+                uint4* v = reinterpret_cast<uint4*>(ring + sg * C::tile_bytes + sl * kTileKeys * 128 + r * 128) + (lane & 7);
                 if (some) {
                   const uint4 x = *v;
                   bad |= nonfinite2<T>(x.x) | nonfinite2<T>(x.y) | nonfinite2<T>(x.z) | nonfinite2<T>(x.w);
@@ -446,6 +453,12 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
             w[k] = T::pack(e, f);
           }
           tmem_st16u(st_addr + c / 2, w);
+          if (c == 32) {  // the products of the first 64 keys can start
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_half + s);
+          }
         }
         tmem_st_wait();
         tc_fence_before();
