@@ -15,6 +15,7 @@ namespace coli {
 namespace {
 
 constexpr int kAppendWarps = 8;
+constexpr int kAhead = 4;  // groups of heads a warp has in flight
 
 template <class T>
 __device__ __forceinline__ void rotate8(uint4& a, uint4& b, const float (&cs)[8], const float (&sn)[8],
@@ -48,6 +49,35 @@ __global__ void __launch_bounds__(kAppendWarps * 32) attn_append_kernel(const At
   const int64_t gw = (int64_t)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
   const int token = (int)(gw / warps_per_token), part = (int)(gw - (int64_t)token * warps_per_token);
   if (token >= a.n_tokens) return;
+  const int e = lane % LPH, sub = lane / LPH;  // 16 values e of head sub of a group of HPW heads
+  const bool rot = e < a.rot / 16;
+  // first value of the lane's two 8-value vectors
+  const int i0 = rot && !a.interleaved ? 8 * e : 16 * e;
+  const int i1 = rot && !a.interleaved ? a.rot / 2 + 8 * e : 16 * e + 8;
+  const int nq = a.q ? a.n_q : 0;
+  const int groups = (nq + 2 * a.n_kv + HPW - 1) / HPW;
+  const auto source = [&](int h) -> const uint16_t* {
+    if (h < nq) return static_cast<const uint16_t*>(a.q) + token * a.q_stride + (int64_t)h * D;
+    if ((h -= nq) < a.n_kv) return static_cast<const uint16_t*>(a.k) + token * a.k_stride + (int64_t)h * D;
+    if ((h -= a.n_kv) < a.n_kv) return static_cast<const uint16_t*>(a.v) + token * a.v_stride + (int64_t)h * D;
+    return nullptr;
+  };
+  // the first values are asked for before the token's place is looked up
+  uint4 x[kAhead], y[kAhead];
+  const auto load = [&](int g) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int gk = g + k * warps_per_token;
+      const uint16_t* src = gk < groups ? source(gk * HPW + sub) : nullptr;
+      x[k] = y[k] = make_uint4(0, 0, 0, 0);
+      if (src) {
+        x[k] = __ldg(reinterpret_cast<const uint4*>(src + i0));
+        y[k] = __ldg(reinterpret_cast<const uint4*>(src + i1));
+      }
+    }
+  };
+  load(part);
+
   int b = 0;  // the first sequence that ends after the token
   for (int b0 = 0; b0 < a.n_seqs; b0 += 32) {
     const bool before = b0 + lane < a.n_seqs && __ldg(a.q_start + b0 + lane + 1) <= token;
@@ -67,25 +97,12 @@ __global__ void __launch_bounds__(kAppendWarps * 32) attn_append_kernel(const At
     store = false;
   }
   int64_t page = 0;
-  if (store) {
-    page = __ldg(a.table + (int64_t)b * a.table_stride + (pos >> a.page_shift));
-    if (page < 0 || page >= a.n_pages) {
-      if (lane == 0) atomicExch(a.status, COLI_EINVAL);
-      store = false;
-    }
-  }
-  const int64_t slot = pos & ((1 << a.page_shift) - 1);
-
-  const int64_t at = pos + (int64_t)(a.pos_base ? __ldg(a.pos_base) : 0);
-  const int e = lane % LPH, sub = lane / LPH;  // 16 values e of head sub of a group of HPW heads
-  const bool rot = e < a.rot / 16;
-  // first value of the lane's two 8-value vectors
-  const int i0 = rot && !a.interleaved ? 8 * e : 16 * e;
-  const int i1 = rot && !a.interleaved ? a.rot / 2 + 8 * e : 16 * e + 8;
+  if (store) page = __ldg(a.table + (int64_t)b * a.table_stride + (pos >> a.page_shift));
   float cs[8], sn[8];
 #pragma unroll
   for (int w = 0; w < 8; ++w) cs[w] = 1.f, sn[w] = 0.f;
   if (rot) {
+    const int64_t at = pos + (int64_t)(a.pos_base ? __ldg(a.pos_base) : 0);
 #pragma unroll
     for (int w = 0; w < 8; ++w) {
       const uint64_t turn = __ldg(a.turn + 8 * e + w) * (uint64_t)at;
@@ -93,31 +110,38 @@ __global__ void __launch_bounds__(kAppendWarps * 32) attn_append_kernel(const At
       sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &sn[w], &cs[w]);
     }
   }
-  const int nq = a.q ? a.n_q : 0;
-  const int groups = (nq + 2 * a.n_kv + HPW - 1) / HPW;
-#pragma unroll 4
-  for (int g = part; g < groups; g += warps_per_token) {
-    int h = g * HPW + sub;
-    const uint16_t* src = nullptr;
-    uint16_t* dst = nullptr;
-    bool turn = rot;
-    if (h < nq) {
-      src = static_cast<const uint16_t*>(a.q) + token * a.q_stride + (int64_t)h * D;
-      dst = static_cast<uint16_t*>(a.q_out) + token * a.q_out_stride + (int64_t)h * D;
-    } else if ((h -= nq) < a.n_kv) {
-      src = static_cast<const uint16_t*>(a.k) + token * a.k_stride + (int64_t)h * D;
-      if (store) dst = static_cast<uint16_t*>(a.kc) + page * a.kp + h * a.kh + slot * a.ks;
-    } else if ((h -= a.n_kv) < a.n_kv) {
-      src = static_cast<const uint16_t*>(a.v) + token * a.v_stride + (int64_t)h * D;
-      if (store) dst = static_cast<uint16_t*>(a.vc) + page * a.vp + h * a.vh + slot * a.vs;
-      turn = false;
+  if (store && (page < 0 || page >= a.n_pages)) {
+    if (lane == 0) atomicExch(a.status, COLI_EINVAL);
+    store = false;
+  }
+  const int64_t slot = pos & ((1 << a.page_shift) - 1);
+
+#pragma unroll 1
+  for (int g = part;;) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int gk = g + k * warps_per_token;
+      if (gk >= groups) break;
+      int h = gk * HPW + sub;
+      uint16_t* dst = nullptr;
+      bool turn = rot;
+      if (h < nq) {
+        dst = static_cast<uint16_t*>(a.q_out) + token * a.q_out_stride + (int64_t)h * D;
+      } else if ((h -= nq) < a.n_kv) {
+        if (store) dst = static_cast<uint16_t*>(a.kc) + page * a.kp + h * a.kh + slot * a.ks;
+      } else if ((h -= a.n_kv) < a.n_kv) {
+        if (store) dst = static_cast<uint16_t*>(a.vc) + page * a.vp + h * a.vh + slot * a.vs;
+        turn = false;
+      }
+      if (dst) {
+        if (turn) rotate8<T>(x[k], y[k], cs, sn, a.interleaved);
+        *reinterpret_cast<uint4*>(dst + i0) = x[k];
+        *reinterpret_cast<uint4*>(dst + i1) = y[k];
+      }
     }
-    if (dst) {
-      uint4 x = *reinterpret_cast<const uint4*>(src + i0), y = *reinterpret_cast<const uint4*>(src + i1);
-      if (turn) rotate8<T>(x, y, cs, sn, a.interleaved);
-      *reinterpret_cast<uint4*>(dst + i0) = x;
-      *reinterpret_cast<uint4*>(dst + i1) = y;
-    }
+    g += kAhead * warps_per_token;
+    if (g >= groups) break;
+    load(g);
   }
 }
 
