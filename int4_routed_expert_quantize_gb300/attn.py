@@ -39,6 +39,10 @@ class AttnBatch(ctypes.Structure):
                 ("max_pages", _i), ("n_tokens", _i), ("max_q", _i)]
 
 
+# torch.cuda.current_stream() makes a Stream object on every call (3 us on a Grace core, this 0.1 us)
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
+    lambda device: torch.cuda.current_stream(device).cuda_stream
+
 _lib = None
 
 
@@ -144,6 +148,9 @@ class PagedAttention:
         self.n_q, self.n_kv, self.head_dim, self.page, self.dtype = n_q, n_kv, head_dim, page, dtype
         self.max_tokens, self.max_seqs, self.rot_dim = max_tokens, max_seqs, rot
         self.scale = 1.0 / math.sqrt(head_dim)
+        self.device = torch.cuda.current_device()
+        L = lib()
+        self._c_append, self._c_window, self._c_prefix = L.coli_attn_append, L.coli_attn_window, L.coli_attn_prefix
 
     def close(self):
         if getattr(self, "h", None) is not None and self.h.value:
@@ -155,72 +162,85 @@ class PagedAttention:
     def bind_cache(self, k_cache, v_cache):
         return KvCache(self, k_cache, v_cache)
 
+    # The calls below take a few microseconds of host time, most of it the launches: what can be looked up
+    # once is, and a new output's layout is not checked again.
+
     def _heads(self, t, heads, batch, what):
         """the token stride of t [n_tokens, heads, head_dim]"""
-        D = self.head_dim
-        if (t.dtype is not self.dtype or t.shape != (batch.n_tokens, heads, D) or not t.is_cuda
-                or t.stride(2) != 1 or (heads > 1 and t.stride(1) != D)):
-            raise ValueError(f"{what}: [{batch.n_tokens}, {heads}, {D}] of {self.dtype} on the device, heads contiguous")
-        return t.stride(0) if batch.n_tokens > 1 else heads * D
+        D, n = self.head_dim, batch.n_tokens
+        if t.dtype is not self.dtype or t.shape != (n, heads, D) or not t.is_cuda:
+            raise ValueError(f"{what}: [{n}, {heads}, {D}] of {self.dtype} on the device")
+        st, sh, sd = t.stride()
+        if sd != 1 or (sh != D and heads > 1):
+            raise ValueError(f"{what}: a token's heads are contiguous")
+        return st if n > 1 else heads * D
+
+    def _stream(self, stream):
+        if stream is None:
+            return _raw_stream(self.device)
+        return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else stream
 
     def _out(self, out, batch, stream, like):
-        if out is None:
-            out = torch.empty((batch.n_tokens, self.n_q, self.head_dim), dtype=self.dtype, device=like.device)
-            if stream is not None and isinstance(stream, torch.cuda.Stream):
-                out.record_stream(stream)
-        return out
+        """the output and its token stride"""
+        if out is not None:
+            return out, self._heads(out, self.n_q, batch, "out")
+        out = torch.empty((batch.n_tokens, self.n_q, self.head_dim), dtype=self.dtype, device=like.device)
+        if stream is not None and isinstance(stream, torch.cuda.Stream):
+            out.record_stream(stream)
+        return out, self.n_q * self.head_dim
+
+    def _lse(self, lse, batch):
+        if lse.dtype is not torch.float32 or lse.shape != (batch.n_tokens, self.n_q) or not lse.is_contiguous():
+            raise ValueError(f"lse: contiguous float32 [{batch.n_tokens}, {self.n_q}]")
+        return lse.data_ptr()
 
     def append(self, cache, batch, k, v, q=None, q_out=None, pos_base=None, stream=None):
         """Stores the batch's new keys (rotated) and values in the cache; rotates q into q_out (new by
         default, q itself for in place) and returns it.  pos_base: int32 [1] on the device, added to the
         positions for the rotation (the length of a shared prefix).  coli_attn_append"""
         ks, vs = self._heads(k, self.n_kv, batch, "k"), self._heads(v, self.n_kv, batch, "v")
-        qp = op = None
+        qp = op = base = None
         qs = os = 0
         if q is not None:
             qs = self._heads(q, self.n_q, batch, "q")
-            q_out = self._out(q_out, batch, stream, q)
-            os = self._heads(q_out, self.n_q, batch, "q_out")
+            q_out, os = self._out(q_out, batch, stream, q)
             qp, op = q.data_ptr(), q_out.data_ptr()
-        base = None if pos_base is None else _int32(pos_base, 1, "pos_base").data_ptr()
-        coli._check(lib().coli_attn_append(self.h, cache.h, batch.ref, qp, qs, k.data_ptr(), ks, v.data_ptr(), vs,
-                                           op, os, base, coli._stream(stream)), "coli_attn_append")
+        if pos_base is not None:
+            base = _int32(pos_base, 1, "pos_base").data_ptr()
+        rc = self._c_append(self.h, cache.h, batch.ref, qp, qs, k.data_ptr(), ks, v.data_ptr(), vs, op, os, base,
+                            self._stream(stream))
+        if rc:
+            raise coli.ColiError(rc, "coli_attn_append")
         return q_out
 
     def window(self, cache, batch, q, window=-1, sinks=0, scale=None, out=None, lse=None, stream=None):
         """Causal attention over the last `window` keys (all with -1) and the first `sinks` ones ->
         [n_tokens, n_q, head_dim]; lse: float32 [n_tokens, n_q] to fill, or None.  coli_attn_window"""
         qs = self._heads(q, self.n_q, batch, "q")
-        out = self._out(out, batch, stream, q)
-        coli._check(lib().coli_attn_window(self.h, cache.h, batch.ref, q.data_ptr(), qs, window, sinks,
-                                           self.scale if scale is None else scale, out.data_ptr(),
-                                           self._heads(out, self.n_q, batch, "out"), self._lse(lse, batch),
-                                           coli._stream(stream)), "coli_attn_window")
+        out, os = self._out(out, batch, stream, q)
+        rc = self._c_window(self.h, cache.h, batch.ref, q.data_ptr(), qs, window, sinks,
+                            self.scale if scale is None else scale, out.data_ptr(), os,
+                            None if lse is None else self._lse(lse, batch), self._stream(stream))
+        if rc:
+            raise coli.ColiError(rc, "coli_attn_window")
         return out
 
     def prefix(self, cache, batch, prefix_table, prefix_len, q, scale=None, out=None, lse=None, stream=None):
         """Attention of a batch behind a shared prefix: prefix_len (int32 [1] on the device) tokens in the
         pages prefix_table (int32 [pages]), then each sequence's own cache.  coli_attn_prefix"""
         qs = self._heads(q, self.n_q, batch, "q")
-        out = self._out(out, batch, stream, q)
+        out, os = self._out(out, batch, stream, q)
         _int32(prefix_table, 1, "prefix_table"), _int32(prefix_len, 1, "prefix_len")
-        coli._check(lib().coli_attn_prefix(self.h, cache.h, batch.ref, prefix_table.data_ptr(),
-                                           prefix_table.shape[0], prefix_len.data_ptr(), q.data_ptr(), qs,
-                                           self.scale if scale is None else scale, out.data_ptr(),
-                                           self._heads(out, self.n_q, batch, "out"), self._lse(lse, batch),
-                                           coli._stream(stream)), "coli_attn_prefix")
+        rc = self._c_prefix(self.h, cache.h, batch.ref, prefix_table.data_ptr(), prefix_table.shape[0],
+                            prefix_len.data_ptr(), q.data_ptr(), qs, self.scale if scale is None else scale,
+                            out.data_ptr(), os, None if lse is None else self._lse(lse, batch), self._stream(stream))
+        if rc:
+            raise coli.ColiError(rc, "coli_attn_prefix")
         return out
-
-    def _lse(self, lse, batch):
-        if lse is None:
-            return None
-        if lse.dtype is not torch.float32 or lse.shape != (batch.n_tokens, self.n_q) or not lse.is_contiguous():
-            raise ValueError(f"lse: contiguous float32 [{batch.n_tokens}, {self.n_q}]")
-        return lse.data_ptr()
 
     def status(self, stream=None):
         """device status of earlier calls (coli_attn_status); 0 when all went well"""
-        return int(lib().coli_attn_status(self.h, coli._stream(stream)))
+        return int(lib().coli_attn_status(self.h, self._stream(stream)))
 
     def launches(self, op, max_q):
         """kernels one call launches; op "append", "window" or "prefix" (coli_attn_launches)"""
