@@ -21,11 +21,31 @@ struct Join {
 #pragma unroll
     for (int i = 0; i < V; ++i) o[i] = 0.f;
   }
+  template <class At>
+  static __device__ __forceinline__ void load4(float (&v)[4][V], const float* ob, int c, int n, int lane, At at) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[j][i] = 0.f;
+      if (j < n) {
+        const float* src = ob + at(c + j) * D + lane * V;
+        if constexpr (V == 4) {
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
+          v[j][0] = x.x, v[j][1] = x.y, v[j][2] = x.z, v[j][3] = x.w;
+        } else {
+          const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
+          v[j][0] = x.x, v[j][1] = x.y;
+        }
+      }
+    }
+  }
   // parts i = 0..n-1 of the row at o_base + at(i) * D, ml_base[at(i)]
   template <class At>
   __device__ __forceinline__ void add(const float* ob, const float2* mlb, int n, int lane, At at) {
     for (int c = 0; c < n; c += 32) {
       const int k = min(32, n - c);
+      float first[4][V];  // asked for before the weights are known
+      load4(first, ob, c, k, lane, at);
       float2 ml = make_float2(-INFINITY, 0.f);
       if (lane < k) ml = __ldcg(mlb + at(c + lane));
       float top = fmaxf(m, warp_max(ml.x));
@@ -39,21 +59,16 @@ struct Join {
       m = top;
 #pragma unroll
       for (int i = 0; i < V; ++i) o[i] *= keep;
-#pragma unroll 4
-      for (int j = 0; j < k; ++j) {
-        const float wj = __shfl_sync(FULL, w, j);
-        const float* src = ob + at(c + j) * D + lane * V;
-        float v[V];
-        if constexpr (V == 4) {
-          const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
-          v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-        } else {
-          const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
-          v[0] = x.x, v[1] = x.y;
-        }
-        if (wj != 0.f)  // a part without keys holds zeros
+#pragma unroll 1
+      for (int j0 = 0; j0 < k; j0 += 4) {
+        if (j0 > 0) load4(first, ob, c + j0, k - j0, lane, at);
 #pragma unroll
-          for (int i = 0; i < V; ++i) o[i] = fmaf(wj, v[i], o[i]);
+        for (int j = 0; j < 4; ++j) {
+          const float wj = __shfl_sync(FULL, w, j0 + j);  // 0 past the end, and for a part without keys
+          if (wj != 0.f)
+#pragma unroll
+            for (int i = 0; i < V; ++i) o[i] = fmaf(wj, first[j][i], o[i]);
+        }
       }
     }
   }
@@ -198,20 +213,18 @@ __global__ void __launch_bounds__(kWarps * 32)
 
 // where one row's results of one source are
 struct Parts {
-  int n;        // parts; 1 with dense: the row sits in the dense buffer
+  int n;       // parts; dense: the row sits in the dense buffer
   bool dense;
   int first_cta, rows, row;
 };
 
+// Token i of sequence b on a list of stretches of `per` positions, the sequence's first one being `at`.
 template <int KT>
-__device__ __forceinline__ Parts find_parts(const AttnParams& p, int rows, int b, int i, int head, int g) {
-  // token i of sequence b
-  const SeqInfo s = seq_info(p, b);
-  const uint32_t per = __ldcg(p.seq_pos + p.n_seqs + 1);
+__device__ __forceinline__ Parts find_parts(const AttnParams& p, int rows, const SeqInfo& s, int i, int head, int g,
+                                            uint32_t at, uint32_t per) {
   const int blk = i / p.block_tokens;
-  uint32_t at = __ldcg(p.seq_pos + b);
   Tiles<KT> t;
-  if (p.causal) {
+  if (s.causal) {
 #pragma unroll 1
     for (int k = 0; k < blk; ++k) {
       t.set(p, s, k);
@@ -234,48 +247,71 @@ __device__ __forceinline__ Parts find_parts(const AttnParams& p, int rows, int b
 }
 
 template <int D>
-__device__ __forceinline__ void add_parts(Join<D>& j, const AttnParams& p, const Parts& r, int64_t dense_row,
+__device__ __forceinline__ void add_parts(Join<D>& j, const AttnParams& p, const Parts& r, int which, int64_t dense_row,
                                           int lane) {
-  if (r.dense)
-    j.add(p.dense_o, p.dense_ml, 1, lane, [&](int) { return dense_row; });
-  else
-    j.add(p.part_o, p.part_ml, r.n, lane, [&](int c) {
-      return ((int64_t)(r.first_cta + c) * 2 + (c == 0 ? 1 : 0)) * r.rows + r.row;
-    });
+  // one call for both kinds: a dense row is a part at its own place
+  const float* ob = r.dense ? p.dense_o[which] : p.part_o;
+  const float2* ml = r.dense ? p.dense_ml[which] : p.part_ml;
+  j.add(ob, ml, r.n, lane, [&](int c) {
+    return r.dense ? dense_row : ((int64_t)(r.first_cta + c) * 2 + (c == 0 ? 1 : 0)) * r.rows + r.row;
+  });
 }
 
-template <class T, int D, int OWN, int SHARED>
-__device__ __forceinline__ void join_row(const AttnParams& own, int own_rows, const AttnParams& shared, int shared_rows,
-                                         int64_t row, int lane, bool redo) {
-  const int token = (int)(row / own.n_q), hq = (int)(row - (int64_t)token * own.n_q);
+// Every row is the join of its own sequence's parts and the prefix's.  SAME: one launch made both, so everything waits
+// for it.  Otherwise the launch before last made the own parts, and the last one had waited for it before it
+// let this one start: all but the prefix's parts is read while that one runs.
+template <class T, int D, bool SAME>
+__global__ void __launch_bounds__(kWarps * 32)
+    attn_join_kernel(const AttnParams own, int own_rows, const AttnParams shared, int shared_ctas) {
+  if (SAME) {
+    griddep_wait();
+    griddep_launch_dependents();
+  }
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const bool live = row < (int64_t)own.n_tokens * own.n_q;
+  const int token = live ? (int)(row / own.n_q) : 0, hq = live ? (int)(row - (int64_t)token * own.n_q) : 0;
   const int head = hq / own.group, g = hq - head * own.group;
+  const bool redo = __ldcg(own.redo_any) != 0;
   Join<D> j;
-  add_parts(j, shared, find_parts<SHARED>(shared, shared_rows, 0, token, head, g), row, lane);
-  const int b = seq_of(own, token, lane);
-  if (b < own.n_seqs) {
-    const SeqInfo s = seq_info(own, b);
-    const int i = token - s.start;
-    if (i >= 0 && i < s.n) {
-      if (redo && __ldcg(own.redo + (int64_t)token * own.n_kv + head)) {
-        __shared__ float qf[kWarps][D];
-        add_direct<T, D>(j, own, s, b, i, hq, qf[threadIdx.x >> 5], lane);
-      } else {
-        add_parts(j, own, find_parts<OWN>(own, own_rows, b, i, head, g), row, lane);
+  Parts far;
+  if (live) {
+    const int b = seq_of(own, token, lane), lists = n_lists(own);
+    const uint32_t per = __ldcg(own.seq_pos + lists + 1);
+    const uint32_t pre_at = SAME ? __ldcg(own.seq_pos + own.n_seqs) : 0;
+    const SeqInfo pre = seq_info(shared, shared.n_seqs);
+    if (SAME) {
+      far = find_parts<kSplitKeys>(shared, own_rows, pre, token, head, g, pre_at, per);
+    } else {  // the prefix alone on its list: the stretch follows from its length
+      Tiles<kTileKeys> t;
+      t.set(shared, pre, 0);
+      const uint32_t blocks = (pre.n + shared.block_tokens - 1) / shared.block_tokens;
+      const uint32_t total = blocks * shared.n_kv * (t.count + shared.unit_cost);
+      far = find_parts<kTileKeys>(shared, kTileRows, pre, token, head, g, 0,
+                                  max(1u, (total + shared_ctas - 1) / shared_ctas));
+    }
+    if (b < own.n_seqs) {
+      const uint32_t at = __ldcg(own.seq_pos + b);
+      const SeqInfo s = seq_info(own, b);
+      const int i = token - s.start;
+      if (i >= 0 && i < s.n) {
+        if (redo && __ldcg(own.redo + (int64_t)token * own.n_kv + head)) {
+          __shared__ float qf[kWarps][D];
+          add_direct<T, D>(j, own, s, b, i, hq, qf[threadIdx.x >> 5], lane);
+        } else {
+          add_parts(j, own, find_parts<kSplitKeys>(own, own_rows, s, i, head, g, at, per), 0, row, lane);
+        }
       }
     }
   }
-  j.template write<T>(own, token, hq, lane);
-}
-
-template <class T, int D, int OWN, int SHARED>
-__global__ void __launch_bounds__(kWarps * 32)
-    attn_join_kernel(const AttnParams own, int own_rows, const AttnParams shared, int shared_rows) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const bool redo = __ldcg(own.redo_any) != 0;
-  if (row < (int64_t)own.n_tokens * own.n_q) join_row<T, D, OWN, SHARED>(own, own_rows, shared, shared_rows, row, lane, redo);
+  if (!SAME) {
+    griddep_wait();
+    griddep_launch_dependents();
+  }
+  if (live) {
+    add_parts(j, shared, far, 1, row, lane);
+    j.template write<T>(own, token, hq, lane);
+  }
   if (redo) clear_flags(own);
 }
 
@@ -294,14 +330,11 @@ cudaError_t go(K kernel, dim3 grid, cudaStream_t stream, A... args) {
 }
 
 template <class T, int D>
-cudaError_t join(const AttnParams& own, int own_rows, const AttnParams& shared, int shared_rows, int ot,
-                 int st, cudaStream_t stream) {
+cudaError_t join(const AttnParams& own, int own_rows, const AttnParams& shared, bool same, int shared_ctas,
+                 cudaStream_t stream) {
   const dim3 grid((unsigned)(((int64_t)own.n_tokens * own.n_q + kWarps - 1) / kWarps));
-  if (ot == kSplitKeys && st == kSplitKeys)
-    return go(attn_join_kernel<T, D, kSplitKeys, kSplitKeys>, grid, stream, own, own_rows, shared, shared_rows);
-  if (ot == kSplitKeys && st == kTileKeys)
-    return go(attn_join_kernel<T, D, kSplitKeys, kTileKeys>, grid, stream, own, own_rows, shared, shared_rows);
-  return cudaErrorInvalidValue;
+  return same ? go(attn_join_kernel<T, D, true>, grid, stream, own, own_rows, shared, shared_ctas)
+              : go(attn_join_kernel<T, D, false>, grid, stream, own, own_rows, shared, shared_ctas);
 }
 
 }  // namespace
@@ -316,14 +349,13 @@ cudaError_t launch_attn_combine(const AttnParams& p, int rows, int ctas, int dty
                           : go(attn_combine_kernel<Fp16, 128>, grid, stream, p, rows, rpb);
 }
 
-cudaError_t launch_attn_join(const AttnParams& own, int own_rows, const AttnParams& shared,
-                             int shared_rows, int own_tile, int shared_tile, int dtype,
-                             cudaStream_t stream) {
+cudaError_t launch_attn_join(const AttnParams& own, int own_rows, const AttnParams& shared, bool same_list,
+                             int shared_ctas, int dtype, cudaStream_t stream) {
   if (dtype == COLI_ATTN_BF16)
-    return own.head_dim == 64 ? join<Bf16, 64>(own, own_rows, shared, shared_rows, own_tile, shared_tile, stream)
-                              : join<Bf16, 128>(own, own_rows, shared, shared_rows, own_tile, shared_tile, stream);
-  return own.head_dim == 64 ? join<Fp16, 64>(own, own_rows, shared, shared_rows, own_tile, shared_tile, stream)
-                            : join<Fp16, 128>(own, own_rows, shared, shared_rows, own_tile, shared_tile, stream);
+    return own.head_dim == 64 ? join<Bf16, 64>(own, own_rows, shared, same_list, shared_ctas, stream)
+                              : join<Bf16, 128>(own, own_rows, shared, same_list, shared_ctas, stream);
+  return own.head_dim == 64 ? join<Fp16, 64>(own, own_rows, shared, same_list, shared_ctas, stream)
+                            : join<Fp16, 128>(own, own_rows, shared, same_list, shared_ctas, stream);
 }
 
 }  // namespace coli

@@ -129,20 +129,25 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
+// the page table of a list entry
+__device__ __forceinline__ const int32_t* table_of(const AttnParams& p, int b) {
+  return b < p.n_seqs ? p.table + (int64_t)b * p.table_stride : p.pre_table;
+}
+
 // One warp fills the stage of a KT-key tile of K and of V: the boxes that hold keys some row of the block
 // sees.  Lane i takes box i: K's, and (N = 2) V's at v_offset; N = 1 takes one map.  Pages whose id is out of
 // range read as zeros (page coordinate past the end) and are reported.
 template <int KT, int D, int N>
 __device__ __forceinline__ void fill_boxes(const AttnParams& p, const CUtensorMap* kmap, const CUtensorMap* vmap,
                                            uint8_t* dst, uint64_t* kbar, uint64_t* vbar, int v_offset,
-                                           int64_t table_row, int p0, int p1, int j0, int head, int lane) {
+                                           const int32_t* table, int p0, int p1, int j0, int head, int lane) {
   const int page = 1 << p.page_shift;
   const int rows = min(page, KT);  // slots per box
   const int boxes = KT / rows;     // per 64 values
   const int a = j0 + lane * rows, e = a + rows - 1;  // the lane's keys
   const bool need = lane < boxes && a <= p1 && (e > p0 - p.window || a < p.sinks);
   int id = 0;
-  if (need) id = __ldg(p.table + table_row + (a >> p.page_shift));
+  if (need) id = __ldg(table + (a >> p.page_shift));
   const uint32_t bytes = (uint32_t)__popc(__ballot_sync(FULL, need)) * (uint32_t)rows * D * 2;
   if (lane == 0) {
     if (N == 2 && kbar == vbar) {

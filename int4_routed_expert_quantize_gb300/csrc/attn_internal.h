@@ -38,15 +38,19 @@ struct AttnParams {
   void* out;
   int64_t out_stride;
   float* lse;
-  const int32_t* q_start;  // nullptr: one sequence of all n_tokens tokens (the shared prefix)
+  const int32_t* q_start;
   const int32_t* kv_len;
   const int32_t* table;
   int64_t table_stride;
-  int n_seqs, n_tokens, max_pages;
+  int n_seqs, n_tokens, max_pages;  // n_seqs 0: the shared prefix alone
+  // the shared prefix, or nullptr: one more sequence (number n_seqs) with all n_tokens queries, each of which
+  // sees all its keys
+  const int32_t* pre_len;
+  const int32_t* pre_table;
+  int pre_pages;
   int n_q, n_kv, group, head_dim;
   int page_shift, n_pages;
   int window, sinks;  // window >= kAttnNoWindow: none (and sinks 0)
-  int causal;         // 0: every query sees all kv_len keys
   float scale_log2;   // scale * log2(e)
   int block_tokens;   // query tokens per block
   int unit_cost;      // list positions of a unit besides its tiles
@@ -56,8 +60,10 @@ struct AttnParams {
   float2* part_ml;   // [2 * CTAs][rows per block] their maximum (log2 units) and sum
   AttnRec* rec;      // [CTAs]
   uint32_t* seq_pos;  // [n_seqs + 2] first list position of each sequence, the total, the stretch; or nullptr
-  float* dense_o;    // prefix only: rows of uncut units go here, unnormalised, by (token, head)
-  float2* dense_ml;
+  // prefix calls only: rows of uncut units go here, unnormalised, by (token, head); [0] those of the sequences'
+  // own keys, [1] those of the prefix
+  float* dense_o[2];
+  float2* dense_ml[2];
   uint8_t* redo;   // [max_tokens][n_kv] rows the joining kernel computes again (flag_unit), zero otherwise
   int* redo_any;   // [0] some are; [1] blocks of that kernel that are done
   int64_t k_page, k_head, k_slot, v_page, v_head, v_slot;  // cache strides, for those units
@@ -96,10 +102,10 @@ cudaError_t launch_attn_tile(const AttnParams& p, const CUtensorMap& q, const CU
 // merges the partials of cut units into out / lse
 cudaError_t launch_attn_combine(const AttnParams& p, int rows, int ctas, int dtype,
                                 cudaStream_t stream);
-// merges, for every row, the prefix's and the sequence's own results into out / lse
-cudaError_t launch_attn_join(const AttnParams& own, int own_rows, const AttnParams& shared,
-                             int shared_rows, int own_tile, int shared_tile, int dtype,
-                             cudaStream_t stream);
+// merges, for every row, the sequence's own and the prefix's results into out / lse; own and shared are the same
+// list when one launch made both, else the prefix's came from the tensor-memory kernel
+cudaError_t launch_attn_join(const AttnParams& own, int own_rows, const AttnParams& shared, bool same_list,
+                             int shared_ctas, int dtype, cudaStream_t stream);
 cudaError_t launch_attn_append(const AttnAppend& a, int dtype, int num_sms, cudaStream_t stream);
 
 }  // namespace coli

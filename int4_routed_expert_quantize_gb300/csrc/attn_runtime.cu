@@ -140,7 +140,7 @@ AttnParams params(const coli_attn* h, const coli_attn_kv* kv, const coli_attn_ba
   p.n_seqs = b->n_seqs, p.n_tokens = b->n_tokens, p.max_pages = b->max_pages;
   p.n_q = h->cfg.n_q, p.n_kv = h->cfg.n_kv, p.group = h->cfg.n_q / h->cfg.n_kv, p.head_dim = h->cfg.head_dim;
   p.page_shift = h->page_shift, p.n_pages = (int)kv->c.n_pages;
-  p.window = kAttnNoWindow, p.sinks = 0, p.causal = 1;
+  p.window = kAttnNoWindow, p.sinks = 0;
   p.scale_log2 = scale * 1.44269504088896340736f;
   p.rows_lo = 0, p.rows_hi = INT64_MAX;
   p.part_o = h->part_o, p.part_ml = h->part_ml, p.rec = h->rec, p.seq_pos = h->seq_pos;
@@ -244,11 +244,11 @@ extern "C" int coli_attn_create(const coli_attn_config* cfg, coli_attn** out) {
     if (!rc) rc = dalloc(h, &h->part_o, rows * D);
     if (!rc) rc = dalloc(h, &h->part_ml, rows);
     if (!rc) rc = dalloc(h, &h->rec, ctas);
-    if (!rc) rc = dalloc(h, &h->seq_pos, c.max_seqs + 2);
+    if (!rc) rc = dalloc(h, &h->seq_pos, c.max_seqs + 3);
     if (!rc) rc = dalloc(h, &h->part_o2, rows2 * D);
     if (!rc) rc = dalloc(h, &h->part_ml2, rows2);
     if (!rc) rc = dalloc(h, &h->rec2, ctas);
-    if (!rc) rc = dalloc(h, &h->seq_pos2, c.max_seqs + 2);
+    if (!rc) rc = dalloc(h, &h->seq_pos2, c.max_seqs + 3);
     if (!rc) rc = dalloc(h, &h->dense_o, dense * D);
     if (!rc) rc = dalloc(h, &h->dense_ml, dense);
     if (!rc) rc = dalloc(h, &h->dense_o2, dense * D);
@@ -386,21 +386,29 @@ extern "C" int coli_attn_prefix(coli_attn* h, const coli_attn_kv* kv, const coli
   if (rc) return rc;
   cudaStream_t st = (cudaStream_t)stream;
   AttnParams own = params(h, kv, b, q, q_stride, out, out_stride, lse, scale);
-  own.dense_o = h->dense_o, own.dense_ml = h->dense_ml;
+  own.dense_o[0] = h->dense_o, own.dense_ml[0] = h->dense_ml;
+  own.dense_o[1] = h->dense_o2, own.dense_ml[1] = h->dense_ml2;
+  // Few rows in all: one launch of the split kernel takes the prefix as one more sequence.  More: the prefix is a matrix
+  // product for the tensor-memory kernel, in a launch of its own.
+  const bool same = (int64_t)b->n_tokens * own.group <= kSplitMaxRows;
   AttnParams pre = own;
-  use_tile(h, &pre);
-  pre.q_start = nullptr, pre.kv_len = prefix_len, pre.table = prefix_table, pre.table_stride = prefix_pages;
-  pre.n_seqs = 1, pre.max_pages = prefix_pages, pre.causal = 0;
-  pre.dense_o = h->dense_o2, pre.dense_ml = h->dense_ml2;
-  const int own_rows = rows_of(h, b->max_q);
-  own.block_tokens = own_rows / own.group;
-  CUtensorMap qm;
-  if (!query_map(&qm, h, q, q_stride, b->n_tokens)) return COLI_ECUDA;
-  cudaError_t e = launch_attn_split(own, kv->maps.k64, kv->maps.v64, own_rows, h->cfg.dtype, h->num_sms, st);
-  if (e == cudaSuccess)
-    e = launch_attn_tile(pre, qm, kv->maps.k128, kv->maps.v128, h->cfg.dtype, h->num_sms, st);
-  if (e == cudaSuccess)
-    e = launch_attn_join(own, own_rows, pre, kTileRows, kSplitKeys, kTileKeys, h->cfg.dtype, st);
+  pre.pre_len = prefix_len, pre.pre_table = prefix_table, pre.pre_pages = prefix_pages;
+  const int rows = rows_of(h, same ? b->n_tokens : b->max_q);
+  own.block_tokens = pre.block_tokens = rows / own.group;
+  cudaError_t e;
+  if (same) {
+    own = pre;
+    e = launch_attn_split(own, kv->maps.k64, kv->maps.v64, rows, h->cfg.dtype, h->num_sms, st);
+  } else {
+    use_tile(h, &pre);
+    pre.n_seqs = 0;
+    CUtensorMap qm;
+    if (!query_map(&qm, h, q, q_stride, b->n_tokens)) return COLI_ECUDA;
+    e = launch_attn_split(own, kv->maps.k64, kv->maps.v64, rows, h->cfg.dtype, h->num_sms, st);
+    if (e == cudaSuccess)
+      e = launch_attn_tile(pre, qm, kv->maps.k128, kv->maps.v128, h->cfg.dtype, h->num_sms, st);
+  }
+  if (e == cudaSuccess) e = launch_attn_join(own, rows, pre, same, h->num_sms, h->cfg.dtype, st);
   return e == cudaSuccess ? COLI_OK : COLI_ECUDA;
 }
 

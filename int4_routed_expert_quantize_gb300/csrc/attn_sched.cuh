@@ -10,11 +10,14 @@ namespace coli {
 
 struct SeqInfo {
   int start, n, len;  // first query token, query tokens, cached tokens
+  bool causal;        // false: the prefix, of which every query sees every key
 };
 
 __device__ __forceinline__ SeqInfo seq_info(const AttnParams& p, int b) {
   SeqInfo s;
-  if (p.q_start) {
+  const bool own = b < p.n_seqs;
+  s.causal = own;
+  if (own) {
     const int a = __ldg(p.q_start + b), e = __ldg(p.q_start + b + 1);
     s.start = min(max(a, 0), p.n_tokens);
     s.n = min(max(e, s.start), p.n_tokens) - s.start;
@@ -24,18 +27,21 @@ __device__ __forceinline__ SeqInfo seq_info(const AttnParams& p, int b) {
     s.start = 0;
     s.n = p.n_tokens;
   }
-  const int64_t cap = (int64_t)p.max_pages << p.page_shift;
-  const int l = __ldg(p.kv_len + b);
+  const int64_t cap = (int64_t)(own ? p.max_pages : p.pre_pages) << p.page_shift;
+  const int l = __ldg(own ? p.kv_len + b : p.pre_len);
   s.len = max(l, 0);
   if (s.len > cap) s.len = (int)cap;
   return s;
 }
 
+__device__ __forceinline__ int n_lists(const AttnParams& p) { return p.n_seqs + (p.pre_len ? 1 : 0); }
+
 // what seq_info clamps is reported once per call
 __device__ __forceinline__ void seq_check(const AttnParams& p, int b) {
-  const int l = __ldg(p.kv_len + b);
-  bool bad = l < 0 || (int64_t)l > ((int64_t)p.max_pages << p.page_shift);
-  if (p.q_start) {
+  const bool own = b < p.n_seqs;
+  const int l = __ldg(own ? p.kv_len + b : p.pre_len);
+  bool bad = l < 0 || (int64_t)l > ((int64_t)(own ? p.max_pages : p.pre_pages) << p.page_shift);
+  if (own) {
     const int a = __ldg(p.q_start + b), e = __ldg(p.q_start + b + 1);
     bad = bad || a < 0 || e < a || e > p.n_tokens || (b == 0 && a != 0);
   }
@@ -52,8 +58,8 @@ struct Tiles {
   __device__ __forceinline__ void set(const AttnParams& p, const SeqInfo& s, int blk) {
     const int t0 = blk * p.block_tokens;
     const int nt = min(p.block_tokens, s.n - t0);
-    p0 = p.causal ? s.len - s.n + t0 : s.len - 1;
-    p1 = p.causal ? p0 + nt - 1 : s.len - 1;
+    p0 = s.causal ? s.len - s.n + t0 : s.len - 1;
+    p1 = s.causal ? p0 + nt - 1 : s.len - 1;
     const int hi = p1 < 0 ? -1 : p1 / KT;
     const int lo = p.window >= kAttnNoWindow ? 0 : max(0, p0 - p.window + 1) / KT;
     sink = p.sinks > 0 ? min((p.sinks - 1) / KT, hi) + 1 : 0;
@@ -89,9 +95,10 @@ struct alignas(16) Unit {
   int sink, base;
   int i0, i1;        // i1 = 0: the end
   int head, b, blk;
-  int whole;         // 1: all of its tiles; otherwise a part goes to slot (i0 > 0 ? 0 : 1) of the workspace
+  int flags;         // kWhole: all of its tiles (otherwise a part goes to slot (i0 > 0 ? 0 : 1) of the workspace)
   __device__ __forceinline__ int tile(int i) const { return i < sink ? i : base + i - sink; }
 };
+constexpr int kWhole = 1, kCausal = 2;  // Unit::flags
 static_assert(sizeof(Unit) == 48, "three 16-byte words");
 
 constexpr int kUnitSlots = 4;
@@ -112,7 +119,7 @@ __device__ __forceinline__ void weigh(const AttnParams& p, uint32_t* pos) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarps = blockDim.x >> 5;
   bool any_long = false;
 #pragma unroll 1
-  for (int b = tid; b < p.n_seqs; b += blockDim.x) {
+  for (int b = tid; b < n_lists(p); b += blockDim.x) {
     const SeqInfo s = seq_info(p, b);
     if (blockIdx.x == 0) seq_check(p, b);
     uint32_t w = 0;
@@ -128,7 +135,7 @@ __device__ __forceinline__ void weigh(const AttnParams& p, uint32_t* pos) {
   }
   if (!__syncthreads_or(any_long)) return;
 #pragma unroll 1
-  for (int b = warp; b < p.n_seqs; b += nwarps) {  // long sequences: one warp over the blocks
+  for (int b = warp; b < n_lists(p); b += nwarps) {  // long sequences: one warp over the blocks
     const uint32_t have = pos[b + 1];
     __syncwarp();
     if (have != 0xFFFFFFFFu) continue;
@@ -158,15 +165,16 @@ struct Walk {
   __device__ __forceinline__ void start(const AttnParams& p, uint32_t* pos, int lane) {
     uint32_t run = 0;
     if (lane == 0) pos[0] = 0;
+    const int ns = n_lists(p);
 #pragma unroll 1
-    for (int b0 = 0; b0 < p.n_seqs; b0 += 32) {
-      uint32_t v = b0 + lane < p.n_seqs ? pos[b0 + lane + 1] : 0;
+    for (int b0 = 0; b0 < ns; b0 += 32) {
+      uint32_t v = b0 + lane < ns ? pos[b0 + lane + 1] : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const uint32_t u = __shfl_up_sync(FULL, v, o);
         if (lane >= o) v += u;
       }
-      if (b0 + lane < p.n_seqs) pos[b0 + lane + 1] = run + v;
+      if (b0 + lane < ns) pos[b0 + lane + 1] = run + v;
       run += __shfl_sync(FULL, v, 31);
     }
     __syncwarp();
@@ -177,11 +185,11 @@ struct Walk {
     at = end;  // nothing to do
     if (blockIdx.x == 0 && p.seq_pos) {
 #pragma unroll 1
-      for (int i = lane; i <= p.n_seqs; i += 32) p.seq_pos[i] = pos[i];
-      if (lane == 0) p.seq_pos[p.n_seqs + 1] = per;
+      for (int i = lane; i <= ns; i += 32) p.seq_pos[i] = pos[i];
+      if (lane == 0) p.seq_pos[ns + 1] = per;
     }
     if (begin >= end) return;
-    int hi = p.n_seqs - 1;  // the sequence with pos[b] <= begin < pos[b+1]
+    int hi = ns - 1;  // the sequence with pos[b] <= begin < pos[b+1]
 #pragma unroll 1
     while (b < hi) {
       const int mid = (b + hi + 1) >> 1;
@@ -228,7 +236,7 @@ struct Walk {
       u.p0 = t.p0, u.p1 = t.p1, u.sink = t.sink, u.base = t.base;
       u.tok0 = s.start + blk * p.block_tokens;
       u.nt = min(p.block_tokens, s.n - blk * p.block_tokens);
-      u.whole = u.i0 == 0 && u.i1 == t.count;
+      u.flags = (u.i0 == 0 && u.i1 == t.count ? kWhole : 0) | (s.causal ? kCausal : 0);
       const uint32_t here = at;
       at += t.count + p.unit_cost;
       if (++head == p.n_kv && at < end) {

@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(SplitCfg<D, RG>::threads, SplitCfg<D, RG>::cta
     bool ok = true;
     while (ok && walk.next(p, u)) {
       ok = give_unit(units, u, n++, lane, wait);
-      const int64_t row = (int64_t)u.b * p.table_stride;
+      const int32_t* row = table_of(p, u.b);
 #pragma unroll 1
       for (int i = u.i0; i < u.i1 && ok; ++i, ++it) {
         const int sgi = it % NST;
@@ -192,6 +192,9 @@ __global__ void __launch_bounds__(SplitCfg<D, RG>::threads, SplitCfg<D, RG>::cta
   Unit u;
   for (int n = 0; take_unit(units, u, n, lane, wait); ++n) {
     const int tok0 = u.tok0, nt = u.nt, p0 = u.p0;
+    const bool causal = u.flags & kCausal, whole = u.flags & kWhole;
+    float* const dense_o = p.dense_o[causal ? 0 : 1];
+    float2* const dense_ml = p.dense_ml[causal ? 0 : 1];
     int pos[2], tok[2];
     bool live[2];
     uint32_t qf[D / 16][4];
@@ -200,7 +203,7 @@ __global__ void __launch_bounds__(SplitCfg<D, RG>::threads, SplitCfg<D, RG>::cta
       const int row = row0 + (lane >> 2) + r * 8;
       tok[r] = row / p.group;
       live[r] = tok[r] < nt;
-      pos[r] = p.causal ? p0 + tok[r] : p0;
+      pos[r] = causal ? p0 + tok[r] : p0;
       const uint32_t* src = reinterpret_cast<const uint32_t*>(
           static_cast<const uint16_t*>(p.q) + (int64_t)(tok0 + tok[r]) * p.q_stride +
           (int64_t)(u.head * p.group + row - tok[r] * p.group) * D);
@@ -212,7 +215,7 @@ __global__ void __launch_bounds__(SplitCfg<D, RG>::threads, SplitCfg<D, RG>::cta
     }
     // the warp's own tokens and their positions
     const int tok_lo = row0 / p.group, tok_hi = min(nt - 1, (row0 + 15) / p.group);
-    const int w0 = p.causal ? p0 + tok_lo : p0, w1 = p.causal ? p0 + tok_hi : p0;
+    const int w0 = causal ? p0 + tok_lo : p0, w1 = causal ? p0 + tok_hi : p0;
     uint32_t bad = 0;
     float o[D / 8][4], mx[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
 #pragma unroll
@@ -286,7 +289,7 @@ __global__ void __launch_bounds__(SplitCfg<D, RG>::threads, SplitCfg<D, RG>::cta
       for (int r = 0; r < 2; ++r) {
         const int row = row0 + (lane >> 2) + r * 8;
         const float m2 = mx[r] * p.scale_log2;  // -inf stays -inf
-        if (u.whole && !p.dense_o) {
+        if (whole && !dense_o) {
           if (!live[r]) continue;
           const int hq = u.head * p.group + row - tok[r] * p.group;
           const float inv = sum[r] == 0.f ? 0.f : 1.f / sum[r];
@@ -302,10 +305,10 @@ __global__ void __launch_bounds__(SplitCfg<D, RG>::threads, SplitCfg<D, RG>::cta
           int64_t at;
           float* dst;
           float2* ml;
-          if (u.whole) {
+          if (whole) {
             if (!live[r]) continue;
             at = (int64_t)(tok0 + tok[r]) * p.n_q + u.head * p.group + row - tok[r] * p.group;
-            dst = p.dense_o, ml = p.dense_ml;
+            dst = dense_o, ml = dense_ml;
           } else {
             at = ((int64_t)blockIdx.x * 2 + (u.i0 > 0 ? 0 : 1)) * C::rows + row;
             dst = p.part_o, ml = p.part_ml;

@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
           }
           __syncwarp();
         }
-        const int64_t row = (int64_t)u.b * p.table_stride;
+        const int32_t* row = table_of(p, u.b);
 #pragma unroll 1
         for (int i = 2 * u.i0; i < 2 * u.i1 && ok; ++i, ++it) {
           const int j0 = u.tile(i >> 1) * kTileKeys, sg = it % NST;
@@ -381,9 +381,11 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
     for (int n = 0; take_unit(units, u, n, lane, wait); ++n) {
       const int nt = min(half_tokens, u.nt - s * half_tokens);
       if (nt <= 0) continue;
-      const int pa = p.causal ? u.p0 + s * half_tokens : u.p0;  // the row tile's positions
-      const int pb = p.causal ? pa + nt - 1 : pa;
-      const int pos = p.causal ? pa + tok : pa;
+      const bool causal = u.flags & kCausal, whole = u.flags & kWhole;
+      float* const dense_o = p.dense_o[causal ? 0 : 1];
+      const int pa = causal ? u.p0 + s * half_tokens : u.p0;  // the row tile's positions
+      const int pb = causal ? pa + nt - 1 : pa;
+      const int pos = causal ? pa + tok : pa;
       float ref = -INFINITY, sum0 = 0.f, sum1 = 0.f;
       bool ok = true;
 #pragma unroll 1
@@ -480,7 +482,7 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
       const float sum = sum0 + sum1, m2 = ref * p.scale_log2;
       const int token = u.tok0 + s * half_tokens + tok, hq = u.head * p.group + row - tok * p.group;
       const bool live = tok < nt;
-      if (u.whole && !p.dense_o) {
+      if (whole && !dense_o) {
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         uint16_t* dst = static_cast<uint16_t*>(p.out) + (int64_t)token * p.out_stride + (int64_t)hq * D;
 #pragma unroll 1
@@ -502,10 +504,10 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
           p.lse[(int64_t)token * p.n_q + hq] = sum == 0.f ? -INFINITY : (m2 + log2f(sum)) * 0.69314718055994530942f;
       } else {
         // a cut unit's rows are numbered over both row tiles: row tile 1 starts at half_tokens * group
-        const int64_t at = u.whole ? (int64_t)token * p.n_q + hq
+        const int64_t at = whole ? (int64_t)token * p.n_q + hq
                                    : ((int64_t)blockIdx.x * 2 + (u.i0 > 0 ? 0 : 1)) * kTileRows +
                                          s * half_tokens * p.group + row;
-        float* dst = (u.whole ? p.dense_o : p.part_o) + at * D;
+        float* dst = (whole ? dense_o : p.part_o) + at * D;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           float o[32];
@@ -521,7 +523,7 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
             }
           }
         }
-        if (live) (u.whole ? p.dense_ml : p.part_ml)[at] = make_float2(m2, sum);
+        if (live) (whole ? p.dense_ml[causal ? 0 : 1] : p.part_ml)[at] = make_float2(m2, sum);
       }
       tc_fence_before();  // the next unit's products overwrite O after this row tile's next arrival
     }

@@ -258,6 +258,25 @@ def test_prefix(n_q, n_kv, D, page, dt, layout, news, lens, prefix):
     assert torch.equal(s.eng.prefix(s.cache, s.batch, s.prefix_table, s.prefix_len, s.q), a)
 
 
+@pytest.mark.parametrize("n_q,n_kv", [(4, 2), (32, 1)])
+def test_prefix_ignores_what_a_row_does_not_see(n_q, n_kv):
+    """infinities and NaN in a later token's key and value, behind the suffix and behind the prefix"""
+    for bad in (math.nan, math.inf):
+        s = Setup([3, 2, 1], [40, 7, 90], n_q, n_kv, 64, 16, BF, prefix=70)
+        s.shared()
+        ref = s.reference()
+        j = 39  # the last token of the first sequence: its two earlier queries do not see it
+        pg = int(s.table[0, j // 16])
+        s.kc[pg, :, j % 16], s.vc[pg, :, j % 16] = bad, bad
+        out = s.eng.prefix(s.cache, s.batch, s.prefix_table, s.prefix_len, s.q)
+        keep = torch.ones(6, dtype=torch.bool, device="cuda")
+        keep[2] = False
+        assert (s.off(out, ref)[keep] <= 1).all() and not torch.isfinite(out[2]).any()
+        # the flags of that call are gone: the next one is clean again
+        s.kc[pg, :, j % 16], s.vc[pg, :, j % 16] = s.keys[0][:, j].to(BF), s.vals[0][:, j].to(BF)
+        s.shared()
+
+
 # ---- append ----
 
 def rotated(x, pos, freq, rot, interleaved):
