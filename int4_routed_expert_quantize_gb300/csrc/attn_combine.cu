@@ -11,20 +11,22 @@ namespace coli {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kFew = 4, kMany = 8;  // parts a row has on its way: a cut unit's are few, a prefix's many
 
 // running join of one row over a warp; lane holds D/32 consecutive values
-template <int D>
+template <int D, int Loads>
 struct Join {
   static constexpr int V = D / 32;
+  static constexpr int kLoads = Loads;  // parts in flight
   float m = -INFINITY, l = 0.f, o[V];
   __device__ __forceinline__ Join() {
 #pragma unroll
     for (int i = 0; i < V; ++i) o[i] = 0.f;
   }
   template <class At>
-  static __device__ __forceinline__ void load4(float (&v)[4][V], const float* ob, int c, int n, int lane, At at) {
+  static __device__ __forceinline__ void load(float (&v)[kLoads][V], const float* ob, int c, int n, int lane, At at) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < kLoads; ++j) {
 #pragma unroll
       for (int i = 0; i < V; ++i) v[j][i] = 0.f;
       if (j < n) {
@@ -44,8 +46,8 @@ struct Join {
   __device__ __forceinline__ void add(const float* ob, const float2* mlb, int n, int lane, At at) {
     for (int c = 0; c < n; c += 32) {
       const int k = min(32, n - c);
-      float first[4][V];  // asked for before the weights are known
-      load4(first, ob, c, k, lane, at);
+      float first[kLoads][V];  // asked for before the weights are known
+      load(first, ob, c, k, lane, at);
       float2 ml = make_float2(-INFINITY, 0.f);
       if (lane < k) ml = __ldcg(mlb + at(c + lane));
       float top = fmaxf(m, warp_max(ml.x));
@@ -60,10 +62,10 @@ struct Join {
 #pragma unroll
       for (int i = 0; i < V; ++i) o[i] *= keep;
 #pragma unroll 1
-      for (int j0 = 0; j0 < k; j0 += 4) {
-        if (j0 > 0) load4(first, ob, c + j0, k - j0, lane, at);
+      for (int j0 = 0; j0 < k; j0 += kLoads) {
+        if (j0 > 0) load(first, ob, c + j0, k - j0, lane, at);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kLoads; ++j) {
           const float wj = __shfl_sync(FULL, w, j0 + j);  // 0 past the end, and for a part without keys
           if (wj != 0.f)
 #pragma unroll
@@ -88,8 +90,8 @@ struct Join {
 
 // Adds one query row's attention to its own cache, from the definition, by one warp: for the rare blocks with
 // values that are not finite and that only some of the block's rows see.  qf: D floats of shared memory.
-template <class T, int D>
-__device__ __noinline__ void add_direct(Join<D>& r, const AttnParams& p, const SeqInfo& s, int b, int i, int hq,
+template <class T, int D, class J>
+__device__ __noinline__ void add_direct(J& r, const AttnParams& p, const SeqInfo& s, int b, int i, int hq,
                                         float* qf, int lane) {
   constexpr int V = D / 32;
   const int pos = s.len - s.n + i, head = hq / p.group;
@@ -161,7 +163,7 @@ __device__ __forceinline__ int seq_of(const AttnParams& p, int token, int lane) 
 __device__ __noinline__ void clear_flags(const AttnParams& p) {
   __shared__ int last;
   __syncthreads();  // this block has read what it needs
-  if (threadIdx.x == 0) last = atomicAdd(p.redo_any + 1, 1) == (int)(gridDim.x * gridDim.y) - 1;
+  if (threadIdx.x == 0) last = atomicAdd(p.redo_any + 1, 1) == (int)gridDim.x - 1;
   __syncthreads();
   if (!last) return;
   for (int64_t k = threadIdx.x; k < (int64_t)p.n_tokens * p.n_kv; k += blockDim.x) p.redo[k] = 0;
@@ -169,40 +171,36 @@ __device__ __noinline__ void clear_flags(const AttnParams& p) {
 }
 
 template <class T, int D>
-__device__ __forceinline__ void join_parts(const AttnParams& p, const AttnRec& r, int rows, int rows_per_block,
-                                           int warp, int lane) {
-  for (int i = warp; i < rows_per_block; i += kWarps) {
-    const int row = blockIdx.y * rows_per_block + i;
-    const int tok = row / p.group;
-    if (tok >= r.tokens) break;
-    Join<D> j;
-    j.add(p.part_o, p.part_ml, r.last_cta - r.first_cta + 1, lane, [&](int c) {
-      return ((int64_t)(r.first_cta + c) * 2 + (c == 0 ? 1 : 0)) * rows + row;
-    });
-    j.template write<T>(p, r.token0 + tok, r.head * p.group + row - tok * p.group, lane);
-  }
-}
-
-template <class T, int D>
-__global__ void __launch_bounds__(kWarps * 32)
-    attn_combine_kernel(const AttnParams p, int rows, int rows_per_block) {
+__global__ void __launch_bounds__(kWarps * 32) attn_combine_kernel(const AttnParams p, const AttnLists lists) {
   griddep_wait();
   griddep_launch_dependents();
-  const AttnRec r = p.rec[blockIdx.x];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int which = (int)blockIdx.x >= lists.l[0].blocks ? 1 : 0;
+  AttnList l = lists.l[0];
+  if (which) l = lists.l[1];  // (an indexed parameter would be copied to local memory)
+  const int block = blockIdx.x - (which ? lists.l[0].blocks : 0), cta = block % l.ctas;
+  const AttnRec r = l.rec[cta];
   const bool redo = __ldcg(p.redo_any) != 0;
   if (r.first_cta >= 0 && !(redo && __ldcg(p.redo + (int64_t)r.token0 * p.n_kv + r.head)))
-    join_parts<T, D>(p, r, rows, rows_per_block, warp, lane);
+    for (int i = warp; i < l.block_rows; i += kWarps) {
+      const int row = block / l.ctas * l.block_rows + i;
+      const int tok = row / p.group;
+      if (tok >= r.tokens) break;
+      Join<D, kFew> j;
+      j.add(l.part_o, l.part_ml, r.last_cta - r.first_cta + 1, lane, [&](int c) {
+        return ((int64_t)(r.first_cta + c) * 2 + (c == 0 ? 1 : 0)) * l.rows + row;
+      });
+      j.template write<T>(p, r.token0 + tok, r.head * p.group + row - tok * p.group, lane);
+    }
   if (!redo) return;
   __shared__ float qf[kWarps][D];
-  const int64_t stride = (int64_t)gridDim.x * gridDim.y * kWarps;
-  for (int64_t k = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kWarps + warp; k < (int64_t)p.n_tokens * p.n_kv;
-       k += stride) {
+  for (int64_t k = (int64_t)blockIdx.x * kWarps + warp; k < (int64_t)p.n_tokens * p.n_kv;
+       k += (int64_t)gridDim.x * kWarps) {
     if (!__ldcg(p.redo + k)) continue;
     const int token = (int)(k / p.n_kv), b = seq_of(p, token, lane);
     const SeqInfo s = seq_info(p, b);
     for (int g = 0; g < p.group; ++g) {
-      Join<D> j;
+      Join<D, kFew> j;
       const int hq = (int)(k % p.n_kv) * p.group + g;
       add_direct<T, D>(j, p, s, b, token - s.start, hq, qf[warp], lane);
       j.template write<T>(p, token, hq, lane);
@@ -246,8 +244,8 @@ __device__ __forceinline__ Parts find_parts(const AttnParams& p, int rows, const
   return r;
 }
 
-template <int D>
-__device__ __forceinline__ void add_parts(Join<D>& j, const AttnParams& p, const Parts& r, int which, int64_t dense_row,
+template <class J>
+__device__ __forceinline__ void add_parts(J& j, const AttnParams& p, const Parts& r, int which, int64_t dense_row,
                                           int lane) {
   // one call for both kinds: a dense row is a part at its own place
   const float* ob = r.dense ? p.dense_o[which] : p.part_o;
@@ -273,7 +271,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   const int token = live ? (int)(row / own.n_q) : 0, hq = live ? (int)(row - (int64_t)token * own.n_q) : 0;
   const int head = hq / own.group, g = hq - head * own.group;
   const bool redo = __ldcg(own.redo_any) != 0;
-  Join<D> j;
+  Join<D, kMany> j;
   Parts far;
   if (live) {
     const int b = seq_of(own, token, lane), lists = n_lists(own);
@@ -339,14 +337,18 @@ cudaError_t join(const AttnParams& own, int own_rows, const AttnParams& shared, 
 
 }  // namespace
 
-cudaError_t launch_attn_combine(const AttnParams& p, int rows, int ctas, int dtype, cudaStream_t stream) {
-  const int rpb = rows >= 64 ? 16 : 4;
-  const dim3 grid(ctas, rows / rpb);
+AttnList attn_list(const AttnParams& p, int rows, int ctas) {
+  const int block_rows = rows >= 64 ? 16 : 4;
+  return AttnList{p.part_o, p.part_ml, p.rec, ctas, rows, block_rows, ctas * (rows / block_rows)};
+}
+
+cudaError_t launch_attn_combine(const AttnParams& p, const AttnLists& lists, int dtype, cudaStream_t stream) {
+  const dim3 grid(lists.l[0].blocks + lists.l[1].blocks);
   if (dtype == COLI_ATTN_BF16)
-    return p.head_dim == 64 ? go(attn_combine_kernel<Bf16, 64>, grid, stream, p, rows, rpb)
-                            : go(attn_combine_kernel<Bf16, 128>, grid, stream, p, rows, rpb);
-  return p.head_dim == 64 ? go(attn_combine_kernel<Fp16, 64>, grid, stream, p, rows, rpb)
-                          : go(attn_combine_kernel<Fp16, 128>, grid, stream, p, rows, rpb);
+    return p.head_dim == 64 ? go(attn_combine_kernel<Bf16, 64>, grid, stream, p, lists)
+                            : go(attn_combine_kernel<Bf16, 128>, grid, stream, p, lists);
+  return p.head_dim == 64 ? go(attn_combine_kernel<Fp16, 64>, grid, stream, p, lists)
+                          : go(attn_combine_kernel<Fp16, 128>, grid, stream, p, lists);
 }
 
 cudaError_t launch_attn_join(const AttnParams& own, int own_rows, const AttnParams& shared, bool same_list,

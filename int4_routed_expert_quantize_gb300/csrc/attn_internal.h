@@ -29,7 +29,7 @@ struct AttnRec {
   int first_cta, last_cta;  // CTAs with a part of the unit; first_cta < 0: no record
   int token0, tokens;       // the unit's query tokens
   int head;                 // key head
-  int seq, blk, pad;
+  int pad[3];
 };
 
 struct AttnParams {
@@ -91,7 +91,7 @@ struct AttnAppend {
 };
 
 int split_rows(int rows);  // rows per block the split kernel takes for units of `rows` rows
-int split_grid(int rows, int num_sms);
+int split_grid(int num_sms);  // CTAs
 cudaError_t configure_attn_split();
 cudaError_t launch_attn_split(const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v,
                               int rows, int dtype, int num_sms, cudaStream_t stream);
@@ -99,9 +99,21 @@ int tile_block_tokens(int group);  // tokens per block of the tensor-memory kern
 cudaError_t configure_attn_tile();
 cudaError_t launch_attn_tile(const AttnParams& p, const CUtensorMap& q, const CUtensorMap& k,
                              const CUtensorMap& v, int dtype, int num_sms, cudaStream_t stream);
+// One launch's partials; a combine kernel merges those of up to two launches.
+struct AttnList {
+  const float* part_o;
+  const float2* part_ml;
+  const AttnRec* rec;
+  int ctas, rows;  // CTAs, rows per block of theirs
+  int block_rows;  // of which a block of the combine kernel takes so many
+  int blocks;      // blocks of the combine kernel for this list
+};
+struct AttnLists {
+  AttnList l[2];
+};
+AttnList attn_list(const AttnParams& p, int rows, int ctas);
 // merges the partials of cut units into out / lse
-cudaError_t launch_attn_combine(const AttnParams& p, int rows, int ctas, int dtype,
-                                cudaStream_t stream);
+cudaError_t launch_attn_combine(const AttnParams& p, const AttnLists& lists, int dtype, cudaStream_t stream);
 // merges, for every row, the sequence's own and the prefix's results into out / lse; own and shared are the same
 // list when one launch made both, else the prefix's came from the tensor-memory kernel
 cudaError_t launch_attn_join(const AttnParams& own, int own_rows, const AttnParams& shared, bool same_list,

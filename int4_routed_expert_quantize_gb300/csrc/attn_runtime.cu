@@ -234,9 +234,9 @@ extern "C" int coli_attn_create(const coli_attn_config* cfg, coli_attn** out) {
   if (!rc) {
     h->num_sms = prop.multiProcessorCount;
     const size_t D = c.head_dim, ctas = (size_t)2 * h->num_sms;
-    // partials: two per CTA of the split kernel (2 CTAs an SM of 16 rows or one of up to 64) and of the
+    // partials: two per CTA of the split kernel (2 CTAs an SM, up to 64 rows) and of the
     // tensor-memory kernel
-    const size_t rows = 2 * (size_t)h->num_sms * 64, rows2 = 2 * (size_t)h->num_sms * kTileRows;
+    const size_t rows = 2 * ctas * 64, rows2 = 2 * (size_t)h->num_sms * kTileRows;
     // the prefix call keeps every row twice: up to kAttnPrefixRows tokens a sequence
     const int64_t pt = (int64_t)kAttnPrefixRows * c.max_seqs;
     h->prefix_tokens = (int)(pt < c.max_tokens ? pt : c.max_tokens);
@@ -353,22 +353,24 @@ extern "C" int coli_attn_window(coli_attn* h, const coli_attn_kv* kv, const coli
   // sequences of up to kSplitMaxRows rows go to the split kernel, longer ones to the tensor-memory kernel
   const bool many = (int64_t)b->max_q * p.group > kSplitMaxRows;
   cudaError_t e = cudaSuccess;
-  if (many) {
-    AttnParams t = p;
-    use_tile(h, &t);
-    t.rows_lo = kSplitMaxRows;
-    CUtensorMap qm;
-    if (!query_map(&qm, h, q, q_stride, b->n_tokens)) return COLI_ECUDA;
-    e = launch_attn_tile(t, qm, kv->maps.k128, kv->maps.v128, h->cfg.dtype, h->num_sms, st);
-    if (e == cudaSuccess) e = launch_attn_combine(t, kTileRows, h->num_sms, h->cfg.dtype, st);
-    p.rows_hi = kSplitMaxRows;
-  }
-  if (e == cudaSuccess && (!many || b->n_seqs > 1)) {
+  AttnLists lists = {};
+  int n = 0;
+  if (!many || b->n_seqs > 1) {
+    if (many) p.rows_hi = kSplitMaxRows;
     const int rows = rows_of(h, b->max_q);
     p.block_tokens = rows / p.group;
     e = launch_attn_split(p, kv->maps.k64, kv->maps.v64, rows, h->cfg.dtype, h->num_sms, st);
-    if (e == cudaSuccess) e = launch_attn_combine(p, rows, split_grid(rows, h->num_sms), h->cfg.dtype, st);
+    lists.l[n++] = attn_list(p, rows, split_grid(h->num_sms));
   }
+  if (e == cudaSuccess && many) {
+    use_tile(h, &p);
+    p.rows_lo = kSplitMaxRows, p.rows_hi = INT64_MAX;
+    CUtensorMap qm;
+    if (!query_map(&qm, h, q, q_stride, b->n_tokens)) return COLI_ECUDA;
+    e = launch_attn_tile(p, qm, kv->maps.k128, kv->maps.v128, h->cfg.dtype, h->num_sms, st);
+    lists.l[n++] = attn_list(p, kTileRows, h->num_sms);
+  }
+  if (e == cudaSuccess) e = launch_attn_combine(p, lists, h->cfg.dtype, st);
   return e == cudaSuccess ? COLI_OK : COLI_ECUDA;
 }
 
@@ -427,5 +429,5 @@ extern "C" int coli_attn_status(coli_attn* h, void* stream) {
 extern "C" int coli_attn_launches(const coli_attn* h, int op, int max_q) {
   if (!h || op < 0 || op > 2 || max_q < 1) return COLI_EINVAL;
   const bool many = (int64_t)max_q * (h->cfg.n_q / h->cfg.n_kv) > kSplitMaxRows;
-  return op == 0 ? 1 : op == 1 ? (many ? 4 : 2) : 3;
+  return op == 0 ? 1 : op == 1 ? (many ? 3 : 2) : 3;
 }

@@ -264,7 +264,7 @@ struct Walk {
     if (c0 + 1 != (int)blockIdx.x || (threadIdx.x & 31) != 0) return;
     AttnRec r;
     r.first_cta = c0, r.last_cta = (first + count - 1) / per;
-    r.token0 = u.tok0, r.tokens = u.nt, r.head = u.head, r.seq = u.b, r.blk = u.blk, r.pad = 0;
+    r.token0 = u.tok0, r.tokens = u.nt, r.head = u.head, r.pad[0] = r.pad[1] = r.pad[2] = 0;
     p.rec[blockIdx.x] = r;
   }
 };

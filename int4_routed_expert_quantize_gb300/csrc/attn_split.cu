@@ -18,16 +18,16 @@ namespace {
 
 template <int D, int RG>
 struct SplitCfg {
-  static constexpr int KG = RG == 4 ? 2 : 4;  // key groups: warps that share 16 rows
-  static constexpr int warps = RG * KG;
+  static constexpr int KG = 4 / RG;  // key groups: warps that share 16 rows
+  static constexpr int warps = 4;
   static constexpr int threads = (warps + 1) * 32;
   static constexpr int rows = RG * 16;
   static constexpr int kw = kSplitKeys / KG;  // keys per warp and tile
-  static constexpr int ctas = RG == 1 ? 2 : 1;  // per SM
+  static constexpr int ctas = 2;  // per SM
   static constexpr int tile_bytes = kSplitKeys * D * 2;
-  static constexpr int stages = (RG == 1 ? 98304 : 163840) / (2 * tile_bytes);
+  static constexpr int stages = 98304 / (2 * tile_bytes);
   static constexpr int merge_floats = 16 * D + 32;
-  static constexpr int merge_bytes = RG * (KG / 2) * merge_floats * 4;
+  static constexpr int merge_bytes = 2 * merge_floats * 4;  // RG * KG / 2 buffers
   static constexpr int smem = stages * 2 * tile_bytes + merge_bytes + 2 * stages * 8 + (int)sizeof(UnitRing) + 24;
 };
 
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(SplitCfg<D, RG>::threads, SplitCfg<D, RG>::cta
     }
     // join the warps that share these rows: the upper half hands over to the lower half
 #pragma unroll
-    for (int half = C::KG / 2; half >= 1; half >>= 1) {
+    for (int half = C::KG / 2; half >= 1; half >>= 1) {  // (one key group: nothing to join)
       const int slot = (kg % half) * RG + rg;
       float4* buf = reinterpret_cast<float4*>(merge + slot * C::merge_floats);
       float2* ml = reinterpret_cast<float2*>(merge + slot * C::merge_floats + 16 * D);
@@ -360,7 +360,7 @@ cudaError_t launch_rows(const AttnParams& p, const CUtensorMap& k, const CUtenso
 }  // namespace
 
 int split_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
-int split_grid(int rows, int num_sms) { return split_rows(rows) == 16 ? 2 * num_sms : num_sms; }
+int split_grid(int num_sms) { return 2 * num_sms; }
 
 cudaError_t configure_attn_split() {
   cudaError_t e = cudaSuccess;
@@ -375,7 +375,7 @@ cudaError_t configure_attn_split() {
 
 cudaError_t launch_attn_split(const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v,
                               int rows, int dtype, int num_sms, cudaStream_t stream) {
-  const int r = split_rows(rows), grid = split_grid(rows, num_sms);
+  const int r = split_rows(rows), grid = split_grid(num_sms);
   if (dtype == COLI_ATTN_BF16)
     return p.head_dim == 64 ? launch_rows<Bf16, 64>(p, k, v, r, grid, stream)
                             : launch_rows<Bf16, 128>(p, k, v, r, grid, stream);
