@@ -57,6 +57,18 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(FULL, ok);
 }
 
+// The same by one lane on its own; a wait that gives up returns all the same (the abort flag is up then).
+__device__ __forceinline__ void lane_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  if (mbar_try_wait(bar, parity)) return;
+  const uint64_t t0 = global_ns();
+#pragma unroll 1
+  for (uint32_t it = 1; !mbar_try_wait(bar, parity) && !*abort_flag; ++it)
+    if ((it & 63u) == 0 && global_ns() - t0 > kWaitLimitNs) {
+      *abort_flag = 1;
+      atomicExch(status, COLI_ETIMEOUT);
+    }
+}
+
 // drain_fills, inline for the same reason
 __device__ __forceinline__ void drain_ring(uint64_t* full, int stages, int issued) {
 #pragma unroll 1

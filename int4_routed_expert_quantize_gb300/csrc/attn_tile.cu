@@ -248,9 +248,13 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
       // the 14-bit address field: shared memory ends below 2^18 bytes)
       const uint64_t q_desc = smem_desc_sw128(qs), k_desc = smem_desc_sw128(ring), v_desc = smem_desc_values(ring);
       // Scores run one key tile ahead of values: a_* is the unit they are in (a_left tiles to go, a_first: none
-      // yet), b_* the values' one.  Each round issues, for either row tile, values of tile it and scores of it + 1.
-      int units_taken = 0, it = -1;
-      uint32_t qn0 = 0, qn1 = 0, pn0 = 0, pn1 = 0;
+      // yet), b_* the values' one.  Each round issues, for either row tile, values of one tile and scores of the
+      // next.  This warp's instructions are what the matrix unit waits for, so a round is one elected lane's, with
+      // everything that is the same for all lanes worked out before it, and a wait that gives up does not leave
+      // the loop: the later ones then return at once.
+      int units_taken = 0;
+      int vs = NST - 1, ks = 0;  // stages of the value and the key tile (the first round has no values)
+      uint32_t vphase = 1, kphase = 0, pphase0 = 0, pphase1 = 0, qphase0 = 0, qphase1 = 0;
       int a_left = 0, b_left = 0;
       bool a_two = false, b_two = false, a_first = false, b_first = false;
       const auto take = [&]() {
@@ -258,65 +262,51 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
         a_left = u.i1 - u.i0, a_two = u.nt > half_tokens, a_first = true;
         return true;
       };
+      const auto wait1 = [&](uint64_t* bar, uint32_t parity) { lane_wait(bar, parity, abort_flag, p.status); };
       bool more = take();
 #pragma unroll 1
-      while (ok && (more || b_left > 0)) {
-        const bool s_last = a_left == 1;
-#pragma unroll 1
-        for (int s = 0; s < 2 && ok; ++s) {
-          if (b_left > 0 && (s == 0 || b_two)) {
-            const int item = 2 * it + 1, sg = item % NST;
-            const uint32_t phase = (s ? pn1++ : pn0++) & 1;
-            ok = wait(checked + sg, (item / NST) & 1) && wait(p_half + s, phase);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t b = v_desc + sg * (C::tile_bytes >> 4);
-            const uint32_t d = tmem + C::o_col + s * D, a = tmem + s * 128;
-            if (elect_one()) {  // the first 64 keys' weights are there
-              tc_mma_ts(d, a, b, pv_idesc, !b_first);
+      while (more || b_left > 0) {
+        const uint64_t bv = v_desc + vs * (C::tile_bytes >> 4), bk = k_desc + ks * (C::tile_bytes >> 4);
+        const bool pv0 = b_left > 0, pv1 = pv0 && b_two, qk1 = more && a_two, o_last = b_left == 1, s_last = a_left == 1;
+        if (elect_one()) {
+          if (pv0) wait1(checked + vs, vphase);
 #pragma unroll
-              for (int k = 1; k < 4; ++k) tc_mma_ts(d, a + k * 8, b + k * (2048 >> 4), pv_idesc, true);
-            }
-            __syncwarp();
-            ok = wait(p_full + s, phase);
-            if (!ok) break;
-            tc_fence_after();
-            if (elect_one()) {
+          for (int s = 0; s < 2; ++s) {
+            if (s ? pv1 : pv0) {
+              const uint32_t d = tmem + C::o_col + s * D, a = tmem + s * 128;
+              wait1(p_half + s, s ? pphase1 : pphase0);  // the first 64 keys' weights are there
+              tc_fence_after();
+              tc_mma_ts(d, a, bv, pv_idesc, !b_first);
 #pragma unroll
-              for (int k = 4; k < 8; ++k) tc_mma_ts(d, a + k * 8, b + k * (2048 >> 4), pv_idesc, true);
-              if (b_left == 1) tc_commit(o_full + s);
+              for (int k = 1; k < 4; ++k) tc_mma_ts(d, a + k * 8, bv + k * (2048 >> 4), pv_idesc, true);
+              wait1(p_full + s, s ? pphase1 : pphase0);
+              tc_fence_after();
+#pragma unroll
+              for (int k = 4; k < 8; ++k) tc_mma_ts(d, a + k * 8, bv + k * (2048 >> 4), pv_idesc, true);
+              if (o_last) tc_commit(o_full + s);
+              if (s == 1 || !pv1) tc_commit(empty + vs);
             }
-            __syncwarp();
-          }
-          if (more && (s == 0 || a_two)) {
-            if (a_first) {
-              ok = wait(q_full + s, (s ? qn1 : qn0) & 1);
-              s ? ++qn1 : ++qn0;
-            }
-            const int item = 2 * it + 2, sg = item % NST;
-            ok = ok && wait(checked + sg, (item / NST) & 1);
-            if (!ok) break;
-            tc_fence_after();
-            if (elect_one()) {
-              const uint64_t a = q_desc + s * (C::tile_bytes >> 4), b = k_desc + sg * (C::tile_bytes >> 4);
+            if (s ? qk1 : more) {
+              if (a_first) wait1(q_full + s, s ? qphase1 : qphase0);
+              if (s == 0) wait1(checked + ks, kphase);
+              tc_fence_after();
+              const uint64_t a = q_desc + s * (C::tile_bytes >> 4);
 #pragma unroll
               for (int k = 0; k < D / 16; ++k) {
                 const int off = ((k >> 2) * kTileKeys * 128 + (k & 3) * 32) >> 4;
-                tc_mma_bf16(tmem + s * 128, a + off, b + off, qk_idesc, k > 0);
+                tc_mma_bf16(tmem + s * 128, a + off, bk + off, qk_idesc, k > 0);
               }
               tc_commit(s_full + s);
               if (s_last) tc_commit(q_empty + s);
             }
-            __syncwarp();
           }
-        }
-        if (!ok) break;
-        if (elect_one()) {
-          if (b_left > 0) tc_commit(empty + (2 * it + 1) % NST);
-          if (more) tc_commit(empty + (2 * it + 2) % NST);
+          if (more) tc_commit(empty + ks);
         }
         __syncwarp();
-        ++it;
+        pphase0 ^= pv0, pphase1 ^= pv1;
+        if (a_first) qphase0 ^= more, qphase1 ^= qk1;
+        if ((vs += 2) >= NST) vs -= NST, vphase ^= 1;
+        if ((ks += 2) >= NST) ks -= NST, kphase ^= 1;
         if (b_left > 0) --b_left, b_first = false;
         if (b_left == 0 && more) b_left = a_left, b_two = a_two, b_first = true;  // the scores of its first tile are out
         if (more) {
