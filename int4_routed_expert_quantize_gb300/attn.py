@@ -184,7 +184,10 @@ class PagedAttention:
         """the output and its token stride"""
         if out is not None:
             return out, self._heads(out, self.n_q, batch, "out")
-        out = torch.empty((batch.n_tokens, self.n_q, self.head_dim), dtype=self.dtype, device=like.device)
+        if like.is_contiguous():  # the quicker call
+            out = torch.empty_like(like)
+        else:
+            out = torch.empty((batch.n_tokens, self.n_q, self.head_dim), dtype=self.dtype, device=like.device)
         if stream is not None and isinstance(stream, torch.cuda.Stream):
             out.record_stream(stream)
         return out, self.n_q * self.head_dim

@@ -216,28 +216,41 @@ struct Parts {
   int first_cta, rows, row;
 };
 
-// Token i of sequence b on a list of stretches of `per` positions, the sequence's first one being `at`.
+// Where token i of a sequence is on the list, from the sequence's first position on: the first tile of its unit, the
+// unit's tiles and the row within its block.
+struct Place {
+  uint32_t first;
+  int tiles, row;
+};
 template <int KT>
-__device__ __forceinline__ Parts find_parts(const AttnParams& p, int rows, const SeqInfo& s, int i, int head, int g,
-                                            uint32_t at, uint32_t per) {
+__device__ __forceinline__ Place find_place(const AttnParams& p, const SeqInfo& s, int i, int head, int g) {
   const int blk = i / p.block_tokens;
   Tiles<KT> t;
+  Place r;
+  r.first = 0;
   if (s.causal) {
 #pragma unroll 1
     for (int k = 0; k < blk; ++k) {
       t.set(p, s, k);
-      at += (t.count + p.unit_cost) * p.n_kv;
+      r.first += (t.count + p.unit_cost) * p.n_kv;
     }
     t.set(p, s, blk);
   } else {  // every block has the same tiles
     t.set(p, s, blk);
-    at += blk * (t.count + p.unit_cost) * p.n_kv;
+    r.first = blk * (t.count + p.unit_cost) * p.n_kv;
   }
-  at += head * (t.count + p.unit_cost) + p.unit_cost;
-  Parts r;
+  r.first += head * (t.count + p.unit_cost) + p.unit_cost;
+  r.tiles = t.count;
   r.row = (i - blk * p.block_tokens) * p.group + g;
+  return r;
+}
+// its parts, once the sequence's first position and the stretch are known
+__device__ __forceinline__ Parts find_parts(const Place& w, int rows, uint32_t at, uint32_t per) {
+  Parts r;
+  r.row = w.row;
   r.rows = rows;
-  const int c0 = at / per, c1 = (at + t.count - 1) / per;
+  at += w.first;
+  const int c0 = at / per, c1 = (at + w.tiles - 1) / per;
   r.dense = c0 == c1;
   r.n = c1 - c0 + 1;
   r.first_cta = c0;
@@ -255,51 +268,47 @@ __device__ __forceinline__ void add_parts(J& j, const AttnParams& p, const Parts
   });
 }
 
-// Every row is the join of its own sequence's parts and the prefix's.  SAME: one launch made both, so everything waits
-// for it.  Otherwise the launch before last made the own parts, and the last one had waited for it before it
-// let this one start: all but the prefix's parts is read while that one runs.
+// Every row is the join of its own sequence's parts and the prefix's.  The kernel starts while the launch before it
+// runs and looks its rows up meanwhile (that launch had waited for whatever wrote the lengths).  SAME: that
+// launch made both, so all results wait for it.  Otherwise the launch before that one made the own parts,
+// which are read ahead as well.
 template <class T, int D, bool SAME>
 __global__ void __launch_bounds__(kWarps * 32)
     attn_join_kernel(const AttnParams own, int own_rows, const AttnParams shared, int shared_ctas) {
-  if (SAME) {
-    griddep_wait();
-    griddep_launch_dependents();
-  }
   const int lane = threadIdx.x & 31;
   const int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const bool live = row < (int64_t)own.n_tokens * own.n_q;
   const int token = live ? (int)(row / own.n_q) : 0, hq = live ? (int)(row - (int64_t)token * own.n_q) : 0;
   const int head = hq / own.group, g = hq - head * own.group;
+  const int b = seq_of(own, token, lane);
+  const SeqInfo pre = seq_info(shared, shared.n_seqs);
+  SeqInfo s = {0, 0, 0, true};
+  if (b < own.n_seqs) s = seq_info(own, b);
+  const int i = token - s.start;
+  const bool has_own = i >= 0 && i < s.n;
+  const Place far = find_place<SAME ? kSplitKeys : kTileKeys>(shared, pre, token, head, g);
+  Place near = {0, 0, 0};
+  if (has_own) near = find_place<kSplitKeys>(own, s, i, head, g);
+  uint32_t far_per = 1;
+  if (!SAME) {  // the prefix alone on its list: the stretch follows from its length
+    const uint32_t blocks = (pre.n + shared.block_tokens - 1) / shared.block_tokens;
+    const uint32_t total = blocks * shared.n_kv * (far.tiles + shared.unit_cost);
+    far_per = max(1u, (total + shared_ctas - 1) / shared_ctas);
+  }
+  if (SAME) {
+    griddep_wait();
+    griddep_launch_dependents();
+  }
   const bool redo = __ldcg(own.redo_any) != 0;
+  const uint32_t per = __ldcg(own.seq_pos + n_lists(own) + 1), near_at = has_own ? __ldcg(own.seq_pos + b) : 0;
+  const uint32_t far_at = SAME ? __ldcg(own.seq_pos + own.n_seqs) : 0;
   Join<D, kMany> j;
-  Parts far;
-  if (live) {
-    const int b = seq_of(own, token, lane), lists = n_lists(own);
-    const uint32_t per = __ldcg(own.seq_pos + lists + 1);
-    const uint32_t pre_at = SAME ? __ldcg(own.seq_pos + own.n_seqs) : 0;
-    const SeqInfo pre = seq_info(shared, shared.n_seqs);
-    if (SAME) {
-      far = find_parts<kSplitKeys>(shared, own_rows, pre, token, head, g, pre_at, per);
-    } else {  // the prefix alone on its list: the stretch follows from its length
-      Tiles<kTileKeys> t;
-      t.set(shared, pre, 0);
-      const uint32_t blocks = (pre.n + shared.block_tokens - 1) / shared.block_tokens;
-      const uint32_t total = blocks * shared.n_kv * (t.count + shared.unit_cost);
-      far = find_parts<kTileKeys>(shared, kTileRows, pre, token, head, g, 0,
-                                  max(1u, (total + shared_ctas - 1) / shared_ctas));
-    }
-    if (b < own.n_seqs) {
-      const uint32_t at = __ldcg(own.seq_pos + b);
-      const SeqInfo s = seq_info(own, b);
-      const int i = token - s.start;
-      if (i >= 0 && i < s.n) {
-        if (redo && __ldcg(own.redo + (int64_t)token * own.n_kv + head)) {
-          __shared__ float qf[kWarps][D];
-          add_direct<T, D>(j, own, s, b, i, hq, qf[threadIdx.x >> 5], lane);
-        } else {
-          add_parts(j, own, find_parts<kSplitKeys>(own, own_rows, s, i, head, g, at, per), 0, row, lane);
-        }
-      }
+  if (live && has_own) {
+    if (redo && __ldcg(own.redo + (int64_t)token * own.n_kv + head)) {
+      __shared__ float qf[kWarps][D];
+      add_direct<T, D>(j, own, s, b, i, hq, qf[threadIdx.x >> 5], lane);
+    } else {
+      add_parts(j, own, find_parts(near, own_rows, near_at, per), 0, row, lane);
     }
   }
   if (!SAME) {
@@ -307,7 +316,8 @@ __global__ void __launch_bounds__(kWarps * 32)
     griddep_launch_dependents();
   }
   if (live) {
-    add_parts(j, shared, far, 1, row, lane);
+    add_parts(j, shared, SAME ? find_parts(far, own_rows, far_at, per) : find_parts(far, kTileRows, 0, far_per), 1, row,
+              lane);
     j.template write<T>(own, token, hq, lane);
   }
   if (redo) clear_flags(own);

@@ -200,7 +200,7 @@ struct Walk {
     s = seq_info(p, b);
     const int nb = (s.n + p.block_tokens - 1) / p.block_tokens;
 #pragma unroll 1
-    for (int blk0 = 0; blk0 < nb; blk0 += 32) {
+    for (int blk0 = 0; blk0 < nb && nb > 1; blk0 += 32) {
       uint32_t w = 0;
       if (blk0 + lane < nb) {
         t.set(p, s, blk0 + lane);

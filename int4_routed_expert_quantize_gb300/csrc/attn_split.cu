@@ -26,8 +26,7 @@ struct SplitCfg {
   static constexpr int ctas = 2;  // per SM
   static constexpr int tile_bytes = kSplitKeys * D * 2;
   static constexpr int stages = 98304 / (2 * tile_bytes);
-  static constexpr int merge_floats = 16 * D + 32;
-  static constexpr int merge_bytes = 2 * merge_floats * 4;  // RG * KG / 2 buffers
+  static constexpr int merge_bytes = 4 * (8 * D + 32) * 4;  // a buffer a warp: half its columns
   static constexpr int smem = stages * 2 * tile_bytes + merge_bytes + 2 * stages * 8 + (int)sizeof(UnitRing) + 24;
 };
 
@@ -118,6 +117,49 @@ __device__ __forceinline__ void tile_step(const AttnParams& p, uint32_t ks, uint
       mma16816<T>(o[2 * d + 1], pf, b[2], b[3]);
     }
   }
+}
+
+// Buffer of a warp: H 8-column groups of its 16 rows in fragment order, then the rows' maxima and sums.
+template <int D, int H>
+__device__ __forceinline__ void hand_over(float* merge, int buffer, const float (&o)[D / 8][4], int first,
+                                          const float (&mx)[2], const float (&sum)[2], int lane) {
+  float* base = merge + buffer * (8 * D + 32);
+  float4* buf = reinterpret_cast<float4*>(base);
+#pragma unroll
+  for (int d = 0; d < D / 8; ++d)
+    if ((d / H) * H == first) buf[(d % H) * 32 + lane] = make_float4(o[d][0], o[d][1], o[d][2], o[d][3]);
+  if ((lane & 3) == 0) {
+    float2* ml = reinterpret_cast<float2*>(base + 8 * D);
+    ml[lane >> 2] = make_float2(mx[0], sum[0]);
+    ml[(lane >> 2) + 8] = make_float2(mx[1], sum[1]);
+  }
+}
+template <int D, int H>
+__device__ __forceinline__ void take_over(const float* merge, int buffer, float (&o)[D / 8][4], int first,
+                                          float scale_log2, float (&mx)[2], float (&sum)[2], int lane) {
+  const float* base = merge + buffer * (8 * D + 32);
+  const float4* buf = reinterpret_cast<const float4*>(base);
+  const float2* ml = reinterpret_cast<const float2*>(base + 8 * D);
+  float fa[2], fb[2];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const float2 other = ml[(lane >> 2) + r * 8];
+    const float m = fmaxf(mx[r], other.x);
+    const float base2 = m == -INFINITY ? 0.f : m * scale_log2;
+    fa[r] = ex2(mx[r] * scale_log2 - base2);
+    fb[r] = ex2(other.x * scale_log2 - base2);
+    mx[r] = m;
+    sum[r] = sum[r] * fa[r] + other.y * fb[r];
+  }
+#pragma unroll
+  for (int d = 0; d < D / 8; ++d)
+    if ((d / H) * H == first) {
+      const float4 v = buf[(d % H) * 32 + lane];
+      o[d][0] = o[d][0] * fa[0] + v.x * fb[0];
+      o[d][1] = o[d][1] * fa[0] + v.y * fb[0];
+      o[d][2] = o[d][2] * fa[1] + v.z * fb[1];
+      o[d][3] = o[d][3] * fa[1] + v.w * fb[1];
+    }
 }
 
 template <class T, int D, int RG>
@@ -246,79 +288,57 @@ __global__ void __launch_bounds__(SplitCfg<D, RG>::threads, SplitCfg<D, RG>::cta
       sum[r] += __shfl_xor_sync(FULL, sum[r], 1);
       sum[r] += __shfl_xor_sync(FULL, sum[r], 2);
     }
-    // join the warps that share these rows: the upper half hands over to the lower half
-#pragma unroll
-    for (int half = C::KG / 2; half >= 1; half >>= 1) {  // (one key group: nothing to join)
-      const int slot = (kg % half) * RG + rg;
-      float4* buf = reinterpret_cast<float4*>(merge + slot * C::merge_floats);
-      float2* ml = reinterpret_cast<float2*>(merge + slot * C::merge_floats + 16 * D);
+    // Join the KG warps that share these rows.  Each step halves the columns a warp keeps: it hands the other
+    // half to its partner and takes its own half's counterpart, so the last step leaves every warp
+    // D / KG finished columns.  Buffer A_w holds what was handed to warp w; only w reads it in the first step and
+    // writes its second handover there.
+    constexpr int NC = D / 8 / C::KG;  // 8-column groups a warp ends with
+    int col = 0;                       // the first of them
+    if (C::KG > 1) {
+      constexpr int H = D / 16;
+      if (!meet()) return;  // the buffers are free
+      const int other = rg + RG * (kg ^ (C::KG / 2));
+      const bool up = kg & (C::KG / 2);
+      hand_over<D, H>(merge, other, o, up ? 0 : H, mx, sum, lane);
       if (!meet()) return;
-      if (kg >= half && kg < 2 * half) {
-#pragma unroll
-        for (int d = 0; d < D / 8; ++d) buf[d * 32 + lane] = make_float4(o[d][0], o[d][1], o[d][2], o[d][3]);
-        if ((lane & 3) == 0) {
-          ml[lane >> 2] = make_float2(mx[0], sum[0]);
-          ml[(lane >> 2) + 8] = make_float2(mx[1], sum[1]);
-        }
-      }
-      if (!meet()) return;
-      if (kg < half) {
-        float fa[2], fb[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float2 other = ml[(lane >> 2) + r * 8];
-          const float m = fmaxf(mx[r], other.x);
-          const float base = m == -INFINITY ? 0.f : m * p.scale_log2;
-          fa[r] = ex2(mx[r] * p.scale_log2 - base);
-          fb[r] = ex2(other.x * p.scale_log2 - base);
-          mx[r] = m;
-          sum[r] = sum[r] * fa[r] + other.y * fb[r];
-        }
-#pragma unroll
-        for (int d = 0; d < D / 8; ++d) {
-          const float4 v = buf[d * 32 + lane];
-          o[d][0] = o[d][0] * fa[0] + v.x * fb[0];
-          o[d][1] = o[d][1] * fa[0] + v.y * fb[0];
-          o[d][2] = o[d][2] * fa[1] + v.z * fb[1];
-          o[d][3] = o[d][3] * fa[1] + v.w * fb[1];
-        }
-      }
+      take_over<D, H>(merge, warp, o, up ? H : 0, p.scale_log2, mx, sum, lane);
+      col = up ? H : 0;
     }
-    if (kg == 0) {
+    if (C::KG > 2) {
+      constexpr int H = D / 32;
+      const bool up = kg & 1;
+      hand_over<D, H>(merge, warp, o, col + (up ? 0 : H), mx, sum, lane);
+      if (!meet()) return;
+      take_over<D, H>(merge, rg + RG * (kg ^ 1), o, col + (up ? H : 0), p.scale_log2, mx, sum, lane);
+      col += up ? H : 0;
+    }
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int row = row0 + (lane >> 2) + r * 8;
-        const float m2 = mx[r] * p.scale_log2;  // -inf stays -inf
-        if (whole && !dense_o) {
-          if (!live[r]) continue;
-          const int hq = u.head * p.group + row - tok[r] * p.group;
-          const float inv = sum[r] == 0.f ? 0.f : 1.f / sum[r];
-          uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) +
-                                                      (int64_t)(tok0 + tok[r]) * p.out_stride + (int64_t)hq * D);
+    for (int r = 0; r < 2; ++r) {
+      const int row = row0 + (lane >> 2) + r * 8;
+      const float m2 = mx[r] * p.scale_log2;  // -inf stays -inf
+      const int hq = u.head * p.group + row - tok[r] * p.group;
+      if (whole && !live[r]) continue;
+      if (whole && !dense_o) {
+        const float inv = sum[r] == 0.f ? 0.f : 1.f / sum[r];
+        uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) +
+                                                    (int64_t)(tok0 + tok[r]) * p.out_stride + (int64_t)hq * D);
 #pragma unroll
-          for (int d = 0; d < D / 8; ++d)
+        for (int d = 0; d < D / 8; ++d)
+          if (C::KG == 1 || (d / NC) * NC == col)
             dst[d * 4 + (lane & 3)] = T::pack(o[d][2 * r] * inv, o[d][2 * r + 1] * inv);
-          if (p.lse && (lane & 3) == 0)
-            p.lse[(int64_t)(tok0 + tok[r]) * p.n_q + hq] =
-                sum[r] == 0.f ? -INFINITY : (m2 + log2f(sum[r])) * 0.69314718055994530942f;
-        } else {
-          int64_t at;
-          float* dst;
-          float2* ml;
-          if (whole) {
-            if (!live[r]) continue;
-            at = (int64_t)(tok0 + tok[r]) * p.n_q + u.head * p.group + row - tok[r] * p.group;
-            dst = dense_o, ml = dense_ml;
-          } else {
-            at = ((int64_t)blockIdx.x * 2 + (u.i0 > 0 ? 0 : 1)) * C::rows + row;
-            dst = p.part_o, ml = p.part_ml;
-          }
+        if (p.lse && kg == 0 && (lane & 3) == 0)
+          p.lse[(int64_t)(tok0 + tok[r]) * p.n_q + hq] =
+              sum[r] == 0.f ? -INFINITY : (m2 + log2f(sum[r])) * 0.69314718055994530942f;
+      } else {
+        const int64_t at = whole ? (int64_t)(tok0 + tok[r]) * p.n_q + hq
+                                 : ((int64_t)blockIdx.x * 2 + (u.i0 > 0 ? 0 : 1)) * C::rows + row;
+        float* dst = whole ? dense_o : p.part_o;
 #pragma unroll
-          for (int d = 0; d < D / 8; ++d)
+        for (int d = 0; d < D / 8; ++d)
+          if (C::KG == 1 || (d / NC) * NC == col)
             *reinterpret_cast<float2*>(dst + at * D + d * 8 + (lane & 3) * 2) =
                 make_float2(o[d][2 * r], o[d][2 * r + 1]);
-          if ((lane & 3) == 0) ml[at] = make_float2(m2, sum[r]);
-        }
+        if (kg == 0 && (lane & 3) == 0) (whole ? dense_ml : p.part_ml)[at] = make_float2(m2, sum[r]);
       }
     }
   }
