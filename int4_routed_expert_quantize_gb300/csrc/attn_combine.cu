@@ -11,7 +11,11 @@ namespace coli {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kFew = 4, kMany = 8;  // parts a row has on its way: a cut unit's are few, a prefix's many
+// Parts a row has on its way.  More hide more of the L2's latency where the grid is small, and cost registers, so warps,
+// where it is large.  us with 4 / 8 / 16 on their way: one token's decode 10.6 / 10.2 / 9.4, 13 x 5 tokens
+// 15.7 / 15.8 / 16.1, mixed batch 139 / 141 / 150; prefix with 8 / 16: 24 rows a key head 14.9 / 14.1, 32 chats
+// 48.1 / 47.1, 256 sequences 303 / 316.
+constexpr int kSmallCombine = 1024, kSmallJoin = 4096;  // rows (tokens x heads) up to which 16 are taken
 
 // running join of one row over a warp; lane holds D/32 consecutive values
 template <int D, int Loads>
@@ -170,7 +174,7 @@ __device__ __noinline__ void clear_flags(const AttnParams& p) {
   if (threadIdx.x == 0) p.redo_any[0] = p.redo_any[1] = 0;
 }
 
-template <class T, int D>
+template <class T, int D, int Loads>
 __global__ void __launch_bounds__(kWarps * 32) attn_combine_kernel(const AttnParams p, const AttnLists lists) {
   griddep_wait();
   griddep_launch_dependents();
@@ -186,7 +190,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_combine_kernel(const AttnPar
       const int row = block / l.ctas * l.block_rows + i;
       const int tok = row / p.group;
       if (tok >= r.tokens) break;
-      Join<D, kFew> j;
+      Join<D, Loads> j;
       j.add(l.part_o, l.part_ml, r.last_cta - r.first_cta + 1, lane, [&](int c) {
         return ((int64_t)(r.first_cta + c) * 2 + (c == 0 ? 1 : 0)) * l.rows + row;
       });
@@ -200,7 +204,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_combine_kernel(const AttnPar
     const int token = (int)(k / p.n_kv), b = seq_of(p, token, lane);
     const SeqInfo s = seq_info(p, b);
     for (int g = 0; g < p.group; ++g) {
-      Join<D, kFew> j;
+      Join<D, Loads> j;
       const int hq = (int)(k % p.n_kv) * p.group + g;
       add_direct<T, D>(j, p, s, b, token - s.start, hq, qf[warp], lane);
       j.template write<T>(p, token, hq, lane);
@@ -272,7 +276,7 @@ __device__ __forceinline__ void add_parts(J& j, const AttnParams& p, const Parts
 // runs and looks its rows up meanwhile (that launch had waited for whatever wrote the lengths).  SAME: that
 // launch made both, so all results wait for it.  Otherwise the launch before that one made the own parts,
 // which are read ahead as well.
-template <class T, int D, bool SAME>
+template <class T, int D, bool SAME, int Loads>
 __global__ void __launch_bounds__(kWarps * 32)
     attn_join_kernel(const AttnParams own, int own_rows, const AttnParams shared, int shared_ctas) {
   const int lane = threadIdx.x & 31;
@@ -302,7 +306,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   const bool redo = __ldcg(own.redo_any) != 0;
   const uint32_t per = __ldcg(own.seq_pos + n_lists(own) + 1), near_at = has_own ? __ldcg(own.seq_pos + b) : 0;
   const uint32_t far_at = SAME ? __ldcg(own.seq_pos + own.n_seqs) : 0;
-  Join<D, kMany> j;
+  Join<D, Loads> j;
   if (live && has_own) {
     if (redo && __ldcg(own.redo + (int64_t)token * own.n_kv + head)) {
       __shared__ float qf[kWarps][D];
@@ -341,8 +345,17 @@ template <class T, int D>
 cudaError_t join(const AttnParams& own, int own_rows, const AttnParams& shared, bool same, int shared_ctas,
                  cudaStream_t stream) {
   const dim3 grid((unsigned)(((int64_t)own.n_tokens * own.n_q + kWarps - 1) / kWarps));
-  return same ? go(attn_join_kernel<T, D, true>, grid, stream, own, own_rows, shared, shared_ctas)
-              : go(attn_join_kernel<T, D, false>, grid, stream, own, own_rows, shared, shared_ctas);
+  const bool small = (int64_t)own.n_tokens * own.n_q <= kSmallJoin;
+  return same    ? go(attn_join_kernel<T, D, true, 16>, grid, stream, own, own_rows, shared, shared_ctas)
+         : small ? go(attn_join_kernel<T, D, false, 16>, grid, stream, own, own_rows, shared, shared_ctas)
+                 : go(attn_join_kernel<T, D, false, 8>, grid, stream, own, own_rows, shared, shared_ctas);
+}
+
+template <class T, int D>
+cudaError_t combine(const AttnParams& p, const AttnLists& lists, cudaStream_t stream) {
+  const dim3 grid(lists.l[0].blocks + lists.l[1].blocks);
+  return (int64_t)p.n_tokens * p.n_q <= kSmallCombine ? go(attn_combine_kernel<T, D, 16>, grid, stream, p, lists)
+                                                      : go(attn_combine_kernel<T, D, 4>, grid, stream, p, lists);
 }
 
 }  // namespace
@@ -353,12 +366,9 @@ AttnList attn_list(const AttnParams& p, int rows, int ctas) {
 }
 
 cudaError_t launch_attn_combine(const AttnParams& p, const AttnLists& lists, int dtype, cudaStream_t stream) {
-  const dim3 grid(lists.l[0].blocks + lists.l[1].blocks);
   if (dtype == COLI_ATTN_BF16)
-    return p.head_dim == 64 ? go(attn_combine_kernel<Bf16, 64>, grid, stream, p, lists)
-                            : go(attn_combine_kernel<Bf16, 128>, grid, stream, p, lists);
-  return p.head_dim == 64 ? go(attn_combine_kernel<Fp16, 64>, grid, stream, p, lists)
-                          : go(attn_combine_kernel<Fp16, 128>, grid, stream, p, lists);
+    return p.head_dim == 64 ? combine<Bf16, 64>(p, lists, stream) : combine<Bf16, 128>(p, lists, stream);
+  return p.head_dim == 64 ? combine<Fp16, 64>(p, lists, stream) : combine<Fp16, 128>(p, lists, stream);
 }
 
 cudaError_t launch_attn_join(const AttnParams& own, int own_rows, const AttnParams& shared, bool same_list,
