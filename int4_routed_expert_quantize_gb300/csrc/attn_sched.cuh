@@ -154,6 +154,15 @@ __device__ __forceinline__ void weigh(const AttnParams& p, uint32_t* pos) {
   __syncthreads();
 }
 
+__device__ __forceinline__ uint32_t warp_scan(uint32_t v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t u = __shfl_up_sync(FULL, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+
 // Walks a CTA's stretch; one warp, all lanes alike.
 template <int KT>
 struct Walk {
@@ -161,28 +170,26 @@ struct Walk {
   Tiles<KT> t;
   uint32_t begin, end, per, at;  // at: the current unit's first position
   int b, blk, head;
-  // pos as weigh() left it; becomes the sequences' first positions
-  __device__ __forceinline__ void start(const AttnParams& p, uint32_t* pos, int lane) {
-    uint32_t run = 0;
-    if (lane == 0) pos[0] = 0;
-    const int ns = n_lists(p);
-#pragma unroll 1
-    for (int b0 = 0; b0 < ns; b0 += 32) {
-      uint32_t v = b0 + lane < ns ? pos[b0 + lane + 1] : 0;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t u = __shfl_up_sync(FULL, v, o);
-        if (lane >= o) v += u;
-      }
-      if (b0 + lane < ns) pos[b0 + lane + 1] = run + v;
-      run += __shfl_sync(FULL, v, 31);
-    }
-    __syncwarp();
+  __device__ __forceinline__ void cut(const AttnParams& p, uint32_t run) {
     per = max(1u, (run + gridDim.x - 1) / gridDim.x);
     begin = min(blockIdx.x * per, run);
     end = min(begin + per, run);
     b = blk = head = 0;
     at = end;  // nothing to do
+  }
+  // More than 32 sequences: pos as weigh() left it; becomes their first positions.
+  __device__ __forceinline__ void start(const AttnParams& p, uint32_t* pos, int lane) {
+    const int ns = n_lists(p);
+    uint32_t run = 0;
+    if (lane == 0) pos[0] = 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < ns; b0 += 32) {
+      const uint32_t v = warp_scan(b0 + lane < ns ? pos[b0 + lane + 1] : 0, lane);
+      if (b0 + lane < ns) pos[b0 + lane + 1] = run + v;
+      run += __shfl_sync(FULL, v, 31);
+    }
+    __syncwarp();
+    cut(p, run);
     if (blockIdx.x == 0 && p.seq_pos) {
 #pragma unroll 1
       for (int i = lane; i <= ns; i += 32) p.seq_pos[i] = pos[i];
@@ -196,8 +203,64 @@ struct Walk {
       if (pos[mid] <= begin) b = mid;
       else hi = mid - 1;
     }
-    at = pos[b];
     s = seq_info(p, b);
+    find_block(p, pos[b], lane);
+  }
+  // Up to 32 sequences: one a lane, nothing through shared memory, and the other warps need not wait.
+  __device__ __forceinline__ void start_few(const AttnParams& p, int lane) {
+    const int ns = n_lists(p);
+    SeqInfo mine = {0, 0, 0, true};
+    if (lane < ns) {
+      mine = seq_info(p, lane);
+      if (blockIdx.x == 0) seq_check(p, lane);
+    }
+    const int nb = (mine.n + p.block_tokens - 1) / p.block_tokens;
+    uint32_t w = 0;
+#pragma unroll 1
+    for (int i = 0; i < nb && nb <= kSerialBlocks; ++i) {
+      Tiles<KT> x;
+      x.set(p, mine, i);
+      w += x.count + p.unit_cost;
+    }
+    unsigned many = __ballot_sync(FULL, nb > kSerialBlocks);
+#pragma unroll 1
+    for (; many; many &= many - 1) {
+      const int l = __ffs(many) - 1;
+      take_lane(mine, l);
+      const int n = __shfl_sync(FULL, nb, l);
+      uint32_t sum = 0;
+#pragma unroll 1
+      for (int i = lane; i < n; i += 32) {
+        Tiles<KT> x;
+        x.set(p, s, i);
+        sum += x.count + p.unit_cost;
+      }
+      sum = __reduce_add_sync(FULL, sum);
+      if (lane == l) w = sum;
+    }
+    w *= p.n_kv;
+    const uint32_t v = warp_scan(w, lane);
+    cut(p, __shfl_sync(FULL, v, 31));
+    if (blockIdx.x == 0 && p.seq_pos) {
+      if (lane <= ns && lane < 31) p.seq_pos[lane] = v - w;
+      if (lane == 31) p.seq_pos[31] = v - w, p.seq_pos[32] = v;
+      __syncwarp();
+      if (lane == 0) p.seq_pos[ns + 1] = per;
+    }
+    if (begin >= end) return;
+    b = __ffs(__ballot_sync(FULL, begin < v)) - 1;
+    take_lane(mine, b);
+    find_block(p, __shfl_sync(FULL, v - w, b), lane);
+  }
+  __device__ __forceinline__ void take_lane(const SeqInfo& mine, int l) {
+    s.start = __shfl_sync(FULL, mine.start, l);
+    s.n = __shfl_sync(FULL, mine.n, l);
+    s.len = __shfl_sync(FULL, mine.len, l);
+    s.causal = __shfl_sync(FULL, (int)mine.causal, l);
+  }
+  // the block and key head at `begin` in sequence b, whose first position is `first`
+  __device__ __forceinline__ void find_block(const AttnParams& p, uint32_t first, int lane) {
+    at = first;
     const int nb = (s.n + p.block_tokens - 1) / p.block_tokens;
 #pragma unroll 1
     for (int blk0 = 0; blk0 < nb && nb > 1; blk0 += 32) {
@@ -206,12 +269,7 @@ struct Walk {
         t.set(p, s, blk0 + lane);
         w = (t.count + p.unit_cost) * p.n_kv;
       }
-      uint32_t v = w;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t u = __shfl_up_sync(FULL, v, o);
-        if (lane >= o) v += u;
-      }
+      const uint32_t v = warp_scan(w, lane);
       const unsigned in = __ballot_sync(FULL, begin < at + v);
       if (in) {
         const int l = __ffs(in) - 1;

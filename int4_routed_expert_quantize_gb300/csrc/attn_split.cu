@@ -190,11 +190,13 @@ __global__ void __launch_bounds__(SplitCfg<D, RG>::threads, SplitCfg<D, RG>::cta
   griddep_wait();
   griddep_launch_dependents();
   uint32_t* weights = reinterpret_cast<uint32_t*>(smem);  // in the ring, before the first copy
-  weigh<kSplitKeys>(p, weights);
+  const bool few = n_lists(p) <= 32;
+  if (few) __syncthreads();
+  else weigh<kSplitKeys>(p, weights);
 
   if (warp == C::warps) {  // ---- copies
     Walk<kSplitKeys> walk;
-    walk.start(p, weights, lane);
+    few ? walk.start_few(p, lane) : walk.start(p, weights, lane);
     if (lane == 0) p.rec[blockIdx.x].first_cta = -1;
     __syncwarp();
     fence_proxy_async_smem();

@@ -189,7 +189,9 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
   griddep_launch_dependents();
   uint32_t* weights = reinterpret_cast<uint32_t*>(smem);  // in the ring, before the first copy
   tc_fence_before();
-  weigh<kTileKeys>(p, weights);
+  const bool few = n_lists(p) <= 32;
+  if (few) __syncthreads();
+  else weigh<kTileKeys>(p, weights);
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int half_tokens = p.block_tokens / 2;  // tokens of one row tile
@@ -201,7 +203,7 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
     bool ok = true;
     if (warp == 9) {  // ---- copies
       Walk<kTileKeys> walk;
-      walk.start(p, weights, lane);
+      few ? walk.start_few(p, lane) : walk.start(p, weights, lane);
       if (lane == 0) p.rec[blockIdx.x].first_cta = -1;
       __syncwarp();
       fence_proxy_async_smem();
