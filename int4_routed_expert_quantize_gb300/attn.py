@@ -7,7 +7,8 @@
     o = eng.window(cache, batch, q, window=4096, sinks=4)
     o = eng.prefix(cache, batch, prefix_table, prefix_len, q)
 
-Argument marshalling only; every step runs in the library's CUDA kernels.
+Argument marshalling only (the three calls' in _attn_py, csrc/attn_py.cpp); every step runs in the library's CUDA
+kernels.
 """
 import ctypes
 import math
@@ -39,15 +40,16 @@ class AttnBatch(ctypes.Structure):
                 ("max_pages", _i), ("n_tokens", _i), ("max_q", _i)]
 
 
-# torch.cuda.current_stream() makes a Stream object on every call (3 us on a Grace core, this 0.1 us)
-_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
-    lambda device: torch.cuda.current_stream(device).cuda_stream
+class Engine(ctypes.Structure):  # csrc/attn_py.cpp
+    _fields_ = [("handle", _vp), ("n_q", _i), ("n_kv", _i), ("head_dim", _i), ("dtype", _i), ("device", _i),
+                ("scale", _f)]
 
-_lib = None
+
+_lib = _calls = None
 
 
 def lib():
-    global _lib
+    global _lib, _calls
     L = coli.lib()
     if _lib is not L:
         L.coli_attn_create.argtypes = [ctypes.POINTER(AttnConfig), ctypes.POINTER(_vp)]
@@ -61,7 +63,8 @@ def lib():
         L.coli_attn_prefix.argtypes = [_vp, _vp, _vp, _vp, _i, _vp, _vp, _i64, _f, _vp, _i64, _vp, _vp]
         L.coli_attn_status.argtypes = [_vp, _vp]
         L.coli_attn_launches.argtypes = [_vp, _i, _i]
-        _lib = L
+        from . import _attn_py
+        _lib, _calls = L, _attn_py
     return L
 
 
@@ -110,11 +113,12 @@ class KvCache:
         h = _vp()
         coli._check(lib().coli_attn_cache_bind(engine.h, ctypes.byref(c), ctypes.byref(h)), "coli_attn_cache_bind")
         self.h = h
+        self.ref = h.value
 
     def close(self):
         if getattr(self, "h", None) is not None and self.h.value:
             lib().coli_attn_cache_release(self.h)
-            self.h = _vp()
+            self.h, self.ref = _vp(), 0
 
     def __del__(self):
         if sys.is_finalizing():  # the process is exiting: no native calls during teardown
@@ -123,6 +127,20 @@ class KvCache:
             self.close()
         except Exception:
             pass
+
+
+def _handle(stream):
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _done(out, given, stream, what):
+    """a call's output, or the error that its status stands for; a new output made on another stream than the
+    current one is kept from reuse until that stream is done with it"""
+    if out.__class__ is int:
+        raise coli.ColiError(out, what)
+    if given is None and out is not None and isinstance(stream, torch.cuda.Stream):
+        out.record_stream(stream)
+    return out
 
 
 class PagedAttention:
@@ -149,101 +167,45 @@ class PagedAttention:
         self.max_tokens, self.max_seqs, self.rot_dim = max_tokens, max_seqs, rot
         self.scale = 1.0 / math.sqrt(head_dim)
         self.device = torch.cuda.current_device()
-        L = lib()
-        self._c_append, self._c_window, self._c_prefix = L.coli_attn_append, L.coli_attn_window, L.coli_attn_prefix
+        self.c = Engine(h, n_q, n_kv, head_dim, DTYPES[dtype], self.device, self.scale)
+        self.ref = ctypes.addressof(self.c)
 
     def close(self):
         if getattr(self, "h", None) is not None and self.h.value:
             lib().coli_attn_destroy(self.h)
-            self.h = _vp()
+            self.h = self.c.handle = _vp()
 
     __del__ = KvCache.__del__
 
     def bind_cache(self, k_cache, v_cache):
         return KvCache(self, k_cache, v_cache)
 
-    # The calls below take a few microseconds of host time, most of it the launches: what can be looked up
-    # once is, and a new output's layout is not checked again.
-
-    def _heads(self, t, heads, batch, what):
-        """the token stride of t [n_tokens, heads, head_dim]"""
-        D, n = self.head_dim, batch.n_tokens
-        if t.dtype is not self.dtype or t.shape != (n, heads, D) or not t.is_cuda:
-            raise ValueError(f"{what}: [{n}, {heads}, {D}] of {self.dtype} on the device")
-        st, sh, sd = t.stride()
-        if sd != 1 or (sh != D and heads > 1):
-            raise ValueError(f"{what}: a token's heads are contiguous")
-        return st if n > 1 else heads * D
-
-    def _stream(self, stream):
-        if stream is None:
-            return _raw_stream(self.device)
-        return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else stream
-
-    def _out(self, out, batch, stream, like):
-        """the output and its token stride"""
-        if out is not None:
-            return out, self._heads(out, self.n_q, batch, "out")
-        if like.is_contiguous():  # the quicker call
-            out = torch.empty_like(like)
-        else:
-            out = torch.empty((batch.n_tokens, self.n_q, self.head_dim), dtype=self.dtype, device=like.device)
-        if stream is not None and isinstance(stream, torch.cuda.Stream):
-            out.record_stream(stream)
-        return out, self.n_q * self.head_dim
-
-    def _lse(self, lse, batch):
-        if lse.dtype is not torch.float32 or lse.shape != (batch.n_tokens, self.n_q) or not lse.is_contiguous():
-            raise ValueError(f"lse: contiguous float32 [{batch.n_tokens}, {self.n_q}]")
-        return lse.data_ptr()
-
     def append(self, cache, batch, k, v, q=None, q_out=None, pos_base=None, stream=None):
         """Stores the batch's new keys (rotated) and values in the cache; rotates q into q_out (new by
-        default, q itself for in place) and returns it.  pos_base: int32 [1] on the device, added to the
-        positions for the rotation (the length of a shared prefix).  coli_attn_append"""
-        ks, vs = self._heads(k, self.n_kv, batch, "k"), self._heads(v, self.n_kv, batch, "v")
-        qp = op = base = None
-        qs = os = 0
-        if q is not None:
-            qs = self._heads(q, self.n_q, batch, "q")
-            q_out, os = self._out(q_out, batch, stream, q)
-            qp, op = q.data_ptr(), q_out.data_ptr()
-        if pos_base is not None:
-            base = _int32(pos_base, 1, "pos_base").data_ptr()
-        rc = self._c_append(self.h, cache.h, batch.ref, qp, qs, k.data_ptr(), ks, v.data_ptr(), vs, op, os, base,
-                            self._stream(stream))
-        if rc:
-            raise coli.ColiError(rc, "coli_attn_append")
-        return q_out
+        default, q itself for in place) and returns it.  k, v [n_tokens, n_kv, head_dim] and q [n_tokens, n_q,
+        head_dim] may be slices of a wider row.  pos_base: int32 [1] on the device, added to the positions
+        for the rotation (the length of a shared prefix).  coli_attn_append"""
+        out = _calls.append(self.ref, cache.ref, batch.ref, k, v, q, q_out, pos_base,
+                            stream if stream is None else _handle(stream))
+        return out if stream is None and out.__class__ is not int else _done(out, q_out, stream, "coli_attn_append")
 
     def window(self, cache, batch, q, window=-1, sinks=0, scale=None, out=None, lse=None, stream=None):
         """Causal attention over the last `window` keys (all with -1) and the first `sinks` ones ->
         [n_tokens, n_q, head_dim]; lse: float32 [n_tokens, n_q] to fill, or None.  coli_attn_window"""
-        qs = self._heads(q, self.n_q, batch, "q")
-        out, os = self._out(out, batch, stream, q)
-        rc = self._c_window(self.h, cache.h, batch.ref, q.data_ptr(), qs, window, sinks,
-                            self.scale if scale is None else scale, out.data_ptr(), os,
-                            None if lse is None else self._lse(lse, batch), self._stream(stream))
-        if rc:
-            raise coli.ColiError(rc, "coli_attn_window")
-        return out
+        o = _calls.window(self.ref, cache.ref, batch.ref, q, window, sinks, scale, out, lse,
+                          stream if stream is None else _handle(stream))
+        return o if stream is None and o.__class__ is not int else _done(o, out, stream, "coli_attn_window")
 
     def prefix(self, cache, batch, prefix_table, prefix_len, q, scale=None, out=None, lse=None, stream=None):
         """Attention of a batch behind a shared prefix: prefix_len (int32 [1] on the device) tokens in the
         pages prefix_table (int32 [pages]), then each sequence's own cache.  coli_attn_prefix"""
-        qs = self._heads(q, self.n_q, batch, "q")
-        out, os = self._out(out, batch, stream, q)
-        _int32(prefix_table, 1, "prefix_table"), _int32(prefix_len, 1, "prefix_len")
-        rc = self._c_prefix(self.h, cache.h, batch.ref, prefix_table.data_ptr(), prefix_table.shape[0],
-                            prefix_len.data_ptr(), q.data_ptr(), qs, self.scale if scale is None else scale,
-                            out.data_ptr(), os, None if lse is None else self._lse(lse, batch), self._stream(stream))
-        if rc:
-            raise coli.ColiError(rc, "coli_attn_prefix")
-        return out
+        o = _calls.prefix(self.ref, cache.ref, batch.ref, prefix_table, prefix_len, q, scale, out, lse,
+                          stream if stream is None else _handle(stream))
+        return o if stream is None and o.__class__ is not int else _done(o, out, stream, "coli_attn_prefix")
 
     def status(self, stream=None):
         """device status of earlier calls (coli_attn_status); 0 when all went well"""
-        return int(lib().coli_attn_status(self.h, self._stream(stream)))
+        return int(lib().coli_attn_status(self.h, coli._stream(stream)))
 
     def launches(self, op, max_q):
         """kernels one call launches; op "append", "window" or "prefix" (coli_attn_launches)"""
