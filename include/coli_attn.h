@@ -108,8 +108,10 @@ int coli_attn_append(coli_attn* h, const coli_attn_kv* kv, const coli_attn_batch
 
 /* out_dev [n_tokens, n_q, head_dim] = attention of the batch's queries over its cache: query p sees
  * key j when j <= p and (p - j < window or j < sinks).  window < 0: all keys up to p; window = 0:
- * the sinks alone.  scale > 0.  lse_dev [n_tokens, n_q]: natural log-sum-exp of the scaled scores, or
- * NULL.  Strides as in append.  q_dev must not overlap out_dev. */
+ * the sinks alone.  sinks >= 0, scale > 0.  lse_dev [n_tokens, n_q]: natural log-sum-exp of the scaled scores, or
+ * NULL.  Strides as in append.  q_dev must not overlap out_dev (their rows may lie
+ * between one another).  EUNSUPPORTED: the batch's key tiles could exceed 2^31 (tokens / 2, sequences and
+ * key heads times max_pages * page / 64, or the window: split the call). */
 int coli_attn_window(coli_attn* h, const coli_attn_kv* kv, const coli_attn_batch* batch,
                      const void* q_dev, int64_t q_stride, int window, int sinks, float scale,
                      void* out_dev, int64_t out_stride, float* lse_dev, void* stream);

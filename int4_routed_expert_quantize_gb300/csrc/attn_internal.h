@@ -13,6 +13,7 @@ namespace coli {
 constexpr int kAttnMaxSeqs = 4096;
 constexpr int kAttnMaxGroup = 64;     // query heads per key head
 constexpr int kAttnPrefixRows = 8;    // tokens per sequence the prefix workspace is sized for
+constexpr int kAttnMaxPairs = 64;     // rotated pairs of a head
 constexpr int kAttnNoWindow = 1 << 30;
 constexpr int kSplitUnitCost = 1;     // AttnParams::unit_cost of the two kernels
 constexpr int kTileUnitCost = 3;

@@ -6,7 +6,6 @@
 #include <cmath>
 #include <mutex>
 #include <new>
-#include <vector>
 
 #include "attn_internal.h"
 
@@ -15,7 +14,7 @@ using namespace coli;
 struct coli_attn {
   coli_attn_config cfg{};
   int device = 0, num_sms = 0, page_shift = 0, prefix_tokens = 0;
-  std::vector<void*> allocs;
+  char* arena = nullptr;  // the workspace: one allocation
   float* part_o = nullptr;
   float2* part_ml = nullptr;
   AttnRec* rec = nullptr;
@@ -24,7 +23,6 @@ struct coli_attn {
   float* part_o2 = nullptr;
   float2* part_ml2 = nullptr;
   AttnRec* rec2 = nullptr;
-  uint32_t* seq_pos2 = nullptr;
   float *dense_o = nullptr, *dense_o2 = nullptr;
   float2 *dense_ml = nullptr, *dense_ml2 = nullptr;
   uint8_t* redo = nullptr;
@@ -77,21 +75,39 @@ bool cache_map(CUtensorMap* map, const void* base, const coli_attn_kv& kv, int64
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// carves `count` elements off the arena at byte `at`, 256-byte aligned
 template <class T>
-int dalloc(coli_attn* h, T** p, size_t count) {
-  void* q = nullptr;
-  if (cudaMalloc(&q, (count ? count : 1) * sizeof(T)) != cudaSuccess) {
-    cudaGetLastError();
-    return COLI_ENOMEM;
-  }
-  h->allocs.push_back(q);
-  *p = static_cast<T*>(q);
-  return COLI_OK;
+void carve(T** p, char* arena, size_t* at, size_t count) {
+  *p = reinterpret_cast<T*>(arena + *at);
+  *at += (count * sizeof(T) + 255) / 256 * 256;
 }
 
-void free_all(coli_attn* h) {
-  for (void* p : h->allocs) cudaFree(p);
-  h->allocs.clear();
+// the workspace in the arena (nullptr: its size alone); what has to be zero comes first, *zero bytes of it
+size_t lay_out(coli_attn* h, char* arena, size_t* zero) {
+  const coli_attn_config& c = h->cfg;
+  // partials: two per CTA of the split kernel (2 CTAs an SM, up to 64 rows) and of the tensor-memory kernel
+  const size_t D = c.head_dim, ctas = 2 * (size_t)h->num_sms, rows = 2 * ctas * 64,
+               rows2 = 2 * (size_t)h->num_sms * kTileRows;
+  // the prefix call keeps every row twice
+  const size_t dense = (size_t)h->prefix_tokens * c.n_q;
+  size_t at = 0;
+  carve(&h->status, arena, &at, 4);
+  carve(&h->redo_any, arena, &at, 2);
+  carve(&h->redo, arena, &at, (size_t)c.max_tokens * c.n_kv);
+  *zero = at;
+  carve(&h->turn, arena, &at, kAttnMaxPairs);
+  carve(&h->rec, arena, &at, ctas);
+  carve(&h->rec2, arena, &at, ctas);
+  carve(&h->seq_pos, arena, &at, (size_t)c.max_seqs + 3);
+  carve(&h->part_ml, arena, &at, rows);
+  carve(&h->part_ml2, arena, &at, rows2);
+  carve(&h->dense_ml, arena, &at, dense);
+  carve(&h->dense_ml2, arena, &at, dense);
+  carve(&h->part_o, arena, &at, rows * D);
+  carve(&h->part_o2, arena, &at, rows2 * D);
+  carve(&h->dense_o, arena, &at, dense * D);
+  carve(&h->dense_o2, arena, &at, dense * D);
+  return at;
 }
 
 constexpr int kMaxDevices = 64;
@@ -169,7 +185,7 @@ bool query_map(CUtensorMap* map, const coli_attn* h, const void* q, int64_t q_st
 
 // switches a launch's parameters to the tensor-memory kernel's workspace and blocks
 void use_tile(const coli_attn* h, AttnParams* p) {
-  p->part_o = h->part_o2, p->part_ml = h->part_ml2, p->rec = h->rec2, p->seq_pos = h->seq_pos2;
+  p->part_o = h->part_o2, p->part_ml = h->part_ml2, p->rec = h->rec2, p->seq_pos = nullptr;
   p->unit_cost = kTileUnitCost;
   p->block_tokens = tile_block_tokens(p->group);
 }
@@ -179,16 +195,33 @@ int rows_of(const coli_attn* h, int64_t tokens) {
   return split_rows((int)(rows < 64 ? rows : 64));
 }
 
+// Whether rows of `wa` elements every `sa` from a and of `wb` every `sb` from b (n of either) share memory.  Rows of the
+// same stride may lie between one another (slices of one wider row).
+bool collide(const void* a, int64_t sa, int64_t wa, const void* b, int64_t sb, int64_t wb, int64_t n) {
+  const int64_t x = (int64_t)((uintptr_t)a / 2), y = (int64_t)((uintptr_t)b / 2);
+  if (x + (n - 1) * sa + wa <= y || y + (n - 1) * sb + wb <= x) return false;
+  if (sa != sb) return true;
+  const int64_t gap = (((y - x) % sa) + sa) % sa;  // b's row starts so far behind one of a's
+  return gap < wa || gap + wb > sa;
+}
+
 int query_args(const coli_attn* h, int64_t n_tokens, const void* q, int64_t q_stride, const void* out,
                int64_t out_stride, float scale) {
   const int64_t width = (int64_t)h->cfg.n_q * h->cfg.head_dim;
   if (!q || !out || misaligned(q, q_stride) || misaligned(out, out_stride) || q_stride < width ||
       out_stride < width || !(scale > 0.f) || !std::isfinite(scale))
     return COLI_EINVAL;
-  const char *qa = static_cast<const char*>(q), *oa = static_cast<const char*>(out);
-  // rows may interleave (slices of one buffer); the same start cannot be meant
-  (void)n_tokens;
-  return qa == oa ? COLI_EINVAL : COLI_OK;
+  return collide(q, q_stride, width, out, out_stride, width, n_tokens) ? COLI_EINVAL : COLI_OK;
+}
+
+// the work list's positions are 32-bit: its length is bounded by the page table's width (or the window)
+int list_fits(const coli_attn_batch* b, const AttnParams& p, int64_t pages, int keys) {
+  const int64_t len = pages << p.page_shift;
+  int64_t span = len;
+  if (p.window < kAttnNoWindow && p.window + (int64_t)p.block_tokens + p.sinks + 2 * keys < len)
+    span = p.window + (int64_t)p.block_tokens + p.sinks + 2 * keys;
+  const int64_t units = ((int64_t)b->n_tokens / p.block_tokens + b->n_seqs + 1) * p.n_kv;
+  return units <= 0x7FFFFFFF / (span / keys + 2 + p.unit_cost) ? COLI_OK : COLI_EUNSUPPORTED;
 }
 
 }  // namespace
@@ -205,10 +238,10 @@ extern "C" int coli_attn_create(const coli_attn_config* cfg, coli_attn** out) {
   if ((c.head_dim != 64 && c.head_dim != 128) || (c.dtype != COLI_ATTN_BF16 && c.dtype != COLI_ATTN_FP16) ||
       c.n_q / c.n_kv > kAttnMaxGroup || c.rot_dim > c.head_dim || c.rot_dim % 16)
     return COLI_EUNSUPPORTED;
-  int shift = 0;
+  if (c.page < 16 || c.page > 256 || (c.page & (c.page - 1))) return COLI_EUNSUPPORTED;
+  int shift = 4;
   while ((1 << shift) < c.page) ++shift;
-  if ((1 << shift) != c.page || c.page < 16 || c.page > 256) return COLI_EUNSUPPORTED;
-  std::vector<uint64_t> turn;
+  uint64_t turn[kAttnMaxPairs] = {};
   for (int i = 0; i < c.rot_dim / 2; ++i) {
     const long double f = c.inv_freq ? (long double)c.inv_freq[i]
                                      : powl((long double)c.rope_base, -2.0L * i / c.rot_dim);
@@ -216,7 +249,7 @@ extern "C" int coli_attn_create(const coli_attn_config* cfg, coli_attn** out) {
     long double t = f / 6.283185307179586476925286766559005768L;
     t -= floorl(t);  // whole turns do not count
     long double v = floorl(t * 18446744073709551616.0L + 0.5L);
-    turn.push_back(v >= 18446744073709551616.0L ? 0 : (uint64_t)v);
+    turn[i] = v >= 18446744073709551616.0L ? 0 : (uint64_t)v;
   }
 
   coli_attn* h = new (std::nothrow) coli_attn();
@@ -224,46 +257,30 @@ extern "C" int coli_attn_create(const coli_attn_config* cfg, coli_attn** out) {
   h->cfg = c;
   h->cfg.inv_freq = nullptr;  // read above; not kept
   h->page_shift = shift;
-  cudaDeviceProp prop;
   int rc = COLI_OK;
-  if (cudaGetDevice(&h->device) != cudaSuccess || cudaGetDeviceProperties(&prop, h->device) != cudaSuccess ||
-      configure_device(h->device) != cudaSuccess) {
-    cudaGetLastError();
+  if (cudaGetDevice(&h->device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess ||
+      configure_device(h->device) != cudaSuccess)
     rc = COLI_ECUDA;
-  }
   if (!rc) {
-    h->num_sms = prop.multiProcessorCount;
-    const size_t D = c.head_dim, ctas = (size_t)2 * h->num_sms;
-    // partials: two per CTA of the split kernel (2 CTAs an SM, up to 64 rows) and of the
-    // tensor-memory kernel
-    const size_t rows = 2 * ctas * 64, rows2 = 2 * (size_t)h->num_sms * kTileRows;
-    // the prefix call keeps every row twice: up to kAttnPrefixRows tokens a sequence
     const int64_t pt = (int64_t)kAttnPrefixRows * c.max_seqs;
     h->prefix_tokens = (int)(pt < c.max_tokens ? pt : c.max_tokens);
-    const size_t dense = (size_t)h->prefix_tokens * c.n_q;
-    if (!rc) rc = dalloc(h, &h->part_o, rows * D);
-    if (!rc) rc = dalloc(h, &h->part_ml, rows);
-    if (!rc) rc = dalloc(h, &h->rec, ctas);
-    if (!rc) rc = dalloc(h, &h->seq_pos, c.max_seqs + 3);
-    if (!rc) rc = dalloc(h, &h->part_o2, rows2 * D);
-    if (!rc) rc = dalloc(h, &h->part_ml2, rows2);
-    if (!rc) rc = dalloc(h, &h->rec2, ctas);
-    if (!rc) rc = dalloc(h, &h->seq_pos2, c.max_seqs + 3);
-    if (!rc) rc = dalloc(h, &h->dense_o, dense * D);
-    if (!rc) rc = dalloc(h, &h->dense_ml, dense);
-    if (!rc) rc = dalloc(h, &h->dense_o2, dense * D);
-    if (!rc) rc = dalloc(h, &h->dense_ml2, dense);
-    if (!rc) rc = dalloc(h, &h->redo, (size_t)c.max_tokens * c.n_kv);
-    if (!rc) rc = dalloc(h, &h->redo_any, 2);
-    if (!rc) rc = dalloc(h, &h->turn, turn.size());
-    if (!rc) rc = dalloc(h, &h->status, 4);
-    if (!rc && ((!turn.empty() && cudaMemcpy(h->turn, turn.data(), turn.size() * 8, cudaMemcpyHostToDevice) != cudaSuccess) ||
-                cudaMemset(h->status, 0, 16) != cudaSuccess || cudaMemset(h->redo_any, 0, 8) != cudaSuccess ||
-                cudaMemset(h->redo, 0, (size_t)c.max_tokens * c.n_kv) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess))
-      rc = COLI_ECUDA;
+    size_t zero;
+    void* p = nullptr;
+    if (cudaMalloc(&p, lay_out(h, nullptr, &zero)) != cudaSuccess) {
+      rc = COLI_ENOMEM;
+    } else {
+      h->arena = static_cast<char*>(p);
+      lay_out(h, h->arena, &zero);
+      if (cudaMemset(h->arena, 0, zero) != cudaSuccess ||
+          cudaMemcpy(h->turn, turn, sizeof(turn), cudaMemcpyHostToDevice) != cudaSuccess ||
+          cudaStreamSynchronize(cudaStreamLegacy) != cudaSuccess)
+        rc = COLI_ECUDA;
+    }
   }
   if (rc) {
-    free_all(h);
+    cudaGetLastError();
+    if (h->arena) cudaFree(h->arena);
     delete h;
     return rc;
   }
@@ -274,7 +291,7 @@ extern "C" int coli_attn_create(const coli_attn_config* cfg, coli_attn** out) {
 extern "C" void coli_attn_destroy(coli_attn* h) {
   if (!h) return;
   cudaDeviceSynchronize();
-  free_all(h);
+  cudaFree(h->arena);
   delete h;
 }
 
@@ -321,7 +338,9 @@ extern "C" int coli_attn_append(coli_attn* h, const coli_attn_kv* kv, const coli
     return COLI_EINVAL;
   if ((q == nullptr) != (q_out == nullptr)) return COLI_EINVAL;
   if (q && (misaligned(q, q_stride) || misaligned(q_out, q_out_stride) || q_stride < qw || q_out_stride < qw ||
-            (q == q_out && q_stride != q_out_stride)))
+            ((q != q_out || q_stride != q_out_stride) && collide(q, q_stride, qw, q_out, q_out_stride, qw, b->n_tokens)) ||
+            collide(k, k_stride, kvw, q_out, q_out_stride, qw, b->n_tokens) ||
+            collide(v, v_stride, kvw, q_out, q_out_stride, qw, b->n_tokens)))
     return COLI_EINVAL;
   AttnAppend a = {};
   a.q = q, a.k = k, a.v = v, a.q_out = q_out, a.kc = kv->c.k, a.vc = kv->c.v;
@@ -359,6 +378,8 @@ extern "C" int coli_attn_window(coli_attn* h, const coli_attn_kv* kv, const coli
     if (many) p.rows_hi = kSplitMaxRows;
     const int rows = rows_of(h, b->max_q);
     p.block_tokens = rows / p.group;
+    rc = list_fits(b, p, b->max_pages, kSplitKeys);
+    if (rc) return rc;
     e = launch_attn_split(p, kv->maps.k64, kv->maps.v64, rows, h->cfg.dtype, h->num_sms, st);
     lists.l[n++] = attn_list(p, rows, split_grid(h->num_sms));
   }
@@ -366,6 +387,8 @@ extern "C" int coli_attn_window(coli_attn* h, const coli_attn_kv* kv, const coli
     use_tile(h, &p);
     p.rows_lo = kSplitMaxRows, p.rows_hi = INT64_MAX;
     CUtensorMap qm;
+    rc = list_fits(b, p, b->max_pages, kTileKeys);
+    if (rc) return rc;
     if (!query_map(&qm, h, q, q_stride, b->n_tokens)) return COLI_ECUDA;
     e = launch_attn_tile(p, qm, kv->maps.k128, kv->maps.v128, h->cfg.dtype, h->num_sms, st);
     lists.l[n++] = attn_list(p, kTileRows, h->num_sms);
@@ -397,6 +420,9 @@ extern "C" int coli_attn_prefix(coli_attn* h, const coli_attn_kv* kv, const coli
   pre.pre_len = prefix_len, pre.pre_table = prefix_table, pre.pre_pages = prefix_pages;
   const int rows = rows_of(h, same ? b->n_tokens : b->max_q);
   own.block_tokens = pre.block_tokens = rows / own.group;
+  const int64_t pages = b->max_pages > prefix_pages ? b->max_pages : prefix_pages;
+  rc = list_fits(b, own, pages, kSplitKeys);
+  if (rc) return rc;
   cudaError_t e;
   if (same) {
     own = pre;

@@ -229,6 +229,33 @@ def test_window_strides_streams_and_graphs():
         s.check(buf, None, s.reference(window=90, sinks=2))
 
 
+def test_window_many_sequences():
+    """more than 32 sequences are placed through shared memory; long and short ones in one batch, empty ones between"""
+    r = torch.Generator().manual_seed(5)
+    lens = torch.randint(1, 400, (90,), generator=r).tolist()
+    news = [0 if i % 7 == 3 else 1 for i in range(90)]
+    Setup(news, lens, 8, 2, 64, 16, HF).window(window=150, sinks=5)
+    news = [min(m, 120) if i % 10 == 4 else n for i, (n, m) in enumerate(zip(news, lens))]
+    Setup(news, lens, 8, 2, 64, 16, HF).window(window=150, sinks=5)
+
+
+def test_window_offsets_past_32_bits():
+    """a cache whose elements do not fit 32-bit offsets: pages at its end"""
+    n, page, D = 2 ** 15 + 40, 256, 128  # 2 heads: 2^31 elements and more, 4.3 GB each
+    kc, vc = (torch.zeros((n, 2, page, D), dtype=BF, device="cuda") for _ in range(2))
+    s = Setup([1, 90], [300, 400], 6, 2, D, page, BF, junk=0.0)
+    eng = attn.PagedAttention(6, 2, D, page, max_tokens=91, max_seqs=2, rot_dim=0)
+    cache = eng.bind_cache(kc, vc)
+    far = torch.arange(n - 1, n - 1 - s.kc.shape[0], -1, device="cuda")
+    kc[far], vc[far] = s.kc, s.vc
+    batch = attn.Batch(s.batch.q_start, s.batch.kv_len, far[s.table.long()].int(), n_tokens=91, max_q=90)
+    assert torch.equal(eng.window(cache, batch, s.q, window=200, sinks=3), s.window(window=200, sinks=3))
+    k = torch.randn((91, 2, D), device="cuda").to(BF)
+    eng.append(cache, batch, k, k)
+    s.eng.append(s.cache, s.batch, k, k)
+    assert torch.equal(vc[far], s.vc) and eng.status() == 0
+
+
 def test_window_repeats_bit_for_bit():
     s = Setup([1] * 9, [4000, 1, 2, 900, 901, 77, 65, 64, 63], 48, 8, 128, 64, BF)
     a = s.window(window=2000, sinks=4)
@@ -367,6 +394,18 @@ def test_refusals():
         with pytest.raises(E) as e:
             s.eng.window(s.cache, s.batch, s.q, **kw)
         assert e.value.status == -1
+    both = torch.zeros((2, 12, 64), dtype=BF, device="cuda")  # queries and outputs between one another, then overlapping
+    s.eng.window(s.cache, s.batch, both[:, :4], out=both[:, 4:8])
+    for a, b in ((slice(0, 4), slice(2, 6)), (slice(4, 8), slice(1, 5))):
+        with pytest.raises(E):
+            s.eng.window(s.cache, s.batch, both[:, a], out=both[:, b])
+    with pytest.raises(E):  # rotated queries over the keys
+        s.eng.append(s.cache, s.batch, both[:, 4:6], both[:, 6:8], both[:, :4], q_out=both[:, 3:7])
+    page256 = attn.PagedAttention(4, 2, 64, 256, 4, 4)
+    pages = [torch.zeros((1, 2, 256, 64), dtype=BF, device="cuda") for _ in range(2)]
+    wide = torch.zeros((2, 2 ** 22 + 1), dtype=torch.int32, device="cuda")
+    with pytest.raises(E):  # a table that could hold more than 2^30 tokens
+        page256.window(page256.bind_cache(*pages), attn.Batch(s.batch.q_start, s.batch.kv_len, wide, n_tokens=2, max_q=1), s.q)
     odd = torch.zeros(2 * 4 * 64 + 1, dtype=BF, device="cuda")[1:].view(2, 4, 64)
     with pytest.raises(E):
         s.eng.window(s.cache, s.batch, odd)
