@@ -13,12 +13,13 @@ struct SeqInfo {
   bool causal;        // false: the prefix, of which every query sees every key
 };
 
+// (past L1: a line read before the launch's inputs were final must not be met again)
 __device__ __forceinline__ SeqInfo seq_info(const AttnParams& p, int b) {
   SeqInfo s;
   const bool own = b < p.n_seqs;
   s.causal = own;
   if (own) {
-    const int a = __ldg(p.q_start + b), e = __ldg(p.q_start + b + 1);
+    const int a = __ldcg(p.q_start + b), e = __ldcg(p.q_start + b + 1);
     s.start = min(max(a, 0), p.n_tokens);
     s.n = min(max(e, s.start), p.n_tokens) - s.start;
     const int64_t rows = (int64_t)s.n * p.group;
@@ -28,7 +29,7 @@ __device__ __forceinline__ SeqInfo seq_info(const AttnParams& p, int b) {
     s.n = p.n_tokens;
   }
   const int64_t cap = (int64_t)(own ? p.max_pages : p.pre_pages) << p.page_shift;
-  const int l = __ldg(own ? p.kv_len + b : p.pre_len);
+  const int l = __ldcg(own ? p.kv_len + b : p.pre_len);
   s.len = max(l, 0);
   if (s.len > cap) s.len = (int)cap;
   return s;
@@ -206,13 +207,15 @@ struct Walk {
     s = seq_info(p, b);
     find_block(p, pos[b], lane);
   }
-  // Up to 32 sequences: one a lane, nothing through shared memory, and the other warps need not wait.
-  __device__ __forceinline__ void start_few(const AttnParams& p, int lane) {
+  // Up to 32 sequences: one a lane, nothing through shared memory, and the other warps need not wait.  It is run twice:
+  // first (real = false) while the launches before this one still run, on whatever the lengths are then and with
+  // nothing written, so that its instructions are in the caches when its inputs are final.
+  __device__ __forceinline__ void start_few(const AttnParams& p, int lane, bool real) {
     const int ns = n_lists(p);
     SeqInfo mine = {0, 0, 0, true};
     if (lane < ns) {
       mine = seq_info(p, lane);
-      if (blockIdx.x == 0) seq_check(p, lane);
+      if (blockIdx.x == 0 && real) seq_check(p, lane);
     }
     const int nb = (mine.n + p.block_tokens - 1) / p.block_tokens;
     uint32_t w = 0;
@@ -241,7 +244,7 @@ struct Walk {
     w *= p.n_kv;
     const uint32_t v = warp_scan(w, lane);
     cut(p, __shfl_sync(FULL, v, 31));
-    if (blockIdx.x == 0 && p.seq_pos) {
+    if (blockIdx.x == 0 && p.seq_pos && real) {
       if (lane <= ns && lane < 31) p.seq_pos[lane] = v - w;
       if (lane == 31) p.seq_pos[31] = v - w, p.seq_pos[32] = v;
       __syncwarp();

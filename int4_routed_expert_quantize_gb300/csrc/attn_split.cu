@@ -187,16 +187,28 @@ __global__ void __launch_bounds__(SplitCfg<D, RG>::threads, SplitCfg<D, RG>::cta
     prefetch_map(&kmap);
     prefetch_map(&vmap);
   }
-  griddep_wait();
-  griddep_launch_dependents();
   uint32_t* weights = reinterpret_cast<uint32_t*>(smem);  // in the ring, before the first copy
   const bool few = n_lists(p) <= 32;
-  if (few) __syncthreads();
-  else weigh<kSplitKeys>(p, weights);
+  Walk<kSplitKeys> walk;
+  if (few) {
+    __syncthreads();
+    if (warp == C::warps) {
+#pragma unroll 1
+      for (int real = 0; real < 2; ++real) {
+        if (real) griddep_wait();
+        walk.start_few(p, lane, real);
+      }
+    } else {
+      griddep_wait();
+    }
+  } else {
+    griddep_wait();
+    weigh<kSplitKeys>(p, weights);
+  }
+  griddep_launch_dependents();
 
   if (warp == C::warps) {  // ---- copies
-    Walk<kSplitKeys> walk;
-    few ? walk.start_few(p, lane) : walk.start(p, weights, lane);
+    if (!few) walk.start(p, weights, lane);
     if (lane == 0) p.rec[blockIdx.x].first_cta = -1;
     __syncwarp();
     fence_proxy_async_smem();

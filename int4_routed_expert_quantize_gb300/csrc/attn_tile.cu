@@ -185,14 +185,23 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
     prefetch_map(&qmap), prefetch_map(&kmap), prefetch_map(&vmap);
   }
   if (warp == 8) tmem_alloc(tmem_slot, 512);
-  griddep_wait();
-  griddep_launch_dependents();
   uint32_t* weights = reinterpret_cast<uint32_t*>(smem);  // in the ring, before the first copy
-  tc_fence_before();
   const bool few = n_lists(p) <= 32;
-  if (few) __syncthreads();
-  else weigh<kTileKeys>(p, weights);
+  tc_fence_before();
+  __syncthreads();
   tc_fence_after();
+  Walk<kTileKeys> walk;
+  if (few && warp == 9) {
+#pragma unroll 1
+    for (int real = 0; real < 2; ++real) {
+      if (real) griddep_wait();
+      walk.start_few(p, lane, real);
+    }
+  } else {
+    griddep_wait();
+  }
+  if (!few) weigh<kTileKeys>(p, weights);
+  griddep_launch_dependents();
   const uint32_t tmem = *tmem_slot;
   const int half_tokens = p.block_tokens / 2;  // tokens of one row tile
 
@@ -202,8 +211,7 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
     Unit u;
     bool ok = true;
     if (warp == 9) {  // ---- copies
-      Walk<kTileKeys> walk;
-      few ? walk.start_few(p, lane) : walk.start(p, weights, lane);
+      if (!few) walk.start(p, weights, lane);
       if (lane == 0) p.rec[blockIdx.x].first_cta = -1;
       __syncwarp();
       fence_proxy_async_smem();
