@@ -15,7 +15,9 @@ constexpr int kAttnMaxGroup = 64;     // query heads per key head
 constexpr int kAttnPrefixRows = 8;    // tokens per sequence the prefix workspace is sized for
 constexpr int kAttnMaxPairs = 64;     // rotated pairs of a head
 constexpr int kAttnNoWindow = 1 << 30;
-constexpr int kSplitUnitCost = 1;     // AttnParams::unit_cost of the two kernels
+// AttnParams::unit_cost of the two kernels.  Geometric mean over 23 batches, us, with 1 / 2 / 3 for the split kernel:
+// 35.3 / 34.9 / 35.1; with 2 / 3 / 4 / 6 for the tensor-memory kernel: 35.4 / 35.3 / 35.3 / 35.7.
+constexpr int kSplitUnitCost = 2;
 constexpr int kTileUnitCost = 3;
 constexpr int kSplitMaxRows = 64;     // rows of a sequence up to which the split kernel takes it
 constexpr int kSplitKeys = 64;        // keys per tile of the split kernel

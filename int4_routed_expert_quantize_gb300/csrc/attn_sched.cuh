@@ -171,8 +171,13 @@ struct Walk {
   Tiles<KT> t;
   uint32_t begin, end, per, at;  // at: the current unit's first position
   int b, blk, head;
-  __device__ __forceinline__ void cut(const AttnParams& p, uint32_t run) {
+  // longest: the tiles of the longest unit that may be cut into single tiles (0: none)
+  __device__ __forceinline__ void cut(const AttnParams& p, uint32_t run, int longest) {
     per = max(1u, (run + gridDim.x - 1) / gridDim.x);
+    // Few CTAs' worth of work: a longer stretch costs a tile's time a position, a shorter one costs the joining
+    // kernel a round of loads per 16 parts, so the best stretch grows with the root of the unit (110 tiles of one
+    // unit: 20.0 us in stretches of 1, 15.6 in stretches of 2).
+    while ((int)(per * per) * 12 < longest) ++per;
     begin = min(blockIdx.x * per, run);
     end = min(begin + per, run);
     b = blk = head = 0;
@@ -190,7 +195,7 @@ struct Walk {
       run += __shfl_sync(FULL, v, 31);
     }
     __syncwarp();
-    cut(p, run);
+    cut(p, run, 0);
     if (blockIdx.x == 0 && p.seq_pos) {
 #pragma unroll 1
       for (int i = lane; i <= ns; i += 32) p.seq_pos[i] = pos[i];
@@ -219,11 +224,13 @@ struct Walk {
     }
     const int nb = (mine.n + p.block_tokens - 1) / p.block_tokens;
     uint32_t w = 0;
+    int longest = 0;
 #pragma unroll 1
     for (int i = 0; i < nb && nb <= kSerialBlocks; ++i) {
       Tiles<KT> x;
       x.set(p, mine, i);
       w += x.count + p.unit_cost;
+      if (KT == kSplitKeys) longest = x.count;
     }
     unsigned many = __ballot_sync(FULL, nb > kSerialBlocks);
 #pragma unroll 1
@@ -243,7 +250,7 @@ struct Walk {
     }
     w *= p.n_kv;
     const uint32_t v = warp_scan(w, lane);
-    cut(p, __shfl_sync(FULL, v, 31));
+    cut(p, __shfl_sync(FULL, v, 31), __reduce_max_sync(FULL, longest));
     if (blockIdx.x == 0 && p.seq_pos && real) {
       if (lane <= ns && lane < 31) p.seq_pos[lane] = v - w;
       if (lane == 31) p.seq_pos[31] = v - w, p.seq_pos[32] = v;
