@@ -272,10 +272,8 @@ __device__ __forceinline__ void add_parts(J& j, const AttnParams& p, const Parts
   });
 }
 
-// Every row is the join of its own sequence's parts and the prefix's.  The kernel starts while the launch before it
-// runs and looks its rows up meanwhile (that launch had waited for whatever wrote the lengths).  SAME: that
-// launch made both, so all results wait for it.  Otherwise the launch before that one made the own parts,
-// which are read ahead as well.
+// Every row is the join of its own sequence's parts and the prefix's, which one launch (SAME) or two before this one have
+// made.  Rows are looked up while those run (they had waited for whatever wrote the lengths).
 template <class T, int D, bool SAME, int Loads>
 __global__ void __launch_bounds__(kWarps * 32)
     attn_join_kernel(const AttnParams own, int own_rows, const AttnParams shared, int shared_ctas) {
@@ -299,10 +297,8 @@ __global__ void __launch_bounds__(kWarps * 32)
     const uint32_t total = blocks * shared.n_kv * (far.tiles + shared.unit_cost);
     far_per = max(1u, (total + shared_ctas - 1) / shared_ctas);
   }
-  if (SAME) {
-    griddep_wait();
-    griddep_launch_dependents();
-  }
+  griddep_wait();
+  griddep_launch_dependents();
   const bool redo = __ldcg(own.redo_any) != 0;
   const uint32_t per = __ldcg(own.seq_pos + n_lists(own) + 1), near_at = has_own ? __ldcg(own.seq_pos + b) : 0;
   const uint32_t far_at = SAME ? __ldcg(own.seq_pos + own.n_seqs) : 0;
@@ -314,10 +310,6 @@ __global__ void __launch_bounds__(kWarps * 32)
     } else {
       add_parts(j, own, find_parts(near, own_rows, near_at, per), 0, row, lane);
     }
-  }
-  if (!SAME) {
-    griddep_wait();
-    griddep_launch_dependents();
   }
   if (live) {
     add_parts(j, shared, SAME ? find_parts(far, own_rows, far_at, per) : find_parts(far, kTileRows, 0, far_per), 1, row,

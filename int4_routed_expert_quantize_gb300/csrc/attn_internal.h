@@ -56,6 +56,7 @@ struct AttnParams {
   int window, sinks;  // window >= kAttnNoWindow: none (and sinks 0)
   float scale_log2;   // scale * log2(e)
   int block_tokens;   // query tokens per block
+  int late_wait;      // the launch before this one belongs to the same call and is not read: wait for it at the end
   int unit_cost;      // list positions of a unit besides its tiles
   int64_t rows_lo, rows_hi;  // only sequences with rows_lo < new tokens * group <= rows_hi
   // workspace

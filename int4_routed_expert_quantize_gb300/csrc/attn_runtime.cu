@@ -386,6 +386,7 @@ extern "C" int coli_attn_window(coli_attn* h, const coli_attn_kv* kv, const coli
   if (e == cudaSuccess && many) {
     use_tile(h, &p);
     p.rows_lo = kSplitMaxRows, p.rows_hi = INT64_MAX;
+    p.late_wait = n;
     CUtensorMap qm;
     rc = list_fits(b, p, b->max_pages, kTileKeys);
     if (rc) return rc;
@@ -430,6 +431,7 @@ extern "C" int coli_attn_prefix(coli_attn* h, const coli_attn_kv* kv, const coli
   } else {
     use_tile(h, &pre);
     pre.n_seqs = 0;
+    pre.late_wait = 1;
     CUtensorMap qm;
     if (!query_map(&qm, h, q, q_stride, b->n_tokens)) return COLI_ECUDA;
     e = launch_attn_split(own, kv->maps.k64, kv->maps.v64, rows, h->cfg.dtype, h->num_sms, st);

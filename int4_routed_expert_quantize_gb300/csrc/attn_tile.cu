@@ -193,11 +193,11 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
   Walk<kTileKeys> walk;
   if (few && warp == 9) {
 #pragma unroll 1
-    for (int real = 0; real < 2; ++real) {
-      if (real) griddep_wait();
+    for (int real = p.late_wait ? 1 : 0; real < 2; ++real) {
+      if (real && !p.late_wait) griddep_wait();
       walk.start_few(p, lane, real);
     }
-  } else {
+  } else if (!p.late_wait) {
     griddep_wait();
   }
   if (!few) weigh<kTileKeys>(p, weights);
@@ -528,6 +528,9 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
       tc_fence_before();  // the next unit's products overwrite O after this row tile's next arrival
     }
   }
+  // With a late wait this grid starts as the one before it leaves the SMs, and is done only when that one is: whoever
+  // waits for this grid then has waited for both.
+  if (p.late_wait) griddep_wait();
   __syncthreads();
   if (warp == 8) tmem_dealloc(tmem, 512);
 }
