@@ -12,9 +12,8 @@ namespace {
 
 constexpr int kWarps = 4;
 // Parts a row has on its way.  More hide more of the L2's latency where the grid is small, and cost registers, so warps,
-// where it is large.  us with 4 / 8 / 16 on their way: one token's decode 10.6 / 10.2 / 9.4, 13 x 5 tokens
-// 15.7 / 15.8 / 16.1, mixed batch 139 / 141 / 150; prefix with 8 / 16: 24 rows a key head 14.9 / 14.1, 32 chats
-// 48.1 / 47.1, 256 sequences 303 / 316.
+// where it is large.  us with 4 / 8 / 16 on their way: one token's decode 10.6 / 10.2 / 9.4, mixed batch
+// 139 / 141 / 150; prefix with 8 / 16: 24 rows a key head 14.9 / 14.1, 32 chats 48.1 / 47.1, 256 sequences 303 / 316.
 constexpr int kSmallCombine = 1024, kSmallJoin = 4096;  // rows (tokens x heads) up to which 16 are taken
 
 // running join of one row over a warp; lane holds D/32 consecutive values
@@ -174,7 +173,65 @@ __device__ __noinline__ void clear_flags(const AttnParams& p) {
   if (threadIdx.x == 0) p.redo_any[0] = p.redo_any[1] = 0;
 }
 
-template <class T, int D, int Loads>
+// Four rows of one cut unit by one warp, eight lanes a row, each with a running maximum and sum of its own: nothing crosses
+// lanes, and every load is a whole line.  A lane holds columns 32 k + 4 (lane % 8) .. + 3.
+template <class T, int D>
+__device__ __forceinline__ void join_four(const AttnParams& p, const AttnList& l, const AttnRec& r, int row, int lane) {
+  constexpr int K = D / 32, kAtOnce = 4;
+  const int tok = row / p.group, n = r.last_cta - r.first_cta + 1, lane8 = lane & 7;
+  if (tok >= r.tokens) return;
+  float m = -INFINITY, sum = 0.f;
+  float4 o[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+  for (int c = 0; c < n; c += kAtOnce) {
+    float4 v[kAtOnce][K];
+    float2 ml[kAtOnce];
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      ml[j] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int k = 0; k < K; ++k) v[j][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (c + j < n) {
+        const int64_t at = ((int64_t)(r.first_cta + c + j) * 2 + (c + j == 0 ? 1 : 0)) * l.rows + row;
+        ml[j] = __ldcg(l.part_ml + at);
+#pragma unroll
+        for (int k = 0; k < K; ++k) v[j][k] = __ldcg(reinterpret_cast<const float4*>(l.part_o + at * D) + k * 8 + lane8);
+      }
+    }
+    float top = m;
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) top = fmaxf(top, ml[j].x);
+    const float ref = top == -INFINITY ? 0.f : top, keep = ex2(m - ref);
+    m = top;
+    sum *= keep;
+#pragma unroll
+    for (int k = 0; k < K; ++k) o[k].x *= keep, o[k].y *= keep, o[k].z *= keep, o[k].w *= keep;
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      if (ml[j].y == 0.f) continue;  // no part, or one without keys; a NaN sum stays
+      const float w = ex2(ml[j].x - ref);
+      sum = fmaf(w, ml[j].y, sum);
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        o[k].x = fmaf(w, v[j][k].x, o[k].x), o[k].y = fmaf(w, v[j][k].y, o[k].y);
+        o[k].z = fmaf(w, v[j][k].z, o[k].z), o[k].w = fmaf(w, v[j][k].w, o[k].w);
+      }
+    }
+  }
+  const int token = r.token0 + tok, hq = r.head * p.group + row - tok * p.group;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  uint2* dst = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + (int64_t)token * p.out_stride + (int64_t)hq * D);
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+    dst[k * 8 + lane8] = make_uint2(T::pack(o[k].x * inv, o[k].y * inv), T::pack(o[k].z * inv, o[k].w * inv));
+  if (p.lse && lane8 == 0)
+    p.lse[(int64_t)token * p.n_q + hq] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994530942f;
+}
+
+// SMALL: a warp a row, 16 parts of it on their way; otherwise four rows a warp
+template <class T, int D, bool SMALL>
 __global__ void __launch_bounds__(kWarps * 32) attn_combine_kernel(const AttnParams p, const AttnLists lists) {
   griddep_wait();
   griddep_launch_dependents();
@@ -186,11 +243,15 @@ __global__ void __launch_bounds__(kWarps * 32) attn_combine_kernel(const AttnPar
   const AttnRec r = l.rec[cta];
   const bool redo = __ldcg(p.redo_any) != 0;
   if (r.first_cta >= 0 && !(redo && __ldcg(p.redo + (int64_t)r.token0 * p.n_kv + r.head)))
-    for (int i = warp; i < l.block_rows; i += kWarps) {
+    for (int i = SMALL ? warp : warp * 4 + (lane >> 3); i < l.block_rows; i += SMALL ? kWarps : kWarps * 4) {
       const int row = block / l.ctas * l.block_rows + i;
+      if (!SMALL) {
+        join_four<T, D>(p, l, r, row, lane);
+        continue;
+      }
       const int tok = row / p.group;
       if (tok >= r.tokens) break;
-      Join<D, Loads> j;
+      Join<D, 16> j;
       j.add(l.part_o, l.part_ml, r.last_cta - r.first_cta + 1, lane, [&](int c) {
         return ((int64_t)(r.first_cta + c) * 2 + (c == 0 ? 1 : 0)) * l.rows + row;
       });
@@ -204,7 +265,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_combine_kernel(const AttnPar
     const int token = (int)(k / p.n_kv), b = seq_of(p, token, lane);
     const SeqInfo s = seq_info(p, b);
     for (int g = 0; g < p.group; ++g) {
-      Join<D, Loads> j;
+      Join<D, 4> j;
       const int hq = (int)(k % p.n_kv) * p.group + g;
       add_direct<T, D>(j, p, s, b, token - s.start, hq, qf[warp], lane);
       j.template write<T>(p, token, hq, lane);
@@ -346,14 +407,14 @@ cudaError_t join(const AttnParams& own, int own_rows, const AttnParams& shared, 
 template <class T, int D>
 cudaError_t combine(const AttnParams& p, const AttnLists& lists, cudaStream_t stream) {
   const dim3 grid(lists.l[0].blocks + lists.l[1].blocks);
-  return (int64_t)p.n_tokens * p.n_q <= kSmallCombine ? go(attn_combine_kernel<T, D, 16>, grid, stream, p, lists)
-                                                      : go(attn_combine_kernel<T, D, 4>, grid, stream, p, lists);
+  return (int64_t)p.n_tokens * p.n_q <= kSmallCombine ? go(attn_combine_kernel<T, D, true>, grid, stream, p, lists)
+                                                      : go(attn_combine_kernel<T, D, false>, grid, stream, p, lists);
 }
 
 }  // namespace
 
 AttnList attn_list(const AttnParams& p, int rows, int ctas) {
-  const int block_rows = rows >= 64 ? 16 : 4;
+  const int block_rows = rows >= 64 || (int64_t)p.n_tokens * p.n_q > kSmallCombine ? 16 : 4;
   return AttnList{p.part_o, p.part_ml, p.rec, ctas, rows, block_rows, ctas * (rows / block_rows)};
 }
 
