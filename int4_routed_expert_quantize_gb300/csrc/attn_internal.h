@@ -19,6 +19,7 @@ constexpr int kAttnNoWindow = 1 << 30;
 // 35.3 / 34.9 / 35.1; with 2 / 3 / 4 / 6 for the tensor-memory kernel: 35.4 / 35.3 / 35.3 / 35.7.
 constexpr int kSplitUnitCost = 2;
 constexpr int kTileUnitCost = 3;
+constexpr int64_t kSameWork = 300000;  // rows x prefix tokens up to which one launch takes prefix and own keys
 constexpr int kSplitMaxRows = 64;     // rows of a sequence up to which the split kernel takes it
 constexpr int kSplitKeys = 64;        // keys per tile of the split kernel
 constexpr int kTileKeys = 128;        // keys per tile of the tensor-memory kernel

@@ -414,9 +414,12 @@ extern "C" int coli_attn_prefix(coli_attn* h, const coli_attn_kv* kv, const coli
   AttnParams own = params(h, kv, b, q, q_stride, out, out_stride, lse, scale);
   own.dense_o[0] = h->dense_o, own.dense_ml[0] = h->dense_ml;
   own.dense_o[1] = h->dense_o2, own.dense_ml[1] = h->dense_ml2;
-  // Few rows in all: one launch of the split kernel takes the prefix as one more sequence.  More: the prefix is a matrix
-  // product for the tensor-memory kernel, in a launch of its own.
-  const bool same = (int64_t)b->n_tokens * own.group <= kSplitMaxRows;
+  // Few rows in all, or a short prefix (by its table): one launch of the split kernel takes the prefix as one more sequence,
+  // in blocks of 64 rows.  Otherwise the prefix is a matrix product for the tensor-memory kernel, in a launch of its
+  // own.  us on 8 key heads of 128, one launch / two, by rows a key head and prefix: 72 rows 4000 tokens 23.2 / 26.6,
+  // 8000 29.2 / 29.3; 126 rows 1000 21.8 / 22.2, 4000 29.0 / 26.2; 192 rows 300 22.1 / 24.1, 2000 27.3 / 25.7.
+  const int64_t all_rows = (int64_t)b->n_tokens * own.group;
+  const bool same = all_rows <= kSplitMaxRows || all_rows * ((int64_t)prefix_pages << h->page_shift) <= kSameWork;
   AttnParams pre = own;
   pre.pre_len = prefix_len, pre.pre_table = prefix_table, pre.pre_pages = prefix_pages;
   const int rows = rows_of(h, same ? b->n_tokens : b->max_q);
