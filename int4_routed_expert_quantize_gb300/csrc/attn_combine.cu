@@ -16,6 +16,12 @@ constexpr int kWarps = 4;
 // 139 / 141 / 150; prefix with 8 / 16: 24 rows a key head 14.9 / 14.1, 32 chats 48.1 / 47.1, 256 sequences 303 / 316.
 constexpr int kSmallCombine = 1024, kSmallJoin = 4096;  // rows (tokens x heads) up to which 16 are taken
 
+// one part of a row: its unnormalised output, and its maximum and sum
+struct Part {
+  const float* o;
+  const float2* ml;
+};
+
 // running join of one row over a warp; lane holds D/32 consecutive values
 template <int D, int Loads>
 struct Join {
@@ -27,13 +33,13 @@ struct Join {
     for (int i = 0; i < V; ++i) o[i] = 0.f;
   }
   template <class At>
-  static __device__ __forceinline__ void load(float (&v)[kLoads][V], const float* ob, int c, int n, int lane, At at) {
+  static __device__ __forceinline__ void load(float (&v)[kLoads][V], int c, int n, int lane, At at) {
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) {
 #pragma unroll
       for (int i = 0; i < V; ++i) v[j][i] = 0.f;
       if (j < n) {
-        const float* src = ob + at(c + j) * D + lane * V;
+        const float* src = at(c + j).o + lane * V;
         if constexpr (V == 4) {
           const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
           v[j][0] = x.x, v[j][1] = x.y, v[j][2] = x.z, v[j][3] = x.w;
@@ -44,15 +50,16 @@ struct Join {
       }
     }
   }
-  // parts i = 0..n-1 of the row at o_base + at(i) * D, ml_base[at(i)]
+  // parts at(0..n-1)
   template <class At>
-  __device__ __forceinline__ void add(const float* ob, const float2* mlb, int n, int lane, At at) {
+  __device__ __forceinline__ void add(int n, int lane, At at) {
+#pragma unroll 1
     for (int c = 0; c < n; c += 32) {
       const int k = min(32, n - c);
       float first[kLoads][V];  // asked for before the weights are known
-      load(first, ob, c, k, lane, at);
+      load(first, c, k, lane, at);
       float2 ml = make_float2(-INFINITY, 0.f);
-      if (lane < k) ml = __ldcg(mlb + at(c + lane));
+      if (lane < k) ml = __ldcg(at(c + lane).ml);
       float top = fmaxf(m, warp_max(ml.x));
       const float base = top == -INFINITY ? 0.f : top;
       const float keep = ex2(m - base);
@@ -66,7 +73,7 @@ struct Join {
       for (int i = 0; i < V; ++i) o[i] *= keep;
 #pragma unroll 1
       for (int j0 = 0; j0 < k; j0 += kLoads) {
-        if (j0 > 0) load(first, ob, c + j0, k - j0, lane, at);
+        if (j0 > 0) load(first, c + j0, k - j0, lane, at);
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
           const float wj = __shfl_sync(FULL, w, j0 + j);  // 0 past the end, and for a part without keys
@@ -252,8 +259,9 @@ __global__ void __launch_bounds__(kWarps * 32) attn_combine_kernel(const AttnPar
       const int tok = row / p.group;
       if (tok >= r.tokens) break;
       Join<D, 16> j;
-      j.add(l.part_o, l.part_ml, r.last_cta - r.first_cta + 1, lane, [&](int c) {
-        return ((int64_t)(r.first_cta + c) * 2 + (c == 0 ? 1 : 0)) * l.rows + row;
+      j.add(r.last_cta - r.first_cta + 1, lane, [&](int c) {
+        const int64_t at = ((int64_t)(r.first_cta + c) * 2 + (c == 0 ? 1 : 0)) * l.rows + row;
+        return Part{l.part_o + at * D, l.part_ml + at};
       });
       j.template write<T>(p, r.token0 + tok, r.head * p.group + row - tok * p.group, lane);
     }
@@ -322,15 +330,12 @@ __device__ __forceinline__ Parts find_parts(const Place& w, int rows, uint32_t a
   return r;
 }
 
-template <class J>
-__device__ __forceinline__ void add_parts(J& j, const AttnParams& p, const Parts& r, int which, int64_t dense_row,
-                                          int lane) {
-  // one call for both kinds: a dense row is a part at its own place
-  const float* ob = r.dense ? p.dense_o[which] : p.part_o;
-  const float2* ml = r.dense ? p.dense_ml[which] : p.part_ml;
-  j.add(ob, ml, r.n, lane, [&](int c) {
-    return r.dense ? dense_row : ((int64_t)(r.first_cta + c) * 2 + (c == 0 ? 1 : 0)) * r.rows + r.row;
-  });
+// part c of them; which: own (0) or prefix (1), for the dense buffer
+template <int D>
+__device__ __forceinline__ Part part_of(const AttnParams& p, const Parts& r, int which, int64_t dense_row, int c) {
+  if (r.dense) return Part{p.dense_o[which] + dense_row * D, p.dense_ml[which] + dense_row};
+  const int64_t at = ((int64_t)(r.first_cta + c) * 2 + (c == 0 ? 1 : 0)) * r.rows + r.row;
+  return Part{p.part_o + at * D, p.part_ml + at};
 }
 
 // Every row is the join of its own sequence's parts and the prefix's, which one launch (SAME) or two before this one have
@@ -350,7 +355,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   const int i = token - s.start;
   const bool has_own = i >= 0 && i < s.n;
   const Place far = find_place<SAME ? kSplitKeys : kTileKeys>(shared, pre, token, head, g);
-  Place near = {0, 0, 0};
+  Place near = {0, 1, 0};
   if (has_own) near = find_place<kSplitKeys>(own, s, i, head, g);
   uint32_t far_per = 1;
   if (!SAME) {  // the prefix alone on its list: the stretch follows from its length
@@ -364,17 +369,17 @@ __global__ void __launch_bounds__(kWarps * 32)
   const uint32_t per = __ldcg(own.seq_pos + n_lists(own) + 1), near_at = has_own ? __ldcg(own.seq_pos + b) : 0;
   const uint32_t far_at = SAME ? __ldcg(own.seq_pos + own.n_seqs) : 0;
   Join<D, Loads> j;
-  if (live && has_own) {
-    if (redo && __ldcg(own.redo + (int64_t)token * own.n_kv + head)) {
+  if (live) {
+    const Parts f = SAME ? find_parts(far, own_rows, far_at, per) : find_parts(far, kTileRows, 0, far_per);
+    Parts e = find_parts(near, own_rows, near_at, per);
+    if (!has_own) e.n = 0;
+    if (redo && has_own && __ldcg(own.redo + (int64_t)token * own.n_kv + head)) {
       __shared__ float qf[kWarps][D];
       add_direct<T, D>(j, own, s, b, i, hq, qf[threadIdx.x >> 5], lane);
-    } else {
-      add_parts(j, own, find_parts(near, own_rows, near_at, per), 0, row, lane);
+      e.n = 0;
     }
-  }
-  if (live) {
-    add_parts(j, shared, SAME ? find_parts(far, own_rows, far_at, per) : find_parts(far, kTileRows, 0, far_per), 1, row,
-              lane);
+    j.add(f.n + e.n, lane,
+          [&](int c) { return c < f.n ? part_of<D>(shared, f, 1, row, c) : part_of<D>(own, e, 0, row, c - f.n); });
     j.template write<T>(own, token, hq, lane);
   }
   if (redo) clear_flags(own);

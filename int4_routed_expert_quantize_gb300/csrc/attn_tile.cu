@@ -185,21 +185,15 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
     prefetch_map(&qmap), prefetch_map(&kmap), prefetch_map(&vmap);
   }
   if (warp == 8) tmem_alloc(tmem_slot, 512);
-  uint32_t* weights = reinterpret_cast<uint32_t*>(smem);  // in the ring, before the first copy
   const bool few = n_lists(p) <= 32;
+  Walk<kTileKeys> walk;
+  if (few && warp == 9) walk.start_few(p, lane, p.late_wait);  // without the late wait: the dry run
+  uint32_t* weights = reinterpret_cast<uint32_t*>(smem);  // in the ring, before the first copy
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  Walk<kTileKeys> walk;
-  if (few && warp == 9) {
-#pragma unroll 1
-    for (int real = p.late_wait ? 1 : 0; real < 2; ++real) {
-      if (real && !p.late_wait) griddep_wait();
-      walk.start_few(p, lane, real);
-    }
-  } else if (!p.late_wait) {
-    griddep_wait();
-  }
+  if (!p.late_wait) griddep_wait();
+  if (few && warp == 9 && !p.late_wait) walk.start_few(p, lane, true);
   if (!few) weigh<kTileKeys>(p, weights);
   griddep_launch_dependents();
   const uint32_t tmem = *tmem_slot;
