@@ -131,9 +131,9 @@ int coli_attn_prefix(coli_attn* h, const coli_attn_kv* kv, const coli_attn_batch
  * cleared.  Synchronises `stream`. */
 int coli_attn_status(coli_attn* h, void* stream);
 
-/* Kernels that coli_attn_window (op 1) or coli_attn_prefix (op 2) launches for batches with this max_q;
- * append (op 0) launches one.  At most: a batch of one sequence, or with few rows or a short prefix, takes one less.  EINVAL: bad arguments. */
-int coli_attn_launches(const coli_attn* h, int op, int max_q);
+/* Kernels that coli_attn_append (op 0), coli_attn_window (op 1) or coli_attn_prefix (op 2) launches at most for batches of
+ * n_seqs sequences.  EINVAL: bad arguments. */
+int coli_attn_launches(const coli_attn* h, int op, int n_seqs);
 
 #ifdef __cplusplus
 }

@@ -207,9 +207,9 @@ class PagedAttention:
         """device status of earlier calls (coli_attn_status); 0 when all went well"""
         return int(lib().coli_attn_status(self.h, coli._stream(stream)))
 
-    def launches(self, op, max_q):
-        """kernels one call launches; op "append", "window" or "prefix" (coli_attn_launches)"""
-        n = int(lib().coli_attn_launches(self.h, ("append", "window", "prefix").index(op), max_q))
+    def launches(self, op, n_seqs):
+        """kernels one call launches at most, with n_seqs sequences; op "append", "window" or "prefix" (coli_attn_launches)"""
+        n = int(lib().coli_attn_launches(self.h, ("append", "window", "prefix").index(op), n_seqs))
         if n < 0:
             raise coli.ColiError(n, "coli_attn_launches")
         return n

@@ -183,7 +183,7 @@ __device__ __noinline__ void clear_flags(const AttnParams& p) {
 // Four rows of one cut unit by one warp, eight lanes a row, each with a running maximum and sum of its own: nothing crosses
 // lanes, and every load is a whole line.  A lane holds columns 32 k + 4 (lane % 8) .. + 3.
 template <class T, int D>
-__device__ __forceinline__ void join_four(const AttnParams& p, const AttnList& l, const AttnRec& r, int row, int lane) {
+__device__ __forceinline__ void join_four(const AttnParams& p, int rows, const AttnRec& r, int row, int lane) {
   constexpr int K = D / 32, kAtOnce = 4;
   const int tok = row / p.group, n = r.last_cta - r.first_cta + 1, lane8 = lane & 7;
   if (tok >= r.tokens) return;
@@ -201,10 +201,10 @@ __device__ __forceinline__ void join_four(const AttnParams& p, const AttnList& l
 #pragma unroll
       for (int k = 0; k < K; ++k) v[j][k] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (c + j < n) {
-        const int64_t at = ((int64_t)(r.first_cta + c + j) * 2 + (c + j == 0 ? 1 : 0)) * l.rows + row;
-        ml[j] = __ldcg(l.part_ml + at);
+        const int64_t at = ((int64_t)(r.first_cta + c + j) * 2 + (c + j == 0 ? 1 : 0)) * rows + row;
+        ml[j] = __ldcg(p.part_ml + at);
 #pragma unroll
-        for (int k = 0; k < K; ++k) v[j][k] = __ldcg(reinterpret_cast<const float4*>(l.part_o + at * D) + k * 8 + lane8);
+        for (int k = 0; k < K; ++k) v[j][k] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * D) + k * 8 + lane8);
       }
     }
     float top = m;
@@ -239,29 +239,25 @@ __device__ __forceinline__ void join_four(const AttnParams& p, const AttnList& l
 
 // SMALL: a warp a row, 16 parts of it on their way; otherwise four rows a warp
 template <class T, int D, bool SMALL>
-__global__ void __launch_bounds__(kWarps * 32) attn_combine_kernel(const AttnParams p, const AttnLists lists) {
+__global__ void __launch_bounds__(kWarps * 32) attn_combine_kernel(const AttnParams p, int rows, int ctas, int block_rows) {
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int which = (int)blockIdx.x >= lists.l[0].blocks ? 1 : 0;
-  AttnList l = lists.l[0];
-  if (which) l = lists.l[1];  // (an indexed parameter would be copied to local memory)
-  const int block = blockIdx.x - (which ? lists.l[0].blocks : 0), cta = block % l.ctas;
-  const AttnRec r = l.rec[cta];
+  const AttnRec r = p.rec[blockIdx.x % ctas];
   const bool redo = __ldcg(p.redo_any) != 0;
   if (r.first_cta >= 0 && !(redo && __ldcg(p.redo + (int64_t)r.token0 * p.n_kv + r.head)))
-    for (int i = SMALL ? warp : warp * 4 + (lane >> 3); i < l.block_rows; i += SMALL ? kWarps : kWarps * 4) {
-      const int row = block / l.ctas * l.block_rows + i;
+    for (int i = SMALL ? warp : warp * 4 + (lane >> 3); i < block_rows; i += SMALL ? kWarps : kWarps * 4) {
+      const int row = blockIdx.x / ctas * block_rows + i;
       if (!SMALL) {
-        join_four<T, D>(p, l, r, row, lane);
+        join_four<T, D>(p, rows, r, row, lane);
         continue;
       }
       const int tok = row / p.group;
       if (tok >= r.tokens) break;
       Join<D, 16> j;
       j.add(r.last_cta - r.first_cta + 1, lane, [&](int c) {
-        const int64_t at = ((int64_t)(r.first_cta + c) * 2 + (c == 0 ? 1 : 0)) * l.rows + row;
-        return Part{l.part_o + at * D, l.part_ml + at};
+        const int64_t at = ((int64_t)(r.first_cta + c) * 2 + (c == 0 ? 1 : 0)) * rows + row;
+        return Part{p.part_o + at * D, p.part_ml + at};
       });
       j.template write<T>(p, r.token0 + tok, r.head * p.group + row - tok * p.group, lane);
     }
@@ -338,9 +334,10 @@ __device__ __forceinline__ Part part_of(const AttnParams& p, const Parts& r, int
   return Part{p.part_o + at * D, p.part_ml + at};
 }
 
-// Every row is the join of its own sequence's parts and the prefix's, which one launch (SAME) or two before this one have
-// made.  Rows are looked up while those run (they had waited for whatever wrote the lengths).
-template <class T, int D, bool SAME, int Loads>
+// Every row is the join of its own sequence's parts and the prefix's, which one launch with KT-key tiles has made, or (KT = 0)
+// two: the split kernel's for the sequences, the tensor-memory kernel's for the prefix.  Rows are looked up while those run
+// (they had waited for whatever wrote the lengths).
+template <class T, int D, int KT, int Loads>
 __global__ void __launch_bounds__(kWarps * 32)
     attn_join_kernel(const AttnParams own, int own_rows, const AttnParams shared, int shared_ctas) {
   const int lane = threadIdx.x & 31;
@@ -354,11 +351,11 @@ __global__ void __launch_bounds__(kWarps * 32)
   if (b < own.n_seqs) s = seq_info(own, b);
   const int i = token - s.start;
   const bool has_own = i >= 0 && i < s.n;
-  const Place far = find_place<SAME ? kSplitKeys : kTileKeys>(shared, pre, token, head, g);
+  const Place far = find_place<KT ? KT : kTileKeys>(shared, pre, token, head, g);
   Place near = {0, 1, 0};
-  if (has_own) near = find_place<kSplitKeys>(own, s, i, head, g);
+  if (has_own) near = find_place<KT ? KT : kSplitKeys>(own, s, i, head, g);
   uint32_t far_per = 1;
-  if (!SAME) {  // the prefix alone on its list: the stretch follows from its length
+  if (!KT) {  // the prefix alone on its list: the stretch follows from its length
     const uint32_t blocks = (pre.n + shared.block_tokens - 1) / shared.block_tokens;
     const uint32_t total = blocks * shared.n_kv * (far.tiles + shared.unit_cost);
     far_per = max(1u, (total + shared_ctas - 1) / shared_ctas);
@@ -367,10 +364,10 @@ __global__ void __launch_bounds__(kWarps * 32)
   griddep_launch_dependents();
   const bool redo = __ldcg(own.redo_any) != 0;
   const uint32_t per = __ldcg(own.seq_pos + n_lists(own) + 1), near_at = has_own ? __ldcg(own.seq_pos + b) : 0;
-  const uint32_t far_at = SAME ? __ldcg(own.seq_pos + own.n_seqs) : 0;
+  const uint32_t far_at = KT ? __ldcg(own.seq_pos + own.n_seqs) : 0;
   Join<D, Loads> j;
   if (live) {
-    const Parts f = SAME ? find_parts(far, own_rows, far_at, per) : find_parts(far, kTileRows, 0, far_per);
+    const Parts f = KT ? find_parts(far, own_rows, far_at, per) : find_parts(far, kTileRows, 0, far_per);
     Parts e = find_parts(near, own_rows, near_at, per);
     if (!has_own) e.n = 0;
     if (redo && has_own && __ldcg(own.redo + (int64_t)token * own.n_kv + head)) {
@@ -404,29 +401,28 @@ cudaError_t join(const AttnParams& own, int own_rows, const AttnParams& shared, 
                  cudaStream_t stream) {
   const dim3 grid((unsigned)(((int64_t)own.n_tokens * own.n_q + kWarps - 1) / kWarps));
   const bool small = (int64_t)own.n_tokens * own.n_q <= kSmallJoin;
-  return same    ? go(attn_join_kernel<T, D, true, 16>, grid, stream, own, own_rows, shared, shared_ctas)
-         : small ? go(attn_join_kernel<T, D, false, 16>, grid, stream, own, own_rows, shared, shared_ctas)
-                 : go(attn_join_kernel<T, D, false, 8>, grid, stream, own, own_rows, shared, shared_ctas);
+  const bool tile = same && own_rows == kTileRows;
+  const auto k16 = tile ? attn_join_kernel<T, D, kTileKeys, 16> : same ? attn_join_kernel<T, D, kSplitKeys, 16> : attn_join_kernel<T, D, 0, 16>;
+  const auto k8 = tile ? attn_join_kernel<T, D, kTileKeys, 8> : attn_join_kernel<T, D, 0, 8>;
+  // (the split kernel alone: at most kSplitMaxRows rows a key head)
+  return go(small || (same && !tile) ? k16 : k8, grid, stream, own, own_rows, shared, shared_ctas);
 }
 
 template <class T, int D>
-cudaError_t combine(const AttnParams& p, const AttnLists& lists, cudaStream_t stream) {
-  const dim3 grid(lists.l[0].blocks + lists.l[1].blocks);
-  return (int64_t)p.n_tokens * p.n_q <= kSmallCombine ? go(attn_combine_kernel<T, D, true>, grid, stream, p, lists)
-                                                      : go(attn_combine_kernel<T, D, false>, grid, stream, p, lists);
+cudaError_t combine(const AttnParams& p, int rows, int live, int ctas, cudaStream_t stream) {
+  const bool small = (int64_t)p.n_tokens * p.n_q <= kSmallCombine;
+  const int block_rows = small ? 4 : 16;
+  const dim3 grid(ctas * ((live + block_rows - 1) / block_rows));
+  return small ? go(attn_combine_kernel<T, D, true>, grid, stream, p, rows, ctas, block_rows)
+               : go(attn_combine_kernel<T, D, false>, grid, stream, p, rows, ctas, block_rows);
 }
 
 }  // namespace
 
-AttnList attn_list(const AttnParams& p, int rows, int ctas) {
-  const int block_rows = rows >= 64 || (int64_t)p.n_tokens * p.n_q > kSmallCombine ? 16 : 4;
-  return AttnList{p.part_o, p.part_ml, p.rec, ctas, rows, block_rows, ctas * (rows / block_rows)};
-}
-
-cudaError_t launch_attn_combine(const AttnParams& p, const AttnLists& lists, int dtype, cudaStream_t stream) {
+cudaError_t launch_attn_combine(const AttnParams& p, int rows, int live, int ctas, int dtype, cudaStream_t stream) {
   if (dtype == COLI_ATTN_BF16)
-    return p.head_dim == 64 ? combine<Bf16, 64>(p, lists, stream) : combine<Bf16, 128>(p, lists, stream);
-  return p.head_dim == 64 ? combine<Fp16, 64>(p, lists, stream) : combine<Fp16, 128>(p, lists, stream);
+    return p.head_dim == 64 ? combine<Bf16, 64>(p, rows, live, ctas, stream) : combine<Bf16, 128>(p, rows, live, ctas, stream);
+  return p.head_dim == 64 ? combine<Fp16, 64>(p, rows, live, ctas, stream) : combine<Fp16, 128>(p, rows, live, ctas, stream);
 }
 
 cudaError_t launch_attn_join(const AttnParams& own, int own_rows, const AttnParams& shared, bool same_list,

@@ -146,13 +146,12 @@ __device__ __forceinline__ const int32_t* table_of(const AttnParams& p, int b) {
   return b < p.n_seqs ? p.table + (int64_t)b * p.table_stride : p.pre_table;
 }
 
-// One warp fills the stage of a KT-key tile of K and of V: the boxes that hold keys some row of the block
-// sees.  Lane i takes box i: K's, and (N = 2) V's at v_offset; N = 1 takes one map.  Pages whose id is out of
+// One warp fills the stage of a KT-key tile: the boxes that hold keys some row of the block sees.  Lane i takes box i, from
+// `map` to dst and (N = 2) from `second` to dst + KT * D * 2.  Pages whose id is out of
 // range read as zeros (page coordinate past the end) and are reported.
 template <int KT, int D, int N>
-__device__ __forceinline__ void fill_boxes(const AttnParams& p, const CUtensorMap* kmap, const CUtensorMap* vmap,
-                                           uint8_t* dst, uint64_t* kbar, uint64_t* vbar, int v_offset,
-                                           const int32_t* table, int p0, int p1, int j0, int head, int lane) {
+__device__ __forceinline__ void fill_boxes(const AttnParams& p, const CUtensorMap* map, const CUtensorMap* second,
+                                           uint8_t* dst, uint64_t* bar, const int32_t* table, int p0, int p1, int j0, int head, int lane) {
   const int page = 1 << p.page_shift;
   const int rows = min(page, KT);  // slots per box
   const int boxes = KT / rows;     // per 64 values
@@ -161,14 +160,7 @@ __device__ __forceinline__ void fill_boxes(const AttnParams& p, const CUtensorMa
   int id = 0;
   if (need) id = __ldg(table + (a >> p.page_shift));
   const uint32_t bytes = (uint32_t)__popc(__ballot_sync(FULL, need)) * (uint32_t)rows * D * 2;
-  if (lane == 0) {
-    if (N == 2 && kbar == vbar) {
-      mbar_expect_tx(kbar, 2 * bytes);
-    } else {
-      mbar_expect_tx(kbar, bytes);
-      if (N == 2) mbar_expect_tx(vbar, bytes);
-    }
-  }
+  if (lane == 0) mbar_expect_tx(bar, N * bytes);
   __syncwarp();
   if (need) {
     if (id < 0 || id >= p.n_pages) {
@@ -178,11 +170,11 @@ __device__ __forceinline__ void fill_boxes(const AttnParams& p, const CUtensorMa
     const int slot = a & (page - 1);
     dst += lane * rows * 128;
 #pragma unroll
-    for (int s = 0; s < D / 64; ++s) tma_load_4d(dst + s * KT * 128, kmap, s * 64, slot, head, id, kbar);
+    for (int s = 0; s < D / 64; ++s) tma_load_4d(dst + s * KT * 128, map, s * 64, slot, head, id, bar);
     if (N == 2)
 #pragma unroll
       for (int s = 0; s < D / 64; ++s)
-        tma_load_4d(dst + v_offset + s * KT * 128, vmap, s * 64, slot, head, id, vbar);
+        tma_load_4d(dst + KT * D * 2 + s * KT * 128, second, s * 64, slot, head, id, bar);
   }
   __syncwarp();
 }

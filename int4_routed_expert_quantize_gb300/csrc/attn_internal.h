@@ -19,8 +19,7 @@ constexpr int kAttnNoWindow = 1 << 30;
 // 35.3 / 34.9 / 35.1; with 2 / 3 / 4 / 6 for the tensor-memory kernel: 35.4 / 35.3 / 35.3 / 35.7.
 constexpr int kSplitUnitCost = 2;
 constexpr int kTileUnitCost = 3;
-constexpr int64_t kSameWork = 300000;  // rows x prefix tokens up to which one launch takes prefix and own keys
-constexpr int kSplitMaxRows = 64;     // rows of a sequence up to which the split kernel takes it
+constexpr int kSplitMaxRows = 32;     // rows of a block of the split kernel, and of a sequence it takes
 constexpr int kSplitKeys = 64;        // keys per tile of the split kernel
 constexpr int kTileKeys = 128;        // keys per tile of the tensor-memory kernel
 constexpr int kTileRows = 256;        // query rows per block of the tensor-memory kernel (2 x 128)
@@ -33,7 +32,6 @@ struct AttnRec {
   int first_cta, last_cta;  // CTAs with a part of the unit; first_cta < 0: no record
   int token0, tokens;       // the unit's query tokens
   int head;                 // key head
-  int pad[3];
 };
 
 struct AttnParams {
@@ -59,12 +57,11 @@ struct AttnParams {
   int block_tokens;   // query tokens per block
   int late_wait;      // the launch before this one belongs to the same call and is not read: wait for it at the end
   int unit_cost;      // list positions of a unit besides its tiles
-  int64_t rows_lo, rows_hi;  // only sequences with rows_lo < new tokens * group <= rows_hi
   // workspace
   float* part_o;     // [2 * CTAs][rows per block][head_dim] unnormalised partial outputs
   float2* part_ml;   // [2 * CTAs][rows per block] their maximum (log2 units) and sum
   AttnRec* rec;      // [CTAs]
-  uint32_t* seq_pos;  // [n_seqs + 2] first list position of each sequence, the total, the stretch; or nullptr
+  uint32_t* seq_pos;  // [n_seqs + 3] first list position of each sequence, the total, the stretch; or nullptr
   // prefix calls only: rows of uncut units go here, unnormalised, by (token, head); [0] those of the sequences'
   // own keys, [1] those of the prefix
   float* dense_o[2];
@@ -95,7 +92,7 @@ struct AttnAppend {
   int* status;
 };
 
-int split_rows(int rows);  // rows per block the split kernel takes for units of `rows` rows
+int split_rows(int64_t rows);  // rows per block of the split kernel for sequences of up to `rows` rows
 int split_grid(int num_sms);  // CTAs
 cudaError_t configure_attn_split();
 cudaError_t launch_attn_split(const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v,
@@ -104,23 +101,11 @@ int tile_block_tokens(int group);  // tokens per block of the tensor-memory kern
 cudaError_t configure_attn_tile();
 cudaError_t launch_attn_tile(const AttnParams& p, const CUtensorMap& q, const CUtensorMap& k,
                              const CUtensorMap& v, int dtype, int num_sms, cudaStream_t stream);
-// One launch's partials; a combine kernel merges those of up to two launches.
-struct AttnList {
-  const float* part_o;
-  const float2* part_ml;
-  const AttnRec* rec;
-  int ctas, rows;  // CTAs, rows per block of theirs
-  int block_rows;  // of which a block of the combine kernel takes so many
-  int blocks;      // blocks of the combine kernel for this list
-};
-struct AttnLists {
-  AttnList l[2];
-};
-AttnList attn_list(const AttnParams& p, int rows, int ctas);
-// merges the partials of cut units into out / lse
-cudaError_t launch_attn_combine(const AttnParams& p, const AttnLists& lists, int dtype, cudaStream_t stream);
-// merges, for every row, the sequence's own and the prefix's results into out / lse; own and shared are the same
-// list when one launch made both, else the prefix's came from the tensor-memory kernel
+// merges the partials of cut units into out / lse; the launch before had `ctas` CTAs and blocks of `rows` rows, of
+// which at most `live` are in use
+cudaError_t launch_attn_combine(const AttnParams& p, int rows, int live, int ctas, int dtype, cudaStream_t stream);
+// merges, for every row, the sequence's own and the prefix's results into out / lse; same_list: one launch, with blocks of
+// own_rows rows, made both; else the split kernel made the sequences' and the tensor-memory kernel the prefix's
 cudaError_t launch_attn_join(const AttnParams& own, int own_rows, const AttnParams& shared, bool same_list,
                              int shared_ctas, int dtype, cudaStream_t stream);
 cudaError_t launch_attn_append(const AttnAppend& a, int dtype, int num_sms, cudaStream_t stream);

@@ -85,8 +85,8 @@ void carve(T** p, char* arena, size_t* at, size_t count) {
 // the workspace in the arena (nullptr: its size alone); what has to be zero comes first, *zero bytes of it
 size_t lay_out(coli_attn* h, char* arena, size_t* zero) {
   const coli_attn_config& c = h->cfg;
-  // partials: two per CTA of the split kernel (2 CTAs an SM, up to 64 rows) and of the tensor-memory kernel
-  const size_t D = c.head_dim, ctas = 2 * (size_t)h->num_sms, rows = 2 * ctas * 64,
+  // partials: two per CTA of the split kernel (2 CTAs an SM) and of the tensor-memory kernel
+  const size_t D = c.head_dim, ctas = 2 * (size_t)h->num_sms, rows = 2 * ctas * kSplitMaxRows,
                rows2 = 2 * (size_t)h->num_sms * kTileRows;
   // the prefix call keeps every row twice
   const size_t dense = (size_t)h->prefix_tokens * c.n_q;
@@ -97,7 +97,7 @@ size_t lay_out(coli_attn* h, char* arena, size_t* zero) {
   *zero = at;
   carve(&h->turn, arena, &at, kAttnMaxPairs);
   carve(&h->rec, arena, &at, ctas);
-  carve(&h->rec2, arena, &at, ctas);
+  carve(&h->rec2, arena, &at, (size_t)h->num_sms);
   carve(&h->seq_pos, arena, &at, (size_t)c.max_seqs + 3);
   carve(&h->part_ml, arena, &at, rows);
   carve(&h->part_ml2, arena, &at, rows2);
@@ -158,7 +158,6 @@ AttnParams params(const coli_attn* h, const coli_attn_kv* kv, const coli_attn_ba
   p.page_shift = h->page_shift, p.n_pages = (int)kv->c.n_pages;
   p.window = kAttnNoWindow, p.sinks = 0;
   p.scale_log2 = scale * 1.44269504088896340736f;
-  p.rows_lo = 0, p.rows_hi = INT64_MAX;
   p.part_o = h->part_o, p.part_ml = h->part_ml, p.rec = h->rec, p.seq_pos = h->seq_pos;
   p.k_page = kv->c.k_page_stride, p.k_head = kv->c.k_head_stride, p.k_slot = kv->c.k_slot_stride;
   p.v_page = kv->c.v_page_stride, p.v_head = kv->c.v_head_stride, p.v_slot = kv->c.v_slot_stride;
@@ -185,14 +184,9 @@ bool query_map(CUtensorMap* map, const coli_attn* h, const void* q, int64_t q_st
 
 // switches a launch's parameters to the tensor-memory kernel's workspace and blocks
 void use_tile(const coli_attn* h, AttnParams* p) {
-  p->part_o = h->part_o2, p->part_ml = h->part_ml2, p->rec = h->rec2, p->seq_pos = nullptr;
+  p->part_o = h->part_o2, p->part_ml = h->part_ml2, p->rec = h->rec2;
   p->unit_cost = kTileUnitCost;
   p->block_tokens = tile_block_tokens(p->group);
-}
-
-int rows_of(const coli_attn* h, int64_t tokens) {
-  const int64_t rows = tokens * (h->cfg.n_q / h->cfg.n_kv);
-  return split_rows((int)(rows < 64 ? rows : 64));
 }
 
 // Whether rows of `wa` elements every `sa` from a and of `wb` every `sb` from b (n of either) share memory.  Rows of the
@@ -212,6 +206,15 @@ int query_args(const coli_attn* h, int64_t n_tokens, const void* q, int64_t q_st
       out_stride < width || !(scale > 0.f) || !std::isfinite(scale))
     return COLI_EINVAL;
   return collide(q, q_stride, width, out, out_stride, width, n_tokens) ? COLI_EINVAL : COLI_OK;
+}
+
+// Whether a prefix call of more than kSplitMaxRows rows a key head takes the sequences' own keys and the prefix in one launch
+// of the tensor-memory kernel.  A unit of own keys costs that kernel about 2 us more than the split kernel, a second launch
+// about 5 us, so: up to two such units an SM.  us, one launch / two, by sequences and tokens of prefix + own keys, 8 key
+// heads: 16, 8000 + 40 22.3 / 28.0; 32, 2000 + 1000 39.8 / 41.4, 32000 + 40 51.2 / 56.0; 64, 2000 + 40 40.6 / 32.8,
+// 32000 + 1000 101 / 94.  (The split kernel's blocks cannot hold one token of more than kSplitMaxRows heads a key head.)
+bool one_prefix_launch(const coli_attn* h, int n_seqs) {
+  return h->cfg.n_q / h->cfg.n_kv > kSplitMaxRows || (int64_t)n_seqs * h->cfg.n_kv <= 2 * h->num_sms;
 }
 
 // the work list's positions are 32-bit: its length is bounded by the page table's width (or the window)
@@ -369,32 +372,29 @@ extern "C" int coli_attn_window(coli_attn* h, const coli_attn_kv* kv, const coli
   cudaStream_t st = (cudaStream_t)stream;
   AttnParams p = params(h, kv, b, q, q_stride, out, out_stride, lse, scale);
   if (window >= 0 && window < kAttnNoWindow) p.window = window, p.sinks = sinks;
-  // sequences of up to kSplitMaxRows rows go to the split kernel, longer ones to the tensor-memory kernel
-  const bool many = (int64_t)b->max_q * p.group > kSplitMaxRows;
-  cudaError_t e = cudaSuccess;
-  AttnLists lists = {};
-  int n = 0;
-  if (!many || b->n_seqs > 1) {
-    if (many) p.rows_hi = kSplitMaxRows;
-    const int rows = rows_of(h, b->max_q);
+  // One kernel takes the whole batch: the split kernel where no sequence has more than kSplitMaxRows rows a key head, else
+  // the tensor-memory kernel, its single tokens too.  us, split / tensor memory, 8 key heads of 128, every sequence of so many
+  // rows: 30 rows, one sequence of 8000 tokens 17.2 / 20.0, 8 of them 37.9 / 37.3, 32 of 1000 26.5 / 29.3; 60 rows
+  // 26.8 / 20.6, 52.4 / 38.4, 40.0 / 30.1 (split kernel in blocks of 64 rows).  A launch of either kernel for the sequences that
+  // suit it: 8 of up to 96 rows 26.5 / one launch 16.7, 40 mixed ones of 4000 tokens 146 / 125.
+  const int64_t seq_rows = (int64_t)b->max_q * p.group;
+  cudaError_t e;
+  if (seq_rows <= kSplitMaxRows) {
+    const int rows = split_rows(seq_rows), ctas = split_grid(h->num_sms);
     p.block_tokens = rows / p.group;
     rc = list_fits(b, p, b->max_pages, kSplitKeys);
     if (rc) return rc;
     e = launch_attn_split(p, kv->maps.k64, kv->maps.v64, rows, h->cfg.dtype, h->num_sms, st);
-    lists.l[n++] = attn_list(p, rows, split_grid(h->num_sms));
-  }
-  if (e == cudaSuccess && many) {
+    if (e == cudaSuccess) e = launch_attn_combine(p, rows, (int)seq_rows, ctas, h->cfg.dtype, st);
+  } else {
     use_tile(h, &p);
-    p.rows_lo = kSplitMaxRows, p.rows_hi = INT64_MAX;
-    p.late_wait = n;
     CUtensorMap qm;
     rc = list_fits(b, p, b->max_pages, kTileKeys);
     if (rc) return rc;
     if (!query_map(&qm, h, q, q_stride, b->n_tokens)) return COLI_ECUDA;
     e = launch_attn_tile(p, qm, kv->maps.k128, kv->maps.v128, h->cfg.dtype, h->num_sms, st);
-    lists.l[n++] = attn_list(p, kTileRows, h->num_sms);
+    if (e == cudaSuccess) e = launch_attn_combine(p, kTileRows, (int)(seq_rows < kTileRows ? seq_rows : kTileRows), h->num_sms, h->cfg.dtype, st);
   }
-  if (e == cudaSuccess) e = launch_attn_combine(p, lists, h->cfg.dtype, st);
   return e == cudaSuccess ? COLI_OK : COLI_ECUDA;
 }
 
@@ -414,34 +414,40 @@ extern "C" int coli_attn_prefix(coli_attn* h, const coli_attn_kv* kv, const coli
   AttnParams own = params(h, kv, b, q, q_stride, out, out_stride, lse, scale);
   own.dense_o[0] = h->dense_o, own.dense_ml[0] = h->dense_ml;
   own.dense_o[1] = h->dense_o2, own.dense_ml[1] = h->dense_ml2;
-  // Few rows in all, or a short prefix (by its table): one launch of the split kernel takes the prefix as one more sequence,
-  // in blocks of 64 rows.  Otherwise the prefix is a matrix product for the tensor-memory kernel, in a launch of its
-  // own.  us on 8 key heads of 128, one launch / two, by rows a key head and prefix: 72 rows 4000 tokens 23.2 / 26.6,
-  // 8000 29.2 / 29.3; 126 rows 1000 21.8 / 22.2, 4000 29.0 / 26.2; 192 rows 300 22.1 / 24.1, 2000 27.3 / 25.7.
-  const int64_t all_rows = (int64_t)b->n_tokens * own.group;
-  const bool same = all_rows <= kSplitMaxRows || all_rows * ((int64_t)prefix_pages << h->page_shift) <= kSameWork;
   AttnParams pre = own;
   pre.pre_len = prefix_len, pre.pre_table = prefix_table, pre.pre_pages = prefix_pages;
-  const int rows = rows_of(h, same ? b->n_tokens : b->max_q);
-  own.block_tokens = pre.block_tokens = rows / own.group;
-  const int64_t pages = b->max_pages > prefix_pages ? b->max_pages : prefix_pages;
-  rc = list_fits(b, own, pages, kSplitKeys);
-  if (rc) return rc;
+  const int64_t pages = b->max_pages > prefix_pages ? b->max_pages : prefix_pages, all_rows = (int64_t)b->n_tokens * own.group;
+  CUtensorMap qm;
   cudaError_t e;
-  if (same) {
-    own = pre;
-    e = launch_attn_split(own, kv->maps.k64, kv->maps.v64, rows, h->cfg.dtype, h->num_sms, st);
+  if (all_rows <= kSplitMaxRows) {  // one launch, the prefix as one more sequence of all tokens
+    const int rows = split_rows(all_rows);
+    pre.block_tokens = rows / own.group;
+    rc = list_fits(b, pre, pages, kSplitKeys);
+    if (rc) return rc;
+    e = launch_attn_split(pre, kv->maps.k64, kv->maps.v64, rows, h->cfg.dtype, h->num_sms, st);
+    if (e == cudaSuccess) e = launch_attn_join(pre, rows, pre, true, 0, h->cfg.dtype, st);
+  } else if (one_prefix_launch(h, b->n_seqs)) {  // as above
+    use_tile(h, &pre);
+    rc = list_fits(b, pre, pages, kTileKeys);
+    if (rc) return rc;
+    if (!query_map(&qm, h, q, q_stride, b->n_tokens)) return COLI_ECUDA;
+    e = launch_attn_tile(pre, qm, kv->maps.k128, kv->maps.v128, h->cfg.dtype, h->num_sms, st);
+    if (e == cudaSuccess) e = launch_attn_join(pre, kTileRows, pre, true, 0, h->cfg.dtype, st);
   } else {
+    const int rows = split_rows((int64_t)b->max_q * own.group);
+    own.block_tokens = rows / own.group;
     use_tile(h, &pre);
     pre.n_seqs = 0;
+    pre.seq_pos = nullptr;  // the split kernel's, at the same time
     pre.late_wait = 1;
-    CUtensorMap qm;
+    rc = list_fits(b, own, pages, kSplitKeys);
+    if (rc) return rc;
     if (!query_map(&qm, h, q, q_stride, b->n_tokens)) return COLI_ECUDA;
     e = launch_attn_split(own, kv->maps.k64, kv->maps.v64, rows, h->cfg.dtype, h->num_sms, st);
     if (e == cudaSuccess)
       e = launch_attn_tile(pre, qm, kv->maps.k128, kv->maps.v128, h->cfg.dtype, h->num_sms, st);
+    if (e == cudaSuccess) e = launch_attn_join(own, rows, pre, false, h->num_sms, h->cfg.dtype, st);
   }
-  if (e == cudaSuccess) e = launch_attn_join(own, rows, pre, same, h->num_sms, h->cfg.dtype, st);
   return e == cudaSuccess ? COLI_OK : COLI_ECUDA;
 }
 
@@ -457,8 +463,7 @@ extern "C" int coli_attn_status(coli_attn* h, void* stream) {
   return v;
 }
 
-extern "C" int coli_attn_launches(const coli_attn* h, int op, int max_q) {
-  if (!h || op < 0 || op > 2 || max_q < 1) return COLI_EINVAL;
-  const bool many = (int64_t)max_q * (h->cfg.n_q / h->cfg.n_kv) > kSplitMaxRows;
-  return op == 0 ? 1 : op == 1 ? (many ? 3 : 2) : 3;
+extern "C" int coli_attn_launches(const coli_attn* h, int op, int n_seqs) {
+  if (!h || op < 0 || op > 2 || n_seqs < 1) return COLI_EINVAL;
+  return op == 0 ? 1 : op == 1 ? 2 : one_prefix_launch(h, n_seqs) ? 2 : 3;
 }

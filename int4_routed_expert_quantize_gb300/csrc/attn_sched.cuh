@@ -22,8 +22,6 @@ __device__ __forceinline__ SeqInfo seq_info(const AttnParams& p, int b) {
     const int a = __ldcg(p.q_start + b), e = __ldcg(p.q_start + b + 1);
     s.start = min(max(a, 0), p.n_tokens);
     s.n = min(max(e, s.start), p.n_tokens) - s.start;
-    const int64_t rows = (int64_t)s.n * p.group;
-    if (rows <= p.rows_lo || rows > p.rows_hi) s.n = 0;
   } else {
     s.start = 0;
     s.n = p.n_tokens;
@@ -332,7 +330,7 @@ struct Walk {
     if (c0 + 1 != (int)blockIdx.x || (threadIdx.x & 31) != 0) return;
     AttnRec r;
     r.first_cta = c0, r.last_cta = (first + count - 1) / per;
-    r.token0 = u.tok0, r.tokens = u.nt, r.head = u.head, r.pad[0] = r.pad[1] = r.pad[2] = 0;
+    r.token0 = u.tok0, r.tokens = u.nt, r.head = u.head;
     p.rec[blockIdx.x] = r;
   }
 };

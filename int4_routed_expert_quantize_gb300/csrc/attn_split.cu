@@ -224,8 +224,7 @@ __global__ void __launch_bounds__(SplitCfg<D, RG>::threads, SplitCfg<D, RG>::cta
         if (it >= NST) ok = wait(empty + sgi, ((it / NST) + 1) & 1);
         if (!ok) break;
         uint8_t* dst = smem + sgi * 2 * C::tile_bytes;
-        fill_boxes<kSplitKeys, D, 2>(p, &kmap, &vmap, dst, full + sgi, full + sgi, C::tile_bytes, row, u.p0, u.p1,
-                                     u.tile(i) * kSplitKeys, u.head, lane);
+        fill_boxes<kSplitKeys, D, 2>(p, &kmap, &vmap, dst, full + sgi, row, u.p0, u.p1, u.tile(i) * kSplitKeys, u.head, lane);
       }
     }
     u.i1 = 0;
@@ -308,7 +307,7 @@ __global__ void __launch_bounds__(SplitCfg<D, RG>::threads, SplitCfg<D, RG>::cta
     // writes its second handover there.
     constexpr int NC = D / 8 / C::KG;  // 8-column groups a warp ends with
     int col = 0;                       // the first of them
-    if (C::KG > 1) {
+    {
       constexpr int H = D / 16;
       if (!meet()) return;  // the buffers are free
       const int other = rg + RG * (kg ^ (C::KG / 2));
@@ -338,7 +337,7 @@ __global__ void __launch_bounds__(SplitCfg<D, RG>::threads, SplitCfg<D, RG>::cta
                                                     (int64_t)(tok0 + tok[r]) * p.out_stride + (int64_t)hq * D);
 #pragma unroll
         for (int d = 0; d < D / 8; ++d)
-          if (C::KG == 1 || (d / NC) * NC == col)
+          if ((d / NC) * NC == col)
             dst[d * 4 + (lane & 3)] = T::pack(o[d][2 * r] * inv, o[d][2 * r + 1] * inv);
         if (p.lse && kg == 0 && (lane & 3) == 0)
           p.lse[(int64_t)(tok0 + tok[r]) * p.n_q + hq] =
@@ -349,7 +348,7 @@ __global__ void __launch_bounds__(SplitCfg<D, RG>::threads, SplitCfg<D, RG>::cta
         float* dst = whole ? dense_o : p.part_o;
 #pragma unroll
         for (int d = 0; d < D / 8; ++d)
-          if (C::KG == 1 || (d / NC) * NC == col)
+          if ((d / NC) * NC == col)
             *reinterpret_cast<float2*>(dst + at * D + d * 8 + (lane & 3) * 2) =
                 make_float2(o[d][2 * r], o[d][2 * r + 1]);
         if (kg == 0 && (lane & 3) == 0) (whole ? dense_ml : p.part_ml)[at] = make_float2(m2, sum[r]);
@@ -357,8 +356,6 @@ __global__ void __launch_bounds__(SplitCfg<D, RG>::threads, SplitCfg<D, RG>::cta
     }
   }
 }
-
-typedef void (*SplitKernel)(const AttnParams, const CUtensorMap, const CUtensorMap);
 
 template <class T, int D, int RG>
 cudaError_t configure() {
@@ -386,22 +383,19 @@ cudaError_t launch(const AttnParams& p, const CUtensorMap& k, const CUtensorMap&
 template <class T, int D>
 cudaError_t launch_rows(const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v, int rows,
                         int grid, cudaStream_t stream) {
-  if (rows == 16) return launch<T, D, 1>(p, k, v, grid, stream);
-  if (rows == 32) return launch<T, D, 2>(p, k, v, grid, stream);
-  return launch<T, D, 4>(p, k, v, grid, stream);
+  return rows == 16 ? launch<T, D, 1>(p, k, v, grid, stream) : launch<T, D, 2>(p, k, v, grid, stream);
 }
 
 }  // namespace
 
-int split_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+int split_rows(int64_t rows) { return rows <= 16 ? 16 : kSplitMaxRows; }
 int split_grid(int num_sms) { return 2 * num_sms; }
 
 cudaError_t configure_attn_split() {
   cudaError_t e = cudaSuccess;
 #define COLI_CFG(T, D)                                  \
   if (e == cudaSuccess) e = configure<T, D, 1>();       \
-  if (e == cudaSuccess) e = configure<T, D, 2>();       \
-  if (e == cudaSuccess) e = configure<T, D, 4>();
+  if (e == cudaSuccess) e = configure<T, D, 2>();
   COLI_CFG(Bf16, 64) COLI_CFG(Bf16, 128) COLI_CFG(Fp16, 64) COLI_CFG(Fp16, 128)
 #undef COLI_CFG
   return e;
@@ -409,12 +403,12 @@ cudaError_t configure_attn_split() {
 
 cudaError_t launch_attn_split(const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v,
                               int rows, int dtype, int num_sms, cudaStream_t stream) {
-  const int r = split_rows(rows), grid = split_grid(num_sms);
+  const int grid = split_grid(num_sms);
   if (dtype == COLI_ATTN_BF16)
-    return p.head_dim == 64 ? launch_rows<Bf16, 64>(p, k, v, r, grid, stream)
-                            : launch_rows<Bf16, 128>(p, k, v, r, grid, stream);
-  return p.head_dim == 64 ? launch_rows<Fp16, 64>(p, k, v, r, grid, stream)
-                          : launch_rows<Fp16, 128>(p, k, v, r, grid, stream);
+    return p.head_dim == 64 ? launch_rows<Bf16, 64>(p, k, v, rows, grid, stream)
+                            : launch_rows<Bf16, 128>(p, k, v, rows, grid, stream);
+  return p.head_dim == 64 ? launch_rows<Fp16, 64>(p, k, v, rows, grid, stream)
+                          : launch_rows<Fp16, 128>(p, k, v, rows, grid, stream);
 }
 
 }  // namespace coli

@@ -235,8 +235,7 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
           const int j0 = u.tile(i >> 1) * kTileKeys, sg = it % NST;
           if (it >= NST) ok = wait(empty + sg, ((it / NST) + 1) & 1);
           if (!ok) break;
-          fill_boxes<kTileKeys, D, 1>(p, i & 1 ? &vmap : &kmap, nullptr, ring + sg * C::tile_bytes, full + sg, nullptr, 0,
-                                      row, u.p0, u.p1, j0, u.head, lane);
+          fill_boxes<kTileKeys, D, 1>(p, i & 1 ? &vmap : &kmap, nullptr, ring + sg * C::tile_bytes, full + sg, row, u.p0, u.p1, j0, u.head, lane);
         }
       }
       u.i1 = 0;

@@ -304,6 +304,36 @@ def test_prefix_ignores_what_a_row_does_not_see(n_q, n_kv):
         s.shared()
 
 
+@pytest.mark.parametrize("n_q,n_kv,D,page,dt,seqs,news", [
+    (16, 16, 128, 16, BF, 20, [1, 3, 0, 2]), (48, 8, 128, 64, BF, 70, [1]), (64, 8, 64, 32, HF, 45, [1, 5, 2]),
+    (256, 8, 64, 128, BF, 40, [1, 2]), (10, 5, 128, 256, HF, 150, [4, 1])])
+@pytest.mark.parametrize("prefix", [0, 1, 70, 1500])
+def test_prefix_many_sequences(n_q, n_kv, D, page, dt, seqs, news, prefix):
+    """more than two blocks of own keys an SM: sequences and prefix in launches of their own; equal calls give equal bits"""
+    news = (news * seqs)[:seqs]
+    s = Setup(news, [n + 37 * i % 150 for i, n in enumerate(news)], n_q, n_kv, D, page, dt, prefix=prefix)
+    assert s.eng.launches("prefix", seqs) == 3
+    a = s.shared()
+    for _ in range(20):
+        assert torch.equal(s.eng.prefix(s.cache, s.batch, s.prefix_table, s.prefix_len, s.q), a)
+    assert s.eng.status() == 0
+
+
+def test_prefix_many_sequences_ignore_what_a_row_does_not_see():
+    """the rows that see NaN, and only they, have it; the call after it is clean again"""
+    s = Setup([2] * 160, [20 + i for i in range(160)], 8, 2, 64, 16, BF, prefix=300)
+    a = s.shared()
+    j = s.lens[7] - 1  # the last token of sequence 7: the query before it does not see it
+    pg = int(s.table[7, j // 16])
+    s.kc[pg, :, j % 16], s.vc[pg, :, j % 16] = math.nan, math.nan
+    out = s.eng.prefix(s.cache, s.batch, s.prefix_table, s.prefix_len, s.q)
+    keep = torch.ones(s.T, dtype=torch.bool, device="cuda")
+    keep[15] = False
+    assert (s.off(out, s.reference())[keep] <= 1).all() and not torch.isfinite(out[15]).any()
+    s.kc[pg, :, j % 16], s.vc[pg, :, j % 16] = s.keys[7][:, j].to(BF), s.vals[7][:, j].to(BF)
+    assert torch.equal(s.eng.prefix(s.cache, s.batch, s.prefix_table, s.prefix_len, s.q), a)
+
+
 # ---- append ----
 
 def rotated(x, pos, freq, rot, interleaved):
