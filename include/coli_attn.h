@@ -77,7 +77,7 @@ typedef struct {
   const int32_t* table;   /* device [n_seqs][table_stride]: page ids, 0..n_pages-1 where used        */
   int64_t table_stride;   /* >= max_pages                                                            */
   int32_t n_seqs, max_pages, n_tokens;
-  int32_t max_q; /* at least the new tokens of any sequence (picks the kernels, not the result)       */
+  int32_t max_q; /* at least the new tokens of any sequence (picks the kernels and sizes the last one) */
 } coli_attn_batch;
 
 /* Validates cfg and allocates the workspace on the current device.  EINVAL: a value out of the
@@ -126,7 +126,8 @@ int coli_attn_prefix(coli_attn* h, const coli_attn_kv* kv, const coli_attn_batch
                      void* out_dev, int64_t out_stride, float* lse_dev, void* stream);
 
 /* Device status of the handle: COLI_OK; COLI_EINVAL when an earlier call met lengths, offsets or
- * page ids out of range (lengths are clamped, such a page reads as zeros and is not written);
+ * page ids out of range (lengths are clamped, such a page reads as zeros and is not written), or a window or
+ * prefix call a sequence of more than max_q new tokens (rows of its output may be missing);
  * COLI_ETIMEOUT when a bounded wait gave up (that call's output is undefined).  The word is then
  * cleared.  Synchronises `stream`. */
 int coli_attn_status(coli_attn* h, void* stream);

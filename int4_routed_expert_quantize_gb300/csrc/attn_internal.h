@@ -16,9 +16,9 @@ constexpr int kAttnPrefixRows = 8;    // tokens per sequence the prefix workspac
 constexpr int kAttnMaxPairs = 64;     // rotated pairs of a head
 constexpr int kAttnNoWindow = 1 << 30;
 // AttnParams::unit_cost of the two kernels.  Geometric mean over 23 batches, us, with 1 / 2 / 3 for the split kernel:
-// 35.3 / 34.9 / 35.1; with 2 / 3 / 4 / 6 for the tensor-memory kernel: 35.4 / 35.3 / 35.3 / 35.7.
+// 32.1 / 31.7 / 31.7; with 1 / 2 / 3 / 4 / 6 for the tensor-memory kernel: 31.7 / 31.4 / 31.7 / 32.0 / 32.9.
 constexpr int kSplitUnitCost = 2;
-constexpr int kTileUnitCost = 3;
+constexpr int kTileUnitCost = 2;
 constexpr int kSplitMaxRows = 32;     // rows of a block of the split kernel, and of a sequence it takes
 constexpr int kSplitKeys = 64;        // keys per tile of the split kernel
 constexpr int kTileKeys = 128;        // keys per tile of the tensor-memory kernel
@@ -45,6 +45,7 @@ struct AttnParams {
   const int32_t* table;
   int64_t table_stride;
   int n_seqs, n_tokens, max_pages;  // n_seqs 0: the shared prefix alone
+  int max_q;  // new tokens of a sequence at most (from more, rows of cut units go missing, which is reported)
   // the shared prefix, or nullptr: one more sequence (number n_seqs) with all n_tokens queries, each of which
   // sees all its keys
   const int32_t* pre_len;

@@ -35,14 +35,14 @@ __device__ __forceinline__ SeqInfo seq_info(const AttnParams& p, int b) {
 
 __device__ __forceinline__ int n_lists(const AttnParams& p) { return p.n_seqs + (p.pre_len ? 1 : 0); }
 
-// what seq_info clamps is reported once per call
+// what seq_info clamps, and more new tokens than announced, is reported once per call
 __device__ __forceinline__ void seq_check(const AttnParams& p, int b) {
   const bool own = b < p.n_seqs;
   const int l = __ldg(own ? p.kv_len + b : p.pre_len);
   bool bad = l < 0 || (int64_t)l > ((int64_t)(own ? p.max_pages : p.pre_pages) << p.page_shift);
   if (own) {
     const int a = __ldg(p.q_start + b), e = __ldg(p.q_start + b + 1);
-    bad = bad || a < 0 || e < a || e > p.n_tokens || (b == 0 && a != 0);
+    bad = bad || a < 0 || e < a || e > p.n_tokens || e - a > p.max_q || (b == 0 && a != 0);
   }
   if (bad) atomicExch(p.status, COLI_EINVAL);
 }

@@ -416,6 +416,20 @@ def test_lengths_and_pages_out_of_range_are_reported():
     assert torch.equal(s.kc, kc) and s.eng.status() == -1
 
 
+def test_more_new_tokens_than_announced_is_reported():
+    s = Setup([1, 3], [40, 40], 4, 2, 64, 16, BF, junk=0.0, prefix=50)
+    a = s.eng.window(s.cache, s.batch, s.q)
+    right = s.batch
+    s.batch = attn.Batch(right.q_start, right.kv_len, s.table, n_tokens=4, max_q=2)
+    s.eng.window(s.cache, s.batch, s.q)
+    assert s.eng.status() == -1
+    s.eng.prefix(s.cache, s.batch, s.prefix_table, s.prefix_len, s.q)
+    assert s.eng.status() == -1
+    s.batch = right
+    assert torch.equal(s.eng.window(s.cache, s.batch, s.q), a)
+    s.shared()
+
+
 def test_refusals():
     s = Setup([1, 1], [40, 40], 4, 2, 64, 16, BF, junk=0.0)
     E = coli.ColiError
