@@ -1,9 +1,11 @@
 // Joins partial attention results of the same query rows:
 //   m = max m_i,  o = sum 2^(m_i - m) o_i / sum 2^(m_i - m) l_i
 // with o_i unnormalised, m_i the partial's maximum in log2 units and l_i its sum.  Parts are added in
-// the order of the keys, so equal calls give equal bits.  One warp takes one row: the parts'
-// (m, l) pairs are read one per lane, the outputs four values per lane.  The kernels are bound by the
-// L2 reads of the parts.
+// the order of the keys, so equal calls give equal bits.  The parts of few rows are read by a warp a row, the (m, l)
+// pairs one per lane and the outputs two or four values per lane; of many rows by a warp for four rows, where every load is a
+// whole line.  The kernels are bound by the latency of their L2 reads: after the last part is written, 3 to 5 us of a
+// small call pass before the output is (record, parts, join, store), so every address is worked out while the launch
+// before still runs, and as many parts are on their way as registers allow.
 #include "attn_device.cuh"
 
 namespace coli {
@@ -11,10 +13,14 @@ namespace coli {
 namespace {
 
 constexpr int kWarps = 4;
-// Parts a row has on its way.  More hide more of the L2's latency where the grid is small, and cost registers, so warps,
-// where it is large.  us with 4 / 8 / 16 on their way: one token's decode 10.6 / 10.2 / 9.4, mixed batch
-// 139 / 141 / 150; prefix with 8 / 16: 24 rows a key head 14.9 / 14.1, 32 chats 48.1 / 47.1, 256 sequences 303 / 316.
-constexpr int kSmallCombine = 1024, kSmallJoin = 4096;  // rows (tokens x heads) up to which 16 are taken
+// Parts on their way: more hide more of the L2's latency, and cost registers, so warps.  A row's parts are many where the
+// split kernel has few rows, so there a warp takes one row with 16 of its parts on their way; elsewhere four rows with 4 each
+// (combine), or one with 8 (join).
+// Combine, us, one row a warp / four, after the split kernel: one token 9.4 / 9.8, one sequence of 5 new tokens (240 rows)
+// 17.4 / 18.9, 8 of 4 (1536 rows) 13.9 / 13.0; after the tensor-memory kernel: one of 16 (768 rows) 19.7 / 18.1, 8 of 32
+// 56.3 / 49.3.  Join, 16 / 8 on their way: 32 chats 37.0 / 34.6, 64 sequences behind 2000 tokens 32.5 / 30.1, 256 286 / 276;
+// after the split kernel alone, 24 rows a key head: 14.1 / 14.9.
+constexpr int64_t kSmallCombine = 1024;  // rows (tokens x heads) after the split kernel up to which a warp takes one
 
 // one part of a row: its unnormalised output, and its maximum and sum
 struct Part {
@@ -237,7 +243,7 @@ __device__ __forceinline__ void join_four(const AttnParams& p, int rows, const A
     p.lse[(int64_t)token * p.n_q + hq] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994530942f;
 }
 
-// SMALL: a warp a row, 16 parts of it on their way; otherwise four rows a warp
+// SMALL: a warp a row; otherwise four rows a warp
 template <class T, int D, bool SMALL>
 __global__ void __launch_bounds__(kWarps * 32) attn_combine_kernel(const AttnParams p, int rows, int ctas, int block_rows) {
   griddep_wait();
@@ -400,17 +406,15 @@ template <class T, int D>
 cudaError_t join(const AttnParams& own, int own_rows, const AttnParams& shared, bool same, int shared_ctas,
                  cudaStream_t stream) {
   const dim3 grid((unsigned)(((int64_t)own.n_tokens * own.n_q + kWarps - 1) / kWarps));
-  const bool small = (int64_t)own.n_tokens * own.n_q <= kSmallJoin;
-  const bool tile = same && own_rows == kTileRows;
-  const auto k16 = tile ? attn_join_kernel<T, D, kTileKeys, 16> : same ? attn_join_kernel<T, D, kSplitKeys, 16> : attn_join_kernel<T, D, 0, 16>;
-  const auto k8 = tile ? attn_join_kernel<T, D, kTileKeys, 8> : attn_join_kernel<T, D, 0, 8>;
-  // (the split kernel alone: at most kSplitMaxRows rows a key head)
-  return go(small || (same && !tile) ? k16 : k8, grid, stream, own, own_rows, shared, shared_ctas);
+  const auto kernel = !same                     ? attn_join_kernel<T, D, 0, 8>
+                      : own_rows == kTileRows ? attn_join_kernel<T, D, kTileKeys, 8>
+                                              : attn_join_kernel<T, D, kSplitKeys, 16>;
+  return go(kernel, grid, stream, own, own_rows, shared, shared_ctas);
 }
 
 template <class T, int D>
 cudaError_t combine(const AttnParams& p, int rows, int live, int ctas, cudaStream_t stream) {
-  const bool small = (int64_t)p.n_tokens * p.n_q <= kSmallCombine;
+  const bool small = rows <= kSplitMaxRows && (int64_t)p.n_tokens * p.n_q <= kSmallCombine;
   const int block_rows = small ? 4 : 16;
   const dim3 grid(ctas * ((live + block_rows - 1) / block_rows));
   return small ? go(attn_combine_kernel<T, D, true>, grid, stream, p, rows, ctas, block_rows)
