@@ -110,8 +110,8 @@ int coli_attn_append(coli_attn* h, const coli_attn_kv* kv, const coli_attn_batch
  * key j when j <= p and (p - j < window or j < sinks).  window < 0: all keys up to p; window = 0:
  * the sinks alone.  sinks >= 0, scale > 0.  lse_dev [n_tokens, n_q]: natural log-sum-exp of the scaled scores, or
  * NULL.  Strides as in append.  q_dev must not overlap out_dev (their rows may lie
- * between one another).  EUNSUPPORTED: the batch's key tiles could exceed 2^31 (tokens / 2, sequences and
- * key heads times max_pages * page / 64, or the window: split the call). */
+ * between one another).  EUNSUPPORTED: the batch could have 2^31 key tiles (n_kv times its blocks,
+ * one or more a sequence, times max_pages * page / 64, or the window's share of that): split the call. */
 int coli_attn_window(coli_attn* h, const coli_attn_kv* kv, const coli_attn_batch* batch,
                      const void* q_dev, int64_t q_stride, int window, int sinks, float scale,
                      void* out_dev, int64_t out_stride, float* lse_dev, void* stream);
@@ -119,7 +119,7 @@ int coli_attn_window(coli_attn* h, const coli_attn_kv* kv, const coli_attn_batch
 /* Attention of a batch behind a shared prefix: every query sees all prefix_len_dev[0] tokens of the
  * pages prefix_table_dev [prefix_pages] and the keys up to its own position of its own cache (whose
  * positions count from the end of the prefix; kv_len may be 0).  prefix_len is at most prefix_pages * page.
- * n_tokens <= 8 * max_seqs. */
+ * n_tokens <= 8 * max_seqs.  EUNSUPPORTED as for window, prefix_pages included. */
 int coli_attn_prefix(coli_attn* h, const coli_attn_kv* kv, const coli_attn_batch* batch,
                      const int32_t* prefix_table_dev, int prefix_pages,
                      const int32_t* prefix_len_dev, const void* q_dev, int64_t q_stride, float scale,

@@ -217,13 +217,14 @@ bool one_prefix_launch(const coli_attn* h, int n_seqs) {
   return h->cfg.n_q / h->cfg.n_kv > kSplitMaxRows || (int64_t)n_seqs * h->cfg.n_kv <= 2 * h->num_sms;
 }
 
-// the work list's positions are 32-bit: its length is bounded by the page table's width (or the window)
-int list_fits(const coli_attn_batch* b, const AttnParams& p, int64_t pages, int keys) {
-  const int64_t len = pages << p.page_shift;
+// the work list's positions are 32-bit: its length is bounded by the page tables' widths (or the window)
+int list_fits(const AttnParams& p, int keys) {
+  const int64_t len = (int64_t)(p.pre_pages > p.max_pages ? p.pre_pages : p.max_pages) << p.page_shift;
   int64_t span = len;
   if (p.window < kAttnNoWindow && p.window + (int64_t)p.block_tokens + p.sinks + 2 * keys < len)
     span = p.window + (int64_t)p.block_tokens + p.sinks + 2 * keys;
-  const int64_t units = ((int64_t)b->n_tokens / p.block_tokens + b->n_seqs + 1) * p.n_kv;
+  const int64_t blocks = p.n_tokens / p.block_tokens;  // whole ones: each sequence, and the prefix, may have one more
+  const int64_t units = (blocks + p.n_seqs + (p.pre_len ? blocks + 1 : 0)) * p.n_kv;
   return units <= 0x7FFFFFFF / (span / keys + 2 + p.unit_cost) ? COLI_OK : COLI_EUNSUPPORTED;
 }
 
@@ -382,14 +383,14 @@ extern "C" int coli_attn_window(coli_attn* h, const coli_attn_kv* kv, const coli
   if (seq_rows <= kSplitMaxRows) {
     const int rows = split_rows(seq_rows), ctas = split_grid(h->num_sms);
     p.block_tokens = rows / p.group;
-    rc = list_fits(b, p, b->max_pages, kSplitKeys);
+    rc = list_fits(p, kSplitKeys);
     if (rc) return rc;
     e = launch_attn_split(p, kv->maps.k64, kv->maps.v64, rows, h->cfg.dtype, h->num_sms, st);
     if (e == cudaSuccess) e = launch_attn_combine(p, rows, (int)seq_rows, ctas, h->cfg.dtype, st);
   } else {
     use_tile(h, &p);
     CUtensorMap qm;
-    rc = list_fits(b, p, b->max_pages, kTileKeys);
+    rc = list_fits(p, kTileKeys);
     if (rc) return rc;
     if (!query_map(&qm, h, q, q_stride, b->n_tokens)) return COLI_ECUDA;
     e = launch_attn_tile(p, qm, kv->maps.k128, kv->maps.v128, h->cfg.dtype, h->num_sms, st);
@@ -416,19 +417,19 @@ extern "C" int coli_attn_prefix(coli_attn* h, const coli_attn_kv* kv, const coli
   own.dense_o[1] = h->dense_o2, own.dense_ml[1] = h->dense_ml2;
   AttnParams pre = own;
   pre.pre_len = prefix_len, pre.pre_table = prefix_table, pre.pre_pages = prefix_pages;
-  const int64_t pages = b->max_pages > prefix_pages ? b->max_pages : prefix_pages, all_rows = (int64_t)b->n_tokens * own.group;
+  const int64_t all_rows = (int64_t)b->n_tokens * own.group;
   CUtensorMap qm;
   cudaError_t e;
   if (all_rows <= kSplitMaxRows) {  // one launch, the prefix as one more sequence of all tokens
     const int rows = split_rows(all_rows);
     pre.block_tokens = rows / own.group;
-    rc = list_fits(b, pre, pages, kSplitKeys);
+    rc = list_fits(pre, kSplitKeys);
     if (rc) return rc;
     e = launch_attn_split(pre, kv->maps.k64, kv->maps.v64, rows, h->cfg.dtype, h->num_sms, st);
     if (e == cudaSuccess) e = launch_attn_join(pre, rows, pre, true, 0, h->cfg.dtype, st);
   } else if (one_prefix_launch(h, b->n_seqs)) {  // as above
     use_tile(h, &pre);
-    rc = list_fits(b, pre, pages, kTileKeys);
+    rc = list_fits(pre, kTileKeys);
     if (rc) return rc;
     if (!query_map(&qm, h, q, q_stride, b->n_tokens)) return COLI_ECUDA;
     e = launch_attn_tile(pre, qm, kv->maps.k128, kv->maps.v128, h->cfg.dtype, h->num_sms, st);
@@ -440,7 +441,8 @@ extern "C" int coli_attn_prefix(coli_attn* h, const coli_attn_kv* kv, const coli
     pre.n_seqs = 0;
     pre.seq_pos = nullptr;  // the split kernel's, at the same time
     pre.late_wait = 1;
-    rc = list_fits(b, own, pages, kSplitKeys);
+    rc = list_fits(own, kSplitKeys);
+    if (!rc) rc = list_fits(pre, kTileKeys);
     if (rc) return rc;
     if (!query_map(&qm, h, q, q_stride, b->n_tokens)) return COLI_ECUDA;
     e = launch_attn_split(own, kv->maps.k64, kv->maps.v64, rows, h->cfg.dtype, h->num_sms, st);

@@ -430,6 +430,26 @@ def test_more_new_tokens_than_announced_is_reported():
     s.shared()
 
 
+def test_lists_that_do_not_fit_are_refused():
+    """tables so wide that the positions of the work list could pass 32 bits: refused before anything is launched"""
+    z = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    wide = z(1, 2 ** 22)  # 2^30 tokens: 2^24 tiles of 64 or 2^23 of 128
+    for n_kv, news, group in ((130, 1, 1), (256, 8, 8)):
+        eng = attn.PagedAttention(n_kv * group, n_kv, 64, 256, news, 1)
+        cache = eng.bind_cache(*[torch.zeros((1, n_kv, 256, 64), dtype=BF, device="cuda") for _ in range(2)])
+        q = torch.zeros((news, n_kv * group, 64), dtype=BF, device="cuda")
+        start, length = torch.tensor([0, news], dtype=torch.int32, device="cuda"), torch.tensor([news], dtype=torch.int32, device="cuda")
+        narrow = attn.Batch(start, length, z(1, 1), n_tokens=news, max_q=news)
+        calls = [lambda: eng.window(cache, attn.Batch(start, length, wide, n_tokens=news, max_q=news), q),
+                 lambda: eng.prefix(cache, narrow, wide[0], z(1), q)]
+        for call in calls:
+            before = eng.window(cache, narrow, q)
+            with pytest.raises(coli.ColiError) as e:
+                call()
+            assert e.value.status == -6  # COLI_EUNSUPPORTED
+            assert torch.equal(eng.window(cache, narrow, q), before) and eng.status() == 0
+
+
 def test_refusals():
     s = Setup([1, 1], [40, 40], 4, 2, 64, 16, BF, junk=0.0)
     E = coli.ColiError
