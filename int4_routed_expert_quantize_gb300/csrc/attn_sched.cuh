@@ -212,7 +212,8 @@ struct Walk {
   }
   // Up to 32 sequences: one a lane, nothing through shared memory, and the other warps need not wait.  It is run twice:
   // first (real = false) while the launches before this one still run, on whatever the lengths are then and with
-  // nothing written, so that its instructions are in the caches when its inputs are final.
+  // nothing written, so that its instructions are in the caches when its inputs are final.  us with start() for all / this:
+  // one token 9.8 / 9.4, 13 sequences of 5 14.3 / 13.5, 4 answers behind 7036 tokens 22.2 / 15.0.
   __device__ __forceinline__ void start_few(const AttnParams& p, int lane, bool real) {
     const int ns = n_lists(p);
     SeqInfo mine = {0, 0, 0, true};
