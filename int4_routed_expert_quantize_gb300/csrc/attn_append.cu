@@ -7,16 +7,19 @@
 //
 // A lane holds 16 values (8 pairs) of a head, so D/16 lanes make a head and a warp 4 or 8 heads; its 8 sines
 // and cosines serve all heads that the warp handles for its token.  Bound by HBM: q, k, v are read
-// once, q', k', v written once, in 16-byte accesses.  16384 tokens of 48 query and 8 key heads of 128: 537 MB in 82.8 us,
-// 6.48 TB/s (a copy reaches 6.78); 16 tokens 4.0 us, which is the launch.
+// once, q', k', v written once, in 16-byte accesses.  16384 tokens of 48 query and 8 key heads of 128: 537 MB in 83 us,
+// 6.5 TB/s (a copy reaches 6.78); 16 tokens 2.6 us, which is the launch.
 #include "attn_device.cuh"
 
 namespace coli {
 
 namespace {
 
-constexpr int kAppendWarps = 8;
-// groups of heads a warp has in flight; us with 2 / 4 / 8: 16384 tokens 84.0 / 82.5 / 82.8, 7 chunks of up to 331 8.7 / 8.4 / 10.6
+// warps a block: the warps share nothing, and small blocks spread evenly and start as others end; us with 1 / 2 / 8: 16 tokens
+// 2.6 / 2.6 / 2.9, 700 5.2 / 5.3 / 6.0, 4000 24.3 / 26.8 / 27.8, 16384 83.1 / 82.6 / 82.6
+constexpr int kAppendWarps = 1;
+// groups of heads a warp has in flight; us with 2 / 3 / 4: 700 tokens 5.6 / 5.5 / 5.3, 2000 15.9 / 15.1 /
+// 14.6, 16384 83.8 / 83.7 / 82.6 (8 take so many registers that 16384 take 82.8 and 500 10.4 / 8.5)
 constexpr int kAhead = 4;
 
 template <class T>
