@@ -39,6 +39,7 @@ struct AttnParams {
   int64_t q_stride;
   void* out;
   int64_t out_stride;
+  bool out_sectors;  // every head of out starts on a 32-byte boundary (otherwise on a 16-byte one)
   float* lse;
   const int32_t* q_start;
   const int32_t* kv_len;

@@ -152,6 +152,7 @@ AttnParams params(const coli_attn* h, const coli_attn_kv* kv, const coli_attn_ba
                   int64_t q_stride, void* out, int64_t out_stride, float* lse, float scale) {
   AttnParams p = {};
   p.q = q, p.q_stride = q_stride, p.out = out, p.out_stride = out_stride, p.lse = lse;
+  p.out_sectors = (((uintptr_t)out | (uintptr_t)out_stride * 2) & 31u) == 0;
   p.q_start = b->q_start, p.kv_len = b->kv_len, p.table = b->table, p.table_stride = b->table_stride;
   p.n_seqs = b->n_seqs, p.n_tokens = b->n_tokens, p.max_pages = b->max_pages, p.max_q = b->max_q;
   p.n_q = h->cfg.n_q, p.n_kv = h->cfg.n_kv, p.group = h->cfg.n_q / h->cfg.n_kv, p.head_dim = h->cfg.head_dim;

@@ -151,11 +151,21 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
   return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u;
 }
 
-// 32 bytes of a thread's row at once: a full sector per thread
+// 32 bytes of a thread's row at once: a full sector per thread.  p on a 32-byte boundary
 __device__ __forceinline__ void st_sector(void* p, const uint32_t (&v)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
                "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
+}
+// The same of the caller's output, whose heads start on 16-byte boundaries: in one store where they all start on 32, else
+// in two.  8192 tokens, window 4096, back to back: 449 us in one store, 487 in two.
+__device__ __forceinline__ void st_out(void* p, const uint32_t (&v)[8], bool sectors) {
+  if (sectors) {
+    st_sector(p, v);
+  } else {
+    uint4* q = static_cast<uint4*>(p);
+    q[0] = make_uint4(v[0], v[1], v[2], v[3]), q[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
 }
 
 template <class T, int D>
@@ -494,10 +504,10 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
             uint32_t w[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) w[k] = T::pack(o[2 * k] * inv, o[2 * k + 1] * inv);
-            st_sector(dst + c, w);
+            st_out(dst + c, w, p.out_sectors);
 #pragma unroll
             for (int k = 0; k < 8; ++k) w[k] = T::pack(o[16 + 2 * k] * inv, o[17 + 2 * k] * inv);
-            st_sector(dst + c + 16, w);
+            st_out(dst + c + 16, w, p.out_sectors);
           }
         }
         if (live && p.lse)

@@ -1,0 +1,40 @@
+"""The edges of what the attention calls accept (coli_attn.h): outputs on 16-byte boundaries."""
+import pytest
+import torch
+
+from .test_gpu_attn import BF, HF, Setup
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    torch.cuda.set_device(0)
+
+
+def padded(s, before, after):
+    """an output view `before` values into its buffer, with rows of `after` more values than it needs"""
+    wide = torch.full((before + s.T * (s.n_q * s.D + after),), 7.0, dtype=s.dt, device="cuda")
+    return wide, wide[before:].view(s.T, -1)[:, :s.n_q * s.D].view(s.T, s.n_q, s.D)
+
+
+@pytest.mark.parametrize("before,after", [(8, 0), (0, 8), (8, 8), (24, 40), (16, 16)])
+@pytest.mark.parametrize("D,dt,news,lens", [
+    (128, BF, [40, 300], [40, 900]), (64, HF, [100, 7], [333, 7]), (64, BF, [1, 4], [70, 90]), (128, HF, [1], [2000])])
+def test_outputs_on_16_byte_boundaries(before, after, D, dt, news, lens):
+    """bases and strides of 8 values: whole units, cut ones, and the prefix call's; nothing between the rows is written"""
+    s = Setup(news, lens, 6, 2, D, 16, dt)
+    want = s.window(window=200, sinks=3)
+    wide, out = padded(s, before, after)
+    assert s.eng.window(s.cache, s.batch, s.q, window=200, sinks=3, out=out) is out
+    assert torch.equal(out, want)
+    assert not (wide[:before] != 7).any() and not (wide[before:].view(s.T, -1)[:, s.n_q * s.D:] != 7).any()
+    p = Setup([1, 2, 1], [9, 70, 3], 6, 2, D, 16, dt, prefix=333)
+    want = p.shared()
+    wide, out = padded(p, before, after)
+    p.eng.prefix(p.cache, p.batch, p.prefix_table, p.prefix_len, p.q, out=out)
+    assert torch.equal(out, want)
+    assert not (wide[:before] != 7).any() and not (wide[before:].view(p.T, -1)[:, p.n_q * p.D:] != 7).any()
+    assert s.eng.status() == 0 and p.eng.status() == 0
