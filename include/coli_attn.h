@@ -75,7 +75,7 @@ typedef struct {
   const int32_t* q_start; /* device [n_seqs+1], ascending from 0 to n_tokens                        */
   const int32_t* kv_len;  /* device [n_seqs], 0..max_pages*page                                     */
   const int32_t* table;   /* device [n_seqs][table_stride]: page ids, 0..n_pages-1 where used        */
-  int64_t table_stride;   /* >= max_pages                                                            */
+  int64_t table_stride;   /* >= max_pages, or 0: all sequences share one row                         */
   int32_t n_seqs, max_pages, n_tokens;
   int32_t max_q; /* at least the new tokens of any sequence (picks the kernels and sizes the last one) */
 } coli_attn_batch;

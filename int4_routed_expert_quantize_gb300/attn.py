@@ -74,11 +74,21 @@ def _int32(t, dims, what):
     return t
 
 
+def _row_stride(table):
+    """elements between the rows of a page table; 0: an expanded row, which all sequences share"""
+    rows, width = table.shape
+    if rows < 2:  # one row has no stride of its own
+        return width
+    if 0 < table.stride(0) < width:
+        raise ValueError("table: rows that overlap")
+    return table.stride(0)
+
+
 class Batch:
     """The ragged batch of a call: sequence b has the query tokens q_start[b] .. q_start[b+1]-1, the last
-    of its kv_len[b] cached tokens, whose pages are table[b].  The three int32 tensors stay the
-    caller's (they may be updated in place between calls and are read on the device); n_tokens is the
-    number of query tokens, max_q at least the new tokens of any sequence."""
+    of its kv_len[b] cached tokens, whose pages are table[b] (rows may be slices of wider ones, or one row
+    expanded).  The three int32 tensors stay the caller's (they may be updated in place between calls and are
+    read on the device); n_tokens is the number of query tokens, max_q at least the new tokens of any sequence."""
 
     def __init__(self, q_start, kv_len, table, n_tokens, max_q):
         _int32(q_start, 1, "q_start"), _int32(kv_len, 1, "kv_len"), _int32(table, 2, "table")
@@ -88,7 +98,7 @@ class Batch:
         self.q_start, self.kv_len, self.table = q_start, kv_len, table
         self.n_tokens, self.max_q, self.n_seqs = int(n_tokens), int(max_q), n
         self.c = AttnBatch(q_start.data_ptr(), kv_len.data_ptr(), table.data_ptr(),
-                           max(table.stride(0), table.shape[1]), n, table.shape[1], self.n_tokens, self.max_q)
+                           _row_stride(table), n, table.shape[1], self.n_tokens, self.max_q)
         self.ref = ctypes.addressof(self.c)
 
 

@@ -141,8 +141,8 @@ int check_call(const coli_attn* h, const coli_attn_kv* kv, const coli_attn_batch
     return COLI_EINVAL;
   if (b->n_tokens < 0 || b->n_tokens > c.max_tokens || b->n_seqs < 0 || b->n_seqs > c.max_seqs) return COLI_EINVAL;
   if (b->n_tokens == 0) return COLI_OK;
-  if (b->n_seqs == 0 || !b->q_start || !b->kv_len || b->max_pages < 0 || b->table_stride < b->max_pages ||
-      b->max_q < 1 || (b->max_pages > 0 && !b->table) ||
+  if (b->n_seqs == 0 || !b->q_start || !b->kv_len || b->max_pages < 0 ||
+      (b->table_stride < b->max_pages && b->table_stride != 0) || b->max_q < 1 || (b->max_pages > 0 && !b->table) ||
       ((int64_t)b->max_pages << h->page_shift) > kAttnNoWindow)
     return COLI_EINVAL;
   return check_device(h->device);

@@ -1,6 +1,9 @@
-"""The edges of what the attention calls accept (coli_attn.h): outputs on 16-byte boundaries."""
+"""The edges of what the attention calls accept (coli_attn.h): outputs on 16-byte boundaries, page
+tables of several strides."""
 import pytest
 import torch
+
+from int4_routed_expert_quantize_gb300 import attn
 
 from .test_gpu_attn import BF, HF, Setup
 
@@ -38,3 +41,21 @@ def test_outputs_on_16_byte_boundaries(before, after, D, dt, news, lens):
     assert torch.equal(out, want)
     assert not (wide[:before] != 7).any() and not (wide[before:].view(p.T, -1)[:, p.n_q * p.D:] != 7).any()
     assert s.eng.status() == 0 and p.eng.status() == 0
+
+
+@pytest.mark.parametrize("news", [[1, 1, 1], [40, 1, 60]])
+def test_expanded_page_table(news):
+    """several sequences with one row of pages: what a copy of the row for each gives"""
+    s = Setup(news, [300] * 3, 6, 2, 64, 16, BF, prefix=50)
+    row = s.table[1:2].expand(3, -1)
+    assert row.stride(0) == 0
+    b = s.batch
+    one, each = (attn.Batch(b.q_start, b.kv_len, t, n_tokens=s.T, max_q=b.max_q) for t in (row, row.contiguous()))
+    want = s.eng.window(s.cache, each, s.q, window=100, sinks=5)
+    assert torch.equal(s.eng.window(s.cache, one, s.q, window=100, sinks=5), want)
+    if s.T <= 8 * len(news):
+        want = s.eng.prefix(s.cache, each, s.prefix_table, s.prefix_len, s.q)
+        assert torch.equal(s.eng.prefix(s.cache, one, s.prefix_table, s.prefix_len, s.q), want)
+    assert s.eng.status() == 0
+    with pytest.raises(ValueError):  # rows that overlap
+        attn.Batch(b.q_start, b.kv_len, torch.as_strided(s.table, (3, 10), (4, 1)), n_tokens=s.T, max_q=b.max_q)
