@@ -40,6 +40,11 @@ class AttnBatch(ctypes.Structure):
                 ("max_pages", _i), ("n_tokens", _i), ("max_q", _i)]
 
 
+class BatchArgs(ctypes.Structure):  # csrc/attn_py.cpp
+    _anonymous_ = ("batch",)
+    _fields_ = [("batch", AttnBatch), ("device", _i)]
+
+
 class Engine(ctypes.Structure):  # csrc/attn_py.cpp
     _fields_ = [("handle", _vp), ("n_q", _i), ("n_kv", _i), ("head_dim", _i), ("dtype", _i), ("device", _i),
                 ("scale", _f)]
@@ -97,8 +102,10 @@ class Batch:
             raise ValueError("q_start has one entry more than kv_len, table one row for each sequence")
         self.q_start, self.kv_len, self.table = q_start, kv_len, table
         self.n_tokens, self.max_q, self.n_seqs = int(n_tokens), int(max_q), n
-        self.c = AttnBatch(q_start.data_ptr(), kv_len.data_ptr(), table.data_ptr(),
-                           _row_stride(table), n, table.shape[1], self.n_tokens, self.max_q)
+        if not q_start.device == kv_len.device == table.device:
+            raise ValueError("q_start, kv_len and table are on one device")
+        self.c = BatchArgs(AttnBatch(q_start.data_ptr(), kv_len.data_ptr(), table.data_ptr(), _row_stride(table), n,
+                                     table.shape[1], self.n_tokens, self.max_q), table.device.index)
         self.ref = ctypes.addressof(self.c)
 
 
@@ -108,8 +115,10 @@ class KvCache:
     def __init__(self, engine, k, v):
         dims = (engine.n_kv, engine.page, engine.head_dim)
         for t in (k, v):
-            if t.dim() != 4 or tuple(t.shape[1:]) != dims or t.dtype is not engine.dtype or not t.is_cuda:
-                raise ValueError(f"the cache is [pages, {dims[0]}, {dims[1]}, {dims[2]}] of {engine.dtype} on the device")
+            if t.dim() != 4 or tuple(t.shape[1:]) != dims or t.dtype is not engine.dtype or not t.is_cuda or \
+                    t.device.index != engine.device:
+                raise ValueError(f"the cache is [pages, {dims[0]}, {dims[1]}, {dims[2]}] of {engine.dtype} on the "
+                                 "engine's device")
             if t.stride(3) != 1:
                 raise ValueError("a head's values are contiguous")
         if k.shape[0] != v.shape[0]:

@@ -20,6 +20,12 @@ struct Engine {
   float scale;
 };
 
+// what it keeps of a batch
+struct Batch {
+  coli_attn_batch batch;
+  int32_t device;
+};
+
 struct Error {};  // the Python exception is set
 
 [[noreturn]] void fail(const char* format, const char* what) {
@@ -32,6 +38,13 @@ T* pointer(PyObject* o) {
   void* p = PyLong_AsVoidPtr(o);
   if (!p && PyErr_Occurred()) throw Error();
   return static_cast<T*>(p);
+}
+
+// the batch of a call, whose tensors have to be on the engine's device
+const coli_attn_batch& batch(PyObject* o, const Engine& e) {
+  const Batch& b = *pointer<Batch>(o);
+  if (b.device != e.device) fail("%s on the engine's device", "the batch's tensors are");
+  return b.batch;
 }
 
 int64_t integer(PyObject* o) {
@@ -115,7 +128,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 9, [&] {
     const Engine& e = *pointer<Engine>(a[0]);
     const auto* kv = pointer<coli_attn_kv>(a[1]);
-    const coli_attn_batch& b = *pointer<coli_attn_batch>(a[2]);
+    const coli_attn_batch& b = batch(a[2], e);
     const at::Tensor &k = tensor(a[3], "k"), &v = tensor(a[4], "v");
     const int64_t ks = heads(k, e, e.n_kv, b, "k"), vs = heads(v, e, e.n_kv, b, "v");
     const int32_t* base = a[7] == Py_None ? nullptr : int32s(a[7], e, "pos_base");
@@ -139,7 +152,7 @@ PyObject* window(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 10, [&] {
     const Engine& e = *pointer<Engine>(a[0]);
     const auto* kv = pointer<coli_attn_kv>(a[1]);
-    const coli_attn_batch& b = *pointer<coli_attn_batch>(a[2]);
+    const coli_attn_batch& b = batch(a[2], e);
     const at::Tensor& q = tensor(a[3], "q");
     const int64_t qs = heads(q, e, e.n_q, b, "q");
     int64_t w = integer(a[4]), s = integer(a[5]);
@@ -161,7 +174,7 @@ PyObject* prefix(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 10, [&] {
     const Engine& e = *pointer<Engine>(a[0]);
     const auto* kv = pointer<coli_attn_kv>(a[1]);
-    const coli_attn_batch& b = *pointer<coli_attn_batch>(a[2]);
+    const coli_attn_batch& b = batch(a[2], e);
     const int32_t *table = int32s(a[3], e, "prefix_table"), *len = int32s(a[4], e, "prefix_len");
     const int64_t pages = THPVariable_Unpack(a[3]).size(0);
     if (THPVariable_Unpack(a[4]).numel() < 1 || pages > INT32_MAX) fail("%s: one entry", "prefix_len");

@@ -1,5 +1,5 @@
 """The edges of what the attention calls accept (coli_attn.h): outputs on 16-byte boundaries, page
-tables of several strides."""
+tables of several strides, tensors of another device."""
 import pytest
 import torch
 
@@ -59,3 +59,22 @@ def test_expanded_page_table(news):
     assert s.eng.status() == 0
     with pytest.raises(ValueError):  # rows that overlap
         attn.Batch(b.q_start, b.kv_len, torch.as_strided(s.table, (3, 10), (4, 1)), n_tokens=s.T, max_q=b.max_q)
+
+
+def test_tensors_of_another_device_are_refused():
+    """by their device's number, so that one GPU is enough to see it"""
+    s = Setup([1, 1], [40, 40], 4, 2, 64, 16, BF, junk=0.0, prefix=20)
+    k = torch.zeros((2, 2, 64), dtype=BF, device="cuda")
+    s.batch.c.device = s.eng.device + 1
+    for call in (lambda: s.eng.window(s.cache, s.batch, s.q), lambda: s.eng.append(s.cache, s.batch, k, k),
+                 lambda: s.eng.prefix(s.cache, s.batch, s.prefix_table, s.prefix_len, s.q)):
+        with pytest.raises(ValueError):
+            call()
+    s.batch.c.device = s.eng.device
+    s.shared()
+    b = s.batch
+    with pytest.raises(ValueError):  # not all on one device
+        attn.Batch(b.q_start.cpu(), b.kv_len, s.table, n_tokens=2, max_q=1)
+    s.eng.device += 1
+    with pytest.raises(ValueError):
+        s.eng.bind_cache(s.kc, s.vc)
