@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   if (!KT) {  // the prefix alone on its list: the stretch follows from its length
     const uint32_t blocks = (pre.n + shared.block_tokens - 1) / shared.block_tokens;
     const uint32_t total = blocks * shared.n_kv * (far.tiles + shared.unit_cost);
-    far_per = max(1u, (total + shared_ctas - 1) / shared_ctas);
+    far_per = list_stretch(total, shared_ctas, 0);
   }
   griddep_wait();
   griddep_launch_dependents();

@@ -4,6 +4,7 @@
 #pragma once
 
 #include "attn_internal.h"
+#include "attn_stretch.h"
 #include "coli_device.cuh"
 
 namespace coli {
@@ -169,13 +170,8 @@ struct Walk {
   Tiles<KT> t;
   uint32_t begin, end, per, at;  // at: the current unit's first position
   int b, blk, head;
-  // longest: the tiles of the longest unit that may be cut into single tiles (0: none)
   __device__ __forceinline__ void cut(const AttnParams& p, uint32_t run, int longest) {
-    per = max(1u, (run + gridDim.x - 1) / gridDim.x);
-    // Few CTAs' worth of work: a longer stretch costs a tile's time a position, a shorter one costs the joining
-    // kernel a round of loads per 16 parts, so the best stretch grows with the root of the unit (110 tiles of one
-    // unit: 20.0 us in stretches of 1, 15.6 in stretches of 2).
-    while ((int)(per * per) * 12 < longest) ++per;
+    per = list_stretch(run, gridDim.x, longest);
     begin = min(blockIdx.x * per, run);
     end = min(begin + per, run);
     b = blk = head = 0;

@@ -1,0 +1,26 @@
+// The arithmetic of the attention work list that needs no GPU: the kernels use it, and so do plain host compilers.
+#pragma once
+
+#include <stdint.h>
+
+#ifdef __CUDACC__
+#define COLI_BOTH __host__ __device__ __forceinline__
+#else
+#define COLI_BOTH inline
+#endif
+
+namespace coli {
+
+// Positions of a list of `run` that one of `ctas` CTAs takes.  longest: the tiles of the longest unit that may be cut into
+// single tiles (0: none).
+// Few CTAs' worth of work: a longer stretch costs a tile's time a position, a shorter one costs the joining
+// kernel a round of loads per 16 parts, so the best stretch grows with the root of the unit (110 tiles of one
+// unit: 20.0 us in stretches of 1, 15.6 in stretches of 2).
+COLI_BOTH uint32_t list_stretch(uint32_t run, uint32_t ctas, int longest) {
+  uint32_t per = run / ctas + (run % ctas != 0);
+  if (per == 0) per = 1;
+  while ((uint64_t)per * per * 12 < (uint64_t)longest) ++per;
+  return per;
+}
+
+}  // namespace coli

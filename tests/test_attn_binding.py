@@ -1,8 +1,11 @@
-"""The host side of the attention binding, without a GPU."""
+"""The host side of the attention binding and the arithmetic of its work list, without a GPU."""
+import random
+import subprocess
+
 import pytest
 import torch
 
-from int4_routed_expert_quantize_gb300 import attn
+from int4_routed_expert_quantize_gb300 import _build, attn
 
 
 def test_page_table_rows_are_where_the_tensor_has_them():
@@ -16,3 +19,37 @@ def test_page_table_rows_are_where_the_tensor_has_them():
     for rows, width, stride in ((3, 10, 4), (2, 2, 1)):
         with pytest.raises(ValueError):
             attn._row_stride(torch.as_strided(flat, (rows, width), (stride, 1)))
+
+
+def host_program(tmp_path, body):
+    """a program over csrc/attn_stretch.h that ends with an error at undefined operations; -> a call of it on lines"""
+    src, exe = tmp_path / "stretch.cpp", str(tmp_path / "stretch")
+    src.write_text('#include <cstdio>\n#include "attn_stretch.h"\nusing namespace coli;\nint main() {\n' + body + "}\n")
+    subprocess.check_call(["g++", "-O1", "-std=c++17", "-fsanitize=undefined", "-fno-sanitize-recover=all", "-I", _build.CSRC,
+                           str(src), "-o", exe])
+
+    def call(rows):
+        text = "".join(" ".join(map(str, r)) + "\n" for r in rows)
+        out = subprocess.run([exe], input=text, capture_output=True, text=True, timeout=60)
+        assert out.returncode == 0, out.stderr[-500:]
+        return [int(x) for x in out.stdout.split()]
+    return call
+
+
+def test_stretches_of_long_lists(tmp_path):
+    """the smallest length that covers the list with the CTAs and whose square reaches a twelfth of the longest unit"""
+    call = host_program(tmp_path, """
+  unsigned run, ctas;
+  int longest;
+  while (scanf("%u %u %d", &run, &ctas, &longest) == 3) printf("%u\\n", list_stretch(run, ctas, longest));
+  return 0;
+""")
+    r = random.Random(0)
+    rows = [(0, 304, 0), (1, 304, 1), (110, 304, 110), (13378 * 304, 304, 15000), (14000 * 304, 304, 16384),
+            (2 ** 31 - 1, 304, 2 ** 24), (2 ** 31 - 1, 1, 2 ** 24), (46341 * 152, 152, 5), (65536 * 304, 304, 2 ** 24)]
+    rows += [(int(2 ** r.uniform(0, 31)), r.choice([152, 304]), int(2 ** r.uniform(0, 24))) for _ in range(500)]
+    for (run, ctas, longest), per in zip(rows, call(rows)):
+        want = max(1, -(-run // ctas))
+        while want * want * 12 < longest:
+            want += 1
+        assert per == want, (run, ctas, longest)
