@@ -66,7 +66,7 @@ typedef struct {
 typedef struct {
   void* k;
   void* v;
-  int64_t n_pages; /* 1..2^31-1 */
+  int64_t n_pages; /* 1..2^31-2 */
   int64_t k_page_stride, k_head_stride, k_slot_stride;
   int64_t v_page_stride, v_head_stride, v_slot_stride;
 } coli_attn_cache;
@@ -90,7 +90,8 @@ void coli_attn_destroy(coli_attn* h);
 
 /* Describes the caller's cache memory for the calls below (nothing is copied; the memory stays the
  * caller's and must outlive the binding).  EINVAL: NULL, misaligned or non-positive sizes, strides
- * that let tokens overlap.  The handle's shapes give the dims. */
+ * that let tokens of K, or of V, overlap: in order of size, a stride is at least what the smaller ones
+ * span (a dimension of one entry has none, but is given as at least head_dim).  The handle's shapes give the dims. */
 int coli_attn_cache_bind(coli_attn* h, const coli_attn_cache* cache, coli_attn_kv** out);
 void coli_attn_cache_release(coli_attn_kv* kv);
 

@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <cmath>
 #include <mutex>
 #include <new>
@@ -126,6 +127,20 @@ cudaError_t configure_device(int dev) {
 }
 
 bool misaligned(const void* p, int64_t stride) { return ((uintptr_t)p & 15u) || (stride & 7); }
+
+// Whether heads' tokens of `width` elements share memory: dimensions of `extent` entries every `stride`, in any order.
+// Each has to step over all that the smaller strides cover.
+bool overlap(const int64_t (&stride)[3], const int64_t (&extent)[3], int64_t width) {
+  int by[3] = {0, 1, 2};
+  std::sort(by, by + 3, [&](int a, int b) { return stride[a] < stride[b]; });
+  __int128 span = width;
+  for (int i : by) {
+    if (extent[i] < 2) continue;  // never stepped
+    if (stride[i] < span) return true;
+    span += (__int128)(extent[i] - 1) * stride[i];
+  }
+  return false;
+}
 
 int check_device(int device) {
   int dev = -1;
@@ -310,6 +325,10 @@ extern "C" int coli_attn_cache_bind(coli_attn* h, const coli_attn_cache* cache, 
                               c.v_page_stride, c.v_head_stride, c.v_slot_stride};
   for (int64_t s : strides)
     if (s < D || (s & 7) || s >= (1LL << 38)) return COLI_EINVAL;
+  const int64_t extent[3] = {c.n_pages, h->cfg.n_kv, h->cfg.page};
+  if (overlap({c.k_page_stride, c.k_head_stride, c.k_slot_stride}, extent, D) ||
+      overlap({c.v_page_stride, c.v_head_stride, c.v_slot_stride}, extent, D))
+    return COLI_EINVAL;
   if (((uintptr_t)c.k & 15u) || ((uintptr_t)c.v & 15u)) return COLI_EINVAL;
   int rc = check_device(h->device);
   if (rc) return rc;

@@ -1,5 +1,8 @@
 """The edges of what the attention calls accept (coli_attn.h): outputs on 16-byte boundaries, page
-tables of several strides, tensors of another device."""
+tables of several strides, tensors of another device, cache
+strides."""
+import ctypes
+
 import pytest
 import torch
 
@@ -78,3 +81,28 @@ def test_tensors_of_another_device_are_refused():
     s.eng.device += 1
     with pytest.raises(ValueError):
         s.eng.bind_cache(s.kc, s.vc)
+
+
+def bind(strides, n_pages=3, n_kv=2, page=16, D=64):
+    """the status of binding a cache whose K has these strides, and of one whose V has"""
+    eng = attn.PagedAttention(2 * n_kv, n_kv, D, page, 4, 4)
+    mem, good, out = torch.zeros(1 << 16, dtype=BF, device="cuda"), (n_kv * page * D, page * D, D), []
+    for k, v in ((strides, good), (good, strides)):
+        c, h = attn.AttnCache(mem.data_ptr(), mem.data_ptr() + mem.numel(), n_pages, *k, *v), ctypes.c_void_p()
+        out.append(attn.lib().coli_attn_cache_bind(eng.h, ctypes.byref(c), ctypes.byref(h)))
+        attn.lib().coli_attn_cache_release(h)
+    return out
+
+
+@pytest.mark.parametrize("strides", [(64, 64, 64), (2048, 64, 64), (64, 1024, 64), (2048, 1016, 64), (2040, 1024, 64),
+                                     (2048, 64, 120), (1024, 2048, 64), (2 ** 37, 2 ** 37, 64)])
+def test_cache_strides_that_let_tokens_overlap_are_refused(strides):
+    assert bind(strides) == [-1, -1]
+
+
+@pytest.mark.parametrize("strides,kw", [
+    ((2048, 1024, 64), {}), ((2048, 64, 128), {}), ((64, 3072, 192), {}), ((2048, 64, 64), dict(n_kv=1)),
+    ((64, 1024, 64), dict(n_pages=1)), ((2040, 1016, 64), dict(n_pages=1, n_kv=1)), ((3000, 1400, 72), {})])
+def test_cache_strides_in_any_order(strides, kw):
+    """pages, heads and slots nested in any order, padded, or of one entry"""
+    assert bind(strides, **kw) == [0, 0]
