@@ -127,7 +127,8 @@ int coli_attn_prefix(coli_attn* h, const coli_attn_kv* kv, const coli_attn_batch
                      void* out_dev, int64_t out_stride, float* lse_dev, void* stream);
 
 /* Device status of the handle: COLI_OK; COLI_EINVAL when an earlier call met lengths, offsets or
- * page ids out of range (lengths are clamped, such a page reads as zeros and is not written), or a window or
+ * page ids out of range (lengths are clamped, such a page reads as zeros and is not written; rows of tokens that no
+ * sequence has, as when the offsets end before n_tokens, are not written or not complete), or a window or
  * prefix call a sequence of more than max_q new tokens (rows of its output may be missing);
  * COLI_ETIMEOUT when a bounded wait gave up (that call's output is undefined).  The word is then
  * cleared.  Synchronises `stream`. */

@@ -43,7 +43,8 @@ __device__ __forceinline__ void seq_check(const AttnParams& p, int b) {
   bool bad = l < 0 || (int64_t)l > ((int64_t)(own ? p.max_pages : p.pre_pages) << p.page_shift);
   if (own) {
     const int a = __ldg(p.q_start + b), e = __ldg(p.q_start + b + 1);
-    bad = bad || a < 0 || e < a || e > p.n_tokens || e - a > p.max_q || (b == 0 && a != 0);
+    bad = bad || a < 0 || e < a || e > p.n_tokens || e - a > p.max_q || (b == 0 && a != 0) ||
+          (b == p.n_seqs - 1 && e != p.n_tokens);
   }
   if (bad) atomicExch(p.status, COLI_EINVAL);
 }

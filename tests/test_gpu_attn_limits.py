@@ -1,6 +1,6 @@
 """The edges of what the attention calls accept (coli_attn.h): outputs on 16-byte boundaries, page
 tables of several strides, tensors of another device, cache
-strides."""
+strides, offsets that are not what the header asks for."""
 import ctypes
 
 import pytest
@@ -106,3 +106,20 @@ def test_cache_strides_that_let_tokens_overlap_are_refused(strides):
 def test_cache_strides_in_any_order(strides, kw):
     """pages, heads and slots nested in any order, padded, or of one entry"""
     assert bind(strides, **kw) == [0, 0]
+
+
+@pytest.mark.parametrize("seqs", [3, 45])
+@pytest.mark.parametrize("prefix", [0, 20])
+def test_offsets_that_end_early_are_reported(seqs, prefix):
+    """the last tokens belong to no sequence; the sequences' rows are within their bound all the same (a shorter list is cut
+    elsewhere, so not the same bits)"""
+    news = ([2, 3, 1] * seqs)[:seqs]
+    s = Setup(news, [40 + i for i in range(seqs)], 4, 2, 64, 16, BF, prefix=prefix)
+    call = s.shared if prefix else s.window
+    want, n = call(), s.T - news[-1]
+    s.batch.q_start[-1] -= news[-1]
+    got = s.eng.prefix(s.cache, s.batch, s.prefix_table, s.prefix_len, s.q) if prefix else s.eng.window(s.cache, s.batch, s.q)
+    assert s.eng.status() == -1 and s.eng.status() == 0
+    assert (s.off(got[:n], [x[:n] for x in s.reference()]) <= 1).all()
+    s.batch.q_start[-1] += news[-1]
+    assert torch.equal(call(), want)
