@@ -17,7 +17,7 @@ namespace coli {
 // kernel a round of loads per 16 parts, so the best stretch grows with the root of the unit (110 tiles of one
 // unit: 20.0 us in stretches of 1, 15.6 in stretches of 2).
 COLI_BOTH uint32_t list_stretch(uint32_t run, uint32_t ctas, int longest) {
-  uint32_t per = run / ctas + (run % ctas != 0);
+  uint32_t per = (run + ctas - 1) / ctas;  // (run is below 2^31)
   if (per == 0) per = 1;
   while ((uint64_t)per * per * 12 < (uint64_t)longest) ++per;
   return per;
