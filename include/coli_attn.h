@@ -109,7 +109,7 @@ int coli_attn_append(coli_attn* h, const coli_attn_kv* kv, const coli_attn_batch
 
 /* out_dev [n_tokens, n_q, head_dim] = attention of the batch's queries over its cache: query p sees
  * key j when j <= p and (p - j < window or j < sinks).  window < 0: all keys up to p; window = 0:
- * the sinks alone.  sinks >= 0, scale > 0.  lse_dev [n_tokens, n_q]: natural log-sum-exp of the scaled scores, or
+ * the sinks alone.  sinks >= 0; scale > 0, and finite times log2(e).  lse_dev [n_tokens, n_q]: natural log-sum-exp of the scaled scores, or
  * NULL.  Strides as in append.  q_dev must not overlap out_dev (their rows may lie
  * between one another).  EUNSUPPORTED: the batch could have 2^31 key tiles (n_kv times its blocks,
  * one or more a sequence, times max_pages * page / 64, or the window's share of that): split the call. */

@@ -163,6 +163,8 @@ int check_call(const coli_attn* h, const coli_attn_kv* kv, const coli_attn_batch
   return check_device(h->device);
 }
 
+constexpr float kLog2E = 1.44269504088896340736f;
+
 AttnParams params(const coli_attn* h, const coli_attn_kv* kv, const coli_attn_batch* b, const void* q,
                   int64_t q_stride, void* out, int64_t out_stride, float* lse, float scale) {
   AttnParams p = {};
@@ -173,7 +175,7 @@ AttnParams params(const coli_attn* h, const coli_attn_kv* kv, const coli_attn_ba
   p.n_q = h->cfg.n_q, p.n_kv = h->cfg.n_kv, p.group = h->cfg.n_q / h->cfg.n_kv, p.head_dim = h->cfg.head_dim;
   p.page_shift = h->page_shift, p.n_pages = (int)kv->c.n_pages;
   p.window = kAttnNoWindow, p.sinks = 0;
-  p.scale_log2 = scale * 1.44269504088896340736f;
+  p.scale_log2 = scale * kLog2E;
   p.part_o = h->part_o, p.part_ml = h->part_ml, p.rec = h->rec, p.seq_pos = h->seq_pos;
   p.k_page = kv->c.k_page_stride, p.k_head = kv->c.k_head_stride, p.k_slot = kv->c.k_slot_stride;
   p.v_page = kv->c.v_page_stride, p.v_head = kv->c.v_head_stride, p.v_slot = kv->c.v_slot_stride;
@@ -219,7 +221,7 @@ int query_args(const coli_attn* h, int64_t n_tokens, const void* q, int64_t q_st
                int64_t out_stride, float scale) {
   const int64_t width = (int64_t)h->cfg.n_q * h->cfg.head_dim;
   if (!q || !out || misaligned(q, q_stride) || misaligned(out, out_stride) || q_stride < width ||
-      out_stride < width || !(scale > 0.f) || !std::isfinite(scale))
+      out_stride < width || !(scale > 0.f) || !std::isfinite(scale * kLog2E))
     return COLI_EINVAL;
   return collide(q, q_stride, width, out, out_stride, width, n_tokens) ? COLI_EINVAL : COLI_OK;
 }

@@ -28,6 +28,8 @@
 // pipe is 60 % busy at 4096 tokens, where units of few tiles at the start of the sequence cost more.  A block that
 // fills one row tile takes about 1.2 us a tile, its products and softmax one after another: below the 1.47 us that its
 // keys and values take from DRAM when every SM reads others.
+#include <float.h>
+
 #include "attn_device.cuh"
 
 namespace coli {
@@ -384,7 +386,7 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t st_addr = tmem + lane_base + s * 128, ot_addr = tmem + lane_base + C::o_col + s * D;
     const int tok = row / p.group;
-    const float slack = 8.f / p.scale_log2;
+    const float slack = fminf(8.f / p.scale_log2, FLT_MAX);  // finite: -inf + inf would never let the first keys in
     uint32_t sn = 0, on = 0;
     Unit u;
 #pragma unroll 1

@@ -1,12 +1,12 @@
 """The edges of what the attention calls accept (coli_attn.h): outputs on 16-byte boundaries, page
 tables of several strides, tensors of another device, cache
-strides, offsets that are not what the header asks for."""
+strides, offsets that are not what the header asks for, the smallest and largest scales."""
 import ctypes
 
 import pytest
 import torch
 
-from int4_routed_expert_quantize_gb300 import attn
+from int4_routed_expert_quantize_gb300 import attn, coli
 
 from .test_gpu_attn import BF, HF, Setup
 
@@ -123,3 +123,21 @@ def test_offsets_that_end_early_are_reported(seqs, prefix):
     assert (s.off(got[:n], [x[:n] for x in s.reference()]) <= 1).all()
     s.batch.q_start[-1] += news[-1]
     assert torch.equal(call(), want)
+
+
+@pytest.mark.parametrize("news,lens", [([1], [300]), ([60], [900]), ([300, 1], [700, 50])])
+@pytest.mark.parametrize("scale", [1e-38, 3e-39, 1e-44])
+def test_scales_near_zero(news, lens, scale):
+    """all weights alike, whichever kernel takes the batch; whole units and cut ones"""
+    Setup(news, lens, 8, 2, 64, 16, BF).window(scale=scale)
+    Setup([1, 4, 2], [30, 90, 7], 8, 2, 64, 16, BF, prefix=700).shared(scale=scale)
+
+
+def test_scales_past_the_range_are_refused():
+    """finite, but not times log2(e), which is what the kernels multiply by"""
+    s = Setup([1], [30], 8, 2, 64, 16, BF, prefix=20)
+    for call in (lambda: s.eng.window(s.cache, s.batch, s.q, scale=3e38),
+                 lambda: s.eng.prefix(s.cache, s.batch, s.prefix_table, s.prefix_len, s.q, scale=3e38)):
+        with pytest.raises(coli.ColiError) as e:
+            call()
+        assert e.value.status == -1
