@@ -97,7 +97,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32) attn_append_kernel(const At
   const int start = __ldg(a.q_start + b), end = __ldg(a.q_start + b + 1), len = __ldg(a.kv_len + b);
   const int pos = len - (end - token);
   bool store = pos >= 0;
-  if (token < start || end > a.n_tokens || len < 0 || (pos >> a.page_shift) >= a.max_pages) {
+  // (where the offsets do not ascend, the sequence found need not hold the token)
+  if (token < start || token >= end || end > a.n_tokens || len < 0 || (pos >> a.page_shift) >= a.max_pages) {
     if (lane == 0) atomicExch(a.status, COLI_EINVAL);
     store = false;
   }

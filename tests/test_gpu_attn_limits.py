@@ -141,3 +141,19 @@ def test_scales_past_the_range_are_refused():
         with pytest.raises(coli.ColiError) as e:
             call()
         assert e.value.status == -1
+
+
+def test_append_with_offsets_that_do_not_ascend():
+    """reported, and nothing is stored behind a sequence's cached tokens"""
+    s = Setup([1, 1, 1], [40, 40, 40], 4, 2, 64, 16, BF, junk=0.0)
+    eng = attn.PagedAttention(4, 2, 64, 16, 16, 4, rot_dim=0)
+    kc, vc = s.kc.clone(), s.vc.clone()
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    b = attn.Batch(i32(0, 10, 2, 3), i32(20, 20, 20), s.table, n_tokens=10, max_q=10)
+    k = torch.ones((10, 2, 64), dtype=BF, device="cuda")
+    eng.append(eng.bind_cache(kc, vc), b, k, k)
+    assert eng.status() == -1
+    pages = s.table.long()
+    for got, old in ((kc, s.kc), (vc, s.vc)):
+        got, old = (x[pages].transpose(2, 3).reshape(3, -1, 2, 64)[:, 20:] for x in (got, old))
+        assert torch.equal(got, old)
