@@ -273,11 +273,14 @@ __global__ void __launch_bounds__(kWarps * 32) attn_combine_kernel(const AttnPar
        k += (int64_t)gridDim.x * kWarps) {
     if (!__ldcg(p.redo + k)) continue;
     const int token = (int)(k / p.n_kv), b = seq_of(p, token, lane);
+    if (b >= p.n_seqs) continue;  // (only where the offsets do not ascend, which is reported)
     const SeqInfo s = seq_info(p, b);
+    const int i = token - s.start;
+    if (i < 0 || i >= s.n) continue;  // (likewise: its position would lie outside the sequence's pages)
     for (int g = 0; g < p.group; ++g) {
       Join<D, 4> j;
       const int hq = (int)(k % p.n_kv) * p.group + g;
-      add_direct<T, D>(j, p, s, b, token - s.start, hq, qf[warp], lane);
+      add_direct<T, D>(j, p, s, b, i, hq, qf[warp], lane);
       j.template write<T>(p, token, hq, lane);
     }
   }

@@ -2,6 +2,7 @@
 tables of several strides, tensors of another device, cache
 strides, offsets that are not what the header asks for, the smallest and largest scales."""
 import ctypes
+import math
 
 import pytest
 import torch
@@ -157,3 +158,19 @@ def test_append_with_offsets_that_do_not_ascend():
     for got, old in ((kc, s.kc), (vc, s.vc)):
         got, old = (x[pages].transpose(2, 3).reshape(3, -1, 2, 64)[:, 20:] for x in (got, old))
         assert torch.equal(got, old)
+
+
+@pytest.mark.parametrize("n_q", [4, 64])
+def test_spoilt_rows_with_offsets_that_do_not_ascend(n_q):
+    """rows to compute again whose sequence, looked up by the offsets, is another one: reported, read nowhere, forgotten"""
+    s = Setup([10, 1, 1], [48, 48, 48], n_q, 2, 64, 16, BF, junk=0.0)  # full page tables
+    want = s.window(window=-1)
+    b, pg = s.batch, int(s.table[0, 2])
+    keep = s.vc[pg, :, 12].clone()
+    s.vc[pg, :, 12] = math.nan  # token 44 of 48: the queries 0..5 do not see it
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    # tokens 3.. fall to sequence 2 (its one token is number 2) by the ends at or before them
+    s.eng.window(s.cache, attn.Batch(i32(0, 12, 2, 3), b.kv_len, s.table, n_tokens=12, max_q=12), s.q)
+    assert s.eng.status() == -1
+    s.vc[pg, :, 12] = keep
+    assert torch.equal(s.eng.window(s.cache, b, s.q), want) and s.eng.status() == 0
