@@ -129,7 +129,8 @@ int coli_attn_prefix(coli_attn* h, const coli_attn_kv* kv, const coli_attn_batch
 /* Device status of the handle: COLI_OK; COLI_EINVAL when an earlier call met lengths, offsets or
  * page ids out of range (lengths are clamped, such a page reads as zeros and is not written; rows of tokens that no
  * sequence has, as when the offsets end before n_tokens, are not written or not complete), or a window or
- * prefix call a sequence of more than max_q new tokens (rows of its output may be missing);
+ * prefix call a sequence of more than max_q new tokens (rows of its output may be missing), or offsets that overlap so often
+ * that the call's list of key tiles is full (its output is undefined);
  * COLI_ETIMEOUT when a bounded wait gave up (that call's output is undefined).  The word is then
  * cleared.  Synchronises `stream`. */
 int coli_attn_status(coli_attn* h, void* stream);

@@ -159,7 +159,7 @@ __device__ __forceinline__ uint32_t warp_scan(uint32_t v, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const uint32_t u = __shfl_up_sync(FULL, v, o);
-    if (lane >= o) v += u;
+    if (lane >= o) v = list_add(v, u);
   }
   return v;
 }
@@ -171,8 +171,12 @@ struct Walk {
   Tiles<KT> t;
   uint32_t begin, end, per, at;  // at: the current unit's first position
   int b, blk, head;
-  __device__ __forceinline__ void cut(const AttnParams& p, uint32_t run, int longest) {
+  __device__ __forceinline__ void cut(const AttnParams& p, uint32_t run, int longest, bool real) {
     per = list_stretch(run, gridDim.x, longest);
+    if (run == kListFull) {  // no place is known: nothing is computed, and the joining kernel finds every row in one piece
+      if (blockIdx.x == 0 && (threadIdx.x & 31) == 0 && real) atomicExch(p.status, COLI_EINVAL);
+      run = 0, per = 0xFFFFFFFFu;
+    }
     begin = min(blockIdx.x * per, run);
     end = min(begin + per, run);
     b = blk = head = 0;
@@ -186,11 +190,11 @@ struct Walk {
 #pragma unroll 1
     for (int b0 = 0; b0 < ns; b0 += 32) {
       const uint32_t v = warp_scan(b0 + lane < ns ? pos[b0 + lane + 1] : 0, lane);
-      if (b0 + lane < ns) pos[b0 + lane + 1] = run + v;
-      run += __shfl_sync(FULL, v, 31);
+      if (b0 + lane < ns) pos[b0 + lane + 1] = list_add(run, v);
+      run = list_add(run, __shfl_sync(FULL, v, 31));
     }
     __syncwarp();
-    cut(p, run, 0);
+    cut(p, run, 0, true);
     if (blockIdx.x == 0 && p.seq_pos) {
 #pragma unroll 1
       for (int i = lane; i <= ns; i += 32) p.seq_pos[i] = pos[i];
@@ -246,7 +250,7 @@ struct Walk {
     }
     w *= p.n_kv;
     const uint32_t v = warp_scan(w, lane);
-    cut(p, __shfl_sync(FULL, v, 31), __reduce_max_sync(FULL, longest));
+    cut(p, __shfl_sync(FULL, v, 31), __reduce_max_sync(FULL, longest), real);
     if (blockIdx.x == 0 && p.seq_pos && real) {
       if (lane <= ns && lane < 31) p.seq_pos[lane] = v - w;
       if (lane == 31) p.seq_pos[31] = v - w, p.seq_pos[32] = v;

@@ -11,6 +11,11 @@
 
 namespace coli {
 
+// The sum of two list lengths, which stops at kListFull.  The host bounds the lists of offsets that ascend, and every
+// sequence's share of any list, below that; offsets that overlap can add up to more.
+constexpr uint32_t kListFull = 0x7FFFFFFFu;
+COLI_BOTH uint32_t list_add(uint32_t a, uint32_t b) { return a + b < kListFull ? a + b : kListFull; }
+
 // Positions of a list of `run` that one of `ctas` CTAs takes.  longest: the tiles of the longest unit that may be cut into
 // single tiles (0: none).
 // Few CTAs' worth of work: a longer stretch costs a tile's time a position, a shorter one costs the joining

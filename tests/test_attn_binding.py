@@ -53,3 +53,16 @@ def test_stretches_of_long_lists(tmp_path):
         while want * want * 12 < longest:
             want += 1
         assert per == want, (run, ctas, longest)
+
+
+def test_lengths_of_lists_stop_when_full(tmp_path):
+    call = host_program(tmp_path, """
+  unsigned a, b;
+  while (scanf("%u %u", &a, &b) == 2) printf("%u\\n", list_add(a, b));
+  return 0;
+""")
+    full = 2 ** 31 - 1
+    r = random.Random(1)
+    rows = [(0, 0), (full, full), (full, 0), (0, full), (full - 1, 1), (full - 1, 0), (2 ** 30, 2 ** 30), (2 ** 30, 2 ** 30 - 1)]
+    rows += [(min(full, int(2 ** r.uniform(0, 31))), min(full, int(2 ** r.uniform(0, 31)))) for _ in range(500)]
+    assert call(rows) == [min(full, a + b) for a, b in rows]

@@ -174,3 +174,29 @@ def test_spoilt_rows_with_offsets_that_do_not_ascend(n_q):
     assert s.eng.status() == -1
     s.vc[pg, :, 12] = keep
     assert torch.equal(s.eng.window(s.cache, b, s.q), want) and s.eng.status() == 0
+
+
+@pytest.mark.parametrize("seqs,T,pages", [(4096, 65536, 128), (4096, 65536, 256), (32, 65536, 8192), (4096, 32768, 128)])
+def test_offsets_that_overlap_until_the_list_is_full(seqs, T, pages):
+    """every other sequence claims all tokens: more key tiles than the list has places.  Reported, and the next call is right"""
+    n_q, n_kv, D, page = 64, 8, 64, 256
+    eng = attn.PagedAttention(n_q, n_kv, D, page, T, seqs)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(0)
+    kc, vc = (torch.randn((2, n_kv, page, D), generator=g, device="cuda").to(BF) for _ in range(2))
+    cache, q = eng.bind_cache(kc, vc), torch.randn((T, n_q, D), generator=g, device="cuda").to(BF)
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    small = attn.Batch(i32(0, 1, 3), i32(300, 5), i32(0, 1, 1, 0).view(2, 2), n_tokens=3, max_q=2)
+    lse, out = torch.zeros((T, n_q), device="cuda"), torch.zeros_like(q)
+    bad = attn.Batch(i32(*[0 if b % 2 == 0 else T for b in range(seqs)], T),
+                     torch.full((seqs,), pages * page, dtype=torch.int32, device="cuda"),
+                     torch.zeros((1, pages), dtype=torch.int32, device="cuda").expand(seqs, -1), n_tokens=T, max_q=T)
+    calls = [lambda b, n: eng.window(cache, b, q[:n], out=out[:n], lse=lse[:n])]
+    if T <= 8 * seqs:
+        calls.append(lambda b, n: eng.prefix(cache, b, i32(1), i32(200), q[:n], out=out[:n], lse=lse[:n]))
+    for call in calls:
+        want = call(small, 3).clone()
+        assert eng.status() == 0
+        call(bad, T)
+        assert eng.status() == -1
+        assert torch.equal(call(small, 3), want) and eng.status() == 0
