@@ -232,8 +232,9 @@ __global__ void __launch_bounds__(SplitCfg<D, RG>::threads, SplitCfg<D, RG>::cta
       }
     }
     u.i1 = 0;
-    if (ok) ok = give_unit(units, u, n, lane, wait);
-    if (!ok) drain_ring(full, NST, it);
+    if (ok) give_unit(units, u, n, lane, wait);
+    // the CTA's shared memory must not go while copies to it are on their way, even when the other warps have given up
+    drain_ring(full, NST, it);
     return;
   }
 

@@ -258,12 +258,11 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
         }
       }
       u.i1 = 0;
-      if (ok) ok = give_unit(units, u, n, lane, wait);
-      if (!ok) {
-        drain_ring(full, NST, it);
-        drain_ring(q_full, 1, qn0);
-        drain_ring(q_full + 1, 1, qn1);
-      }
+      if (ok) give_unit(units, u, n, lane, wait);
+      // the CTA's shared memory must not go while copies to it are on their way, even when the other warps have given up
+      drain_ring(full, NST, it);
+      drain_ring(q_full, 1, qn0);
+      drain_ring(q_full + 1, 1, qn1);
     } else if (warp == 8) {  // ---- products (one lane issues; the warp waits together)
       constexpr uint32_t qk_idesc = mma_desc<T>(kTileKeys, false), pv_idesc = mma_desc<T>(D, true);
       // descriptors of the first tiles; others are a whole number of 16-byte units further (no carry out of
@@ -336,11 +335,11 @@ __global__ void __launch_bounds__(kThreadsTile, 1)
           if (--a_left == 0) more = take();
         }
       }
-      if (*reinterpret_cast<volatile int*>(abort_flag)) {  // wait, with a limit of its own, for the products in flight
-        if (elect_one()) tc_commit(drain);
-        __syncwarp();
-        drain_ring(drain, 1, 1);
-      }
+      // Nor must tensor memory while products write to it: usually the softmax warps have waited for them, but not when they
+      // gave up.  (With a limit of its own.)
+      if (elect_one()) tc_commit(drain);
+      __syncwarp();
+      drain_ring(drain, 1, 1);
     } else {
       // ---- values that not every row sees.  These warps pass every item of the ring on to the products' warp, key
       // tiles too: a waiter that skipped items could meet a stage whose previous item is still on its way
