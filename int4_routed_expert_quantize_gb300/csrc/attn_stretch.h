@@ -24,7 +24,8 @@ COLI_BOTH uint32_t list_add(uint32_t a, uint32_t b) { return a + b < kListFull ?
 COLI_BOTH uint32_t list_stretch(uint32_t run, uint32_t ctas, int longest) {
   uint32_t per = (run + ctas - 1) / ctas;  // (run is below 2^31)
   if (per == 0) per = 1;
-  while ((uint64_t)per * per * 12 < (uint64_t)longest) ++per;
+  // (16384 * 16384 * 12 is more than any int, and fits 32 bits)
+  while (per < 16384 && per * per * 12 < (uint32_t)longest) ++per;
   return per;
 }
 
