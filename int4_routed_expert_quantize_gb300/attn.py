@@ -154,18 +154,20 @@ def _handle(stream):
 
 def _done(out, given, stream, what):
     """a call's output, or the error that its status stands for; a new output made on another stream than the
-    current one is kept from reuse until that stream is done with it"""
+    current one is kept from reuse there until the current one is done with it"""
     if out.__class__ is int:
         raise coli.ColiError(out, what)
-    if given is None and out is not None and isinstance(stream, torch.cuda.Stream):
-        out.record_stream(stream)
+    if given is None and out is not None and stream is not None:
+        out.record_stream(torch.cuda.current_stream(out.device))
     return out
 
 
 class PagedAttention:
     """Shapes, rotation and workspace of the attention over a paged cache on the current device.
     rot_dim None rotates the whole head, 0 none of it; inv_freq (rot_dim/2 radians per position) takes
-    the place of rope_base."""
+    the place of rope_base.  A call's `stream` (a torch stream or a handle; the current one by default) has to have
+    waited for what writes its tensors; a new output is that stream's memory, for others to read once they have
+    waited for it."""
 
     def __init__(self, n_q, n_kv, head_dim, page, max_tokens, max_seqs, dtype=torch.bfloat16, rot_dim=None,
                  interleaved=False, rope_base=10000.0, inv_freq=None):

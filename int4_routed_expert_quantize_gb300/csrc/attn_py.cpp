@@ -6,6 +6,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -85,18 +86,27 @@ float* log_sums(PyObject* o, const Engine& e, const coli_attn_batch& b) {
   return static_cast<float*>(t.data_ptr());
 }
 
-void* stream_of(PyObject* o, const Engine& e) {
-  return o == Py_None ? (void*)c10::cuda::getCurrentCUDAStream(e.device).stream() : PyLong_AsVoidPtr(o);
+// the stream of a call: the current one (None), or a handle
+c10::cuda::CUDAStream stream_of(PyObject* o, const Engine& e) {
+  if (o == Py_None) return c10::cuda::getCurrentCUDAStream(e.device);
+  const auto handle = (cudaStream_t)PyLong_AsVoidPtr(o);
+  if (!handle && PyErr_Occurred()) throw Error();
+  if (!handle || handle == cudaStreamLegacy) return c10::cuda::getDefaultCUDAStream(e.device);
+  return c10::cuda::getStreamFromExternal(handle, e.device);
 }
 
-// the caller's output or a new one
-at::Tensor output(PyObject* o, const at::Tensor& like, const Engine& e, const coli_attn_batch& b, int64_t* stride) {
+// The caller's output or a new one, in memory of the call's stream: what an earlier owner of the same memory has queued on
+// another one may not have run when the call does.
+at::Tensor output(PyObject* o, const at::Tensor& like, const Engine& e, const coli_attn_batch& b, int64_t* stride,
+                  const c10::cuda::CUDAStream& stream, bool current) {
   if (o != Py_None) {
     const at::Tensor& t = tensor(o, "out");
     *stride = heads(t, e, e.n_q, b, "out");
     return t;
   }
   *stride = (int64_t)e.n_q * e.head_dim;
+  c10::cuda::OptionalCUDAStreamGuard guard;
+  if (!current) guard.reset_stream(stream);
   return at::empty({b.n_tokens, e.n_q, e.head_dim}, like.options());
 }
 
@@ -132,17 +142,17 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor &k = tensor(a[3], "k"), &v = tensor(a[4], "v");
     const int64_t ks = heads(k, e, e.n_kv, b, "k"), vs = heads(v, e, e.n_kv, b, "v");
     const int32_t* base = a[7] == Py_None ? nullptr : int32s(a[7], e, "pos_base");
-    void* stream = stream_of(a[8], e);
+    const auto stream = stream_of(a[8], e);
     if (a[5] == Py_None)
       return result(coli_attn_append(e.handle, kv, &b, nullptr, 0, k.data_ptr(), ks, v.data_ptr(), vs, nullptr, 0, base,
-                                     stream),
+                                     stream.stream()),
                     nullptr);
     const at::Tensor& q = tensor(a[5], "q");
     const int64_t qs = heads(q, e, e.n_q, b, "q");
     int64_t os;
-    const at::Tensor out = output(a[6], q, e, b, &os);
+    const at::Tensor out = output(a[6], q, e, b, &os, stream, a[8] == Py_None);
     return result(coli_attn_append(e.handle, kv, &b, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
-                                   out.data_ptr(), os, base, stream),
+                                   out.data_ptr(), os, base, stream.stream()),
                   &out);
   });
 }
@@ -162,9 +172,10 @@ PyObject* window(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (PyErr_Occurred()) throw Error();
     float* lse = log_sums(a[8], e, b);
     int64_t os;
-    const at::Tensor out = output(a[7], q, e, b, &os);
+    const auto stream = stream_of(a[9], e);
+    const at::Tensor out = output(a[7], q, e, b, &os, stream, a[9] == Py_None);
     return result(coli_attn_window(e.handle, kv, &b, q.data_ptr(), qs, (int)w, (int)s, scale, out.data_ptr(), os, lse,
-                                   stream_of(a[9], e)),
+                                   stream.stream()),
                   &out);
   });
 }
@@ -184,9 +195,10 @@ PyObject* prefix(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (PyErr_Occurred()) throw Error();
     float* lse = log_sums(a[8], e, b);
     int64_t os;
-    const at::Tensor out = output(a[7], q, e, b, &os);
+    const auto stream = stream_of(a[9], e);
+    const at::Tensor out = output(a[7], q, e, b, &os, stream, a[9] == Py_None);
     return result(coli_attn_prefix(e.handle, kv, &b, table, (int)pages, len, q.data_ptr(), qs, scale, out.data_ptr(), os,
-                                   lse, stream_of(a[9], e)),
+                                   lse, stream.stream()),
                   &out);
   });
 }

@@ -1,6 +1,6 @@
 """The edges of what the attention calls accept (coli_attn.h): outputs on 16-byte boundaries, page
 tables of several strides, tensors of another device, cache
-strides, offsets that are not what the header asks for, the smallest and largest scales."""
+strides, offsets that are not what the header asks for, the smallest and largest scales, new outputs on another stream."""
 import ctypes
 import math
 
@@ -200,3 +200,33 @@ def test_offsets_that_overlap_until_the_list_is_full(seqs, T, pages):
         call(bad, T)
         assert eng.status() == -1
         assert torch.equal(call(small, 3), want) and eng.status() == 0
+
+
+@pytest.mark.parametrize("op", ["append", "window", "prefix"])
+@pytest.mark.parametrize("handle", [False, True])
+def test_new_outputs_on_another_stream(op, handle):
+    """their memory is not what the current stream still has work queued on, nor is it given to their stream again while
+    the current one reads it"""
+    s = Setup([3, 5], [70, 300], 6, 2, 128, 64, BF, prefix=30)
+    k = torch.randn((s.T, 2, 128), device="cuda").to(BF)
+    call = {"append": lambda **kw: s.eng.append(s.cache, s.batch, k, k, s.q, **kw),
+            "window": lambda **kw: s.eng.window(s.cache, s.batch, s.q, **kw),
+            "prefix": lambda **kw: s.eng.prefix(s.cache, s.batch, s.prefix_table, s.prefix_len, s.q, **kw)}[op]
+    want, side = call(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    old = torch.empty_like(want)
+    at = old.data_ptr()
+    torch.cuda._sleep(200_000_000)
+    old.fill_(5)
+    del old  # its memory is free for the current stream's next tensor, and the fill is yet to come
+    got = call(stream=side.cuda_stream if handle else side)
+    assert got.data_ptr() != at
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    torch.cuda._sleep(200_000_000)
+    copy = got.clone()
+    del got
+    with torch.cuda.stream(side):
+        other = torch.empty_like(want).fill_(9)
+    torch.cuda.synchronize()
+    assert torch.equal(copy, want) and (other == 9).all()
