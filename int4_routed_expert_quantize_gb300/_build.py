@@ -2,6 +2,7 @@
 compiler), one object per source compiled in parallel."""
 import os
 import subprocess
+import sys
 import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
@@ -12,6 +13,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 SO = os.path.join(PKG, "libcoli_moe.so")
 PY_SO = os.path.join(PKG, "_attn_py.so")  # the attention calls' Python side (csrc/attn_py.cpp), linked to SO
+PY_TAG = os.path.join(BUILD, "attn_py.tag")  # what it was built for (torch_tag)
 SOURCES = ["pack.cu", "route.cu", "expert_decode.cu", "gateup_w4.cu", "down_w4.cu", "gateup_w8.cu",
            "down_w8.cu", "gateup_w2.cu", "down_w2.cu", "expert_fused.cu", "expert_prefill.cu",
            "runtime.cu", "noalloc.cu", "attn_append.cu", "attn_split.cu", "attn_tile.cu",
@@ -25,11 +27,25 @@ def nvcc_flags(arch="sm_103a"):
             "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 
 
+def torch_tag():
+    """the torch and the Python that _attn_py.so is built for; None where there is no torch (then it is not built)"""
+    try:
+        import torch
+    except ImportError:
+        return None
+    return f"torch {torch.__version__}, {sys.implementation.cache_tag}"
+
+
 def is_stale():
-    """True when a library is missing or older than a source or header it is built from"""
-    if not os.path.exists(SO) or not os.path.exists(PY_SO):
+    """True when a library is missing, older than a source or header it is built from, or built for another torch"""
+    tag, libs = torch_tag(), [SO]
+    if tag is not None:
+        libs.append(PY_SO)
+        if not os.path.exists(PY_TAG) or open(PY_TAG).read() != tag:
+            return True
+    if not all(os.path.exists(p) for p in libs):
         return True
-    built = min(os.path.getmtime(SO), os.path.getmtime(PY_SO))
+    built = min(os.path.getmtime(p) for p in libs)
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + \
         [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)] + [os.path.abspath(__file__)]
     return any(os.path.getmtime(p) > built for p in deps if os.path.isfile(p))
@@ -48,12 +64,16 @@ def build(arch="sm_103a", verbose=False, extra=()):
         return obj
 
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        py = ex.submit(compile_py, verbose)
+        tag = torch_tag()
+        py = ex.submit(compile_py, verbose) if tag is not None else None
         objs = list(ex.map(compile_one, SOURCES))
-        py_obj = py.result()
-    subprocess.check_call(["nvcc", "-shared", "-cudart", "static", "-Xlinker",
-                           "--version-script=" + os.path.join(CSRC, "exports.map"), "-o", SO] + objs)
-    link_py(py_obj)
+        # the C library first: it needs neither torch nor the Python side
+        subprocess.check_call(["nvcc", "-shared", "-cudart", "static", "-Xlinker",
+                               "--version-script=" + os.path.join(CSRC, "exports.map"), "-o", SO] + objs)
+    if py is not None:
+        link_py(py.result())
+        with open(PY_TAG, "w") as f:
+            f.write(tag)
     return SO
 
 
@@ -61,8 +81,10 @@ def compile_py(verbose=False):
     import torch
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
     obj = os.path.join(BUILD, "attn_py.o")
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-           "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-I", "/usr/local/cuda/include"]
+    # (through nvcc, which knows where the CUDA headers are)
+    cmd = ["nvcc", "-O2", "-std=c++17", "-Xcompiler", "-fPIC",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE, "-I",
+           sysconfig.get_paths()["include"]]
     cmd += ["-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-c", os.path.join(CSRC, "attn_py.cpp"), "-o", obj]
     if verbose:
         print(" ".join(cmd))

@@ -1,4 +1,5 @@
 """The host side of the attention binding and the arithmetic of its work list, without a GPU."""
+import os
 import random
 import subprocess
 
@@ -66,3 +67,45 @@ def test_lengths_of_lists_stop_when_full(tmp_path):
     rows = [(0, 0), (full, full), (full, 0), (0, full), (full - 1, 1), (full - 1, 0), (2 ** 30, 2 ** 30), (2 ** 30, 2 ** 30 - 1)]
     rows += [(min(full, int(2 ** r.uniform(0, 31))), min(full, int(2 ** r.uniform(0, 31)))) for _ in range(500)]
     assert call(rows) == [min(full, a + b) for a, b in rows]
+
+
+@pytest.fixture
+def commands(monkeypatch, tmp_path):
+    """the build's commands, recorded instead of run, its outputs in a scratch folder"""
+    seen = []
+    monkeypatch.setattr(_build.subprocess, "check_call", lambda cmd, **kw: seen.append(cmd))
+    for name in ("SO", "PY_SO", "PY_TAG"):
+        monkeypatch.setattr(_build, name, str(tmp_path / os.path.basename(getattr(_build, name))))
+    monkeypatch.setattr(_build, "BUILD", str(tmp_path))
+    return seen
+
+
+def test_the_c_library_is_built_whatever_becomes_of_the_python_side(commands, monkeypatch):
+    def broken(verbose=False):
+        raise subprocess.CalledProcessError(1, "attn_py.cpp")
+    monkeypatch.setattr(_build, "compile_py", broken)
+    with pytest.raises(subprocess.CalledProcessError):
+        _build.build()
+    assert any("-shared" in c and _build.SO in c for c in commands)
+    assert not os.path.exists(_build.PY_TAG)
+
+
+def test_without_torch_the_c_library_alone_is_built(commands, monkeypatch):
+    monkeypatch.setattr(_build, "torch_tag", lambda: None)
+    _build.build()
+    assert any("-shared" in c and _build.SO in c for c in commands)
+    assert not any("attn_py" in str(c) for c in commands)
+
+
+def test_no_fixed_place_of_cuda(commands):
+    _build.build()
+    assert any("attn_py" in str(c) for c in commands) and not any("/usr/local/cuda" in str(c) for c in commands)
+
+
+def test_another_torch_makes_the_build_stale(commands, monkeypatch):
+    _build.build()
+    for p in (_build.SO, _build.PY_SO):
+        open(p, "w").close()
+    assert not _build.is_stale()
+    monkeypatch.setattr(_build, "torch_tag", lambda: "torch 0.0, cpython-312")
+    assert _build.is_stale()
