@@ -230,3 +230,23 @@ def test_new_outputs_on_another_stream(op, handle):
         other = torch.empty_like(want).fill_(9)
     torch.cuda.synchronize()
     assert torch.equal(copy, want) and (other == 9).all()
+
+
+@pytest.mark.parametrize("n_q,n_kv,D,dt", [(48, 8, 128, BF), (32, 8, 64, HF)])
+def test_prefix_of_one_long_sequence_among_many(n_q, n_kv, D, dt):
+    """own keys and prefix in launches of their own, a sequence of many blocks of the first; with and without values that
+    only some of its rows see"""
+    news = [1] * 20 + [230] + [2] * 30
+    s = Setup(news, [60 + n for n in news], n_q, n_kv, D, 32, dt, prefix=150)
+    assert s.eng.launches("prefix", len(news)) == 3 and s.T <= 8 * len(news)
+    want = s.shared()
+    j, ref = 200, s.reference()  # of 290 tokens; the queries are 60..289
+    pg = int(s.table[20, j // 32])
+    keep = s.vc[pg, :, j % 32].clone()
+    s.vc[pg, :, j % 32] = math.nan
+    out = s.eng.prefix(s.cache, s.batch, s.prefix_table, s.prefix_len, s.q)
+    hit = torch.zeros(s.T, dtype=torch.bool, device="cuda")
+    hit[20 + j - 60:250] = True
+    assert (s.off(out, ref)[~hit] <= 1).all() and torch.isnan(out[hit]).all()
+    s.vc[pg, :, j % 32] = keep
+    assert torch.equal(s.eng.prefix(s.cache, s.batch, s.prefix_table, s.prefix_len, s.q), want)
