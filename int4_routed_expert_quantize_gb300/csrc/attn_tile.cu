@@ -22,8 +22,9 @@
 // The list of all blocks' key tiles is cut into one equal stretch per SM (attn_sched.cuh), so few long
 // rows fill the GPU as well as many short ones.
 //
-// Measured: 8192 new tokens, 6 query heads a key head, 8 key heads of 128, window 4096: 416 us, 1.49 PFLOP/s of the
-// scores that rows see (1.61 of those computed; cuBLAS reaches 1.94 in bf16).  A key tile takes both row tiles 1.53 us
+// Measured: 8192 new tokens, 6 query heads a key head, 8 key heads of 128, window 4096: calls in a row 450 us, under the
+// power cap, 1.37 PFLOP/s of the scores that rows see; the first ones after a pause 420 us, 1.47 PFLOP/s (1.59 of those
+// computed; cuBLAS reaches 1.94 in bf16, 1.71 under the cap).  After a pause a key tile takes both row tiles 1.53 us
 // (8.4 MFLOP of each): the products alone 1.0, the rest is what the two softmax chains leave uncovered; the tensor
 // pipe is 60 % busy at 4096 tokens, where units of few tiles at the start of the sequence cost more.  A block that
 // fills one row tile takes about 1.2 us a tile, its products and softmax one after another: below the 1.47 us that its
