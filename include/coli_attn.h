@@ -24,6 +24,15 @@
  * to the type before they multiply V (the tensor cores' operand type), the output once at the end.
  * Work is split over the keys in a fixed order, so equal calls give equal bits.
  *
+ * 8-bit caches.  A cache bound with coli_attn_qcache_bind holds a code of 8 bits for each value and one fp32 scale for each
+ * token and key head; append and window take it as they take a 16-bit one (prefix does not).  With m = max|x| over a head's
+ * values of one token (rotated, in fp32), append stores scale = m / top and code = top * x / m rounded to the nearest, ties to
+ * even: top = 127 for int8, 448 for e4m3.  A head that holds an infinity or NaN is stored as scale NaN and codes 0, so it
+ * reads back as NaN; m = 0 is scale 0.  window computes with code * scale: the codes go into the products as they are (exact),
+ * scores are multiplied by the key's scale in fp32, weights by the value's scale (relative to the largest one that the row has
+ * seen) before they are rounded to fp16 for their product with the codes.  e4m3's codes 0x7F and 0xFF, which append never
+ * stores, count as +480 and -480.
+ *
  * Conventions are those of coli_moe.h: every call returns COLI_OK or a negative status; device
  * pointers are named *_dev or listed as such; calls are asynchronous on `stream` and allocate
  * nothing (safe to capture in a CUDA graph); calls on one handle must not overlap in time (they
@@ -42,6 +51,9 @@ extern "C" {
 
 #define COLI_ATTN_BF16 0
 #define COLI_ATTN_FP16 1
+
+#define COLI_ATTN_CODE_INT8 1
+#define COLI_ATTN_CODE_E4M3 2
 
 typedef struct coli_attn coli_attn;       /* shapes, rotation and workspace; owned by the library */
 typedef struct coli_attn_kv coli_attn_kv; /* a bound cache; owned by the library, its memory is not */
@@ -71,6 +83,16 @@ typedef struct {
   int64_t v_page_stride, v_head_stride, v_slot_stride;
 } coli_attn_cache;
 
+/* The caller's memory of an 8-bit cache.  codes: as above, strides in elements of one byte and multiples of 16.  A page's tokens of a
+ * head have their scales next to one another; strides of the scales are in floats and multiples of 4, bases 16-byte aligned. */
+typedef struct {
+  coli_attn_cache codes;
+  float *k_scale, *v_scale;
+  int64_t k_scale_page_stride, k_scale_head_stride;
+  int64_t v_scale_page_stride, v_scale_head_stride;
+  int type; /* COLI_ATTN_CODE_INT8 or COLI_ATTN_CODE_E4M3 */
+} coli_attn_qcache;
+
 typedef struct {
   const int32_t* q_start; /* device [n_seqs+1], ascending from 0 to n_tokens                        */
   const int32_t* kv_len;  /* device [n_seqs], 0..max_pages*page                                     */
@@ -93,6 +115,9 @@ void coli_attn_destroy(coli_attn* h);
  * that let tokens of K, or of V, overlap: in order of size, a stride is at least what the smaller ones
  * span (a dimension of one entry has none, but is given as at least head_dim).  The handle's shapes give the dims. */
 int coli_attn_cache_bind(coli_attn* h, const coli_attn_cache* cache, coli_attn_kv** out);
+/* The same for an 8-bit cache.  EINVAL also: an unknown type, scales that overlap (by the same rule, a head's page of them being
+ * `page` floats). */
+int coli_attn_qcache_bind(coli_attn* h, const coli_attn_qcache* cache, coli_attn_kv** out);
 void coli_attn_cache_release(coli_attn_kv* kv);
 
 /* Rotates q_dev [n_tokens, n_q, head_dim] into q_out_dev (which may be q_dev itself; both NULL: no
@@ -120,7 +145,7 @@ int coli_attn_window(coli_attn* h, const coli_attn_kv* kv, const coli_attn_batch
 /* Attention of a batch behind a shared prefix: every query sees all prefix_len_dev[0] tokens of the
  * pages prefix_table_dev [prefix_pages] and the keys up to its own position of its own cache (whose
  * positions count from the end of the prefix; kv_len may be 0).  prefix_len is at most prefix_pages * page.
- * n_tokens <= 8 * max_seqs.  EUNSUPPORTED as for window, prefix_pages included. */
+ * n_tokens <= 8 * max_seqs.  EUNSUPPORTED as for window, prefix_pages included; an 8-bit cache. */
 int coli_attn_prefix(coli_attn* h, const coli_attn_kv* kv, const coli_attn_batch* batch,
                      const int32_t* prefix_table_dev, int prefix_pages,
                      const int32_t* prefix_len_dev, const void* q_dev, int64_t q_stride, float scale,

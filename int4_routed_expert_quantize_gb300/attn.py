@@ -7,6 +7,10 @@
     o = eng.window(cache, batch, q, window=4096, sinks=4)
     o = eng.prefix(cache, batch, prefix_table, prefix_len, q)
 
+A cache in 8 bits is bound with its scales, and append and window take it as they take a 16-bit one:
+
+    cache = eng.bind_cache(k_codes, v_codes, k_scale, v_scale)   # int8 or float8_e4m3fn; float32 [pages, n_kv, page]
+
 Argument marshalling only (the three calls' in _attn_py, csrc/attn_py.cpp); every step runs in the library's CUDA
 kernels.
 """
@@ -21,6 +25,7 @@ from . import coli
 _i, _f, _vp, _i64, _d = ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_int64, ctypes.c_double
 
 DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+CODES = {torch.int8: 1, torch.float8_e4m3fn: 2}
 
 
 class AttnConfig(ctypes.Structure):
@@ -33,6 +38,11 @@ class AttnCache(ctypes.Structure):
     _fields_ = [("k", _vp), ("v", _vp), ("n_pages", _i64), ("k_page_stride", _i64), ("k_head_stride", _i64),
                 ("k_slot_stride", _i64), ("v_page_stride", _i64), ("v_head_stride", _i64),
                 ("v_slot_stride", _i64)]
+
+
+class AttnQCache(ctypes.Structure):
+    _fields_ = [("codes", AttnCache), ("k_scale", _vp), ("v_scale", _vp), ("k_scale_page_stride", _i64),
+                ("k_scale_head_stride", _i64), ("v_scale_page_stride", _i64), ("v_scale_head_stride", _i64), ("type", _i)]
 
 
 class AttnBatch(ctypes.Structure):
@@ -61,6 +71,7 @@ def lib():
         L.coli_attn_destroy.argtypes = [_vp]
         L.coli_attn_destroy.restype = None
         L.coli_attn_cache_bind.argtypes = [_vp, ctypes.POINTER(AttnCache), ctypes.POINTER(_vp)]
+        L.coli_attn_qcache_bind.argtypes = [_vp, ctypes.POINTER(AttnQCache), ctypes.POINTER(_vp)]
         L.coli_attn_cache_release.argtypes = [_vp]
         L.coli_attn_cache_release.restype = None
         L.coli_attn_append.argtypes = [_vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp]
@@ -110,27 +121,45 @@ class Batch:
 
 
 class KvCache:
-    """A cache bound to an engine (coli_attn_cache_bind); keeps the two tensors alive."""
+    """A cache bound to an engine (coli_attn_cache_bind, coli_attn_qcache_bind); keeps its tensors alive."""
 
-    def __init__(self, engine, k, v):
+    def __init__(self, engine, k, v, k_scale=None, v_scale=None):
         dims = (engine.n_kv, engine.page, engine.head_dim)
+        quantised = k_scale is not None or v_scale is not None
+        kind = k.dtype if quantised else engine.dtype
+        if quantised and kind not in CODES:
+            raise ValueError(f"{kind}: an 8-bit cache holds int8 or float8_e4m3fn")
         for t in (k, v):
-            if t.dim() != 4 or tuple(t.shape[1:]) != dims or t.dtype is not engine.dtype or not t.is_cuda or \
+            if t.dim() != 4 or tuple(t.shape[1:]) != dims or t.dtype is not kind or not t.is_cuda or \
                     t.device.index != engine.device:
-                raise ValueError(f"the cache is [pages, {dims[0]}, {dims[1]}, {dims[2]}] of {engine.dtype} on the "
+                raise ValueError(f"the cache is [pages, {dims[0]}, {dims[1]}, {dims[2]}] of {kind} on the "
                                  "engine's device")
             if t.stride(3) != 1:
                 raise ValueError("a head's values are contiguous")
         if k.shape[0] != v.shape[0]:
             raise ValueError("K and V have the same number of pages")
-        self.k, self.v = k, v
+        if quantised:
+            for t in (k_scale, v_scale):
+                if t is None or t.dtype is not torch.float32 or tuple(t.shape) != (k.shape[0], dims[0], dims[1]) or \
+                        not t.is_cuda or t.device.index != engine.device:
+                    raise ValueError(f"scales are float32 [pages, {dims[0]}, {dims[1]}] on the engine's device, of K and of V")
+                if t.stride(2) != 1:
+                    raise ValueError("a page's scales of a head are contiguous")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
 
-        def strides(t):  # a dimension of one has no stride of its own
-            return [t.stride(i) if t.shape[i] > 1 else max(t.stride(i), engine.head_dim) // 8 * 8 for i in range(3)]
+        def strides(t, n, unit):  # a dimension of one has no stride of its own
+            least = t.shape[-1] if n == 2 else engine.head_dim
+            return [t.stride(i) if t.shape[i] > 1 else max(t.stride(i), least) // unit * unit for i in range(n)]
 
-        c = AttnCache(k.data_ptr(), v.data_ptr(), k.shape[0], *strides(k), *strides(v))
+        unit = 16 if quantised else 8
+        c = AttnCache(k.data_ptr(), v.data_ptr(), k.shape[0], *strides(k, 3, unit), *strides(v, 3, unit))
         h = _vp()
-        coli._check(lib().coli_attn_cache_bind(engine.h, ctypes.byref(c), ctypes.byref(h)), "coli_attn_cache_bind")
+        if quantised:
+            c = AttnQCache(c, k_scale.data_ptr(), v_scale.data_ptr(), *strides(k_scale, 2, 4), *strides(v_scale, 2, 4),
+                           CODES[kind])
+            coli._check(lib().coli_attn_qcache_bind(engine.h, ctypes.byref(c), ctypes.byref(h)), "coli_attn_qcache_bind")
+        else:
+            coli._check(lib().coli_attn_cache_bind(engine.h, ctypes.byref(c), ctypes.byref(h)), "coli_attn_cache_bind")
         self.h = h
         self.ref = h.value
 
@@ -198,8 +227,10 @@ class PagedAttention:
 
     __del__ = KvCache.__del__
 
-    def bind_cache(self, k_cache, v_cache):
-        return KvCache(self, k_cache, v_cache)
+    def bind_cache(self, k_cache, v_cache, k_scale=None, v_scale=None):
+        """K and V [pages, n_kv, page, head_dim] of the engine's type; or 8-bit codes (int8 or float8_e4m3fn), with float32
+        scales [pages, n_kv, page].  coli_attn_cache_bind, coli_attn_qcache_bind"""
+        return KvCache(self, k_cache, v_cache, k_scale, v_scale)
 
     def append(self, cache, batch, k, v, q=None, q_out=None, pos_base=None, stream=None):
         """Stores the batch's new keys (rotated) and values in the cache; rotates q into q_out (new by

@@ -44,8 +44,71 @@ __device__ __forceinline__ void rotate8(uint4& a, uint4& b, const float (&cs)[8]
   b = make_uint4(x[4], x[5], x[6], x[7]);
 }
 
-// warps_per_token consecutive warps share a token's heads
-template <class T, int D>
+// 16 values as fp32: word w of x[0], x[1] hold values 2w, 2w + 1
+template <class T>
+__device__ __forceinline__ void widen(const uint4& a, const uint4& b, float (&f)[16]) {
+  const uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int w = 0; w < 8; ++w) f[2 * w] = T::lo(x[w]), f[2 * w + 1] = T::hi(x[w]);
+}
+// rotate8 without the rounding
+__device__ __forceinline__ void rotate16(float (&f)[16], const float (&cs)[8], const float (&sn)[8], bool interleaved) {
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    // pair w: values 2w and 2w + 1, or w and w + 8
+    const float u = interleaved ? f[2 * w] : f[w], v = interleaved ? f[2 * w + 1] : f[w + 8];
+    const float p = u * cs[w] - v * sn[w], q = v * cs[w] + u * sn[w];
+    if (interleaved) f[2 * w] = p, f[2 * w + 1] = q;
+    else f[w] = p, f[w + 8] = q;
+  }
+}
+
+// 16 of a head's values -> codes and, by the head's first lane, the scale.  LPH consecutive lanes hold a head; all lanes of
+// the warp take part, those without a destination too.
+template <int CODE, int LPH>
+__device__ __forceinline__ void store_codes(float (&f)[16], uint8_t* d0, uint8_t* d1, float* scale, bool first) {
+  constexpr float top = CODE == COLI_ATTN_CODE_INT8 ? 127.f : 448.f;
+  uint32_t bits = 0;  // of the largest |x|: as integers, infinity and NaN are larger than all others
+#pragma unroll
+  for (int i = 0; i < 16; ++i) bits = max(bits, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+#pragma unroll
+  for (int o = 1; o < LPH; o <<= 1) bits = max(bits, __shfl_xor_sync(FULL, bits, o));
+  if (!d0) return;
+  float m = __uint_as_float(bits);
+  const bool finite = bits < 0x7F800000u;
+  if (first) *scale = finite ? __fdiv_rn(m, top) : __uint_as_float(0x7FFFFFFFu);
+  if (!finite || bits == 0) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) f[i] = 0.f;
+    m = 1.f;
+  } else if (m >= 0x1p100f) {  // top * x must not overflow
+#pragma unroll
+    for (int i = 0; i < 16; ++i) f[i] *= 0x1p-20f;
+    m *= 0x1p-20f;
+  }
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = __fdiv_rn(top * f[4 * k + i], m);
+    if constexpr (CODE == COLI_ATTN_CODE_INT8) {
+      const uint32_t a = (uint32_t)__float2int_rn(y[0]) & 0xFFu, b = (uint32_t)__float2int_rn(y[1]) & 0xFFu,
+                     c = (uint32_t)__float2int_rn(y[2]) & 0xFFu, d = (uint32_t)__float2int_rn(y[3]);
+      w[k] = a | b << 8 | c << 16 | d << 24;
+    } else {
+      uint16_t lo, hi;
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(y[1]), "f"(y[0]));
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(y[3]), "f"(y[2]));
+      w[k] = (uint32_t)lo | (uint32_t)hi << 16;
+    }
+  }
+  *reinterpret_cast<uint2*>(d0) = make_uint2(w[0], w[1]);
+  *reinterpret_cast<uint2*>(d1) = make_uint2(w[2], w[3]);
+}
+
+// warps_per_token consecutive warps share a token's heads.  CODE: the type of an 8-bit cache, or 0
+template <class T, int D, int CODE>
 __global__ void __launch_bounds__(kAppendWarps * 32) attn_append_kernel(const AttnAppend a, int warps_per_token) {
   constexpr int LPH = D / 16, HPW = 32 / LPH;  // lanes per head, heads per warp
   griddep_wait();
@@ -129,14 +192,33 @@ __global__ void __launch_bounds__(kAppendWarps * 32) attn_append_kernel(const At
       const int gk = g + k * warps_per_token;
       if (gk >= groups) break;
       int h = gk * HPW + sub;
+      if constexpr (CODE != 0) {
+        if (gk * HPW + HPW > nq) {  // some of the warp's heads are keys or values
+          float f[16], *scale = nullptr;
+          uint8_t* d = nullptr;
+          widen<T>(x[k], y[k], f);
+          int g = h - nq;
+          const bool value = g >= a.n_kv;
+          if (rot && !value) rotate16(f, cs, sn, a.interleaved);
+          if (value) g -= a.n_kv;
+          if (store && h >= nq && g < a.n_kv) {
+            d = static_cast<uint8_t*>(value ? a.vc : a.kc) + page * (value ? a.vp : a.kp) + g * (value ? a.vh : a.kh) +
+                slot * (value ? a.vs : a.ks);
+            scale = (value ? a.v_scale : a.k_scale) + page * (value ? a.vsp : a.ksp) + g * (value ? a.vsh : a.ksh) + slot;
+          }
+          // (a value's head is not rotated: its lanes hold the same columns, which are stored where they belong)
+          store_codes<CODE, LPH>(f, d ? d + i0 : nullptr, d ? d + i1 : nullptr, scale, e == 0);
+          if (h >= nq) continue;
+        }
+      }
       uint16_t* dst = nullptr;
       bool turn = rot;
       if (h < nq) {
         dst = static_cast<uint16_t*>(a.q_out) + token * a.q_out_stride + (int64_t)h * D;
       } else if ((h -= nq) < a.n_kv) {
-        if (store) dst = static_cast<uint16_t*>(a.kc) + page * a.kp + h * a.kh + slot * a.ks;
+        if (CODE == 0 && store) dst = static_cast<uint16_t*>(a.kc) + page * a.kp + h * a.kh + slot * a.ks;
       } else if ((h -= a.n_kv) < a.n_kv) {
-        if (store) dst = static_cast<uint16_t*>(a.vc) + page * a.vp + h * a.vh + slot * a.vs;
+        if (CODE == 0 && store) dst = static_cast<uint16_t*>(a.vc) + page * a.vp + h * a.vh + slot * a.vs;
         turn = false;
       }
       if (dst) {
@@ -151,7 +233,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) attn_append_kernel(const At
   }
 }
 
-template <class T, int D>
+template <class T, int D, int CODE>
 cudaError_t launch(const AttnAppend& a, int num_sms, cudaStream_t stream) {
   const int groups = ((a.q ? a.n_q : 0) + 2 * a.n_kv + 32 * 16 / D - 1) / (32 * 16 / D);
   // Enough warps to fill the GPU from few tokens, otherwise as few as possible per token, since each computes its token's
@@ -168,15 +250,22 @@ cudaError_t launch(const AttnAppend& a, int num_sms, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_append_kernel<T, D>, a, wpt);
+  return cudaLaunchKernelEx(&cfg, attn_append_kernel<T, D, CODE>, a, wpt);
+}
+
+template <class T, int D>
+cudaError_t launch_code(const AttnAppend& a, int num_sms, cudaStream_t stream) {
+  if (a.code == COLI_ATTN_CODE_INT8) return launch<T, D, COLI_ATTN_CODE_INT8>(a, num_sms, stream);
+  if (a.code == COLI_ATTN_CODE_E4M3) return launch<T, D, COLI_ATTN_CODE_E4M3>(a, num_sms, stream);
+  return launch<T, D, 0>(a, num_sms, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_append(const AttnAppend& a, int dtype, int num_sms, cudaStream_t stream) {
   if (dtype == COLI_ATTN_BF16)
-    return a.head_dim == 64 ? launch<Bf16, 64>(a, num_sms, stream) : launch<Bf16, 128>(a, num_sms, stream);
-  return a.head_dim == 64 ? launch<Fp16, 64>(a, num_sms, stream) : launch<Fp16, 128>(a, num_sms, stream);
+    return a.head_dim == 64 ? launch_code<Bf16, 64>(a, num_sms, stream) : launch_code<Bf16, 128>(a, num_sms, stream);
+  return a.head_dim == 64 ? launch_code<Fp16, 64>(a, num_sms, stream) : launch_code<Fp16, 128>(a, num_sms, stream);
 }
 
 }  // namespace coli

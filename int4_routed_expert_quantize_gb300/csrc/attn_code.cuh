@@ -1,0 +1,83 @@
+// Device helpers of the attention kernels over an 8-bit cache: codes to fp16, and the copies of code tiles and their scales.
+#pragma once
+
+#include "attn_device.cuh"
+
+namespace coli {
+
+// Four codes of a word -> two fp16 pairs: bytes 0 and 2, bytes 1 and 3.  A code is `unit` times its fp16 value, which is exact.
+template <int CODE>
+struct Code;
+
+template <>
+struct Code<COLI_ATTN_CODE_INT8> {
+  static constexpr float unit = 1.f;
+  // offset by 128, the byte is the mantissa of 1024 + c + 128
+  static __device__ __forceinline__ void widen(uint32_t w, uint32_t& even, uint32_t& odd) {
+    const uint32_t u = w ^ 0x80808080u;
+    even = minus(__byte_perm(u, 0x64646464u, 0x4240));
+    odd = minus(__byte_perm(u, 0x64646464u, 0x4341));
+  }
+  static __device__ __forceinline__ uint32_t minus(uint32_t v) {
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x64806480u));  // 1152
+    return r;
+  }
+};
+
+template <>
+struct Code<COLI_ATTN_CODE_E4M3> {
+  static constexpr float unit = 256.f;
+  // e4m3's exponent and mantissa are fp16's, whose exponent is offset by 8 more (so subnormal codes are subnormal too).
+  // Codes 0x7F and 0xFF come out finite, so that a slot that no row sees cannot spoil a product with its zero weight.
+  static __device__ __forceinline__ void widen(uint32_t w, uint32_t& even, uint32_t& odd) {
+    even = ((w << 7) & 0x3F803F80u) | ((w << 8) & 0x80008000u);
+    odd = ((w >> 1) & 0x3F803F80u) | (w & 0x80008000u);
+  }
+};
+
+// One plain bulk copy, completing on `bar`; 16-byte aligned, bytes a multiple of 16.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_addr(dst)),
+               "l"(src), "r"(bytes), "r"(smem_addr(bar))
+               : "memory");
+}
+
+// One warp fills the stage of a KT-key tile: the boxes that hold keys some row of the block sees, lane i box i: the keys' codes
+// to `keys`, the values' to `vals`, their scales to scales[0..KT-1] and scales[KT..2KT-1].  A page whose id is out of range
+// reads as zeros, scales included, and is reported.
+template <int KT, int D>
+__device__ __forceinline__ void fill_codes(const AttnParams& p, const CUtensorMap* kmap, const CUtensorMap* vmap, uint8_t* keys,
+                                           uint8_t* vals, float* scales, uint64_t* bar, const int32_t* table, int p0, int p1,
+                                           int j0, int head, int lane) {
+  const int page = 1 << p.page_shift;
+  const int rows = min(page, KT);  // slots per box
+  const int boxes = KT / rows;
+  const int a = j0 + lane * rows, e = a + rows - 1;  // the lane's keys
+  const bool need = lane < boxes && a <= p1 && (e > p0 - p.window || a < p.sinks);
+  int id = 0;
+  if (need) id = __ldg(table + (a >> p.page_shift));
+  const bool bad = need && (id < 0 || id >= p.n_pages);
+  if (bad) {
+    id = p.n_pages;  // the tensor copies' coordinate past the end
+    atomicExch(p.status, COLI_EINVAL);
+    for (int i = 0; i < rows; ++i) scales[lane * rows + i] = scales[KT + lane * rows + i] = 0.f;
+    fence_proxy_async_smem();  // a later tile's copies go to the same place
+  }
+  const int n = __popc(__ballot_sync(FULL, need)), good = n - __popc(__ballot_sync(FULL, bad));
+  __syncwarp();
+  if (lane == 0) mbar_expect_tx(bar, (uint32_t)rows * (uint32_t)(n * 2 * D + good * 8));
+  __syncwarp();
+  if (need) {
+    const int slot = a & (page - 1);
+    tma_load_4d(keys + lane * rows * D, kmap, 0, slot, head, id, bar);
+    tma_load_4d(vals + lane * rows * D, vmap, 0, slot, head, id, bar);
+    if (!bad) {
+      bulk_load(scales + lane * rows, p.k_scale + id * p.ks_page + head * p.ks_head + slot, rows * 4, bar);
+      bulk_load(scales + KT + lane * rows, p.v_scale + id * p.vs_page + head * p.vs_head + slot, rows * 4, bar);
+    }
+  }
+  __syncwarp();
+}
+
+}  // namespace coli

@@ -72,10 +72,13 @@ struct AttnParams {
   int* redo_any;   // [0] some are; [1] blocks of that kernel that are done
   int64_t k_page, k_head, k_slot, v_page, v_head, v_slot;  // cache strides, for those units
   const void *kc, *vc;
+  // 8-bit caches: a scale for each token and key head, tokens of a page next to one another
+  const float *k_scale, *v_scale;
+  int64_t ks_page, ks_head, vs_page, vs_head;
   int* status;
 };
 
-struct AttnKvMaps {  // boxes of 64 values x min(page, box) slots, 128-byte swizzle
+struct AttnKvMaps {  // boxes of 64 values (8-bit caches: of a head) x min(page, box) slots, swizzled
   CUtensorMap k64, v64;    // box 64 slots: split kernel
   CUtensorMap k128, v128;  // box 128 slots: tensor-memory kernel
 };
@@ -91,6 +94,9 @@ struct AttnAppend {
   int n_q, n_kv, head_dim, rot, interleaved;
   const int32_t* pos_base;  // added to every position for the rotation, or nullptr
   const uint64_t* turn;  // [rot/2] turns per position as a fraction of 2^64
+  int code;              // type of an 8-bit cache (COLI_ATTN_CODE_*), 0: the 16-bit type
+  float *k_scale, *v_scale;
+  int64_t ksp, ksh, vsp, vsh;  // strides of its scales
   int* status;
 };
 
@@ -99,6 +105,10 @@ int split_grid(int num_sms);  // CTAs
 cudaError_t configure_attn_split();
 cudaError_t launch_attn_split(const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v,
                               int rows, int dtype, int num_sms, cudaStream_t stream);
+// the same over an 8-bit cache of type `code`
+cudaError_t configure_attn_qsplit();
+cudaError_t launch_attn_qsplit(const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v,
+                               int rows, int dtype, int code, int num_sms, cudaStream_t stream);
 int tile_block_tokens(int group);  // tokens per block of the tensor-memory kernel
 cudaError_t configure_attn_tile();
 cudaError_t launch_attn_tile(const AttnParams& p, const CUtensorMap& q, const CUtensorMap& k,

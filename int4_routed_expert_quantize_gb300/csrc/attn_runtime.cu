@@ -35,6 +35,9 @@ struct coli_attn {
 struct coli_attn_kv {
   coli_attn_cache c{};
   int n_kv = 0, head_dim = 0, page = 0, dtype = 0, device = 0;
+  int code = 0;  // COLI_ATTN_CODE_*: an 8-bit cache (and dtype is the handle's); 0: of the handle's type
+  float *k_scale = nullptr, *v_scale = nullptr;
+  int64_t ks_page = 0, ks_head = 0, vs_page = 0, vs_head = 0;
   AttnKvMaps maps;
 };
 
@@ -60,19 +63,22 @@ EncodeTiled encoder() {
   return fn;
 }
 
-// cache memory as [page][head][slot][value], boxes of 64 values x `slots` slots
+// cache memory as [page][head][slot][value], boxes of 64 values (8-bit codes: of a whole head) x `slots` slots
 bool cache_map(CUtensorMap* map, const void* base, const coli_attn_kv& kv, int64_t ps, int64_t hs,
                int64_t ss, int slots) {
   EncodeTiled fn = encoder();
   if (!fn) return false;
   const cuuint64_t dims[4] = {(cuuint64_t)kv.head_dim, (cuuint64_t)kv.page, (cuuint64_t)kv.n_kv,
                               (cuuint64_t)kv.c.n_pages};
-  const cuuint64_t strides[3] = {(cuuint64_t)ss * 2, (cuuint64_t)hs * 2, (cuuint64_t)ps * 2};
-  const cuuint32_t box[4] = {64, (cuuint32_t)(kv.page < slots ? kv.page : slots), 1, 1};
+  const cuuint64_t size = kv.code ? 1 : 2;
+  const cuuint64_t strides[3] = {(cuuint64_t)ss * size, (cuuint64_t)hs * size, (cuuint64_t)ps * size};
+  const cuuint32_t box[4] = {kv.code ? (cuuint32_t)kv.head_dim : 64, (cuuint32_t)(kv.page < slots ? kv.page : slots), 1, 1};
   const cuuint32_t unit[4] = {1, 1, 1, 1};
-  return fn(map, kv.dtype == COLI_ATTN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-            4, const_cast<void*>(base), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  const CUtensorMapDataType type = kv.code                       ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : kv.dtype == COLI_ATTN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                                 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  return fn(map, type, 4, const_cast<void*>(base), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            box[0] * size == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -122,6 +128,7 @@ cudaError_t configure_device(int dev) {
   if (g_configured[dev]) return cudaSuccess;
   cudaError_t e = configure_attn_split();
   if (e == cudaSuccess) e = configure_attn_tile();
+  if (e == cudaSuccess) e = configure_attn_qsplit();
   if (e == cudaSuccess) g_configured[dev] = true;
   return e;
 }
@@ -180,6 +187,8 @@ AttnParams params(const coli_attn* h, const coli_attn_kv* kv, const coli_attn_ba
   p.k_page = kv->c.k_page_stride, p.k_head = kv->c.k_head_stride, p.k_slot = kv->c.k_slot_stride;
   p.v_page = kv->c.v_page_stride, p.v_head = kv->c.v_head_stride, p.v_slot = kv->c.v_slot_stride;
   p.kc = kv->c.k, p.vc = kv->c.v;
+  p.k_scale = kv->k_scale, p.v_scale = kv->v_scale;
+  p.ks_page = kv->ks_page, p.ks_head = kv->ks_head, p.vs_page = kv->vs_page, p.vs_head = kv->vs_head;
   p.redo = h->redo, p.redo_any = h->redo_any, p.unit_cost = kSplitUnitCost;
   p.status = h->status;
   return p;
@@ -244,6 +253,41 @@ int list_fits(const AttnParams& p, int keys) {
   const int64_t blocks = p.n_tokens / p.block_tokens;  // whole ones: each sequence, and the prefix, may have one more
   const int64_t units = (blocks + p.n_seqs + (p.pre_len ? blocks + 1 : 0)) * p.n_kv;
   return units <= 0x7FFFFFFF / (span / keys + 2 + p.unit_cost) ? COLI_OK : COLI_EUNSUPPORTED;
+}
+
+// a cache's memory: codes of one byte in units of 16, values of the 16-bit types in units of 8
+int check_cache(const coli_attn* h, const coli_attn_cache& c, int unit) {
+  if (!c.k || !c.v || c.n_pages < 1 || c.n_pages > 0x7FFFFFFE) return COLI_EINVAL;
+  const int64_t D = h->cfg.head_dim;
+  const int64_t strides[6] = {c.k_page_stride, c.k_head_stride, c.k_slot_stride,
+                              c.v_page_stride, c.v_head_stride, c.v_slot_stride};
+  for (int64_t s : strides)
+    if (s < D || (s & (unit - 1)) || s >= (1LL << 38)) return COLI_EINVAL;
+  const int64_t extent[3] = {c.n_pages, h->cfg.n_kv, h->cfg.page};
+  if (overlap({c.k_page_stride, c.k_head_stride, c.k_slot_stride}, extent, D) ||
+      overlap({c.v_page_stride, c.v_head_stride, c.v_slot_stride}, extent, D))
+    return COLI_EINVAL;
+  if (((uintptr_t)c.k & 15u) || ((uintptr_t)c.v & 15u)) return COLI_EINVAL;
+  return COLI_OK;
+}
+
+bool bad_scales(const coli_attn* h, const float* base, int64_t n_pages, int64_t page_stride, int64_t head_stride) {
+  const int64_t width = h->cfg.page, extent[3] = {n_pages, h->cfg.n_kv, 1};
+  for (int64_t s : {page_stride, head_stride})
+    if (s < width || (s & 3) || s >= (1LL << 36)) return true;
+  return !base || ((uintptr_t)base & 15u) || overlap({page_stride, head_stride, width}, extent, width);
+}
+
+int bind(const coli_attn* h, coli_attn_kv* kv, const coli_attn_cache& c) {
+  kv->c = c;
+  kv->n_kv = h->cfg.n_kv, kv->head_dim = h->cfg.head_dim, kv->page = h->cfg.page;
+  kv->dtype = h->cfg.dtype, kv->device = h->device;
+  return cache_map(&kv->maps.k64, c.k, *kv, c.k_page_stride, c.k_head_stride, c.k_slot_stride, kSplitKeys) &&
+                 cache_map(&kv->maps.v64, c.v, *kv, c.v_page_stride, c.v_head_stride, c.v_slot_stride, kSplitKeys) &&
+                 cache_map(&kv->maps.k128, c.k, *kv, c.k_page_stride, c.k_head_stride, c.k_slot_stride, kTileKeys) &&
+                 cache_map(&kv->maps.v128, c.v, *kv, c.v_page_stride, c.v_head_stride, c.v_slot_stride, kTileKeys)
+             ? COLI_OK
+             : COLI_ECUDA;
 }
 
 }  // namespace
@@ -320,31 +364,41 @@ extern "C" void coli_attn_destroy(coli_attn* h) {
 extern "C" int coli_attn_cache_bind(coli_attn* h, const coli_attn_cache* cache, coli_attn_kv** out) {
   if (out) *out = nullptr;
   if (!h || !cache || !out) return COLI_EINVAL;
-  const coli_attn_cache& c = *cache;
-  if (!c.k || !c.v || c.n_pages < 1 || c.n_pages > 0x7FFFFFFE) return COLI_EINVAL;
-  const int64_t D = h->cfg.head_dim;
-  const int64_t strides[6] = {c.k_page_stride, c.k_head_stride, c.k_slot_stride,
-                              c.v_page_stride, c.v_head_stride, c.v_slot_stride};
-  for (int64_t s : strides)
-    if (s < D || (s & 7) || s >= (1LL << 38)) return COLI_EINVAL;
-  const int64_t extent[3] = {c.n_pages, h->cfg.n_kv, h->cfg.page};
-  if (overlap({c.k_page_stride, c.k_head_stride, c.k_slot_stride}, extent, D) ||
-      overlap({c.v_page_stride, c.v_head_stride, c.v_slot_stride}, extent, D))
-    return COLI_EINVAL;
-  if (((uintptr_t)c.k & 15u) || ((uintptr_t)c.v & 15u)) return COLI_EINVAL;
-  int rc = check_device(h->device);
+  int rc = check_cache(h, *cache, 8);
+  if (!rc) rc = check_device(h->device);
   if (rc) return rc;
   coli_attn_kv* kv = new (std::nothrow) coli_attn_kv();
   if (!kv) return COLI_ENOMEM;
-  kv->c = c;
-  kv->n_kv = h->cfg.n_kv, kv->head_dim = h->cfg.head_dim, kv->page = h->cfg.page;
-  kv->dtype = h->cfg.dtype, kv->device = h->device;
-  if (!cache_map(&kv->maps.k64, c.k, *kv, c.k_page_stride, c.k_head_stride, c.k_slot_stride, kSplitKeys) ||
-      !cache_map(&kv->maps.v64, c.v, *kv, c.v_page_stride, c.v_head_stride, c.v_slot_stride, kSplitKeys) ||
-      !cache_map(&kv->maps.k128, c.k, *kv, c.k_page_stride, c.k_head_stride, c.k_slot_stride, kTileKeys) ||
-      !cache_map(&kv->maps.v128, c.v, *kv, c.v_page_stride, c.v_head_stride, c.v_slot_stride, kTileKeys)) {
+  rc = bind(h, kv, *cache);
+  if (rc) {
     delete kv;
-    return COLI_ECUDA;
+    return rc;
+  }
+  *out = kv;
+  return COLI_OK;
+}
+
+extern "C" int coli_attn_qcache_bind(coli_attn* h, const coli_attn_qcache* cache, coli_attn_kv** out) {
+  if (out) *out = nullptr;
+  if (!h || !cache || !out) return COLI_EINVAL;
+  const coli_attn_qcache& q = *cache;
+  if (q.type != COLI_ATTN_CODE_INT8 && q.type != COLI_ATTN_CODE_E4M3) return COLI_EINVAL;
+  int rc = check_cache(h, q.codes, 16);
+  if (!rc && (bad_scales(h, q.k_scale, q.codes.n_pages, q.k_scale_page_stride, q.k_scale_head_stride) ||
+              bad_scales(h, q.v_scale, q.codes.n_pages, q.v_scale_page_stride, q.v_scale_head_stride)))
+    rc = COLI_EINVAL;
+  if (!rc) rc = check_device(h->device);
+  if (rc) return rc;
+  coli_attn_kv* kv = new (std::nothrow) coli_attn_kv();
+  if (!kv) return COLI_ENOMEM;
+  kv->code = q.type;
+  kv->k_scale = q.k_scale, kv->v_scale = q.v_scale;
+  kv->ks_page = q.k_scale_page_stride, kv->ks_head = q.k_scale_head_stride;
+  kv->vs_page = q.v_scale_page_stride, kv->vs_head = q.v_scale_head_stride;
+  rc = bind(h, kv, q.codes);
+  if (rc) {
+    delete kv;
+    return rc;
   }
   *out = kv;
   return COLI_OK;
@@ -379,6 +433,8 @@ extern "C" int coli_attn_append(coli_attn* h, const coli_attn_kv* kv, const coli
   a.n_q = h->cfg.n_q, a.n_kv = h->cfg.n_kv, a.head_dim = h->cfg.head_dim;
   a.rot = h->cfg.rot_dim, a.interleaved = h->cfg.rot_interleaved;
   a.pos_base = pos_base, a.turn = h->turn, a.status = h->status;
+  a.code = kv->code, a.k_scale = kv->k_scale, a.v_scale = kv->v_scale;
+  a.ksp = kv->ks_page, a.ksh = kv->ks_head, a.vsp = kv->vs_page, a.vsh = kv->vs_head;
   return launch_attn_append(a, h->cfg.dtype, h->num_sms, (cudaStream_t)stream) == cudaSuccess ? COLI_OK
                                                                                                : COLI_ECUDA;
 }
@@ -402,7 +458,16 @@ extern "C" int coli_attn_window(coli_attn* h, const coli_attn_kv* kv, const coli
   // suit it: 8 of up to 96 rows 26.5 / one launch 16.7, 40 mixed ones of 4000 tokens 146 / 125.
   const int64_t seq_rows = (int64_t)b->max_q * p.group;
   cudaError_t e;
-  if (seq_rows <= kSplitMaxRows) {
+  if (kv->code) {
+    if (p.group > kSplitMaxRows) return COLI_EUNSUPPORTED;
+    const int rows = split_rows(seq_rows), ctas = split_grid(h->num_sms);
+    p.block_tokens = rows / p.group;
+    rc = list_fits(p, kSplitKeys);
+    if (rc) return rc;
+    e = launch_attn_qsplit(p, kv->maps.k64, kv->maps.v64, rows, h->cfg.dtype, kv->code, h->num_sms, st);
+    if (e == cudaSuccess)
+      e = launch_attn_combine(p, rows, (int)(seq_rows < rows ? seq_rows : rows), ctas, h->cfg.dtype, st);
+  } else if (seq_rows <= kSplitMaxRows) {
     const int rows = split_rows(seq_rows), ctas = split_grid(h->num_sms);
     p.block_tokens = rows / p.group;
     rc = list_fits(p, kSplitKeys);
@@ -427,6 +492,7 @@ extern "C" int coli_attn_prefix(coli_attn* h, const coli_attn_kv* kv, const coli
                                 float* lse, void* stream) {
   int rc = check_call(h, kv, b);
   if (rc) return rc;
+  if (kv->code) return COLI_EUNSUPPORTED;
   if (prefix_pages < 0 || (prefix_pages > 0 && !prefix_table) || !prefix_len ||
       ((int64_t)prefix_pages << h->page_shift) > kAttnNoWindow || b->n_tokens > h->prefix_tokens)
     return COLI_EINVAL;
