@@ -2,6 +2,7 @@
 #pragma once
 
 #include "attn_device.cuh"
+#include "bulk.cuh"
 
 namespace coli {
 
@@ -35,13 +36,6 @@ struct Code<COLI_ATTN_CODE_E4M3> {
     odd = ((w >> 1) & 0x3F803F80u) | (w & 0x80008000u);
   }
 };
-
-// One plain bulk copy, completing on `bar`; 16-byte aligned, bytes a multiple of 16.
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_addr(dst)),
-               "l"(src), "r"(bytes), "r"(smem_addr(bar))
-               : "memory");
-}
 
 // One warp fills the stage of a KT-key tile: the boxes that hold keys some row of the block sees, lane i box i: the keys' codes
 // to `keys`, the values' to `vals`, their scales to scales[0..KT-1] and scales[KT..2KT-1].  A page whose id is out of range

@@ -1,6 +1,7 @@
-// Python calls of the paged-cache attention (coli_attn.h).  A serving loop makes one of these calls per layer and step, and
+// Python calls of the paged-cache attention (coli_attn.h) and of the 4-bit products (coli_linear.h).  A serving loop makes one of these calls per layer and step, and
 // their small forms run for a few microseconds on the GPU, so the checks of the tensors, the new output and the
-// call itself are here and not in Python.  Everything else of the binding is in attn.py.
+// call itself are here and not in Python.  Everything else of the bindings is in attn.py and
+// linear.py.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -11,6 +12,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "coli_attn.h"
+#include "coli_linear.h"
 
 namespace {
 
@@ -25,6 +27,12 @@ struct Engine {
 struct Batch {
   coli_attn_batch batch;
   int32_t device;
+};
+
+// what linear.py keeps of its weights
+struct Linear {
+  coli_linear* handle;
+  int32_t rows, cols, dtype, device;
 };
 
 struct Error {};  // the Python exception is set
@@ -87,7 +95,8 @@ float* log_sums(PyObject* o, const Engine& e, const coli_attn_batch& b) {
 }
 
 // the stream of a call: the current one (None), or a handle
-c10::cuda::CUDAStream stream_of(PyObject* o, const Engine& e) {
+template <class Owner>
+c10::cuda::CUDAStream stream_of(PyObject* o, const Owner& e) {
   if (o == Py_None) return c10::cuda::getCurrentCUDAStream(e.device);
   const auto handle = (cudaStream_t)PyLong_AsVoidPtr(o);
   if (!handle && PyErr_Occurred()) throw Error();
@@ -203,10 +212,42 @@ PyObject* prefix(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// [n, width] of the weights' type on their device, rows contiguous -> the row stride
+int64_t rows_of(const at::Tensor& t, const Linear& l, int64_t n, int32_t width, const char* what) {
+  const auto type = l.dtype == COLI_ATTN_BF16 ? at::kBFloat16 : at::kHalf;
+  if (t.dim() != 2 || t.size(0) != n || t.size(1) != width || t.scalar_type() != type || !t.is_cuda() ||
+      t.get_device() != l.device || n > INT32_MAX)
+    fail("%s: [tokens, columns in or rows out] of the weights' type on their device", what);
+  if (width > 1 && t.stride(1) != 1) fail("%s: a token's values are contiguous", what);
+  return n > 1 ? t.stride(0) : (width + 7) / 8 * 8;
+}
+
+// linear(weights, x, out, stream)
+PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 4, [&] {
+    const Linear& l = *pointer<Linear>(a[0]);
+    const at::Tensor& x = tensor(a[1], "x");
+    const int64_t tokens = x.dim() == 2 ? x.size(0) : 0, xs = rows_of(x, l, tokens, l.cols, "x");
+    const auto stream = stream_of(a[3], l);
+    at::Tensor out;
+    int64_t os = l.rows;
+    if (a[2] != Py_None) {
+      out = tensor(a[2], "out");
+      os = rows_of(out, l, tokens, l.rows, "out");
+    } else {  // memory of the call's stream, as for the attention's outputs
+      c10::cuda::OptionalCUDAStreamGuard guard;
+      if (a[3] != Py_None) guard.reset_stream(stream);
+      out = at::empty({tokens, l.rows}, x.options());
+    }
+    return result(coli_linear_forward(l.handle, x.data_ptr(), xs, (int)tokens, out.data_ptr(), os, stream.stream()), &out);
+  });
+}
+
 PyMethodDef methods[] = {
     {"append", (PyCFunction)(void (*)())append, METH_FASTCALL, nullptr},
     {"window", (PyCFunction)(void (*)())window, METH_FASTCALL, nullptr},
     {"prefix", (PyCFunction)(void (*)())prefix, METH_FASTCALL, nullptr},
+    {"linear", (PyCFunction)(void (*)())linear, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 
