@@ -1,22 +1,25 @@
 // y = W x for few tokens, W in 4-bit codes with a scale for each row and group of columns:
 //   y[t,n] = sum_g s[n,g] sum_{k in g} c[n,k] x[t,k]
 //
-// At up to 16 tokens every weight byte is used by few products, so HBM bounds it and the kernel is built around one stream
-// of weights: a persistent CTA an SM, in which one lane keeps a ring of some 180 KB full with bulk copies.  The weights are the
-// handle's, written by load alone, so the first copies start before the launch that makes x has ended.
+// At up to 16 tokens every weight byte is used by few products, so HBM bounds it, and next to it the instructions that make fp16 of
+// 4-bit codes: a word of 8 takes 5 on the ALU and 4 on the fp16 pipe, and mma.sync gets in their way (together 73 cycles a block and SM
+// partition, where HBM takes 98).  So the 12 product warps of an SM stay clear of one another: each keeps a ring of its own in shared
+// memory full with bulk copies and waits for nobody else, x stays in its registers, and the sums that it shares with others go to
+// warps that do nothing but add.  The weights are the handle's, written by load alone, so the first copies start before the launch that
+// makes x has ended.
 //
-// The store.  8 rows x 128 columns are a block: 32 lanes x 16 bytes of codes (+ 8, so that they are unsigned), then the 8 rows'
-// scales of each group.  A tile of 8 rows is its blocks one after another, so a ring stage is one copy, and a lane's
-// 16 bytes are what it feeds to the matrix instructions.  Lane (n = lane / 4, c = lane % 4) holds 4 words of 8 columns of row n, all of one
-// group for all c: groups of 128 take columns 32 c + 8 j (word j), of 64 columns 64 (j / 2) + 16 c + 8 (j % 2), of 32 columns 32 j + 8 c.
-// Nibble i of a word is column 2 i (i < 4) or 2 i - 7, so that (w >> 4 i) & 0x000F000F is a pair of neighbours.
+// The store.  8 rows x 128 columns are a block: 32 lanes x 16 bytes of codes (+ 8, so that they are unsigned), then each row's
+// scales of the block's groups.  A tile of 8 rows is its blocks one after another.  Lane (n = lane / 4, c = lane % 4) holds 4 words of 8 columns of
+// row n, all of one group for all c: groups of 128 take columns 32 c + 8 j (word j), of 64 columns 64 (j / 2) + 16 c + 8 (j % 2), of 32
+// columns 32 j + 8 c.  Nibble i of a word is column 2 i (i < 4) or 2 i - 7, so that masks take pairs of neighbours.
 //
-// A warp has nb of a tile's blocks, the same ones of every tile: their share of x stays in its registers, as the A operand of
-// mma.sync (16 tokens, or 8 and zeros), and the weights are B: 8 rows a step, so tiles are narrow and the SMs
-// end together.  A code becomes bf16 or fp16 exactly, by its bits under the exponent of 128 or 1024; a group's sum is fp32 and
-// its scale multiplies it in fp32.  The warps' sums of a tile meet in shared memory, where a warp of its own adds them in order.
-// Columns beyond what the registers of one CTA hold (48 blocks at 8 tokens, 32 at 16) are split over a cluster, whose CTAs send
-// their sums to the first one.
+// A warp has NB blocks of every tile that it takes, the same ones each time, 2 or 4 tiles a step: two tiles' weights are the A operand of
+// mma.sync, x of 8 or 2 x 8 tokens is B.  A CTA has a range of tiles, so the SMs end together to within 8 rows.  Columns beyond what
+// the registers of one CTA hold (48 blocks at 8 tokens, 24 at 16) are split over a cluster, whose CTAs send their sums to the first one.
+//
+// x: bf16 becomes fp16 times a power of two for each token and warp, which puts its largest value there in 2^14..2^15 (what is below
+// 2^-39 of that is lost, beyond fp32's share of the sum).  A code becomes fp16 exactly, a group's sum is fp32, its scale and that
+// power multiply it in fp32.
 #include <algorithm>
 #include <new>
 
@@ -36,17 +39,19 @@ struct coli_linear {
 
 namespace {
 
-constexpr int kProduct = 16;                // product warps
-constexpr int kThreads = (kProduct + 2) * 32;  // and one that copies, one that adds
-constexpr int kRing = 184320;               // bytes of the ring, at most
-constexpr int kMaxStages = 16;
-constexpr int kSums = 4;                    // buffers of the warps' sums
-constexpr int kMaxParts = 8;                // CTAs of a cluster
+constexpr int kProduct = 12;  // product warps
+constexpr int kAdd = 4;       // warps that add their sums: 16 in all, of up to 128 registers
+constexpr int kThreads = (kProduct + kAdd) * 32;
+constexpr int kSmem = 232448;  // of a CTA
+constexpr int kMaxSlots = 8;  // of a warp's ring
+constexpr int kRing = 106496;  // bytes of all rings that are enough
+constexpr int kIn = 4;        // buffers of the other CTAs' sums
+constexpr int kMaxParts = 8;  // CTAs of a cluster
 constexpr int kBlockCodes = 512;
 
 __host__ __device__ constexpr int block_bytes(int group) { return kBlockCodes + 16 * (128 / group); }
-
-__host__ __device__ constexpr int max_blocks(int mt) { return mt == 1 ? 3 : 2; }  // of a warp
+__host__ __device__ constexpr int step_tiles(int mt) { return 2 * mt; }    // of a warp
+__host__ __device__ constexpr int sum_buffers(int mt) { return mt == 1 ? 4 : 2; }
 
 struct LinearParams {
   const uint8_t* store;
@@ -54,10 +59,10 @@ struct LinearParams {
   uint16_t* y;
   int64_t x_stride, y_stride;
   int n_tokens, rows, cols;
-  int tiles, blocks;   // of the whole matrix
-  int part;            // blocks of a CTA of the cluster (the last one may have fewer)
-  int nb, kw, rw;      // blocks a warp, warps a tile, tiles a stage
-  int stages;
+  int tiles, blocks;  // of the whole matrix
+  int part;           // blocks of a CTA of the cluster (the last one may have fewer)
+  int kw, rw;         // warps that share a tile, tiles' worth of warps: a step is rw * step_tiles tiles
+  int slots;
   int* status;
 };
 
@@ -67,23 +72,50 @@ __device__ __forceinline__ int word_col(int c, int j) {
   return G == 128 ? 32 * c + 8 * j : G == 64 ? 64 * (j >> 1) + 16 * c + 8 * (j & 1) : 32 * j + 8 * c;
 }
 
-// 8 codes of a word as four pairs of neighbours
-template <class T>
-__device__ __forceinline__ void unpack(uint32_t w, uint32_t (&v)[4]);
-template <>
-__device__ __forceinline__ void unpack<Bf16>(uint32_t w, uint32_t (&v)[4]) {
+// Masks and the exponent of 1024, in registers of their own (as immediates, one of two would be moved to a register each time).
+struct Bits {
+  uint32_t lo, hi, exp;
+  __device__ __forceinline__ Bits() {
+    asm volatile("mov.b32 %0, 0x000F000F;" : "=r"(lo));
+    asm volatile("mov.b32 %0, 0x00F000F0;" : "=r"(hi));
+    asm volatile("mov.b32 %0, 0x64006400;" : "=r"(exp));
+  }
+};
+// 8 codes of a word as four fp16 pairs of neighbours.  Under the exponent of 1024 a nibble in bits 0-3 is 1024 + u, one in bits 4-7 is
+// 1024 + 16 u, so a word takes one shift; u - 8 is exact.
+__device__ __forceinline__ void unpack(const Bits& k, uint32_t w, uint32_t (&v)[4]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t u = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(v[i]) : "r"(u), "r"(0x43084308u));  // 136
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t u = i ? w >> 8 : w;
+    uint32_t lo, hi;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(lo) : "r"(u), "r"(k.lo), "r"(k.exp));  // u & mask | exp
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(hi) : "r"(u), "r"(k.hi), "r"(k.exp));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(v[2 * i]) : "r"(lo), "r"(0x64086408u));                          // 1032
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(v[2 * i + 1]) : "r"(hi), "r"(0x2C002C00u), "r"(0xD480D480u));  // / 16 - 72
   }
 }
-template <>
-__device__ __forceinline__ void unpack<Fp16>(uint32_t w, uint32_t (&v)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t u = ((w >> (4 * i)) & 0x000F000Fu) | 0x64006400u;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(v[i]) : "r"(u), "r"(0x64086408u));  // 1032
+
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ uint16_t lds16(uint32_t at) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts64(uint32_t at, float a, float b) {
+  asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(a), "f"(b) : "memory");
+}
+
+// bounded waits for copies number done .. ahead - 1 of a ring
+__device__ __noinline__ void drain_slots(uint64_t* bars, int slots, int done, int ahead) {
+  for (int i = done; i < ahead; ++i) {
+    const uint64_t t0 = global_ns();
+    while (!mbar_try_wait(bars + i % slots, (uint32_t)((i / slots) & 1)))
+      if (global_ns() - t0 > kWaitLimitNs / 8) break;
   }
 }
 
@@ -98,210 +130,262 @@ __device__ __forceinline__ uint32_t peer(const void* p, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr(p)), "r"(rank));
   return r;
 }
-__device__ __forceinline__ void peer_store(uint32_t addr, float2 v) {
-  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(v.x), "f"(v.y) : "memory");
+// 8 bytes there, which its barrier counts when they have come
+__device__ __forceinline__ void peer_store(uint32_t addr, float2 v, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(addr), "f"(v.x),
+               "f"(v.y), "r"(bar)
+               : "memory");
 }
 __device__ __forceinline__ void peer_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// a bounded wait for what another CTA's peer_arrive releases
-__device__ __forceinline__ bool peer_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
-  const uint64_t t0 = global_ns();
-  bool ok = false;
-#pragma unroll 1
-  for (uint32_t it = 1; !*abort_flag; ++it) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(r)
-        : "r"(smem_addr(bar)), "r"(parity)
-        : "memory");
-    if (r) {
-      ok = true;
-      break;
-    }
-    if ((it & 63u) == 0 && global_ns() - t0 > kWaitLimitNs) {
-      *abort_flag = 1;
-      atomicExch(status, COLI_ETIMEOUT);
-    }
-  }
-  return __all_sync(FULL, ok);
-}
 
-// MT: 1 for up to 8 tokens, 2 for up to 16.  A warp's blocks: at most 3 or 2, 48 or 64 registers of x (18 warps leave 96).
-template <class T, int G, int MT>
+// MT: 1 for up to 8 tokens, 2 for up to 16.  NB: a warp's blocks, at most 4 or 2: 64 registers of x.
+template <class T, int G, int MT, int NB>
 __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearParams p) {
-  constexpr int NB = max_blocks(MT), BLK = block_bytes(G), GPB = 128 / G, OUT = MT * 64;  // OUT: sums of a tile
+  constexpr int BLK = block_bytes(G), GPB = 128 / G, OUT = MT * 64, TP = step_tiles(MT), SUMS = sum_buffers(MT);
+  constexpr int slot_bytes = TP * NB * BLK;  // OUT: sums of a tile
   extern __shared__ __align__(128) uint8_t smem[];
   const int parts = (p.blocks + p.part - 1) / p.part;  // the cluster's size
-  const int stage_bytes = p.rw * p.part * BLK, warps = p.kw * p.rw;
-  float* sums = reinterpret_cast<float*>(smem + (size_t)p.stages * stage_bytes);  // [kSums][warps][OUT]
-  float* inbox = sums + kSums * warps * OUT;                                       // [kSums][parts - 1][rw][OUT]
-  uint64_t* full = reinterpret_cast<uint64_t*>(inbox + kSums * (parts - 1) * p.rw * OUT);
-  uint64_t *empty = full + kMaxStages, *sum_full = empty + kMaxStages, *sum_empty = sum_full + kSums,
-           *in_full = sum_empty + kSums, *in_empty = in_full + kSums;
-  int* abort_flag = reinterpret_cast<int*>(in_empty + kSums);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const auto wait = [&](uint64_t* bar, uint32_t parity) { return warp_wait(bar, parity, abort_flag, p.status); };
+  const int warps = p.kw * p.rw, step = p.rw * TP;
+  const int sum_floats = step * p.kw * OUT, in_floats = step * OUT;
+  // rings [warps][slots], sums [SUMS][step][kw][OUT], the other CTAs' [kIn][parts - 1][step][OUT], barriers
+  float* sums = reinterpret_cast<float*>(smem + warps * p.slots * slot_bytes);
+  float* inbox = sums + SUMS * sum_floats;
+  uint64_t* full = reinterpret_cast<uint64_t*>(inbox + kIn * (parts - 1) * in_floats);
+  uint64_t *sum_full = full + kProduct * kMaxSlots, *sum_empty = sum_full + SUMS, *in_full = sum_empty + SUMS,
+           *in_empty = in_full + kIn;
+  int* abort_flag = reinterpret_cast<int*>(in_empty + kIn);
+  const int tid = threadIdx.x, warp = __shfl_sync(FULL, tid >> 5, 0), lane = tid & 31;
+  const auto wait = [&](uint64_t* bar, uint32_t parity) { return ring_wait(bar, parity, abort_flag, p.status); };
 
   if (tid == 0) {
     *abort_flag = 0;
-    for (int i = 0; i < p.stages; ++i) mbar_init(full + i, 1), mbar_init(empty + i, warps);
-    for (int i = 0; i < kSums; ++i) {
-      mbar_init(sum_full + i, warps), mbar_init(sum_empty + i, 1);
-      mbar_init(in_full + i, parts > 1 ? parts - 1 : 1), mbar_init(in_empty + i, 1);
-    }
-    fence_barrier_init();
+    for (int i = 0; i < SUMS; ++i) mbar_init(sum_full + i, warps), mbar_init(sum_empty + i, kAdd);
+    for (int i = 0; i < kIn; ++i) mbar_init(in_full + i, 1), mbar_init(in_empty + i, kAdd);
   }
-  const int rank = parts > 1 ? (int)cluster_rank() : 0;
-  __syncwarp();
-  if (parts > 1) cluster_sync();
-  else __syncthreads();
+  if (warp < kProduct && lane < kMaxSlots) mbar_init(full + warp * kMaxSlots + lane, 1);
+  fence_barrier_init();
   griddep_launch_dependents();
-
+  const int rank = parts > 1 ? (int)cluster_rank() : 0;
   const int cluster = blockIdx.x / parts, clusters = gridDim.x / parts;
-  const int groups = (p.tiles + p.rw - 1) / p.rw;  // stages' worth of tiles
-  const int g0 = (int)((int64_t)groups * cluster / clusters), g1 = (int)((int64_t)groups * (cluster + 1) / clusters);
+  const int t0 = (int)((int64_t)p.tiles * cluster / clusters), t1 = (int)((int64_t)p.tiles * (cluster + 1) / clusters);
   const int here = min(p.part, p.blocks - rank * p.part);  // blocks of this CTA
   const int tok0 = blockIdx.y * 8 * MT, nt = min(8 * MT, p.n_tokens - tok0);
 
-  if (warp == kProduct) {  // ---- copies
-    int it = 0;
-    bool ok = true;
-#pragma unroll 1
-    for (int g = g0; g < g1; ++g, ++it) {
-      const int s = it % p.stages, n = min(p.rw, p.tiles - g * p.rw);
-      if (it >= p.stages) ok = wait(empty + s, (it / p.stages + 1) & 1);
-      if (!ok) break;
-      if (lane == 0) {
-        mbar_expect_tx(full + s, (uint32_t)(n * here * BLK));
-        for (int r = 0; r < n; ++r)
-          bulk_load(smem + (size_t)s * stage_bytes + r * p.part * BLK,
-                    p.store + ((int64_t)(g * p.rw + r) * p.blocks + rank * p.part) * BLK, here * BLK, full + s);
-      }
+  if (warp < warps) {  // ---- products
+    const int sub = warp / p.kw, ki = warp - sub * p.kw, first = ki * NB;  // the warp's tiles of a step, its blocks of the part
+    const int nb = max(0, min(NB, here - first));  // of which the part has so many; what is behind has x = 0
+    const int64_t tile_bytes = (int64_t)p.blocks * BLK;
+    const uint8_t* src = p.store + (int64_t)(t0 + sub * TP) * tile_bytes + (int64_t)(rank * p.part + first) * BLK;
+    uint8_t* ring = smem + warp * p.slots * slot_bytes;
+    uint64_t* bars = full + warp * kMaxSlots;
+    // what is behind a narrower last share is never copied; its scales must not be NaN
+    for (int i = nb * GPB * 8 + lane; nb < NB && i < NB * GPB * 8; i += 32)
+      for (int k = 0; k < p.slots * TP; ++k)
+        *reinterpret_cast<uint16_t*>(ring + (k * NB + i / (GPB * 8)) * BLK + kBlockCodes + i % (GPB * 8) * 2) = 0;
+    __syncwarp();  // and the barriers that this warp has made
+    int lt = t0 + sub * TP, ls = 0, ahead = 0;  // the copies' tile and slot
+    const auto copy = [&]() {
+      const int n = min(TP, t1 - lt);
+      if (n <= 0) return;
+      if (lane == 0) mbar_expect_tx(bars + ls, (uint32_t)(n * nb * BLK));
       __syncwarp();
-    }
-    drain_ring(full, p.stages, it);  // shared memory must not go while copies are on their way
-  } else if (warp == kProduct + 1) {  // ---- sums
-    griddep_wait();  // (the launch before this one may still read or write y)
-    int it = 0;
-    bool ok = true;
+      if (lane < n && nb > 0) bulk_load(ring + ls * slot_bytes + lane * NB * BLK, src + lane * tile_bytes, nb * BLK, bars + ls);
+      src += step * tile_bytes, lt += step, ++ahead;
+      if (++ls == p.slots) ls = 0;
+    };
 #pragma unroll 1
-    for (int g = g0; g < g1 && ok; ++g, ++it) {
-      const int buf = it % kSums, n = min(p.rw, p.tiles - g * p.rw);
-      const uint32_t phase = (it / kSums) & 1;
-      ok = wait(sum_full + buf, phase);
-      if (ok && rank == 0 && parts > 1) ok = peer_wait(in_full + buf, phase, abort_flag, p.status);
-      if (ok && rank > 0 && it >= kSums) ok = peer_wait(in_empty + buf, phase ^ 1, abort_flag, p.status);
-      if (!ok) break;
-#pragma unroll 1
-      for (int r = 0; r < n; ++r)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const float* src = sums + (size_t)(buf * warps + r * p.kw) * OUT + m * 64 + lane * 2;
-          float2 v = make_float2(0.f, 0.f);
-#pragma unroll 4
-          for (int k = 0; k < p.kw; ++k) {
-            const float2 u = *reinterpret_cast<const float2*>(src + k * OUT);
-            v.x += u.x, v.y += u.y;
-          }
-          if (rank > 0) {
-            peer_store(peer(inbox, 0) + (uint32_t)(((buf * (parts - 1) + rank - 1) * p.rw + r) * OUT + m * 64 + lane * 2) * 4, v);
-            continue;
-          }
-#pragma unroll 1
-          for (int q = 0; q + 1 < parts; ++q) {
-            const float2 u = *reinterpret_cast<const float2*>(inbox + ((buf * (parts - 1) + q) * p.rw + r) * OUT + m * 64 + lane * 2);
-            v.x += u.x, v.y += u.y;
-          }
-          const int t = m * 8 + (lane >> 2), row = (g * p.rw + r) * 8 + (lane & 3) * 2;
-          if (t < nt) {
-            uint16_t* dst = p.y + (tok0 + t) * p.y_stride + row;
-            const uint32_t w = T::pack(v.x, v.y);
-            if (row < p.rows) dst[0] = (uint16_t)w;
-            if (row + 1 < p.rows) dst[1] = (uint16_t)(w >> 16);
-          }
-        }
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(sum_empty + buf);
-        if (rank > 0) peer_arrive(peer(in_full + buf, 0));
-        else
-          for (int q = 1; q < parts; ++q) peer_arrive(peer(in_empty + buf, q));
-      }
-      __syncwarp();
-    }
-  } else if (warp < warps) {  // ---- products
-    const int first = (warp % p.kw) * p.nb, tile = warp / p.kw;  // the warp's blocks of the part; its tile of a stage
-    const int nb = max(0, min(p.nb, here - first));
+    for (int i = 0; i < p.slots; ++i) copy();
+    // the sums' barriers, and the other CTAs'
+    if (parts > 1) cluster_sync();
+    else __syncthreads();
+
     griddep_wait();
-    uint32_t x[NB][8][2 * MT];  // A fragments: step 2j + h is columns 4h..4h+3 of word j
+    // B fragments: x[b][2j + e][m] are columns 4e..4e+3 of word j for token 8m + lane / 4
+    uint32_t x[NB][8][MT][2];
+    float back[MT][2];  // 1 / the power of two, for tokens 8m + 2 (lane % 4) + 0, 1
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
+    for (int m = 0; m < MT; ++m) {
+      const int t = m * 8 + (lane >> 2);
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const int t = m * 8 + (lane >> 2), col = (rank * p.part + first + b) * 128 + word_col<G>(lane & 3, j);
+        for (int j = 0; j < 4; ++j) {
+          const int col = (rank * p.part + first + b) * 128 + word_col<G>(lane & 3, j);
           uint4 v = make_uint4(0, 0, 0, 0);
           if (b < nb && t < nt && col < p.cols)
-            v = __ldg(reinterpret_cast<const uint4*>(p.x + (tok0 + t) * p.x_stride + col));
-          x[b][2 * j][m] = v.x, x[b][2 * j][MT + m] = v.y;
-          x[b][2 * j + 1][m] = v.z, x[b][2 * j + 1][MT + m] = v.w;
+            v = *reinterpret_cast<const uint4*>(p.x + (tok0 + t) * p.x_stride + col);
+          x[b][2 * j][m][0] = v.x, x[b][2 * j][m][1] = v.y;
+          x[b][2 * j + 1][m][0] = v.z, x[b][2 * j + 1][m][1] = v.w;
         }
-    const uint8_t* base = smem + (size_t)(tile * p.part + first) * BLK;
-    int it = 0;
+      back[m][0] = back[m][1] = 1.f;
+      if constexpr (T::kExp != Fp16::kExp) {
+        uint32_t top = 0;  // as 16-bit magnitudes, two at a time
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) top = __vmaxu2(top, x[b][k][m][e] & 0x7FFF7FFFu);
+        top = __vmaxu2(top, __shfl_xor_sync(FULL, top, 1));
+        top = __vmaxu2(top, __shfl_xor_sync(FULL, top, 2));
+        const int exp = (int)(max(top & 0xFFFFu, top >> 16) >> 7) - 127, up = min(120, 14 - exp);
+        const float mul = __uint_as_float((uint32_t)(up + 127) << 23), inv = __uint_as_float((uint32_t)(127 - up) << 23);
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) x[b][k][m][e] = Fp16::pack(T::lo(x[b][k][m][e]) * mul, T::hi(x[b][k][m][e]) * mul);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) back[m][e] = __shfl_sync(FULL, inv, ((lane & 3) * 2 + e) * 4);
+      }
+    }
+
+    const Bits bits;
+    const uint32_t sum_at = smem_addr(sums) + ((sub * TP * p.kw + ki) * OUT + lane * 2) * 4;
+    int s = 0, buf = 0, done = 0;
+    uint32_t phase = 0, sum_phase = 1;
+    bool ok = true;
 #pragma unroll 1
-    for (int g = g0; g < g1; ++g, ++it) {
-      const int s = it % p.stages, buf = it % kSums;
-      if (!wait(full + s, (it / p.stages) & 1)) break;
-      float tot[4] = {0.f, 0.f, 0.f, 0.f};
-      if (g * p.rw + tile < p.tiles) {
-        const uint8_t* at = base + (size_t)s * stage_bytes;
+    for (int t = t0; t < t1; t += step) {
+      ok = wait(sum_empty + buf, sum_phase);
+      if (!ok) break;
+      if (t + sub * TP < t1) {  // (else: no tile for this warp in the last step)
+        ok = wait(bars + s, phase);
+        if (!ok) break;
+        const uint32_t at = smem_addr(ring) + s * slot_bytes;
+        uint32_t dst = sum_at + buf * sum_floats * 4;
+        // two tiles are the upper and lower rows of the products (those behind t1 are not there: what they give is not read)
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          if (b < nb) {
-            const uint4 w4 = *reinterpret_cast<const uint4*>(at + b * BLK + lane * 16);
-            const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-            float acc[GPB][4];
+        for (int h = 0; h < MT; ++h) {
+          float tot[MT][4] = {};  // rows lane / 4 of the first tile [0, 1] and of the second, tokens as in back
 #pragma unroll
-            for (int q = 0; q < GPB; ++q)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) acc[q][i] = 0.f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t v[4];
-              unpack<T>(w[j], v);
-              float(&a)[4] = acc[j * GPB / 4];
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint32_t(&xs)[2 * MT] = x[b][2 * j + h];
-                const uint32_t f[4] = {xs[0], MT == 2 ? xs[1] : 0u, xs[MT], MT == 2 ? xs[MT + 1] : 0u};
-                mma16816<T>(a, f, v[2 * h], v[2 * h + 1]);
-              }
-            }
+          for (int b = 0; b < NB; ++b) {
+            const uint32_t at0 = at + (2 * h * NB + b) * BLK, at1 = at0 + NB * BLK;
+            const uint4 w0 = lds128(at0 + lane * 16), w1 = lds128(at1 + lane * 16);
 #pragma unroll
             for (int q = 0; q < GPB; ++q) {
-              const uint32_t sc = *reinterpret_cast<const uint32_t*>(at + b * BLK + kBlockCodes + q * 16 + (lane & 3) * 4);
-              const float s0 = T::lo(sc), s1 = T::hi(sc);
-              tot[0] = fmaf(acc[q][0], s0, tot[0]), tot[1] = fmaf(acc[q][1], s1, tot[1]);
-              if (MT == 2) tot[2] = fmaf(acc[q][2], s0, tot[2]), tot[3] = fmaf(acc[q][3], s1, tot[3]);
+              float acc[MT][4] = {};
+#pragma unroll
+              for (int j = q * 4 / GPB; j < (q + 1) * 4 / GPB; ++j) {
+                uint32_t u[4], v[4];
+                unpack(bits, j == 0 ? w0.x : j == 1 ? w0.y : j == 2 ? w0.z : w0.w, u);
+                unpack(bits, j == 0 ? w1.x : j == 1 ? w1.y : j == 2 ? w1.z : w1.w, v);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const uint32_t f[4] = {u[2 * e], v[2 * e], u[2 * e + 1], v[2 * e + 1]};
+#pragma unroll
+                  for (int m = 0; m < MT; ++m) mma16816<Fp16>(acc[m], f, x[b][2 * j + e][m][0], x[b][2 * j + e][m][1]);
+                }
+              }
+              const uint32_t sc = kBlockCodes + (lane >> 2) * 2 * GPB + q * 2;
+              const float s0 = T::lo(lds16(at0 + sc)), s1 = T::lo(lds16(at1 + sc));
+#pragma unroll
+              for (int m = 0; m < MT; ++m) {
+                tot[m][0] = fmaf(acc[m][0], s0, tot[m][0]), tot[m][1] = fmaf(acc[m][1], s0, tot[m][1]);
+                tot[m][2] = fmaf(acc[m][2], s1, tot[m][2]), tot[m][3] = fmaf(acc[m][3], s1, tot[m][3]);
+              }
             }
           }
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            sts64(dst + m * 256, tot[m][0] * back[m][0], tot[m][1] * back[m][1]);
+            sts64(dst + m * 256 + p.kw * OUT * 4, tot[m][2] * back[m][0], tot[m][3] * back[m][1]);
+          }
+          dst += 2 * p.kw * OUT * 4;
         }
+        ++done;
+        if (++s == p.slots) s = 0, phase ^= 1;
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(empty + s);
-      if (it >= kSums && !wait(sum_empty + buf, (it / kSums + 1) & 1)) break;
-      float* dst = sums + (size_t)(buf * warps + warp) * OUT + lane * 2;
-      *reinterpret_cast<float2*>(dst) = make_float2(tot[0], tot[1]);
-      if (MT == 2) *reinterpret_cast<float2*>(dst + 64) = make_float2(tot[2], tot[3]);
-      __syncwarp();
       if (lane == 0) mbar_arrive(sum_full + buf);
+      copy();  // into the slot that has just been read
+      if (++buf == SUMS) buf = 0, sum_phase ^= 1;
+    }
+    // a wait that gave up: shared memory must not go while copies to it are on their way
+    if (!ok) drain_slots(bars, p.slots, done, ahead);
+  } else {
+    if (parts > 1) cluster_sync();
+    else __syncthreads();
+    if (warp >= kProduct) {  // ---- sums
+      griddep_wait();        // (the launch before this one may still read or write y)
+      uint32_t phase = 0, in_phase = 0;
+      int buf = 0, in = 0;
+      bool ok = true;
+      const int first = warp - kProduct;
+      const auto add = [&](int i) {  // this CTA's sum of tile i / MT of the step, tokens 8 (i % MT) ..
+        const float* src = sums + buf * sum_floats + i / MT * p.kw * OUT + i % MT * 64 + lane * 2;
+        float2 v = make_float2(0.f, 0.f);
+#pragma unroll 6
+        for (int k = 0; k < p.kw; ++k) {
+          const float2 u = *reinterpret_cast<const float2*>(src + k * OUT);
+          v.x += u.x, v.y += u.y;
+        }
+        return v;
+      };
+      const auto write = [&](int t, int i, float2 v) {
+        const int tok = i % MT * 8 + (lane & 3) * 2, row = (t + i / MT) * 8 + (lane >> 2);
+        if (tok >= nt || row >= p.rows) return;
+        uint16_t* dst = p.y + (tok0 + tok) * p.y_stride + row;
+        const uint32_t w = T::pack(v.x, v.y);
+        dst[0] = (uint16_t)w;
+        if (tok + 1 < nt) dst[p.y_stride] = (uint16_t)(w >> 16);
+      };
+#pragma unroll 1
+      for (int t = t0; t < t1; t += step) {
+        const int n = min(step, t1 - t) * MT;
+        ok = wait(sum_full + buf, phase);
+        if (!ok) break;
+        if (parts == 1) {
+#pragma unroll 1
+          for (int i = first; i < n; i += kAdd) write(t, i, add(i));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sum_empty + buf);
+        } else {  // (rw is 1: at most 2 results a warp)
+          float2 v[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (first + h * kAdd < n) v[h] = add(first + h * kAdd);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sum_empty + buf);
+          if (rank > 0) {
+            ok = wait(in_empty + in, in_phase ^ 1);  // at once in the first round
+            if (!ok) break;
+            const uint32_t dst = peer(inbox, 0) + (uint32_t)((in * (parts - 1) + rank - 1) * in_floats + lane * 2) * 4;
+            const uint32_t bar = peer(in_full + in, 0);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              if (first + h * kAdd < n) peer_store(dst + (first + h * kAdd) * 256, v[h], bar);
+          } else {
+            if (first == 0 && lane == 0) mbar_expect_tx(in_full + in, (uint32_t)((parts - 1) * n * 256));
+            ok = wait(in_full + in, in_phase);
+            if (!ok) break;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              if (first + h * kAdd < n)
+#pragma unroll 1
+                for (int q = 0; q + 1 < parts; ++q) {
+                  const float2 u = *reinterpret_cast<const float2*>(inbox + (in * (parts - 1) + q) * in_floats +
+                                                                    (first + h * kAdd) * 64 + lane * 2);
+                  v[h].x += u.x, v[h].y += u.y;
+                }
+            __syncwarp();
+            if (lane > 0 && lane < parts) peer_arrive(peer(in_empty + in, lane));
+            __syncwarp();
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              if (first + h * kAdd < n) write(t, first + h * kAdd, v[h]);
+          }
+          __syncwarp();
+          if (++in == kIn) in = 0, in_phase ^= 1;
+        }
+        if (++buf == SUMS) buf = 0, phase ^= 1;
+      }
     }
   }
   __syncwarp();
@@ -334,8 +418,8 @@ __global__ void repack_kernel(const uint8_t* packed, const uint16_t* scales, uin
     *reinterpret_cast<uint4*>(dst + unit * 16) = make_uint4(w[0], w[1], w[2], w[3]);
   } else {
     for (int i = 0; i < GPB * 8; ++i) {
-      const int64_t row = tile * 8 + (i & 7);
-      const int g = kb * GPB + (i >> 3);
+      const int64_t row = tile * 8 + i / GPB;
+      const int g = kb * GPB + i % GPB;
       reinterpret_cast<uint16_t*>(dst + kBlockCodes)[i] = row < rows && g * G < cols ? scales[row * (cols / G) + g] : 0;
     }
   }
@@ -369,30 +453,33 @@ int check_device(int device) {
   return dev == device ? COLI_OK : COLI_ESTATE;
 }
 
-size_t smem_bytes(const LinearParams& p, int group, int mt, int parts) {
-  return (size_t)p.stages * p.rw * p.part * block_bytes(group) +
-         (size_t)kSums * (p.kw * p.rw + (parts - 1) * p.rw) * mt * 64 * 4 + (2 * kMaxStages + 4 * kSums) * 8 + 16;
-}
-
 template <class T, int G, int MT>
 cudaError_t launch(LinearParams p, int num_sms, cudaStream_t stream) {
-  constexpr int NB = max_blocks(MT);
-  // the cluster: as few CTAs as hold x in registers; the warps: as few blocks each as that takes
+  constexpr int NB = 4 / MT, BLK = block_bytes(G), TP = step_tiles(MT);
+  // the cluster: as few CTAs as hold x in registers
   int parts = (p.blocks + kProduct * NB - 1) / (kProduct * NB);
   p.part = (p.blocks + parts - 1) / parts;
   parts = (p.blocks + p.part - 1) / p.part;
-  p.nb = (p.part + kProduct - 1) / kProduct;
-  p.kw = (p.part + p.nb - 1) / p.nb;
-  // narrow matrices: several tiles at a time, while every cluster still gets some
-  const int clusters = num_sms / parts;
-  p.rw = std::max(1, std::min(kProduct / p.kw, (p.tiles + clusters - 1) / clusters));
-  p.stages = std::min(kMaxStages, kRing / (p.rw * p.part * block_bytes(G)));
-  const int groups = (p.tiles + p.rw - 1) / p.rw;
-  const size_t smem = smem_bytes(p, G, MT, parts);
+  // The warps: as many of a tile's blocks each as keeps most of them busy (fewer warps a tile are fewer sums to add), several
+  // steps' tiles at once where a tile takes few warps, while every cluster still gets some.
+  const int clusters = std::min(num_sms / parts, p.tiles), most = (p.tiles + clusters - 1) / clusters;
+  int best = -1, blocks = 1;
+  for (int nb = 1; nb <= NB; ++nb) {
+    const int kw = (p.part + nb - 1) / nb;
+    if (kw > kProduct) continue;
+    const int rw = std::max(1, std::min(kProduct / kw, (most + TP - 1) / TP)), busy = p.part * rw * 12 / nb;  // (12 / nb is whole)
+    if (busy >= best) best = busy, blocks = nb, p.kw = kw, p.rw = rw;
+  }
+  const int step = p.rw * TP, ring = p.kw * p.rw * TP * blocks * BLK;  // of one slot of every warp
+  const int rest = step * (sum_buffers(MT) * p.kw + kIn * (parts - 1)) * MT * 64 * 4 +
+                   (kProduct * kMaxSlots + 2 * sum_buffers(MT) + 2 * kIn) * 8 + 16;
+  // Two slots a warp, more while they are small: deeper rings delay x, which waits in the same queues.  us with 2 / 3 / 4 slots of 50 KB:
+  // 8192 x 6144 for one token 8.6 / 9.2 / 9.7, 40000 rows 26.4 / 27.5 / 27.7.
+  p.slots = std::max(2, std::min({kMaxSlots, kRing / ring, (most + step - 1) / step}));
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(std::min(clusters, groups) * parts, (p.n_tokens + 8 * MT - 1) / (8 * MT));
+  cfg.gridDim = dim3(clusters * parts, (p.n_tokens + 8 * MT - 1) / (8 * MT));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = p.slots * ring + rest;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -401,20 +488,24 @@ cudaError_t launch(LinearParams p, int num_sms, cudaStream_t stream) {
   attr[1].val.clusterDim.x = parts, attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = parts > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, linear_kernel<T, G, MT>, p);
+  if constexpr (MT == 1) {
+    if (blocks == 4) return cudaLaunchKernelEx(&cfg, linear_kernel<T, G, 1, 4>, p);
+    if (blocks == 3) return cudaLaunchKernelEx(&cfg, linear_kernel<T, G, 1, 3>, p);
+  }
+  return blocks == 2 ? cudaLaunchKernelEx(&cfg, linear_kernel<T, G, MT, 2>, p)
+                     : cudaLaunchKernelEx(&cfg, linear_kernel<T, G, MT, 1>, p);
 }
 
-static_assert(kProduct * 3 * block_bytes(32) * 6 <= kRing, "at least six stages");
-
-template <class T, int G, int MT>
+template <class T, int G, int MT, int NB>
 cudaError_t configure() {
-  // the device's limit; a launch's own need is below it: the ring, sums of 16 warps (16 or 32 KB) and of 7 other CTAs (7 or 14 KB)
-  return cudaFuncSetAttribute(linear_kernel<T, G, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+  return cudaFuncSetAttribute(linear_kernel<T, G, MT, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
 }
 
 template <class T, int G>
 cudaError_t launch_tokens(const LinearParams& p, int num_sms, cudaStream_t stream) {
-  return p.n_tokens <= 8 ? launch<T, G, 1>(p, num_sms, stream) : launch<T, G, 2>(p, num_sms, stream);
+  // (x of 16 tokens and more columns than a cluster holds: 8 tokens at a time)
+  return p.n_tokens <= 8 || p.blocks > kMaxParts * kProduct * 2 ? launch<T, G, 1>(p, num_sms, stream)
+                                                                 : launch<T, G, 2>(p, num_sms, stream);
 }
 template <class T>
 cudaError_t launch_group(const LinearParams& p, int group, int num_sms, cudaStream_t stream) {
@@ -425,9 +516,13 @@ cudaError_t launch_group(const LinearParams& p, int group, int num_sms, cudaStre
 
 cudaError_t configure_device() {
   cudaError_t e = cudaSuccess;
-#define COLI_CFG(T, G)                                 \
-  if (e == cudaSuccess) e = configure<T, G, 1>();      \
-  if (e == cudaSuccess) e = configure<T, G, 2>();
+#define COLI_CFG(T, G)                                \
+  if (e == cudaSuccess) e = configure<T, G, 1, 1>();  \
+  if (e == cudaSuccess) e = configure<T, G, 1, 2>();  \
+  if (e == cudaSuccess) e = configure<T, G, 1, 3>();  \
+  if (e == cudaSuccess) e = configure<T, G, 1, 4>();  \
+  if (e == cudaSuccess) e = configure<T, G, 2, 1>();  \
+  if (e == cudaSuccess) e = configure<T, G, 2, 2>();
   COLI_CFG(Bf16, 32) COLI_CFG(Bf16, 64) COLI_CFG(Bf16, 128) COLI_CFG(Fp16, 32) COLI_CFG(Fp16, 64) COLI_CFG(Fp16, 128)
 #undef COLI_CFG
   return e;
@@ -453,7 +548,7 @@ extern "C" int coli_linear_create(const coli_linear_config* cfg, coli_linear** o
       c.max_tokens > 1000000)
     return COLI_EINVAL;
   if ((c.group != 32 && c.group != 64 && c.group != 128) || (c.dtype != COLI_ATTN_BF16 && c.dtype != COLI_ATTN_FP16) ||
-      c.cols > kMaxParts * kProduct * 2 * 128)
+      c.cols > 32768)
     return COLI_EUNSUPPORTED;
   coli_linear* h = new (std::nothrow) coli_linear();
   if (!h) return COLI_ENOMEM;

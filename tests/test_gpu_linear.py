@@ -158,7 +158,8 @@ def test_quantize(rows, cols, group, dt):
     w = torch.randn((rows, cols), device="cuda") * torch.exp(torch.randn((rows, 1), device="cuda"))
     w[0, :group] = 0
     packed, scales = linear.quantize(w, group, dt)
-    d = (w.view(rows, -1, group).abs().amax(-1) / 7).to(dt)
+    seven = torch.full((1,), 7.0, device="cuda")  # (a tensor over a number is multiplied by the number's rounded inverse)
+    d = (w.view(rows, -1, group).abs().amax(-1) / seven).to(dt)
     assert torch.equal(scales, d)
     q = w.view(rows, -1, group) / d.float()[..., None]
     c = torch.where(d[..., None] == 0, 0, torch.sign(q) * torch.floor(q.abs() + 0.5)).clamp(-7, 7).view(rows, cols)
