@@ -113,6 +113,10 @@ int tile_block_tokens(int group);  // tokens per block of the tensor-memory kern
 cudaError_t configure_attn_tile();
 cudaError_t launch_attn_tile(const AttnParams& p, const CUtensorMap& q, const CUtensorMap& k,
                              const CUtensorMap& v, int dtype, int num_sms, cudaStream_t stream);
+// the same over an 8-bit cache of type `code`
+cudaError_t configure_attn_qtile();
+cudaError_t launch_attn_qtile(const AttnParams& p, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, int dtype,
+                              int code, int num_sms, cudaStream_t stream);
 // merges the partials of cut units into out / lse; the launch before had `ctas` CTAs and blocks of `rows` rows, of
 // which at most `live` are in use
 cudaError_t launch_attn_combine(const AttnParams& p, int rows, int live, int ctas, int dtype, cudaStream_t stream);

@@ -129,6 +129,7 @@ cudaError_t configure_device(int dev) {
   cudaError_t e = configure_attn_split();
   if (e == cudaSuccess) e = configure_attn_tile();
   if (e == cudaSuccess) e = configure_attn_qsplit();
+  if (e == cudaSuccess) e = configure_attn_qtile();
   if (e == cudaSuccess) g_configured[dev] = true;
   return e;
 }
@@ -458,21 +459,13 @@ extern "C" int coli_attn_window(coli_attn* h, const coli_attn_kv* kv, const coli
   // suit it: 8 of up to 96 rows 26.5 / one launch 16.7, 40 mixed ones of 4000 tokens 146 / 125.
   const int64_t seq_rows = (int64_t)b->max_q * p.group;
   cudaError_t e;
-  if (kv->code) {
-    if (p.group > kSplitMaxRows) return COLI_EUNSUPPORTED;
+  if (seq_rows <= kSplitMaxRows) {
     const int rows = split_rows(seq_rows), ctas = split_grid(h->num_sms);
     p.block_tokens = rows / p.group;
     rc = list_fits(p, kSplitKeys);
     if (rc) return rc;
-    e = launch_attn_qsplit(p, kv->maps.k64, kv->maps.v64, rows, h->cfg.dtype, kv->code, h->num_sms, st);
-    if (e == cudaSuccess)
-      e = launch_attn_combine(p, rows, (int)(seq_rows < rows ? seq_rows : rows), ctas, h->cfg.dtype, st);
-  } else if (seq_rows <= kSplitMaxRows) {
-    const int rows = split_rows(seq_rows), ctas = split_grid(h->num_sms);
-    p.block_tokens = rows / p.group;
-    rc = list_fits(p, kSplitKeys);
-    if (rc) return rc;
-    e = launch_attn_split(p, kv->maps.k64, kv->maps.v64, rows, h->cfg.dtype, h->num_sms, st);
+    e = kv->code ? launch_attn_qsplit(p, kv->maps.k64, kv->maps.v64, rows, h->cfg.dtype, kv->code, h->num_sms, st)
+                 : launch_attn_split(p, kv->maps.k64, kv->maps.v64, rows, h->cfg.dtype, h->num_sms, st);
     if (e == cudaSuccess) e = launch_attn_combine(p, rows, (int)seq_rows, ctas, h->cfg.dtype, st);
   } else {
     use_tile(h, &p);
@@ -480,7 +473,8 @@ extern "C" int coli_attn_window(coli_attn* h, const coli_attn_kv* kv, const coli
     rc = list_fits(p, kTileKeys);
     if (rc) return rc;
     if (!query_map(&qm, h, q, q_stride, b->n_tokens)) return COLI_ECUDA;
-    e = launch_attn_tile(p, qm, kv->maps.k128, kv->maps.v128, h->cfg.dtype, h->num_sms, st);
+    e = kv->code ? launch_attn_qtile(p, qm, kv->maps.k128, kv->maps.v128, h->cfg.dtype, kv->code, h->num_sms, st)
+                 : launch_attn_tile(p, qm, kv->maps.k128, kv->maps.v128, h->cfg.dtype, h->num_sms, st);
     if (e == cudaSuccess) e = launch_attn_combine(p, kTileRows, (int)(seq_rows < kTileRows ? seq_rows : kTileRows), h->num_sms, h->cfg.dtype, st);
   }
   return e == cudaSuccess ? COLI_OK : COLI_ECUDA;

@@ -151,7 +151,7 @@ def test_window_lengths(news, lens, window, sinks, kind):
 
 @pytest.mark.parametrize("n_q,n_kv,D,page,dt,kind,layout", [
     (1, 1, 64, 16, HF, I8, "head"), (8, 1, 128, 32, BF, E4, "slot"), (16, 1, 64, 64, BF, I8, "both"),
-    (17, 1, 128, 128, HF, E4, "head"),
+    (17, 1, 128, 128, HF, E4, "head"), (64, 1, 64, 256, HF, I8, "slot"), (33, 1, 128, 16, BF, E4, "both"),
     (15, 5, 64, 16, BF, E4, "head"), (4, 4, 128, 256, HF, I8, "both")])
 @pytest.mark.parametrize("news,lens", [([1, 1], [500, 33]), ([7, 2], [300, 2]), ([150, 70], [400, 70])])
 def test_window_heads_pages_layouts(n_q, n_kv, D, page, dt, kind, layout, news, lens):
