@@ -2,16 +2,20 @@
 // a warpgroup that widens the code tiles on their way to the products.
 //
 //   tensor memory (512 columns)   S0/P0 | S1/P1 | O0 | O1
-//   shared memory                 Q0, Q1; a ring of code tiles; a ring of widened key and value tiles; scales
+//   shared memory                 Q0, Q1; a ring of key and value tiles; scales
 //   warps 0-3, 4-7   softmax, rescaling and the epilogue of row tile 0, 1
-//   warps 8-11       widen: one key a thread, D codes to D 16-bit values where a tensor copy would have put them
+//   warps 8-11       widen, in place: the codes come into the second half of their tile's place; a thread makes one key's into D
+//                    16-bit values where a tensor copy would have put them
 //   warp 12          issues every product; warp 13 every copy
 //
 // The codes are exact in the products: keys in the queries' type, values in fp16.  A score is multiplied by its key's scale in fp32; a
 // weight is 2^(s - m) vs / g, with g the largest |vs| that the row has seen, so that it is at most 2^8 and rounds to fp16 well.  1 / g
 // is part of the exponent (the row's sum and output are in the same unit, which cancels), m and g move rarely, and the output in
-// tensor memory is rescaled only then.  What a row does not see has weight 0, and codes are always finite, so nothing is
-// computed again here.
+// tensor memory is rescaled only then.  What a row does not see has weight 0; codes are always finite, and values' scales that are not
+// become 0 and a bit that spoils the sums of the rows that see them, so nothing is computed again here.
+//
+// The softmax loop is long straight code and shares the instruction cache with the other roles', so what only masked tiles need is
+// kept out of it.
 #include <float.h>
 
 #include "attn_code.cuh"
@@ -24,19 +28,25 @@ namespace {
 constexpr int kThreadsQTile = 16 * 32;
 constexpr float kNoScale = 0x1p-100f;  // g before the first key
 
+struct TileScales {
+  float keys[kTileKeys], values[kTileKeys];
+  float top[4];     // of 32 keys each: the largest |value scale|
+  uint32_t bad[4];  // and which of them were not finite
+};
+
 template <int D>
 struct QTileCfg {
   static constexpr int tile_bytes = kTileKeys * D * 2;  // of a widened tile; Q of one row tile
   static constexpr int raw_bytes = kTileKeys * D;       // of a code tile
-  static constexpr int stages = 98304 / tile_bytes, raw_stages = 49152 / raw_bytes;
+  static constexpr int stages = 131072 / tile_bytes;
   static constexpr int q_bytes = 2 * tile_bytes;
-  // Scales of a tile's keys and values.  A tile's are asked for when the item raw_stages before its keys has been widened, so the
-  // item `stages` before that has been multiplied, and the tile before that item's has left the softmax.
-  static constexpr int scale_slots = (stages + raw_stages) / 2 + 1;
-  // barriers: rings full/empty, q full/empty, scores, weights (first half, all), output, drain, scales
-  static constexpr int bars = 2 * stages + 2 * raw_stages + 4 + 2 + 4 + 2 + 1 + scale_slots;
-  static constexpr int smem = stages * tile_bytes + raw_stages * raw_bytes + q_bytes + scale_slots * 2 * kTileKeys * 4 +
-                              (int)sizeof(UnitRing) + bars * 8 + 16;
+  // Scales of a tile's keys and values.  A tile's are asked for when the key tile stages / 2 before it has been multiplied, so
+  // the tile before that one has left the softmax.
+  static constexpr int scale_slots = stages / 2 + 1;
+  // barriers: ring codes/full/empty, q full/empty, scores, weights (first half, all), output, drain, reading, scales
+  static constexpr int bars = 3 * stages + 4 + 2 + 4 + 2 + 2 + scale_slots;
+  static constexpr int smem =
+      stages * tile_bytes + q_bytes + scale_slots * (int)sizeof(TileScales) + (int)sizeof(UnitRing) + bars * 8 + 16;
   static constexpr uint32_t o_col = 256;  // first column of O0; O1 follows after D columns
 };
 
@@ -108,21 +118,39 @@ __device__ __forceinline__ void widen_pairs(uint32_t w, uint32_t& a, uint32_t& b
   }
 }
 
-// One key's row of a code tile, as the tensor copies swizzle it, to the same row of a widened tile: boxes of 64 values x 128 keys
-template <class T, int CODE, int D>
-__device__ __forceinline__ void widen_row(const uint8_t* raw, uint8_t* dst, int row) {
+// 16 codes as two 16-byte chunks of a widened row
+template <class T, int CODE>
+__device__ __forceinline__ void write_chunks(const uint4& v, uint8_t* row_at, int ch, int row) {
+  uint4 x, y;
+  widen_pairs<T, CODE>(v.x, x.x, x.y), widen_pairs<T, CODE>(v.y, x.z, x.w);
+  widen_pairs<T, CODE>(v.z, y.x, y.y), widen_pairs<T, CODE>(v.w, y.z, y.w);
+  *reinterpret_cast<uint4*>(row_at + ((ch ^ (row & 7)) << 4)) = x;
+  *reinterpret_cast<uint4*>(row_at + (((ch + 1) ^ (row & 7)) << 4)) = y;
+}
+
+// One key's row: its codes, as the tensor copies swizzle them in the second half of the tile's place, to boxes of 64 values x 128 keys.
+// A row of 128 codes lies just where its own second 64 values go, so nobody else's is overwritten; rows of 64 codes lie where
+// others' values go, and `meet` makes all threads wait until all have read theirs.
+template <class T, int CODE, int D, class Meet>
+__device__ __forceinline__ bool widen_row(uint8_t* tile, int row, Meet meet) {
+  const uint8_t* raw = tile + kTileKeys * D;
+  uint8_t* first = tile + row * 128;
+  uint4 v[4];
+  if constexpr (D == 128) {
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c)
+      write_chunks<T, CODE>(*reinterpret_cast<const uint4*>(raw + row * 128 + ((c ^ (row & 7)) << 4)), first, 2 * c, row);
 #pragma unroll
-  for (int c = 0; c < D / 16; ++c) {
-    const int at = D == 128 ? row * 128 + ((c ^ (row & 7)) << 4) : row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
-    const uint4 v = *reinterpret_cast<const uint4*>(raw + at);
-    uint4 x, y;
-    widen_pairs<T, CODE>(v.x, x.x, x.y), widen_pairs<T, CODE>(v.y, x.z, x.w);
-    widen_pairs<T, CODE>(v.z, y.x, y.y), widen_pairs<T, CODE>(v.w, y.z, y.w);
-    uint8_t* box = dst + (c >> 2) * kTileKeys * 128 + row * 128;
-    const int ch = 2 * c & 7;
-    *reinterpret_cast<uint4*>(box + ((ch ^ (row & 7)) << 4)) = x;
-    *reinterpret_cast<uint4*>(box + (((ch + 1) ^ (row & 7)) << 4)) = y;
+    for (int c = 0; c < 4; ++c) v[c] = *reinterpret_cast<const uint4*>(raw + row * 128 + (((c + 4) ^ (row & 7)) << 4));
+    first += kTileKeys * 128;
+  } else {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) v[c] = *reinterpret_cast<const uint4*>(raw + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
+    if (!meet()) return false;
   }
+#pragma unroll
+  for (int c = 0; c < 4; ++c) write_chunks<T, CODE>(v[c], first, 2 * c, row);
+  return true;
 }
 
 template <class T, int CODE, int D>
@@ -130,18 +158,17 @@ __global__ void __launch_bounds__(kThreadsQTile, 1)
     attn_qtile_kernel(const AttnParams p, const __grid_constant__ CUtensorMap qmap,
                       const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using C = QTileCfg<D>;
-  constexpr int NST = C::stages, NRAW = C::raw_stages, NSC = C::scale_slots;
+  constexpr int NST = C::stages, NSC = C::scale_slots;
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* ring = smem;  // widened: key tile i is item 2i, value tile i item 2i + 1; the same for the codes
+  uint8_t* ring = smem;  // key tile i is item 2i, value tile i item 2i + 1
   uint8_t* qs = smem + NST * C::tile_bytes;
-  uint8_t* raw = qs + C::q_bytes;
-  float* scales = reinterpret_cast<float*>(raw + NRAW * C::raw_bytes);  // [NSC][keys, values][128]
-  UnitRing* units = reinterpret_cast<UnitRing*>(scales + NSC * 2 * kTileKeys);
+  TileScales* scales = reinterpret_cast<TileScales*>(qs + C::q_bytes);  // [NSC]
+  UnitRing* units = reinterpret_cast<UnitRing*>(scales + NSC);
   uint64_t* full = reinterpret_cast<uint64_t*>(units + 1);
-  uint64_t *empty = full + NST, *raw_full = empty + NST, *raw_empty = raw_full + NRAW, *sc_full = raw_empty + NRAW,
+  uint64_t *empty = full + NST, *codes = empty + NST, *sc_full = codes + NST,
            *q_full = sc_full + NSC, *q_empty = q_full + 2, *s_full = q_empty + 2, *p_half = s_full + 2, *p_full = p_half + 2,
-           *o_full = p_full + 2, *drain = o_full + 2;
-  int* abort_flag = reinterpret_cast<int*>(drain + 1);
+           *o_full = p_full + 2, *drain = o_full + 2, *met = drain + 1;
+  int* abort_flag = reinterpret_cast<int*>(met + 1);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(abort_flag + 1);
   // (the shuffle tells the compiler that a warp's number, and with it every role's control flow, is uniform)
   const int tid = threadIdx.x, warp = __shfl_sync(FULL, tid >> 5, 0), lane = tid & 31;
@@ -151,9 +178,7 @@ __global__ void __launch_bounds__(kThreadsQTile, 1)
     *abort_flag = 0;
     units->init(13);  // warps 0 to 12
 #pragma unroll 1
-    for (int i = 0; i < NST; ++i) mbar_init(full + i, 4), mbar_init(empty + i, 1);
-#pragma unroll 1
-    for (int i = 0; i < NRAW; ++i) mbar_init(raw_full + i, 1), mbar_init(raw_empty + i, 4);
+    for (int i = 0; i < NST; ++i) mbar_init(full + i, 4), mbar_init(empty + i, 1), mbar_init(codes + i, 1);
 #pragma unroll 1
     for (int i = 0; i < NSC; ++i) mbar_init(sc_full + i, 4);
 #pragma unroll 1
@@ -161,7 +186,7 @@ __global__ void __launch_bounds__(kThreadsQTile, 1)
       mbar_init(q_full + s, 1), mbar_init(q_empty + s, 1), mbar_init(s_full + s, 1);
       mbar_init(p_half + s, 4), mbar_init(p_full + s, 4), mbar_init(o_full + s, 1);
     }
-    mbar_init(drain, 1);
+    mbar_init(drain, 1), mbar_init(met, 4);
     fence_barrier_init();
     prefetch_map(&qmap), prefetch_map(&kmap), prefetch_map(&vmap);
   }
@@ -214,23 +239,23 @@ __global__ void __launch_bounds__(kThreadsQTile, 1)
         const int32_t* row = table_of(p, u.b);
 #pragma unroll 1
         for (int i = 2 * u.i0; i < 2 * u.i1 && ok; ++i, ++it) {
-          const int j0 = u.tile(i >> 1) * kTileKeys, sg = it % NRAW;
-          if (it >= NRAW) ok = wait(raw_empty + sg, ((it / NRAW) + 1) & 1);
+          const int j0 = u.tile(i >> 1) * kTileKeys, sg = it % NST;
+          if (it >= NST) ok = wait(empty + sg, ((it / NST) + 1) & 1);
           if (!ok) break;
-          uint8_t* dst = raw + sg * C::raw_bytes;
-          float* sc = scales + tile * 2 * kTileKeys;
+          uint8_t* dst = ring + sg * C::tile_bytes + C::raw_bytes;
+          float* sc = scales[tile].keys;
           if (i & 1) {
-            fill_item<D, false>(p, &vmap, dst, sc, raw_full + sg, row, u.p0, u.p1, j0, u.head, lane);
+            fill_item<D, false>(p, &vmap, dst, sc, codes + sg, row, u.p0, u.p1, j0, u.head, lane);
             if (++tile == NSC) tile = 0;
           } else {
-            fill_item<D, true>(p, &kmap, dst, sc, raw_full + sg, row, u.p0, u.p1, j0, u.head, lane);
+            fill_item<D, true>(p, &kmap, dst, sc, codes + sg, row, u.p0, u.p1, j0, u.head, lane);
           }
         }
       }
       u.i1 = 0;
       if (ok) give_unit(units, u, n, lane, wait);
       // the CTA's shared memory must not go while copies to it are on their way, even when the other warps have given up
-      drain_ring(raw_full, NRAW, it);
+      drain_ring(codes, NST, it);
       drain_ring(q_full, 1, qn0);
       drain_ring(q_full + 1, 1, qn1);
     } else if (warp == 12) {  // ---- products (one lane issues; the warp waits together)
@@ -317,21 +342,34 @@ __global__ void __launch_bounds__(kThreadsQTile, 1)
       for (int n = 0; ok && take_unit(units, u, n, lane, wait); ++n) {
 #pragma unroll 1
         for (int i = 2 * u.i0; i < 2 * u.i1; ++i, ++it) {
-          const int sg = it % NST, sr = it % NRAW;
-          ok = wait(raw_full + sr, (it / NRAW) & 1);
-          if (ok && !(i & 1)) {  // both scales have come with the keys
+          const int sg = it % NST;
+          ok = wait(codes + sg, (it / NST) & 1);
+          if (!ok) break;
+          if (!(i & 1)) {  // both scales have come with the keys
+            float* value = scales[slot].values + row;
+            float top = fabsf(*value);
+            const bool bad = !(top < INFINITY);
+            if (bad) *value = top = 0.f;
+            top = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(top)));
+            const uint32_t which = __ballot_sync(FULL, bad);
+            if (lane == 0) {
+              scales[slot].top[warp - 8] = top, scales[slot].bad[warp - 8] = which;
+            }
+            __syncwarp();
             if (lane == 0) mbar_arrive(sc_full + slot);
             if (++slot == NSC) slot = 0;
           }
-          if (ok && it >= NST) ok = wait(empty + sg, ((it / NST) + 1) & 1);
-          if (!ok) break;
-          const uint8_t* src = raw + sr * C::raw_bytes;
+          const auto meet = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(met);
+            return wait(met, it & 1);
+          };
           uint8_t* dst = ring + sg * C::tile_bytes;
-          if (i & 1) widen_row<Fp16, CODE, D>(src, dst, row);
-          else widen_row<T, CODE, D>(src, dst, row);
+          ok = i & 1 ? widen_row<Fp16, CODE, D>(dst, row, meet) : widen_row<T, CODE, D>(dst, row, meet);
+          if (!ok) break;
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(full + sg), mbar_arrive(raw_empty + sr);
+          if (lane == 0) mbar_arrive(full + sg);
         }
       }
     }
@@ -364,8 +402,8 @@ __global__ void __launch_bounds__(kThreadsQTile, 1)
         ++sn;
         if (!ok) break;
         tc_fence_after();
-        const float* ks = scales + slot * 2 * kTileKeys;
-        const float* vs = ks + kTileKeys;
+        const TileScales& sc = scales[slot];
+        const float *ks = sc.keys, *vs = sc.values;
         if (++slot == NSC) slot = 0, sc_phase ^= 1;
         const int j0 = u.tile(i) * kTileKeys;
         float x[128];
@@ -376,11 +414,22 @@ __global__ void __launch_bounds__(kThreadsQTile, 1)
         float m0 = -INFINITY, m1 = m0, m2 = m0, m3 = m0;
         const bool masked = !all_see(p, pa, pb, j0, j0 + kTileKeys - 1);
         const int hi = pos - j0, lo = pos - p.window - j0, sk = p.sinks - j0;
-        float gm = 0.f;  // the largest |vs| of the tile that the row sees
+        float gm;  // the largest |vs| of the tile that the row sees
+        bool spoilt;
         if (!masked) {
-          const float4 v = reinterpret_cast<const float4*>(vs)[lane];
-          gm = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));  // (NaN has no part)
-          gm = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(gm)));
+          const float4 t = *reinterpret_cast<const float4*>(sc.top);
+          const uint4 b = *reinterpret_cast<const uint4*>(sc.bad);
+          gm = fmaxf(fmaxf(t.x, t.y), fmaxf(t.z, t.w)), spoilt = (b.x | b.y | b.z | b.w) != 0;
+        } else {
+          gm = 0.f, spoilt = false;
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 32) {
+            const uint32_t see = low_bits(hi + 1 - c) & (~low_bits(lo + 1 - c) | low_bits(sk - c));
+            spoilt |= (sc.bad[c >> 5] & see) != 0;
+#pragma unroll 4
+            for (int k = 0; k < 32; ++k)
+              if (see >> k & 1) gm = fmaxf(gm, fabsf(vs[c + k]));
+          }
         }
 #pragma unroll
         for (int c = 0; c < 128; c += 32) {
@@ -394,10 +443,8 @@ __global__ void __launch_bounds__(kThreadsQTile, 1)
           if (masked) {  // bit k: the row sees key c + k
             const uint32_t see = low_bits(hi + 1 - c) & (~low_bits(lo + 1 - c) | low_bits(sk - c));
 #pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              if (see & (1u << k)) gm = fmaxf(gm, fabsf(vs[c + k]));
-              else x[c + k] = -INFINITY;
-            }
+            for (int k = 0; k < 32; ++k)
+              if (!(see & (1u << k))) x[c + k] = -INFINITY;
           }
 #pragma unroll
           for (int k = 0; k < 32; k += 8) {
@@ -408,6 +455,7 @@ __global__ void __launch_bounds__(kThreadsQTile, 1)
           }
         }
         const float top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+        if (spoilt) sum0 = NAN;
         const bool grow = top > ref + slack || gm > g;  // ref = -inf: the row's first keys
         if (__any_sync(FULL, grow)) {
           float fix = 1.f;
@@ -416,7 +464,6 @@ __global__ void __launch_bounds__(kThreadsQTile, 1)
             if (ref != -INFINITY) fix = ex2((ref - to) * rs) * (g / wide);  // (else nothing has been added up yet)
             ref = to, g = wide, lg = log2f(wide);
             sum0 *= fix, sum1 *= fix;
-            if (g == INFINITY) sum0 = NAN;  // all weights are 0 or NaN now; a part whose sum is 0 would be left out of the row
           }
           // the scores' commit also covers the products before them: O is complete
           if (i > u.i0 && __any_sync(FULL, fix != 1.f)) {
@@ -447,12 +494,6 @@ __global__ void __launch_bounds__(kThreadsQTile, 1)
               mul2_rn(h ? v.z : v.x, h ? v.w : v.y, e, f);
               w[k + h] = Fp16::pack(e, f);
             }
-          }
-          if (masked) {  // (a scale that the row does not see may be NaN)
-            const uint32_t see = low_bits(hi + 1 - c) & (~low_bits(lo + 1 - c) | low_bits(sk - c));
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-              w[k] &= (see >> (2 * k) & 1 ? 0xFFFFu : 0u) | (see >> (2 * k + 1) & 1 ? 0xFFFF0000u : 0u);
           }
           tmem_st16u(st_addr + c / 2, w);
           if (c == 32) {  // the products of the first 64 keys can start
