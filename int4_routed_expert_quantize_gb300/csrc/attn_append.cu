@@ -20,7 +20,10 @@ namespace {
 constexpr int kAppendWarps = 1;
 // groups of heads a warp has in flight; us with 2 / 3 / 4: 700 tokens 5.6 / 5.5 / 5.3, 2000 15.9 / 15.1 /
 // 14.6, 16384 83.8 / 83.7 / 82.6 (8 take so many registers that 16384 take 82.8 and 500 10.4 / 8.5)
-constexpr int kAhead = 4;
+// Into an 8-bit cache 2, with registers for 28 blocks an SM, and two warps a token: 16384 tokens 86.5 us (4 ahead, 18 blocks, one warp 94.8; 3
+// ahead with 28 blocks 89.9, and two warps 85.9, where 16 tokens take 3.6 for 3.2).
+__host__ __device__ constexpr int ahead(int code) { return code ? 2 : 4; }
+constexpr int blocks_per_sm(int code) { return code ? 28 : 0; }  // 0: as many as come
 
 template <class T>
 __device__ __forceinline__ void rotate8(uint4& a, uint4& b, const float (&cs)[8], const float (&sn)[8],
@@ -77,25 +80,32 @@ __device__ __forceinline__ void store_codes(float (&f)[16], uint8_t* d0, uint8_t
   float m = __uint_as_float(bits);
   const bool finite = bits < 0x7F800000u;
   if (first) *scale = finite ? __fdiv_rn(m, top) : __uint_as_float(0x7FFFFFFFu);
+  // neither top * x may overflow nor a residual underflow
+  const float fit = m >= 0x1p100f ? 0x1p-20f : m < 0x1p-60f ? 0x1p64f : 1.f;
   if (!finite || bits == 0) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) f[i] = 0.f;
     m = 1.f;
-  } else if (m >= 0x1p100f) {  // top * x must not overflow
+  } else if (fit != 1.f) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) f[i] *= 0x1p-20f;
-    m *= 0x1p-20f;
+    for (int i = 0; i < 16; ++i) f[i] *= fit;
+    m *= fit;
   }
+  const float r = __frcp_rn(m);
   uint32_t w[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     float y[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = __fdiv_rn(top * f[4 * k + i], m);
-    if constexpr (CODE == COLI_ATTN_CODE_INT8) {
-      const uint32_t a = (uint32_t)__float2int_rn(y[0]) & 0xFFu, b = (uint32_t)__float2int_rn(y[1]) & 0xFFu,
-                     c = (uint32_t)__float2int_rn(y[2]) & 0xFFu, d = (uint32_t)__float2int_rn(y[3]);
-      w[k] = a | b << 8 | c << 16 | d << 24;
+    for (int i = 0; i < 4; ++i) {
+      const float t = top * f[4 * k + i], q = t * r;
+      y[i] = fmaf(fmaf(-q, m, t), r, q);
+    }
+    if constexpr (CODE == COLI_ATTN_CODE_INT8) {  // under the exponent of 2^23 the lowest byte is the nearest integer
+      uint32_t u[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[i] = __float_as_uint(y[i] + 12582912.f);
+      w[k] = __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
     } else {
       uint16_t lo, hi;
       asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(y[1]), "f"(y[0]));
@@ -109,8 +119,9 @@ __device__ __forceinline__ void store_codes(float (&f)[16], uint8_t* d0, uint8_t
 
 // warps_per_token consecutive warps share a token's heads.  CODE: the type of an 8-bit cache, or 0
 template <class T, int D, int CODE>
-__global__ void __launch_bounds__(kAppendWarps * 32) attn_append_kernel(const AttnAppend a, int warps_per_token) {
+__global__ void __launch_bounds__(kAppendWarps * 32, blocks_per_sm(CODE)) attn_append_kernel(const AttnAppend a, int warps_per_token) {
   constexpr int LPH = D / 16, HPW = 32 / LPH;  // lanes per head, heads per warp
+  constexpr int kAhead = ahead(CODE);
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31;
@@ -239,7 +250,8 @@ cudaError_t launch(const AttnAppend& a, int num_sms, cudaStream_t stream) {
   // Enough warps to fill the GPU from few tokens, otherwise as few as possible per token, since each computes its token's
   // angles: double them up to 6 an SM.  us with 1 warp a token / up to 3, 6, 12, 32 an SM: 16 tokens 6.7 / 3.0, 3.0, 3.0, 3.0;
   // 250 - / 4.7, 3.6, 4.6, 5.9; 500 6.9 / 6.9, 4.7, 5.5, 8.5; 700 - / 6.8, 6.1, 5.6, 7.3; 2000 14.9 / 15.0 for all.
-  int wpt = 1;
+  // Into an 8-bit cache two at least, where a token has work for them (quantising takes more instructions).
+  int wpt = CODE && groups >= 8 ? 2 : 1;
   while (wpt < groups && (int64_t)a.n_tokens * wpt < (int64_t)num_sms * 6) wpt *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(((int64_t)a.n_tokens * wpt + kAppendWarps - 1) / kAppendWarps));
