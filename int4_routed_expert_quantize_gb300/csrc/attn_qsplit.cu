@@ -27,16 +27,18 @@ struct QSplitCfg {
   static constexpr int threads = (warps + 1) * 32;
   static constexpr int rows = RG * 16;
   static constexpr int kw = kSplitKeys / KG;  // keys per warp and tile
-  static constexpr int ctas = 2;  // per SM
+  static constexpr int ctas = kQSplitCtas;  // per SM
   static constexpr int tile_bytes = kSplitKeys * D;
-  static constexpr int stages = 81920 / (2 * tile_bytes);
+  static constexpr int stages = 49152 / (2 * tile_bytes);
   static constexpr int scale_bytes = stages * 2 * kSplitKeys * 4;
-  static constexpr int merge_bytes = 4 * (8 * D + 32) * 4;  // a buffer a warp: half its columns
+  // a buffer a warp, of half its columns; between joins, the queries' fragments of RG x 16 rows
+  static constexpr int merge_bytes = 4 * (8 * D + 32) * 4;
+  static_assert(merge_bytes >= RG * (D / 16) * 512, "the queries fit");
   static constexpr int smem =
       stages * 2 * tile_bytes + scale_bytes + merge_bytes + 2 * stages * 8 + (int)sizeof(UnitRing) + 24;
 };
 
-constexpr float kNoScale = 0x1p-120f;  // g before the first key
+constexpr float kNoScale = 0x1p-100f, kNoScaleLog = -100.f;  // g before the first key
 
 // 16-byte chunk `ch` of row `row` of a code tile, as the tensor copies swizzle it: rows of 128 bytes by row % 8, of 64
 // bytes by row / 2 % 4
@@ -54,36 +56,41 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
 // What a thread keeps of its two rows (lane / 4 and 8 more).
 template <int D>
 struct Rows {
-  uint32_t q[D / 16][4];  // fragments: D / 4 values from (lane % 4) D / 4 on, four a step: 0 and 2, 1 and 3
-  float rs[2];            // score of a product of codes and q, times log2(e)
-  float o[D / 8][4];      // columns 16 c + 4 (lane % 4) + 0, 2 in o[2c], 1, 3 in o[2c + 1]; in units of g
-  float ref[2], sum[2], g[2], ig[2];  // ref in units of rs; ig = 1 / g
-  float slack[2];         // 8 in units of rs, finite: -inf + inf would never let the first keys in
+  float rs[2];        // score of a product of codes and q, times log2(e)
+  float slack[2];     // 8 in units of rs, finite: -inf + inf would never let the first keys in
+  float o[D / 8][4];  // columns 16 c + 4 (lane % 4) + 0, 2 in o[2c], 1, 3 in o[2c + 1]
+  float ref[2], g[2], lg[2], sum[2];  // ref in units of rs; lg = log2(g); o and sum are in units of 2^(ref rs) g
 };
 
-// 16 rows at positions pos x kw keys of one tile for one warp; tile: its keys' codes, the values' D * 64 bytes further
+// 16 rows at positions pos x kw keys of one tile for one warp; q: its rows' fragments, ks: the keys' codes (the values' D * 64 bytes
+// further), all shared-memory addresses.  Step k of the fragments: of the D / 4 values from (lane % 4) D / 4 on, values 4k and 4k + 2,
+// 4k + 1 and 4k + 3
 template <int CODE, int D, int RG, bool Masked>
-__device__ __forceinline__ void tile_step(const AttnParams& p, uint32_t ks, const float* scales, int key0, const int (&pos)[2],
-                                          Rows<D>& r, int lane) {
+__device__ __forceinline__ void tile_step(const AttnParams& p, uint32_t q, uint32_t ks, const float* scales, int key0,
+                                          const int (&pos)[2], Rows<D>& r, int lane) {
   using C = QSplitCfg<D, RG>;
   constexpr int NT = C::kw / 8;
   const int c2 = (lane & 3) * 2;
   const int kloc = key0 & (kSplitKeys - 1);  // the warp's first key within the tile
   float s[NT][4];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int i = 0; i < 4; ++i) s[n][i] = 0.f;
-    const int row = kloc + n * 8 + (lane >> 2);
 #pragma unroll
-    for (int h = 0; h < D / 64; ++h) {
-      const uint4 v = lds128(ks + code_chunk<D>(row, (lane & 3) * (D / 64) + h));
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  for (int h = 0; h < D / 64; ++h) {
+    uint4 v[NT];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
+    for (int n = 0; n < NT; ++n) v[n] = lds128(ks + code_chunk<D>(kloc + n * 8 + (lane >> 2), (lane & 3) * (D / 64) + h));
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const uint4 f = lds128(q + (h * 4 + t) * 512 + lane * 16);
+      const uint32_t a[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
         uint32_t b0, b1;
-        Code<CODE>::widen(w[t], b0, b1);
-        mma16816<Fp16>(s[n], r.q[h * 4 + t], b0, b1);
+        Code<CODE>::widen(t == 0 ? v[n].x : t == 1 ? v[n].y : t == 2 ? v[n].z : v[n].w, b0, b1);
+        mma16816<Fp16>(s[n], a, b0, b1);
       }
     }
   }
@@ -118,29 +125,27 @@ __device__ __forceinline__ void tile_step(const AttnParams& p, uint32_t ks, cons
       float a = fmaxf(m[i], r.ref[i]), b = fmaxf(gm[i], r.g[i]);
       a = fmaxf(a, __shfl_xor_sync(FULL, a, 1)), b = fmaxf(b, __shfl_xor_sync(FULL, b, 1));
       a = fmaxf(a, __shfl_xor_sync(FULL, a, 2)), b = fmaxf(b, __shfl_xor_sync(FULL, b, 2));
-      const float keep = a == -INFINITY ? 1.f : ex2((r.ref[i] - a) * r.rs[i]);  // ref = -inf: 0, and o, sum are 0
-      const float fix = keep * (r.g[i] / b);
-      r.ref[i] = a, r.g[i] = b, r.ig[i] = 1.f / b;
-      r.sum[i] *= keep;
+      const float fix = a == -INFINITY ? 1.f : ex2((r.ref[i] - a) * r.rs[i]) * (r.g[i] / b);  // ref = -inf: 0, and o, sum are 0
+      r.ref[i] = a, r.g[i] = b, r.lg[i] = log2f(b);
+      // (with an infinite g all weights are 0 or NaN; a part whose sum is 0 would be left out of the row)
+      r.sum[i] = b == INFINITY ? NAN : r.sum[i] * fix;
 #pragma unroll
       for (int d = 0; d < D / 8; ++d) r.o[d][2 * i] *= fix, r.o[d][2 * i + 1] *= fix;
     }
   }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const float base = r.ref[i] == -INFINITY ? 0.f : r.ref[i] * r.rs[i];
-    float a = 0.f;
+    const float base = r.ref[i] == -INFINITY ? 0.f : fmaf(-r.ref[i], r.rs[i], -r.lg[i]);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const float e = ex2(fmaf(s[n][2 * i + k], r.rs[i], -base));
-        a += e;
-        float w = e * (vs[n][k] * r.ig[i]);
+        const float e = ex2(fmaf(s[n][2 * i + k], r.rs[i], base));
+        r.sum[i] += e;  // this thread's share of the row; joined at the end
+        float w = e * vs[n][k];
         if (Masked && !(see >> (4 * n + 2 * i + k) & 1)) w = 0.f;  // (its scale may be NaN)
         s[n][2 * i + k] = w;
       }
-    r.sum[i] += a;  // this thread's share of the row; joined at the end
   }
 #pragma unroll
   for (int n = 0; n < NT; n += 2) {
@@ -162,7 +167,7 @@ __device__ __forceinline__ void tile_step(const AttnParams& p, uint32_t ks, cons
   }
 }
 
-// Buffer of a warp: H 8-column groups of its 16 rows in fragment order, then the rows' maxima and sums.
+// Buffer of a warp: H 8-column groups of its 16 rows in fragment order, then the rows' units (lg is ref rs + lg by then) and sums.
 template <int D, int H>
 __device__ __forceinline__ void hand_over(float* merge, int buffer, const Rows<D>& r, int first, int lane) {
   float* base = merge + buffer * (8 * D + 32);
@@ -172,8 +177,8 @@ __device__ __forceinline__ void hand_over(float* merge, int buffer, const Rows<D
     if ((d / H) * H == first) buf[(d % H) * 32 + lane] = make_float4(r.o[d][0], r.o[d][1], r.o[d][2], r.o[d][3]);
   if ((lane & 3) == 0) {
     float2* ml = reinterpret_cast<float2*>(base + 8 * D);
-    ml[lane >> 2] = make_float2(r.ref[0], r.sum[0]);
-    ml[(lane >> 2) + 8] = make_float2(r.ref[1], r.sum[1]);
+    ml[lane >> 2] = make_float2(r.lg[0], r.sum[0]);
+    ml[(lane >> 2) + 8] = make_float2(r.lg[1], r.sum[1]);
   }
 }
 template <int D, int H>
@@ -185,10 +190,10 @@ __device__ __forceinline__ void take_over(const float* merge, int buffer, Rows<D
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const float2 other = ml[(lane >> 2) + i * 8];
-    const float m = fmaxf(r.ref[i], other.x), at = m == -INFINITY ? 0.f : m;
-    fa[i] = ex2((r.ref[i] - at) * r.rs[i]);
-    fb[i] = ex2((other.x - at) * r.rs[i]);
-    r.ref[i] = m;
+    const float m = fmaxf(r.lg[i], other.x), at = m == -INFINITY ? 0.f : m;
+    fa[i] = ex2(r.lg[i] - at);
+    fb[i] = ex2(other.x - at);
+    r.lg[i] = m;
     r.sum[i] = r.sum[i] * fa[i] + other.y * fb[i];
   }
 #pragma unroll
@@ -288,6 +293,7 @@ __global__ void __launch_bounds__(QSplitCfg<D, RG>::threads, QSplitCfg<D, RG>::c
   int it = 0;
   Unit u;
   for (int n = 0; take_unit(units, u, n, lane, wait); ++n) {
+    if (n > 0 && !meet()) return;  // the last unit's sums have been taken over
     const int tok0 = u.tok0, nt = u.nt, p0 = u.p0;
     const bool whole = u.flags & kWhole;
     int pos[2], tok[2];
@@ -321,16 +327,20 @@ __global__ void __launch_bounds__(QSplitCfg<D, RG>::threads, QSplitCfg<D, RG>::c
       const int up = min(60, 14 - ((int)(__float_as_uint(top) >> 23) - 127));
       const float mul = __uint_as_float((uint32_t)(up + 127) << 23), back = __uint_as_float((uint32_t)(127 - up) << 23);
       r.rs[i] = fmaxf(p.scale_log2 * Code<CODE>::unit * back, FLT_MIN);
+      r.slack[i] = fminf(8.f / r.rs[i], FLT_MAX);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
+        if (k % C::KG != kg) continue;  // the others' share
         const float a = T::lo(x[2 * k]) * mul, b = T::hi(x[2 * k]) * mul;
         const float c = T::lo(x[2 * k + 1]) * mul, d = T::hi(x[2 * k + 1]) * mul;
-        r.q[k][i] = Fp16::pack(a, c);
-        r.q[k][i + 2] = Fp16::pack(b, d);
+        uint32_t* at = reinterpret_cast<uint32_t*>(merge) + ((rg * (D / 16) + k) * 32 + lane) * 4 + i;
+        at[0] = Fp16::pack(a, c);
+        at[2] = Fp16::pack(b, d);
       }
-      r.slack[i] = fminf(8.f / r.rs[i], FLT_MAX);
-      r.ref[i] = -INFINITY, r.sum[i] = 0.f, r.g[i] = kNoScale, r.ig[i] = 1.f / kNoScale;
+      r.ref[i] = -INFINITY, r.sum[i] = 0.f, r.g[i] = kNoScale, r.lg[i] = kNoScaleLog;
     }
+    if (!meet()) return;  // all fragments are there
+    const uint32_t q_at = smem_addr(merge) + rg * (D / 16) * 512;
     // the warp's own tokens and their positions
     const int tok_lo = row0 / p.group, tok_hi = min(nt - 1, (row0 + 15) / p.group);
     const int w0 = p0 + tok_lo, w1 = p0 + tok_hi;
@@ -348,9 +358,9 @@ __global__ void __launch_bounds__(QSplitCfg<D, RG>::threads, QSplitCfg<D, RG>::c
         const float* sc = scales + sgi * 2 * kSplitKeys;
         const int key0 = u.tile(i) * kSplitKeys + kg * C::kw;
         if (all_see(p, w0, w1, key0, key0 + C::kw - 1))
-          tile_step<CODE, D, RG, false>(p, ks, sc, key0, pos, r, lane);
+          tile_step<CODE, D, RG, false>(p, q_at, ks, sc, key0, pos, r, lane);
         else
-          tile_step<CODE, D, RG, true>(p, ks, sc, key0, pos, r, lane);
+          tile_step<CODE, D, RG, true>(p, q_at, ks, sc, key0, pos, r, lane);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(empty + sgi);
@@ -359,9 +369,7 @@ __global__ void __launch_bounds__(QSplitCfg<D, RG>::threads, QSplitCfg<D, RG>::c
     for (int i = 0; i < 2; ++i) {
       r.sum[i] += __shfl_xor_sync(FULL, r.sum[i], 1);
       r.sum[i] += __shfl_xor_sync(FULL, r.sum[i], 2);
-      const float unit = r.g[i] * Code<CODE>::unit;
-#pragma unroll
-      for (int d = 0; d < D / 8; ++d) r.o[d][2 * i] *= unit, r.o[d][2 * i + 1] *= unit;
+      r.lg[i] = fmaf(r.ref[i], r.rs[i], r.lg[i]);  // -inf stays -inf
     }
     // Join the KG warps that share these rows.  Each step halves the columns a warp keeps: it hands the other
     // half to its partner and takes its own half's counterpart, so the last step leaves every warp
@@ -371,7 +379,7 @@ __global__ void __launch_bounds__(QSplitCfg<D, RG>::threads, QSplitCfg<D, RG>::c
     int col = 0;                       // the first of them
     {
       constexpr int H = D / 16;
-      if (!meet()) return;  // the buffers are free
+      if (!meet()) return;  // nobody reads the queries any more
       const int other = rg + RG * (kg ^ (C::KG / 2));
       const bool up = kg & (C::KG / 2);
       hand_over<D, H>(merge, other, r, up ? 0 : H, lane);
@@ -390,11 +398,11 @@ __global__ void __launch_bounds__(QSplitCfg<D, RG>::threads, QSplitCfg<D, RG>::c
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int row = row0 + (lane >> 2) + i * 8;
-      const float m2 = r.ref[i] * r.rs[i];  // -inf stays -inf
+      const float m2 = r.lg[i], unit = Code<CODE>::unit;
       const int hq = u.head * p.group + row - tok[i] * p.group;
       if (whole && !live[i]) continue;
       if (whole) {
-        const float inv = r.sum[i] == 0.f ? 0.f : 1.f / r.sum[i];
+        const float inv = r.sum[i] == 0.f ? 0.f : unit / r.sum[i];
         uint16_t* dst = static_cast<uint16_t*>(p.out) + (int64_t)(tok0 + tok[i]) * p.out_stride + (int64_t)hq * D;
 #pragma unroll
         for (int d = 0; d < D / 8; d += 2)
@@ -411,7 +419,7 @@ __global__ void __launch_bounds__(QSplitCfg<D, RG>::threads, QSplitCfg<D, RG>::c
         for (int d = 0; d < D / 8; d += 2)
           if ((d / NC) * NC == col)
             *reinterpret_cast<float4*>(p.part_o + at * D + d * 8 + (lane & 3) * 4) =
-                make_float4(r.o[d][2 * i], r.o[d + 1][2 * i], r.o[d][2 * i + 1], r.o[d + 1][2 * i + 1]);
+                make_float4(r.o[d][2 * i] * unit, r.o[d + 1][2 * i] * unit, r.o[d][2 * i + 1] * unit, r.o[d + 1][2 * i + 1] * unit);
         if (kg == 0 && (lane & 3) == 0) p.part_ml[at] = make_float2(m2, r.sum[i]);
       }
     }
@@ -457,6 +465,8 @@ cudaError_t launch_code(const AttnParams& p, const CUtensorMap& k, const CUtenso
 
 }  // namespace
 
+int qsplit_grid(int num_sms) { return kQSplitCtas * num_sms; }
+
 cudaError_t configure_attn_qsplit() {
   cudaError_t e = cudaSuccess;
 #define COLI_CFG(T, D)                                                  \
@@ -471,7 +481,7 @@ cudaError_t configure_attn_qsplit() {
 
 cudaError_t launch_attn_qsplit(const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v, int rows, int dtype, int code,
                                int num_sms, cudaStream_t stream) {
-  const int grid = split_grid(num_sms);
+  const int grid = qsplit_grid(num_sms);
   return dtype == COLI_ATTN_BF16 ? launch_code<Bf16>(p, k, v, rows, code, grid, stream)
                                  : launch_code<Fp16>(p, k, v, rows, code, grid, stream);
 }
