@@ -20,7 +20,6 @@ constexpr int kAttnNoWindow = 1 << 30;
 constexpr int kSplitUnitCost = 2;
 constexpr int kTileUnitCost = 2;
 constexpr int kSplitMaxRows = 32;     // rows of a block of the split kernel, and of a sequence it takes
-constexpr int kQSplitCtas = 3;        // CTAs an SM of the split kernel for 8-bit caches
 constexpr int kSplitKeys = 64;        // keys per tile of the split kernel
 constexpr int kTileKeys = 128;        // keys per tile of the tensor-memory kernel
 constexpr int kTileRows = 256;        // query rows per block of the tensor-memory kernel (2 x 128)
@@ -102,8 +101,7 @@ struct AttnAppend {
 };
 
 int split_rows(int64_t rows);  // rows per block of the split kernel for sequences of up to `rows` rows
-int split_grid(int num_sms);   // CTAs
-int qsplit_grid(int num_sms);  // of the one for 8-bit caches
+int split_grid(int num_sms);  // CTAs
 cudaError_t configure_attn_split();
 cudaError_t launch_attn_split(const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v,
                               int rows, int dtype, int num_sms, cudaStream_t stream);

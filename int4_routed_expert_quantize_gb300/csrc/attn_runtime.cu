@@ -92,8 +92,8 @@ void carve(T** p, char* arena, size_t* at, size_t count) {
 // the workspace in the arena (nullptr: its size alone); what has to be zero comes first, *zero bytes of it
 size_t lay_out(coli_attn* h, char* arena, size_t* zero) {
   const coli_attn_config& c = h->cfg;
-  // partials: two per CTA of the split kernels (3 CTAs an SM at most) and of the tensor-memory kernels
-  const size_t D = c.head_dim, ctas = qsplit_grid(h->num_sms), rows = 2 * ctas * kSplitMaxRows,
+  // partials: two per CTA of the split kernels (2 CTAs an SM) and of the tensor-memory kernels
+  const size_t D = c.head_dim, ctas = split_grid(h->num_sms), rows = 2 * ctas * kSplitMaxRows,
                rows2 = 2 * (size_t)h->num_sms * kTileRows;
   // the prefix call keeps every row twice
   const size_t dense = (size_t)h->prefix_tokens * c.n_q;
@@ -460,7 +460,7 @@ extern "C" int coli_attn_window(coli_attn* h, const coli_attn_kv* kv, const coli
   const int64_t seq_rows = (int64_t)b->max_q * p.group;
   cudaError_t e;
   if (seq_rows <= kSplitMaxRows) {
-    const int rows = split_rows(seq_rows), ctas = kv->code ? qsplit_grid(h->num_sms) : split_grid(h->num_sms);
+    const int rows = split_rows(seq_rows), ctas = split_grid(h->num_sms);
     p.block_tokens = rows / p.group;
     rc = list_fits(p, kSplitKeys);
     if (rc) return rc;
