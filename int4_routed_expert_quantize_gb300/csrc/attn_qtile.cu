@@ -9,9 +9,10 @@
 //   warp 12          issues every product; warp 13 every copy
 //
 // The codes are exact in the products: keys in the queries' type, values in fp16.  A score is multiplied by its key's scale in fp32; a
-// weight is 2^(s - m) vs / g, with g the largest |vs| that the row has seen, so that it is at most 2^8 and rounds to fp16 well.  1 / g
+// weight is 2^(s - m) vs / g, with g the largest |vs| that the row has seen, to within 8, so that it is below 2^11 and rounds to fp16 well.  1 / g
 // is part of the exponent (the row's sum and output are in the same unit, which cancels), m and g move rarely, and the output in
-// tensor memory is rescaled only then.  What a row does not see has weight 0; codes are always finite, and values' scales that are not
+// tensor memory is rescaled only then.  So a tile's scores become exponents in one step, t = acc ks - (m + log2 g), and a tile in which some
+// t is too large is the exception that moves m and g.  What a row does not see has weight 0; codes are always finite, and values' scales that are not
 // become 0 and a bit that spoils the sums of the rows that see them, so nothing is computed again here.
 //
 // The softmax loop is long straight code and shares the instruction cache with the other roles', so what only masked tiles need is
@@ -26,7 +27,8 @@ namespace coli {
 namespace {
 
 constexpr int kThreadsQTile = 16 * 32;
-constexpr float kNoScale = 0x1p-100f;  // g before the first key
+constexpr float kNoScale = 0x1p-100f, kNoScaleLog = -100.f;  // g before the first key
+constexpr float kSlack = 8.f;  // |vs| / g that weights have room for: they stay below 2^11
 
 struct TileScales {
   float keys[kTileKeys], values[kTileKeys];
@@ -129,27 +131,28 @@ __device__ __forceinline__ void write_chunks(const uint4& v, uint8_t* row_at, in
 }
 
 // One key's row: its codes, as the tensor copies swizzle them in the second half of the tile's place, to boxes of 64 values x 128 keys.
-// A row of 128 codes lies just where its own second 64 values go, so nobody else's is overwritten; rows of 64 codes lie where
-// others' values go, and `meet` makes all threads wait until all have read theirs.
+// A row of 128 codes lies just where its own second 64 values go, chunk by chunk behind those that have been read, so nothing is
+// overwritten before its time; rows of 64 codes lie where others' values go, and `meet` makes all threads wait until all have read
+// theirs.  (In a loop: unrolled by 2 or 4 its instructions came late, 866 / 934 / 966 us for 8192 tokens.)
 template <class T, int CODE, int D, class Meet>
 __device__ __forceinline__ bool widen_row(uint8_t* tile, int row, Meet meet) {
   const uint8_t* raw = tile + kTileKeys * D;
-  uint8_t* first = tile + row * 128;
-  uint4 v[4];
   if constexpr (D == 128) {
+    uint4 next = *reinterpret_cast<const uint4*>(raw + row * 128 + ((row & 7) << 4));
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c)
-      write_chunks<T, CODE>(*reinterpret_cast<const uint4*>(raw + row * 128 + ((c ^ (row & 7)) << 4)), first, 2 * c, row);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) v[c] = *reinterpret_cast<const uint4*>(raw + row * 128 + (((c + 4) ^ (row & 7)) << 4));
-    first += kTileKeys * 128;
+    for (int c = 0; c < 8; ++c) {
+      const uint4 v = next;
+      if (c < 7) next = *reinterpret_cast<const uint4*>(raw + row * 128 + (((c + 1) ^ (row & 7)) << 4));
+      write_chunks<T, CODE>(v, tile + (c >> 2) * kTileKeys * 128 + row * 128, 2 * c & 7, row);
+    }
   } else {
+    uint4 v[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) v[c] = *reinterpret_cast<const uint4*>(raw + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
     if (!meet()) return false;
-  }
 #pragma unroll
-  for (int c = 0; c < 4; ++c) write_chunks<T, CODE>(v[c], first, 2 * c, row);
+    for (int c = 0; c < 4; ++c) write_chunks<T, CODE>(v[c], tile + row * 128, 2 * c, row);
+  }
   return true;
 }
 
@@ -337,6 +340,7 @@ __global__ void __launch_bounds__(kThreadsQTile, 1)
       drain_ring(drain, 1, 1);
     } else if (warp < 12) {  // ---- codes to 16-bit values; thread = key
       const int row = (warp - 8) * 32 + lane;
+      const float rs = p.scale_log2 * Code<CODE>::unit;  // of a product of codes and q times its key's scale: log2 units
       int it = 0, slot = 0;
 #pragma unroll 1
       for (int n = 0; ok && take_unit(units, u, n, lane, wait); ++n) {
@@ -346,6 +350,7 @@ __global__ void __launch_bounds__(kThreadsQTile, 1)
           ok = wait(codes + sg, (it / NST) & 1);
           if (!ok) break;
           if (!(i & 1)) {  // both scales have come with the keys
+            scales[slot].keys[row] *= rs;
             float* value = scales[slot].values + row;
             float top = fabsf(*value);
             const bool bad = !(top < INFINITY);
@@ -379,8 +384,6 @@ __global__ void __launch_bounds__(kThreadsQTile, 1)
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t st_addr = tmem + lane_base + s * 128, ot_addr = tmem + lane_base + C::o_col + s * D;
     const int tok = row / p.group;
-    const float rs = p.scale_log2 * Code<CODE>::unit;  // a product of codes and q times its key's scale, in log2 units
-    const float slack = fminf(8.f / rs, FLT_MAX);      // finite: -inf + inf would never let the first keys in
     uint32_t sn = 0, on = 0, sc_phase = 0;
     int slot = 0;
     Unit u;
@@ -393,7 +396,8 @@ __global__ void __launch_bounds__(kThreadsQTile, 1)
       }
       const bool whole = u.flags & kWhole;
       const int pa = u.p0 + s * half_tokens, pb = pa + nt - 1, pos = pa + tok;  // the row tile's positions, the row's
-      float ref = -INFINITY, sum0 = 0.f, sum1 = 0.f, g = kNoScale, lg = log2f(kNoScale);
+      // -(m + log2 g); the t from which the row needs another m: 8 - log2 g, or -inf before its first key
+      float off = 0.f, limit = -INFINITY, g = kNoScale, sum0 = 0.f, sum1 = 0.f;
       bool ok = true;
 #pragma unroll 1
       for (int i = u.i0; i < u.i1; ++i) {
@@ -414,13 +418,13 @@ __global__ void __launch_bounds__(kThreadsQTile, 1)
         float m0 = -INFINITY, m1 = m0, m2 = m0, m3 = m0;
         const bool masked = !all_see(p, pa, pb, j0, j0 + kTileKeys - 1);
         const int hi = pos - j0, lo = pos - p.window - j0, sk = p.sinks - j0;
-        float gm;  // the largest |vs| of the tile that the row sees
-        bool spoilt;
-        if (!masked) {
-          const float4 t = *reinterpret_cast<const float4*>(sc.top);
-          const uint4 b = *reinterpret_cast<const uint4*>(sc.bad);
-          gm = fmaxf(fmaxf(t.x, t.y), fmaxf(t.z, t.w)), spoilt = (b.x | b.y | b.z | b.w) != 0;
-        } else {
+        // What the values' scales ask of the row: the tile's largest |vs|, a bit for each that is not finite.  Which of them the row sees
+        // counts only where they ask for something.
+        const float4 tops = *reinterpret_cast<const float4*>(sc.top);
+        const uint4 bads = *reinterpret_cast<const uint4*>(sc.bad);
+        float gm = fmaxf(fmaxf(tops.x, tops.y), fmaxf(tops.z, tops.w));
+        bool spoilt = (bads.x | bads.y | bads.z | bads.w) != 0;
+        if (masked && (gm > kSlack * g || spoilt)) {
           gm = 0.f, spoilt = false;
 #pragma unroll 1
           for (int c = 0; c < 128; c += 32) {
@@ -437,8 +441,10 @@ __global__ void __launch_bounds__(kThreadsQTile, 1)
 #pragma unroll
           for (int k = 0; k < 32; k += 4) {
             const float4 v = *reinterpret_cast<const float4*>(ks + c + k);
-            mul2_rn(v.x, v.y, x[c + k], x[c + k + 1]);
-            mul2_rn(v.z, v.w, x[c + k + 2], x[c + k + 3]);
+            float a = off, b = off, e = off, f = off;
+            fma2_rn(x[c + k], x[c + k + 1], v.x, v.y, a, b);
+            fma2_rn(x[c + k + 2], x[c + k + 3], v.z, v.w, e, f);
+            x[c + k] = a, x[c + k + 1] = b, x[c + k + 2] = e, x[c + k + 3] = f;
           }
           if (masked) {  // bit k: the row sees key c + k
             const uint32_t see = low_bits(hi + 1 - c) & (~low_bits(lo + 1 - c) | low_bits(sk - c));
@@ -456,15 +462,23 @@ __global__ void __launch_bounds__(kThreadsQTile, 1)
         }
         const float top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
         if (spoilt) sum0 = NAN;
-        const bool grow = top > ref + slack || gm > g;  // ref = -inf: the row's first keys
+        const bool grow = top > limit || gm > kSlack * g;
         if (__any_sync(FULL, grow)) {
-          float fix = 1.f;
+          const bool begun = limit != -INFINITY;
+          float fix = 1.f, by = 0.f;  // by: added to the row's t
           if (grow) {
-            const float to = top > ref + slack ? top : ref, wide = fmaxf(gm, g);
-            if (ref != -INFINITY) fix = ex2((ref - to) * rs) * (g / wide);  // (else nothing has been added up yet)
-            ref = to, g = wide, lg = log2f(wide);
-            sum0 *= fix, sum1 *= fix;
+            const float to = gm > kSlack * g ? gm : g, lg = begun ? 8.f - limit : kNoScaleLog;
+            g = to;
+            if (top > limit || begun) {
+              const float up = !begun || top + lg > 8.f ? top + (begun ? lg : 0.f) : 0.f, now = log2f(to);  // m moves by `up`
+              by = begun ? lg - now - up : -up - now;
+              if (begun) fix = ex2(by);
+              off += by, limit = 8.f - now;
+              sum0 *= fix, sum1 *= fix;
+            }
           }
+#pragma unroll
+          for (int c = 0; c < 128; c += 2) add2_rn(by, by, x[c], x[c + 1]);
           // the scores' commit also covers the products before them: O is complete
           if (i > u.i0 && __any_sync(FULL, fix != 1.f)) {
 #pragma unroll 1
@@ -478,7 +492,6 @@ __global__ void __launch_bounds__(kThreadsQTile, 1)
             }
           }
         }
-        const float base = ref == -INFINITY ? 0.f : fmaf(-ref, rs, -lg);
 #pragma unroll
         for (int c = 0; c < 128; c += 32) {
           uint32_t w[16];
@@ -487,9 +500,7 @@ __global__ void __launch_bounds__(kThreadsQTile, 1)
             const float4 v = *reinterpret_cast<const float4*>(vs + c + 2 * k);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              float e = base, f = base;
-              fma2_rn(x[c + 2 * (k + h)], x[c + 2 * (k + h) + 1], rs, rs, e, f);
-              e = ex2(e), f = ex2(f);
+              float e = ex2(x[c + 2 * (k + h)]), f = ex2(x[c + 2 * (k + h) + 1]);
               x[c + 2 * (k + h)] = e, x[c + 2 * (k + h) + 1] = f;
               mul2_rn(h ? v.z : v.x, h ? v.w : v.y, e, f);
               w[k + h] = Fp16::pack(e, f);
@@ -520,7 +531,7 @@ __global__ void __launch_bounds__(kThreadsQTile, 1)
       ++on;
       if (!ok) break;
       tc_fence_after();
-      const float sum = sum0 + sum1, m2 = fmaf(ref, rs, lg);  // -inf stays -inf
+      const float sum = sum0 + sum1, m2 = limit == -INFINITY ? -INFINITY : -off;
       const int token = u.tok0 + s * half_tokens + tok, hq = u.head * p.group + row - tok * p.group;
       const bool live = tok < nt;
       if (whole) {

@@ -12,23 +12,32 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
-// A bounded wait by a whole warp: every lane sees the phase, and the lanes are together afterwards.  Reading the global timer takes
-// longer than most waits (a lane of a ring's reader waits some hundred cycles; the timer takes about a thousand), so the limit
-// counts from the 16th try on.
+// mbar_try_wait that may sleep up to 20 us for the phase
+__device__ __forceinline__ bool mbar_sleep_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// A bounded wait by a whole warp: every lane sees the phase, and the lanes are together afterwards.  A waiting warp sleeps and takes no
+// issue slots from the working ones; the limit counts from the second try on.
 __device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
-  bool ok = mbar_try_wait(bar, parity);
+  bool ok = mbar_sleep_wait(bar, parity);
   if (!ok) {
-    uint64_t t0 = 0;
+    const uint64_t t0 = global_ns();
 #pragma unroll 1
-    for (uint32_t it = 1; !*abort_flag; ++it) {
-      if (mbar_try_wait(bar, parity)) {
+    while (!*abort_flag) {
+      if (mbar_sleep_wait(bar, parity)) {
         ok = true;
         break;
       }
-      if (it < 16) continue;
-      const uint64_t now = global_ns();
-      if (it == 16) t0 = now;
-      if (now - t0 > kWaitLimitNs) {
+      if (global_ns() - t0 > kWaitLimitNs) {
         *abort_flag = 1;
         atomicExch(status, COLI_ETIMEOUT);
       }
