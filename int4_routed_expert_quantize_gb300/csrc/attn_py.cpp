@@ -1,7 +1,7 @@
-// Python calls of the paged-cache attention (coli_attn.h) and of the 4-bit products (coli_linear.h).  A serving loop makes one of these calls per layer and step, and
-// their small forms run for a few microseconds on the GPU, so the checks of the tensors, the new output and the
-// call itself are here and not in Python.  Everything else of the bindings is in attn.py and
-// linear.py.
+// Python calls of the paged-cache attention (coli_attn.h) and of the 4-bit products (coli_linear.h).  A serving loop makes one
+// of these calls per layer and step, and their small forms run for a few microseconds on the GPU, so the checks of the
+// tensors, the new output and the call itself are here and not in Python.  Everything else of the bindings is in attn.py
+// and linear.py.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 

@@ -48,6 +48,7 @@ constexpr int kRing = 106496;  // bytes of all rings that are enough
 constexpr int kIn = 4;        // buffers of the other CTAs' sums
 constexpr int kMaxParts = 8;  // CTAs of a cluster
 constexpr int kBlockCodes = 512;
+constexpr int kLaunchTokens = 8 * 65535;  // of one launch: a grid's y goes up to 65535, at 8 tokens or more each
 
 __host__ __device__ constexpr int block_bytes(int group) { return kBlockCodes + 16 * (128 / group); }
 __host__ __device__ constexpr int step_tiles(int mt) { return 2 * mt; }    // of a warp
@@ -389,7 +390,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearParams 
     }
   }
   __syncwarp();
-  if (parts > 1) cluster_sync();  // a CTA's shared memory stays until the others are done with it
+  if (parts > 1) {  // a CTA's shared memory stays until the others are done with it
+    cluster_sync();
+    // Sums that nobody has waited for may still be on their way when a wait gave up.
+    if (rank == 0 && *reinterpret_cast<volatile int*>(abort_flag))
+      for (const uint64_t t0 = global_ns(); global_ns() - t0 < 100000;) {}
+  }
 }
 
 // one 16-byte unit of the store, or the scales of a block, a thread; the grid covers tiles * blocks * 33 units
@@ -502,16 +508,16 @@ cudaError_t configure() {
 }
 
 template <class T, int G>
-cudaError_t launch_tokens(const LinearParams& p, int num_sms, cudaStream_t stream) {
+cudaError_t launch_tokens(const LinearParams& p, bool few, int num_sms, cudaStream_t stream) {
   // (x of 16 tokens and more columns than a cluster holds: 8 tokens at a time)
-  return p.n_tokens <= 8 || p.blocks > kMaxParts * kProduct * 2 ? launch<T, G, 1>(p, num_sms, stream)
+  return few || p.blocks > kMaxParts * kProduct * 2 ? launch<T, G, 1>(p, num_sms, stream)
                                                                  : launch<T, G, 2>(p, num_sms, stream);
 }
 template <class T>
-cudaError_t launch_group(const LinearParams& p, int group, int num_sms, cudaStream_t stream) {
-  return group == 128  ? launch_tokens<T, 128>(p, num_sms, stream)
-         : group == 64 ? launch_tokens<T, 64>(p, num_sms, stream)
-                       : launch_tokens<T, 32>(p, num_sms, stream);
+cudaError_t launch_group(const LinearParams& p, int group, bool few, int num_sms, cudaStream_t stream) {
+  return group == 128  ? launch_tokens<T, 128>(p, few, num_sms, stream)
+         : group == 64 ? launch_tokens<T, 64>(p, few, num_sms, stream)
+                       : launch_tokens<T, 32>(p, few, num_sms, stream);
 }
 
 cudaError_t configure_device() {
@@ -614,12 +620,16 @@ extern "C" int coli_linear_forward(const coli_linear* h, const void* x, int64_t 
   const int rc = check_device(h->device);
   if (rc) return rc;
   LinearParams p = {};
-  p.store = h->store, p.x = static_cast<const uint16_t*>(x), p.y = static_cast<uint16_t*>(y);
-  p.x_stride = x_stride, p.y_stride = y_stride;
-  p.n_tokens = n_tokens, p.rows = c.rows, p.cols = c.cols, p.tiles = h->tiles, p.blocks = h->blocks;
+  p.store = h->store, p.x_stride = x_stride, p.y_stride = y_stride;
+  p.rows = c.rows, p.cols = c.cols, p.tiles = h->tiles, p.blocks = h->blocks;
   p.status = h->status;
-  const cudaError_t e = c.dtype == COLI_ATTN_BF16 ? launch_group<Bf16>(p, c.group, h->num_sms, (cudaStream_t)stream)
-                                                  : launch_group<Fp16>(p, c.group, h->num_sms, (cudaStream_t)stream);
+  cudaError_t e = cudaSuccess;
+  for (int at = 0; at < n_tokens && e == cudaSuccess; at += kLaunchTokens) {
+    p.x = static_cast<const uint16_t*>(x) + at * x_stride, p.y = static_cast<uint16_t*>(y) + at * y_stride;
+    p.n_tokens = std::min(n_tokens - at, kLaunchTokens);
+    e = c.dtype == COLI_ATTN_BF16 ? launch_group<Bf16>(p, c.group, n_tokens <= 8, h->num_sms, (cudaStream_t)stream)
+                                  : launch_group<Fp16>(p, c.group, n_tokens <= 8, h->num_sms, (cudaStream_t)stream);
+  }
   return e == cudaSuccess ? COLI_OK : COLI_ECUDA;
 }
 

@@ -46,8 +46,9 @@ def lib():
 def quantize(w, group=128, dtype=torch.bfloat16, stream=None):
     """w float32 [rows, cols] on the current device -> codes uint8 [rows, cols/2], scales of dtype [rows, cols/group], in memory
     of the current stream.  coli_linear_quantize"""
-    if w.dtype is not torch.float32 or w.dim() != 2 or not w.is_contiguous() or not w.is_cuda:
-        raise ValueError("w: contiguous float32 [rows, cols] on the device")
+    if w.dtype is not torch.float32 or w.dim() != 2 or not w.is_contiguous() or not w.is_cuda or \
+            w.device.index != torch.cuda.current_device():
+        raise ValueError("w: contiguous float32 [rows, cols] on the current device")
     if dtype not in DTYPES:
         raise ValueError(f"{dtype}: scales are bfloat16 or float16")
     if group not in (32, 64, 128) or w.shape[1] % group or w.shape[1] == 0:

@@ -79,6 +79,18 @@ def test_many_tokens():
     assert lin.forward(x[:0]).shape == (0, 300) and lin.status() == 0
 
 
+@pytest.mark.parametrize("cols,tokens", [(32, 600001), (24704, 524291)])
+def test_more_tokens_than_one_launch_takes(cols, tokens):
+    packed, scales = weights(3, cols, 32, HF)
+    lin = linear.Int4Linear(packed, scales, max_tokens=1000000)
+    x = torch.zeros((tokens, cols), dtype=HF, device="cuda")
+    some = torch.cat((torch.arange(9), torch.arange(524270, 524291), torch.arange(tokens - 9, tokens))).cuda()
+    x[some] = torch.randn((len(some), cols), device="cuda").to(HF)
+    y = lin.forward(x)
+    check(y[some], x[some], expanded(packed, scales), 32, HF)
+    assert torch.equal(y[some[:9]], lin.forward(x[:17])[:9]) and lin.status() == 0  # a call's sums have one order
+
+
 def test_store_past_32_bits():
     """weights of more than 2^32 bytes: the first and the last rows"""
     rows, cols = 1500000, 6144
