@@ -9,6 +9,7 @@
 // and cosines serve all heads that the warp handles for its token.  Bound by HBM: q, k, v are read
 // once, q', k', v written once, in 16-byte accesses.  16384 tokens of 48 query and 8 key heads of 128: 537 MB in 83 us,
 // 6.5 TB/s (a copy reaches 6.78); 16 tokens 2.6 us, which is the launch.
+// Into an 8-bit cache (codes and scales as coli_attn.h defines them) 504 MB in 87 us: issue slots are 68 % used beside HBM at 5.8 TB/s.
 #include "attn_device.cuh"
 
 namespace coli {

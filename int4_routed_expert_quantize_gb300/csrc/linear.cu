@@ -17,6 +17,9 @@
 // mma.sync, x of 8 or 2 x 8 tokens is B.  A CTA has a range of tiles, so the SMs end together to within 8 rows.  Columns beyond what
 // the registers of one CTA hold (48 blocks at 8 tokens, 24 at 16) are split over a cluster, whose CTAs send their sums to the first one.
 //
+// Measured: 8192 x 6144 with groups of 128 for one token 8.4 us, of which 3.3 are launch and prologue; from 20000 to 40000 rows 11.0 us more, 5.7
+// TB/s (a copy reaches 6.79).  100000 x 6144 for 16 tokens 78 us, 4.1 TB/s: there the instructions bound it.
+//
 // x: bf16 becomes fp16 times a power of two for each token and warp, which puts its largest value there in 2^14..2^15 (what is below
 // 2^-39 of that is lost, beyond fp32's share of the sum).  A code becomes fp16 exactly, a group's sum is fp32, its scale and that
 // power multiply it in fp32.
