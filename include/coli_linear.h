@@ -11,10 +11,10 @@
  *
  * Numbers.  x, s and y are bf16 or fp16 (one type per handle).  Codes and x multiply exactly; sums are fp32, over a group
  * first, which its scale then multiplies; y is rounded once.  The order of the sums depends on the shape and on whether a call
- * has up to 8 tokens or more, not on the other tokens, and equal calls give equal bits.
+ * has up to 8, up to 16 or more tokens, not on the other tokens, and equal calls give equal bits.
  *
- * A call of up to 16 tokens (8, with more than 24576 columns) reads the weights once; a larger one reads them once for every 16
- * (8) tokens, from L2 as far as they fit.
+ * A call of up to 16 tokens (8, with more than 24576 columns) reads the weights once; a larger one reads them once for every 64
+ * tokens with groups of 128, else for every 16 (8), from L2 as far as they fit.
  *
  * Conventions are those of coli_moe.h.  forward allocates nothing, keeps nothing between calls and may be captured in a CUDA
  * graph; calls on one handle may overlap in time, but not with coli_linear_load.

@@ -17,7 +17,7 @@ PY_TAG = os.path.join(BUILD, "attn_py.tag")  # what it was built for (torch_tag)
 SOURCES = ["pack.cu", "route.cu", "expert_decode.cu", "gateup_w4.cu", "down_w4.cu", "gateup_w8.cu",
            "down_w8.cu", "gateup_w2.cu", "down_w2.cu", "expert_fused.cu", "expert_prefill.cu",
            "runtime.cu", "noalloc.cu", "attn_append.cu", "attn_split.cu", "attn_qsplit.cu", "attn_tile.cu", "attn_qtile.cu",
-           "attn_combine.cu", "attn_runtime.cu", "linear.cu", "tier.cpp", "status.cpp"]
+           "attn_combine.cu", "attn_runtime.cu", "linear.cu", "linear_many.cu", "tier.cpp", "status.cpp"]
 HOST_SOURCES = ["tier.cpp", "status.cpp"]  # the parts that need no CUDA
 
 

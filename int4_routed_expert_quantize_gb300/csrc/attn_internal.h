@@ -101,6 +101,8 @@ struct AttnAppend {
 };
 
 int split_rows(int64_t rows);  // rows per block of the split kernel for sequences of up to `rows` rows
+// x [tokens, cols] of a 16-bit type, boxes of 64 columns x `box` tokens, 128-byte swizzle; false: no map
+bool rows_map(CUtensorMap* map, const void* x, int dtype, int cols, int tokens, int64_t stride, int box);
 int split_grid(int num_sms);  // CTAs
 cudaError_t configure_attn_split();
 cudaError_t launch_attn_split(const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v,

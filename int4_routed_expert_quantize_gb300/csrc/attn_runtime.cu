@@ -293,6 +293,16 @@ int bind(const coli_attn* h, coli_attn_kv* kv, const coli_attn_cache& c) {
 
 }  // namespace
 
+bool coli::rows_map(CUtensorMap* map, const void* x, int dtype, int cols, int tokens, int64_t stride, int box) {
+  EncodeTiled fn = encoder();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)tokens}, strides[1] = {(cuuint64_t)stride * 2};
+  const cuuint32_t boxes[2] = {64, (cuuint32_t)box}, unit[2] = {1, 1};
+  return fn(map, dtype == COLI_ATTN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+            const_cast<void*>(x), dims, strides, boxes, unit, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 extern "C" int coli_attn_create(const coli_attn_config* cfg, coli_attn** out) {
   if (out) *out = nullptr;
   if (!cfg || !out) return COLI_EINVAL;

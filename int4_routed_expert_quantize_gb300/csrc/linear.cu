@@ -1,4 +1,4 @@
-// y = W x for few tokens, W in 4-bit codes with a scale for each row and group of columns:
+// y = W x for few tokens (more than 16 with groups of 128: linear_many.cu), W in 4-bit codes with a scale for each row and group of columns:
 //   y[t,n] = sum_g s[n,g] sum_{k in g} c[n,k] x[t,k]
 //
 // At up to 16 tokens every weight byte is used by few products, so HBM bounds it, and next to it the instructions that make fp16 of
@@ -7,11 +7,6 @@
 // memory full with bulk copies and waits for nobody else, x stays in its registers, and the sums that it shares with others go to
 // warps that do nothing but add.  The weights are the handle's, written by load alone, so the first copies start before the launch that
 // makes x has ended.
-//
-// The store.  8 rows x 128 columns are a block: 32 lanes x 16 bytes of codes (+ 8, so that they are unsigned), then each row's
-// scales of the block's groups.  A tile of 8 rows is its blocks one after another.  Lane (n = lane / 4, c = lane % 4) holds 4 words of 8 columns of
-// row n, all of one group for all c: groups of 128 take columns 32 c + 8 j (word j), of 64 columns 64 (j / 2) + 16 c + 8 (j % 2), of 32
-// columns 32 j + 8 c.  Nibble i of a word is column 2 i (i < 4) or 2 i - 7, so that masks take pairs of neighbours.
 //
 // A warp has NB blocks of every tile that it takes, the same ones each time, 2 or 4 tiles a step: two tiles' weights are the A operand of
 // mma.sync, x of 8 or 2 x 8 tokens is B.  A CTA has a range of tiles, so the SMs end together to within 8 rows.  Columns beyond what
@@ -26,9 +21,8 @@
 #include <algorithm>
 #include <new>
 
-#include "attn_device.cuh"
-#include "bulk.cuh"
 #include "coli_linear.h"
+#include "linear_store.cuh"
 
 using namespace coli;
 
@@ -50,31 +44,10 @@ constexpr int kMaxSlots = 8;  // of a warp's ring
 constexpr int kRing = 106496;  // bytes of all rings that are enough
 constexpr int kIn = 4;        // buffers of the other CTAs' sums
 constexpr int kMaxParts = 8;  // CTAs of a cluster
-constexpr int kBlockCodes = 512;
 constexpr int kLaunchTokens = 8 * 65535;  // of one launch: a grid's y goes up to 65535, at 8 tokens or more each
 
-__host__ __device__ constexpr int block_bytes(int group) { return kBlockCodes + 16 * (128 / group); }
 __host__ __device__ constexpr int step_tiles(int mt) { return 2 * mt; }    // of a warp
 __host__ __device__ constexpr int sum_buffers(int mt) { return mt == 1 ? 4 : 2; }
-
-struct LinearParams {
-  const uint8_t* store;
-  const uint16_t* x;
-  uint16_t* y;
-  int64_t x_stride, y_stride;
-  int n_tokens, rows, cols;
-  int tiles, blocks;  // of the whole matrix
-  int part;           // blocks of a CTA of the cluster (the last one may have fewer)
-  int kw, rw;         // warps that share a tile, tiles' worth of warps: a step is rw * step_tiles tiles
-  int slots;
-  int* status;
-};
-
-// column of a lane's word j within a block
-template <int G>
-__device__ __forceinline__ int word_col(int c, int j) {
-  return G == 128 ? 32 * c + 8 * j : G == 64 ? 64 * (j >> 1) + 16 * c + 8 * (j & 1) : 32 * j + 8 * c;
-}
 
 // Masks and the exponent of 1024, in registers of their own (as immediates, one of two would be moved to a register each time).
 struct Bits {
@@ -566,7 +539,7 @@ extern "C" int coli_linear_create(const coli_linear_config* cfg, coli_linear** o
   int rc = COLI_OK;
   if (cudaGetDevice(&h->device) != cudaSuccess ||
       cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess ||
-      configure_device() != cudaSuccess)
+      configure_device() != cudaSuccess || configure_linear_many() != cudaSuccess)
     rc = COLI_ECUDA;
   if (!rc) {
     const size_t size = (size_t)h->tiles * h->blocks * block_bytes(c.group);  // a multiple of 16
@@ -630,8 +603,11 @@ extern "C" int coli_linear_forward(const coli_linear* h, const void* x, int64_t 
   for (int at = 0; at < n_tokens && e == cudaSuccess; at += kLaunchTokens) {
     p.x = static_cast<const uint16_t*>(x) + at * x_stride, p.y = static_cast<uint16_t*>(y) + at * y_stride;
     p.n_tokens = std::min(n_tokens - at, kLaunchTokens);
-    e = c.dtype == COLI_ATTN_BF16 ? launch_group<Bf16>(p, c.group, n_tokens <= 8, h->num_sms, (cudaStream_t)stream)
-                                  : launch_group<Fp16>(p, c.group, n_tokens <= 8, h->num_sms, (cudaStream_t)stream);
+    if (n_tokens > 16 && c.group == 128)  // both sides' times: linear_many.cu
+      e = launch_linear_many(p, c.dtype, h->num_sms, (cudaStream_t)stream);
+    else
+      e = c.dtype == COLI_ATTN_BF16 ? launch_group<Bf16>(p, c.group, n_tokens <= 8, h->num_sms, (cudaStream_t)stream)
+                                    : launch_group<Fp16>(p, c.group, n_tokens <= 8, h->num_sms, (cudaStream_t)stream);
   }
   return e == cudaSuccess ? COLI_OK : COLI_ECUDA;
 }

@@ -79,6 +79,22 @@ def test_many_tokens():
     assert lin.forward(x[:0]).shape == (0, 300) and lin.status() == 0
 
 
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("rows,cols", [(40000, 640), (19460, 1536), (50001, 128)])
+def test_tokens_and_rows_of_several_passes(rows, cols, dt):
+    packed, scales = weights(rows, cols, 128, dt)
+    w = expanded(packed, scales)
+    lin = linear.Int4Linear(packed, scales, max_tokens=200)
+    wide = torch.randn((200, cols + 8), device="cuda").to(dt)
+    for tokens in (17, 32, 33, 64, 65, 100, 200):
+        y = torch.full((tokens, rows + 3), 7.0, dtype=dt, device="cuda")
+        lin.forward(wide[:tokens, 8:], out=y[:, 1:rows + 1])
+        check(y[:, 1:rows + 1], wide[:tokens, 8:], w, 128, dt)
+        assert not (y[:, :1] != 7).any() and not (y[:, rows + 1:] != 7).any()
+        assert torch.equal(y[:17, 1:rows + 1], lin.forward(wide[:17, 8:]))  # a token's sums do not depend on the others
+    assert lin.status() == 0
+
+
 @pytest.mark.parametrize("cols,tokens", [(32, 600001), (24704, 524291)])
 def test_more_tokens_than_one_launch_takes(cols, tokens):
     packed, scales = weights(3, cols, 32, HF)
