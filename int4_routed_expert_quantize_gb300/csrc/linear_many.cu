@@ -9,8 +9,9 @@
 //   warps 0-3, 4-7   codes to A, D to sums: even and odd blocks
 //   warp 8           issues every product; warp 9 copies weights, 4 blocks of every tile a stage; warp 10 copies x, a block at a time
 //
-// The weights are read once for 64 tokens.  A block takes 800 to 900 cycles, in which HBM could bring two and a half: a warpgroup needs 1,100 of
-// 1,750 for its own one, the rest are its waits for products, of which one of 16 columns takes about 50 cycles however few tokens there are.
+// The weights are read once for 64 tokens.  A block takes 800 to 900 cycles, in which HBM could bring two and a half.  Four warpgroups in place of
+// two took as long (100000 rows, 32 tokens: 109 us for 108), so it is the products: about 100 cycles for each 16 columns, whose A comes from tensor
+// memory, however few tokens there are.
 // So 16 tokens are better off with linear.cu's kernel, and groups of 32 or 64, whose D would not all fit, at any number.  us, here / there, groups of 128:
 //   8192 x 6144    16 tokens 20.1 / 12.9   24 19.5 / 24.9   64 21.6 / 49.7   128 42.4 / 98.9
 //   100000 x 6144  16 tokens 109 / 78      24 108 / 156     64 118 / 309     128 235 / 617
