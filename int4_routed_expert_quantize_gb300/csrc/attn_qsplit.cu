@@ -130,6 +130,9 @@ __device__ __forceinline__ void tile_step(const AttnParams& p, uint32_t q, uint3
       float a = fmaxf(m[i], r.ref[i]), b = fmaxf(gm[i], r.g[i]);
       a = fmaxf(a, __shfl_xor_sync(FULL, a, 1)), b = fmaxf(b, __shfl_xor_sync(FULL, b, 1));
       a = fmaxf(a, __shfl_xor_sync(FULL, a, 2)), b = fmaxf(b, __shfl_xor_sync(FULL, b, 2));
+      // A row moves when its own keys ask for it, whatever the others of the warp do: rows without a token see slots that nobody has
+      // asked for, and a row's roundings must not depend on those.
+      if (!(a > r.ref[i] + r.slack[i] || b > r.g[i])) continue;
       const float fix = a == -INFINITY ? 1.f : ex2((r.ref[i] - a) * r.rs[i]) * (r.g[i] / b);  // ref = -inf: 0, and o, sum are 0
       r.ref[i] = a, r.g[i] = b, r.lg[i] = log2f(b);
       // (with an infinite g all weights are 0 or NaN; a part whose sum is 0 would be left out of the row)

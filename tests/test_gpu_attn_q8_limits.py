@@ -1,0 +1,56 @@
+"""Window over an 8-bit cache where rows meet what is not theirs: bits that depend on other rows, scales that are not finite one at
+a time, queries with an outlier, pages out of range.  Bounds are those of test_gpu_attn_q8.py."""
+import math
+
+import pytest
+import torch
+
+from .test_gpu_attn_q8 import BF, E4, HF, I8, Setup
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    torch.cuda.set_device(0)
+
+
+def call(s, **kw):
+    lse = torch.empty((s.T, s.n_q), device="cuda")
+    out = s.eng.window(s.cache, s.batch, s.q, lse=lse, **kw)
+    return out, lse
+
+
+def place(s, b, j):
+    return int(s.table[b, j // s.page]), j % s.page
+
+
+@pytest.mark.parametrize("kind", [I8, E4])
+@pytest.mark.parametrize("n_q,n_kv,D,page,new,length", [
+    (5, 1, 64, 64, 5, 300), (40, 8, 64, 64, 5, 2999), (6, 1, 128, 64, 1, 700), (3, 1, 128, 128, 3, 200), (1, 1, 64, 16, 40, 300)])
+def test_bits_do_not_come_from_unused_slots(n_q, n_kv, D, page, new, length, kind):
+    """a block has more rows than the sequence has tokens: what those would see does not move the others' roundings"""
+    s = Setup([new], [length], n_q, n_kv, D, page, HF, kind, junk=0.0)
+    want = call(s)
+    used = torch.arange(page, device="cuda") < (length - 1) % page + 1
+    pg = place(s, 0, length - 1)[0]
+    for junk in (1.0, 2.0 ** 40, math.inf, math.nan):
+        s.ks[pg][:, ~used] = junk
+        s.vs[pg][:, ~used] = junk
+        got = call(s)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert s.eng.status() == 0
+
+
+@pytest.mark.parametrize("kind", [I8, E4])
+@pytest.mark.parametrize("new", [3, 40])
+def test_bits_do_not_come_from_other_rows(new, kind):
+    s = Setup([new], [900], 4, 1, 64, 16, HF, kind)
+    want = call(s)
+    for factor in (0.0, 64.0, math.nan):  # the last token's scores move much more often, or not at all
+        s.q[-1] *= factor
+        got = call(s)
+        assert torch.equal(got[0][:-1], want[0][:-1]) and torch.equal(got[1][:-1], want[1][:-1])
+        s.q[-1] = torch.randn_like(s.q[-1])
