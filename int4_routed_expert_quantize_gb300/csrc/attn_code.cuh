@@ -37,6 +37,9 @@ struct Code<COLI_ATTN_CODE_E4M3> {
   }
 };
 
+// A finite scale as it is, any other as NaN: the sign of a score would make an infinite one's weight 0.
+__device__ __forceinline__ float spoil(float scale) { return fmaf(scale, 0.f, scale); }
+
 // One warp fills the stage of a KT-key tile: the boxes that hold keys some row of the block sees, lane i box i: the keys' codes
 // to `keys`, the values' to `vals`, their scales to scales[0..KT-1] and scales[KT..2KT-1].  A page whose id is out of range
 // reads as zeros, scales included, and is reported.

@@ -111,7 +111,8 @@ __device__ __forceinline__ void tile_step(const AttnParams& p, uint32_t q, uint3
   float vs[NT][2], m[2] = {-INFINITY, -INFINITY}, gm[2] = {0.f, 0.f};
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    const float2 k2 = *reinterpret_cast<const float2*>(scales + kloc + n * 8 + c2);
+    float2 k2 = *reinterpret_cast<const float2*>(scales + kloc + n * 8 + c2);
+    k2.x = spoil(k2.x), k2.y = spoil(k2.y);
     const float2 v2 = *reinterpret_cast<const float2*>(scales + kSplitKeys + kloc + n * 8 + c2);
     vs[n][0] = v2.x, vs[n][1] = v2.y;
 #pragma unroll

@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kThreadsQTile, 1)
           ok = wait(codes + sg, (it / NST) & 1);
           if (!ok) break;
           if (!(i & 1)) {  // both scales have come with the keys
-            scales[slot].keys[row] *= rs;
+            scales[slot].keys[row] = spoil(scales[slot].keys[row]) * rs;
             float* value = scales[slot].values + row;
             float top = fabsf(*value);
             const bool bad = !(top < INFINITY);

@@ -27,6 +27,24 @@ def place(s, b, j):
     return int(s.table[b, j // s.page]), j % s.page
 
 
+def one_bad_scale(s, scales):
+    """rows that see a scale that is not finite are NaN, the others are right"""
+    new, W = s.T, 64
+    p = torch.arange(400 - new, 400, device="cuda")
+    ref = s.reference(window=W, sinks=3)
+    for j in (398, 399 - W // 2, 1):
+        pg, sl = place(s, 0, j)
+        keep = scales[pg, :, sl].clone()
+        blind = ~((j <= p) & ((p - j < W) | (j < 3)))
+        for bad in (math.inf, -math.inf, math.nan):
+            scales[pg, :, sl] = bad
+            out, lse = call(s, window=W, sinks=3)
+            s.check(out, lse, ref, blind)
+            assert torch.isnan(out[~blind]).all() and torch.isnan(lse[~blind]).all()
+        scales[pg, :, sl] = keep
+    assert s.eng.status() == 0
+
+
 @pytest.mark.parametrize("kind", [I8, E4])
 @pytest.mark.parametrize("n_q,n_kv,D,page,new,length", [
     (5, 1, 64, 64, 5, 300), (40, 8, 64, 64, 5, 2999), (6, 1, 128, 64, 1, 700), (3, 1, 128, 128, 3, 200), (1, 1, 64, 16, 40, 300)])
@@ -54,3 +72,11 @@ def test_bits_do_not_come_from_other_rows(new, kind):
         got = call(s)
         assert torch.equal(got[0][:-1], want[0][:-1]) and torch.equal(got[1][:-1], want[1][:-1])
         s.q[-1] = torch.randn_like(s.q[-1])
+
+
+@pytest.mark.parametrize("kind", [I8, E4])
+@pytest.mark.parametrize("new", [1, 6, 300])
+def test_a_key_scale_that_is_not_finite(new, kind):
+    """whatever the sign of the row's product with the key"""
+    s = Setup([new], [400], 8, 2, 128, 32, BF, kind)
+    one_bad_scale(s, s.ks)
