@@ -58,6 +58,13 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   return v;
 }
 
+// the larger of two, NaN where one is
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 // What a thread keeps of its two rows (lane / 4 and 8 more).
 template <int D>
 struct Rows {
@@ -121,22 +128,24 @@ __device__ __forceinline__ void tile_step(const AttnParams& p, uint32_t q, uint3
       const bool in = !Masked || (see >> (4 * n + i) & 1);
       if (!in) s[n][i] = -INFINITY;
       m[i >> 1] = fmaxf(m[i >> 1], s[n][i]);
-      if (in) gm[i >> 1] = fmaxf(gm[i >> 1], fabsf(vs[n][i & 1]));
+      if (in) gm[i >> 1] = max_nan(gm[i >> 1], fabsf(vs[n][i & 1]));
     }
   }
-  const bool grow = m[0] > r.ref[0] + r.slack[0] || m[1] > r.ref[1] + r.slack[1] || gm[0] > r.g[0] || gm[1] > r.g[1];
+  // (a NaN among the values' scales is above any g)
+  const bool grow = m[0] > r.ref[0] + r.slack[0] || m[1] > r.ref[1] + r.slack[1] || !(gm[0] <= r.g[0]) || !(gm[1] <= r.g[1]);
   if (__any_sync(FULL, grow)) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      float a = fmaxf(m[i], r.ref[i]), b = fmaxf(gm[i], r.g[i]);
-      a = fmaxf(a, __shfl_xor_sync(FULL, a, 1)), b = fmaxf(b, __shfl_xor_sync(FULL, b, 1));
-      a = fmaxf(a, __shfl_xor_sync(FULL, a, 2)), b = fmaxf(b, __shfl_xor_sync(FULL, b, 2));
+      float a = fmaxf(m[i], r.ref[i]), b = max_nan(gm[i], r.g[i]);
+      a = fmaxf(a, __shfl_xor_sync(FULL, a, 1)), b = max_nan(b, __shfl_xor_sync(FULL, b, 1));
+      a = fmaxf(a, __shfl_xor_sync(FULL, a, 2)), b = max_nan(b, __shfl_xor_sync(FULL, b, 2));
       // A row moves when its own keys ask for it, whatever the others of the warp do: rows without a token see slots that nobody has
       // asked for, and a row's roundings must not depend on those.
-      if (!(a > r.ref[i] + r.slack[i] || b > r.g[i])) continue;
+      if (!(a > r.ref[i] + r.slack[i] || !(b <= r.g[i]))) continue;
+      if (!(b < INFINITY)) b = INFINITY;
       const float fix = a == -INFINITY ? 1.f : ex2((r.ref[i] - a) * r.rs[i]) * (r.g[i] / b);  // ref = -inf: 0, and o, sum are 0
       r.ref[i] = a, r.g[i] = b, r.lg[i] = log2f(b);
-      // (with an infinite g all weights are 0 or NaN; a part whose sum is 0 would be left out of the row)
+      // (with an infinite g all weights are 0 or NaN, and a part whose sum is 0, or whose weight is, would be left out of the row)
       r.sum[i] = b == INFINITY ? NAN : r.sum[i] * fix;
 #pragma unroll
       for (int d = 0; d < D / 8; ++d) r.o[d][2 * i] *= fix, r.o[d][2 * i + 1] *= fix;

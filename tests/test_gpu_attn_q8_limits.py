@@ -80,3 +80,31 @@ def test_a_key_scale_that_is_not_finite(new, kind):
     """whatever the sign of the row's product with the key"""
     s = Setup([new], [400], 8, 2, 128, 32, BF, kind)
     one_bad_scale(s, s.ks)
+
+
+@pytest.mark.parametrize("kind", [I8, E4])
+@pytest.mark.parametrize("new", [1, 6, 300])
+def test_a_value_scale_that_is_not_finite(new, kind):
+    s = Setup([new], [400], 8, 2, 128, 32, BF, kind)
+    one_bad_scale(s, s.vs)
+
+
+@pytest.mark.parametrize("kind", [I8, E4])
+@pytest.mark.parametrize("new,sinks", [(1, 0), (40, 0)])
+def test_a_scale_that_is_not_finite_at_keys_of_no_weight(new, sinks, kind):
+    """a whole part of the keys has scores 1000 below the others': its NaN is the row's all the same"""
+    s = Setup([new], [6000], 4, 1, 64, 64, BF, kind)
+    s.q = torch.ones_like(s.q)
+    pages = s.table[0, :32].long()  # 2048 keys
+    s.kc.view(torch.uint8)[pages] = torch.full((1, 64), -100.0 if kind is I8 else -448.0, device="cuda").to(kind).view(torch.uint8)
+    s.ks[pages] = 1.0
+    for scales in (s.vs, s.ks):
+        for bad in (math.nan, math.inf):
+            pg, sl = place(s, 0, 70)
+            keep = scales[pg, :, sl].clone()
+            scales[pg, :, sl] = bad
+            out, lse = call(s)
+            assert torch.isnan(out).all() and torch.isnan(lse).all()
+            scales[pg, :, sl] = keep
+    out, lse = call(s)
+    s.check(out, lse, s.reference())
