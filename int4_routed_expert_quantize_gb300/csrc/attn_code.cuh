@@ -1,4 +1,4 @@
-// Device helpers of the attention kernels over an 8-bit cache: codes to fp16, and the copies of code tiles and their scales.
+// Device helpers of the attention kernels over an 8-bit cache: codes to 16-bit values, and the copies of code tiles and their scales.
 #pragma once
 
 #include "attn_device.cuh"
@@ -6,22 +6,32 @@
 
 namespace coli {
 
-// Four codes of a word -> two fp16 pairs: bytes 0 and 2, bytes 1 and 3.  A code is `unit` times its fp16 value, which is exact.
+// widen: four codes of a word -> two pairs of type T: bytes 0 and 2, bytes 1 and 3.  A code is `unit` times its value, which is exact.
 template <int CODE>
 struct Code;
 
 template <>
 struct Code<COLI_ATTN_CODE_INT8> {
   static constexpr float unit = 1.f;
-  // offset by 128, the byte is the mantissa of 1024 + c + 128
+  template <class T>
   static __device__ __forceinline__ void widen(uint32_t w, uint32_t& even, uint32_t& odd) {
-    const uint32_t u = w ^ 0x80808080u;
-    even = minus(__byte_perm(u, 0x64646464u, 0x4240));
-    odd = minus(__byte_perm(u, 0x64646464u, 0x4341));
+    if constexpr (T::kExp == Bf16::kExp) {
+      even = less(__byte_perm(w, 0x43434343u, 0x4240)), odd = less(__byte_perm(w, 0x43434343u, 0x4341));
+    } else {  // offset by 128, the byte is the mantissa of 1024 + c + 128
+      const uint32_t u = w ^ 0x80808080u;
+      even = minus(__byte_perm(u, 0x64646464u, 0x4240));
+      odd = minus(__byte_perm(u, 0x64646464u, 0x4341));
+    }
   }
   static __device__ __forceinline__ uint32_t minus(uint32_t v) {
     uint32_t r;
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x64806480u));  // 1152
+    return r;
+  }
+  // codes under bf16's exponent of 128: 128 + (c & 127), less 128 or, for a negative c, 256
+  static __device__ __forceinline__ uint32_t less(uint32_t v) {
+    uint32_t r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v & 0xFF7FFF7Fu), "r"(v & 0xFF80FF80u));
     return r;
   }
 };
@@ -29,11 +39,22 @@ struct Code<COLI_ATTN_CODE_INT8> {
 template <>
 struct Code<COLI_ATTN_CODE_E4M3> {
   static constexpr float unit = 256.f;
-  // e4m3's exponent and mantissa are fp16's, whose exponent is offset by 8 more (so subnormal codes are subnormal too).
-  // Codes 0x7F and 0xFF come out finite, so that a slot that no row sees cannot spoil a product with its zero weight.
+  // e4m3's exponent and mantissa are fp16's, whose exponent is offset by 8 more (so subnormal codes are subnormal too); or bf16's
+  // at its lowest exponents.  Codes 0x7F and 0xFF come out finite, so that a slot that no row sees cannot spoil a product with its
+  // zero weight.
+  template <class T>
   static __device__ __forceinline__ void widen(uint32_t w, uint32_t& even, uint32_t& odd) {
-    even = ((w << 7) & 0x3F803F80u) | ((w << 8) & 0x80008000u);
-    odd = ((w >> 1) & 0x3F803F80u) | (w & 0x80008000u);
+    if constexpr (T::kExp == Bf16::kExp) {
+      even = raise(((w << 4) & 0x07F007F0u) | ((w << 8) & 0x80008000u));
+      odd = raise(((w >> 4) & 0x07F007F0u) | (w & 0x80008000u));
+    } else {
+      even = ((w << 7) & 0x3F803F80u) | ((w << 8) & 0x80008000u);
+      odd = ((w >> 1) & 0x3F803F80u) | (w & 0x80008000u);
+    }
+  }
+  static __device__ __forceinline__ uint32_t raise(uint32_t v) {  // times 2^112
+    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(v) : "r"(0x77807780u));
+    return v;
   }
 };
 

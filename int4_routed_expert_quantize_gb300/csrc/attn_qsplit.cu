@@ -3,20 +3,20 @@
 // in one pass over the keys, with attn_split.cu's plan: a warp copies tiles of 64 keys, four warps take 16 or 32 of a
 // tile's keys for 16 rows each, the list of all units' tiles is cut into equal stretches.
 //
-// The codes are widened to fp16, which is exact, on their way from shared memory to mma.sync; what the rows bring is brought
-// into fp16's range.  Queries: a row is multiplied by the power of two that puts its largest value in 2^14 .. 2^15 (values
-// 2^-39 of that are lost, beyond fp32's share of the sum).  Weights: 2^(s_j - m) vs_j / g, where m follows the row's
-// maximum to within 2^8 and g is the largest |vs| that the row has seen, so neither runs out of range, and what a row
-// does not see has no part in it; they are rounded to fp16 once.  m and g rarely grow, and the accumulators are rescaled only then.
+// The codes are widened on their way from shared memory to mma.sync, which is exact: keys to the queries' type, values to fp16, the
+// weights' type.  Weights: 2^(s_j - m) vs_j / g, where m follows the row's maximum to within 2^8 and g is the largest |vs| that the
+// row has seen, so that they do not run out of fp16's range, and what a row does not see has no part in it; they are rounded to fp16
+// once.  m and g rarely grow, and the accumulators are rescaled only then.
 //
 // A lane's codes of a key are contiguous in shared memory (the order of the products' inner dimension is free as long as the
 // queries follow it), and a 16-bit transposing load of the values brings two columns' codes of a key in one half, so
-// both operands take one widening of a word for four codes: 5 instructions (int8) or 7 (e4m3).
+// both operands take one widening of a word for four codes: to fp16 5 instructions (int8) or 7 (e4m3), to bf16 8 or 9.
 //
-// Measured, with the combine kernel: 64 sequences' next tokens, 6 query heads a key head, 8 key heads of 128, windows of 4096 keys, int8:
-// 556 MB in 111 us, 5.0 TB/s; the copies alone take 97 (pages of 8 KB a head in random order).  e4m3 about 10 us more: 29 instructions a
-// word and lane for 24.  Three CTAs an SM (128 registers) took 112, 32 keys a warp of every other tile 110 and 11.4 instead of 10.1 for
-// one token, the queries' fragments in registers 141.
+// Measured, with the combine kernel: 64 sequences' next tokens, 6 query heads a key head, 8 key heads of 128, windows of 4096 keys: 556 MB
+// in bf16 with int8 118.6 us, 4.7 TB/s, with e4m3 125.6, in fp16 110.6 and 121.7; the copies alone take 97 (pages of 8 KB a head in random
+// order).  Keys as fp16 for bf16 queries too took 112 (and 0.5 us more for one token), which holds only queries whose values are within
+// 2^31 of one another.  Beside 111 of an earlier form: three CTAs an SM (128 registers) 112, 32 keys a warp of every other tile 110 and
+// 11.4 instead of 10.1 for one token, the queries' fragments in registers 141.
 #include <float.h>
 
 #include "attn_code.cuh"
@@ -68,8 +68,8 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // What a thread keeps of its two rows (lane / 4 and 8 more).
 template <int D>
 struct Rows {
-  float rs[2];        // score of a product of codes and q, times log2(e)
-  float slack[2];     // 8 in units of rs, finite: -inf + inf would never let the first keys in
+  float rs;           // score of a product of codes and q, times log2(e)
+  float slack;        // 8 in units of rs, finite: -inf + inf would never let the first keys in
   float o[D / 8][4];  // columns 16 c + 4 (lane % 4) + 0, 2 in o[2c], 1, 3 in o[2c + 1]
   float ref[2], g[2], lg[2], sum[2];  // ref in units of rs; lg = log2(g); o and sum are in units of 2^(ref rs) g
 };
@@ -77,7 +77,7 @@ struct Rows {
 // 16 rows at positions pos x kw keys of one tile for one warp; q: its rows' fragments, ks: the keys' codes (the values' D * 64 bytes
 // further), all shared-memory addresses.  Step k of the fragments: of the D / 4 values from (lane % 4) D / 4 on, values 4k and 4k + 2,
 // 4k + 1 and 4k + 3
-template <int CODE, int D, int RG, bool Masked>
+template <class T, int CODE, int D, int RG, bool Masked>
 __device__ __forceinline__ void tile_step(const AttnParams& p, uint32_t q, uint32_t ks, const float* scales, int key0,
                                           const int (&pos)[2], Rows<D>& r, int lane) {
   using C = QSplitCfg<D, RG>;
@@ -101,8 +101,8 @@ __device__ __forceinline__ void tile_step(const AttnParams& p, uint32_t q, uint3
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         uint32_t b0, b1;
-        Code<CODE>::widen(t == 0 ? v[n].x : t == 1 ? v[n].y : t == 2 ? v[n].z : v[n].w, b0, b1);
-        mma16816<Fp16>(s[n], a, b0, b1);
+        Code<CODE>::template widen<T>(t == 0 ? v[n].x : t == 1 ? v[n].y : t == 2 ? v[n].z : v[n].w, b0, b1);
+        mma16816<T>(s[n], a, b0, b1);
       }
     }
   }
@@ -132,7 +132,7 @@ __device__ __forceinline__ void tile_step(const AttnParams& p, uint32_t q, uint3
     }
   }
   // (a NaN among the values' scales is above any g)
-  const bool grow = m[0] > r.ref[0] + r.slack[0] || m[1] > r.ref[1] + r.slack[1] || !(gm[0] <= r.g[0]) || !(gm[1] <= r.g[1]);
+  const bool grow = m[0] > r.ref[0] + r.slack || m[1] > r.ref[1] + r.slack || !(gm[0] <= r.g[0]) || !(gm[1] <= r.g[1]);
   if (__any_sync(FULL, grow)) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -141,9 +141,9 @@ __device__ __forceinline__ void tile_step(const AttnParams& p, uint32_t q, uint3
       a = fmaxf(a, __shfl_xor_sync(FULL, a, 2)), b = max_nan(b, __shfl_xor_sync(FULL, b, 2));
       // A row moves when its own keys ask for it, whatever the others of the warp do: rows without a token see slots that nobody has
       // asked for, and a row's roundings must not depend on those.
-      if (!(a > r.ref[i] + r.slack[i] || !(b <= r.g[i]))) continue;
+      if (!(a > r.ref[i] + r.slack || !(b <= r.g[i]))) continue;
       if (!(b < INFINITY)) b = INFINITY;
-      const float fix = a == -INFINITY ? 1.f : ex2((r.ref[i] - a) * r.rs[i]) * (r.g[i] / b);  // ref = -inf: 0, and o, sum are 0
+      const float fix = a == -INFINITY ? 1.f : ex2((r.ref[i] - a) * r.rs) * (r.g[i] / b);  // ref = -inf: 0, and o, sum are 0
       r.ref[i] = a, r.g[i] = b, r.lg[i] = log2f(b);
       // (with an infinite g all weights are 0 or NaN, and a part whose sum is 0, or whose weight is, would be left out of the row)
       r.sum[i] = b == INFINITY ? NAN : r.sum[i] * fix;
@@ -153,12 +153,12 @@ __device__ __forceinline__ void tile_step(const AttnParams& p, uint32_t q, uint3
   }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const float base = r.ref[i] == -INFINITY ? 0.f : fmaf(-r.ref[i], r.rs[i], -r.lg[i]);
+    const float base = r.ref[i] == -INFINITY ? 0.f : fmaf(-r.ref[i], r.rs, -r.lg[i]);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const float e = ex2(fmaf(s[n][2 * i + k], r.rs[i], base));
+        const float e = ex2(fmaf(s[n][2 * i + k], r.rs, base));
         r.sum[i] += e;  // this thread's share of the row; joined at the end
         float w = e * vs[n][k];
         if (Masked && !(see >> (4 * n + 2 * i + k) & 1)) w = 0.f;  // (its scale may be NaN)
@@ -176,8 +176,8 @@ __device__ __forceinline__ void tile_step(const AttnParams& p, uint32_t q, uint3
       ldsm4t(ks + kSplitKeys * D + code_chunk<D>(row, c + (lane >> 4)), b);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        Code<CODE>::widen(b[2 * h], x[0], y[0]);
-        Code<CODE>::widen(b[2 * h + 1], x[1], y[1]);
+        Code<CODE>::template widen<Fp16>(b[2 * h], x[0], y[0]);
+        Code<CODE>::template widen<Fp16>(b[2 * h + 1], x[1], y[1]);
         mma16816<Fp16>(r.o[2 * (c + h)], pf, x[0], x[1]);
         mma16816<Fp16>(r.o[2 * (c + h) + 1], pf, y[0], y[1]);
       }
@@ -317,6 +317,8 @@ __global__ void __launch_bounds__(QSplitCfg<D, RG>::threads, QSplitCfg<D, RG>::c
     int pos[2], tok[2];
     bool live[2];
     Rows<D> r;
+    r.rs = p.scale_log2 * Code<CODE>::unit;
+    r.slack = fminf(8.f / r.rs, FLT_MAX);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int row = row0 + (lane >> 2) + i * 8;
@@ -336,24 +338,12 @@ __global__ void __launch_bounds__(QSplitCfg<D, RG>::threads, QSplitCfg<D, RG>::c
           x[4 * k] = v.x, x[4 * k + 1] = v.y, x[4 * k + 2] = v.z, x[4 * k + 3] = v.w;
         }
       }
-      float top = 0.f;
-#pragma unroll
-      for (int k = 0; k < D / 8; ++k) top = fmaxf(top, fmaxf(fabsf(T::lo(x[k])), fabsf(T::hi(x[k]))));
-      top = fmaxf(top, __shfl_xor_sync(FULL, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(FULL, top, 2));
-      // 2^up brings the largest value's exponent to 14 (not for the smallest rows, whose scores are 0 all the same)
-      const int up = min(60, 14 - ((int)(__float_as_uint(top) >> 23) - 127));
-      const float mul = __uint_as_float((uint32_t)(up + 127) << 23), back = __uint_as_float((uint32_t)(127 - up) << 23);
-      r.rs[i] = fmaxf(p.scale_log2 * Code<CODE>::unit * back, FLT_MIN);
-      r.slack[i] = fminf(8.f / r.rs[i], FLT_MAX);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         if (k % C::KG != kg) continue;  // the others' share
-        const float a = T::lo(x[2 * k]) * mul, b = T::hi(x[2 * k]) * mul;
-        const float c = T::lo(x[2 * k + 1]) * mul, d = T::hi(x[2 * k + 1]) * mul;
         uint32_t* at = reinterpret_cast<uint32_t*>(merge) + ((rg * (D / 16) + k) * 32 + lane) * 4 + i;
-        at[0] = Fp16::pack(a, c);
-        at[2] = Fp16::pack(b, d);
+        at[0] = __byte_perm(x[2 * k], x[2 * k + 1], 0x5410);
+        at[2] = __byte_perm(x[2 * k], x[2 * k + 1], 0x7632);
       }
       r.ref[i] = -INFINITY, r.sum[i] = 0.f, r.g[i] = kNoScale, r.lg[i] = kNoScaleLog;
     }
@@ -376,9 +366,9 @@ __global__ void __launch_bounds__(QSplitCfg<D, RG>::threads, QSplitCfg<D, RG>::c
         const float* sc = scales + sgi * 2 * kSplitKeys;
         const int key0 = u.tile(i) * kSplitKeys + kg * C::kw;
         if (all_see(p, w0, w1, key0, key0 + C::kw - 1))
-          tile_step<CODE, D, RG, false>(p, q_at, ks, sc, key0, pos, r, lane);
+          tile_step<T, CODE, D, RG, false>(p, q_at, ks, sc, key0, pos, r, lane);
         else
-          tile_step<CODE, D, RG, true>(p, q_at, ks, sc, key0, pos, r, lane);
+          tile_step<T, CODE, D, RG, true>(p, q_at, ks, sc, key0, pos, r, lane);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(empty + sgi);
@@ -387,7 +377,7 @@ __global__ void __launch_bounds__(QSplitCfg<D, RG>::threads, QSplitCfg<D, RG>::c
     for (int i = 0; i < 2; ++i) {
       r.sum[i] += __shfl_xor_sync(FULL, r.sum[i], 1);
       r.sum[i] += __shfl_xor_sync(FULL, r.sum[i], 2);
-      r.lg[i] = fmaf(r.ref[i], r.rs[i], r.lg[i]);  // -inf stays -inf
+      r.lg[i] = fmaf(r.ref[i], r.rs, r.lg[i]);  // -inf stays -inf
     }
     // Join the KG warps that share these rows.  Each step halves the columns a warp keeps: it hands the other
     // half to its partner and takes its own half's counterpart, so the last step leaves every warp

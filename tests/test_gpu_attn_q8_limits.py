@@ -108,3 +108,44 @@ def test_a_scale_that_is_not_finite_at_keys_of_no_weight(new, sinks, kind):
             scales[pg, :, sl] = keep
     out, lse = call(s)
     s.check(out, lse, s.reference())
+
+
+@pytest.mark.parametrize("kind", [I8, E4])
+@pytest.mark.parametrize("n_q,n_kv,D,new", [(6, 1, 128, 1), (4, 2, 64, 5), (17, 1, 64, 1), (8, 2, 64, 60)])
+def test_queries_multiply_exactly(n_q, n_kv, D, new, kind):
+    """a query value 2^41 times the others', whose codes are 0, leaves the scores of the others alone"""
+    s = Setup([new], [500], n_q, n_kv, D, 16, BF, kind)
+    s.kc.view(torch.uint8)[..., 5] = 0
+    s.q[..., 5] = 2.0 ** 41
+    out, lse = call(s)
+    s.check(out, lse, s.reference())
+
+
+@pytest.mark.parametrize("kind", [I8, E4])
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("new", [1, 40])
+def test_every_code_is_exact(new, dt, kind):
+    """one key and one-hot queries: the log-sum-exp is the key's value, for each of the 256 codes, a code of the value is the
+    output.  (e4m3's 0x7F and 0xFF count as 480 and -480.)  The score is one fp32 product; log2(e) and ln 2 in fp32 and the sum of m and
+    log2(1) round it by no more than 2^-22 of itself."""
+    D, n = 64, 4
+    s = Setup([new] * n, [new] * n, D, 1, D, 64, dt, kind, junk=1.0)
+    codes = torch.arange(256, dtype=torch.uint8, device="cuda").view(n, D)
+    value = codes.view(kind).float()
+    if kind is E4:
+        value = torch.where(codes == 127, 480.0, torch.where(codes == 255, -480.0, value))
+    for b in range(n):
+        pg = int(s.table[b, 0])
+        s.kc.view(torch.uint8)[pg], s.vc.view(torch.uint8)[pg] = codes[b], codes[b]
+    s.ks.fill_(1.0), s.vs.fill_(1.0)
+    s.q = torch.eye(D, device="cuda").to(dt).repeat(s.T, 1, 1)
+    out, lse = call(s, scale=1.0)
+    m = value.repeat_interleave(new, 0).double()
+    own = math.log(1.0)
+    count = torch.arange(1, new + 1, device="cuda").repeat(n).double()  # a token sees as many equal keys
+    ref = m + torch.log(count)[:, None] + own
+    assert ((lse.double() - ref).abs() <= 2.0 ** -22 * (ref.abs() + m.abs()) + 2.0 ** -22).all()
+    u = 2.0 ** -8 if dt is BF else 2.0 ** -11
+    # equal weights: their fp16 roundings and the sum's cancel to within 2^-11 + 2^-20
+    assert ((out.double() - m[:, None]).abs() <= (u + 2.0 ** -11 + 2.0 ** -20) * m[:, None].abs()).all()
+    assert s.eng.status() == 0
