@@ -1,9 +1,9 @@
 // y = W x for few tokens (more than 16 with groups of 128: linear_many.cu), W in 4-bit codes with a scale for each row and group of columns:
 //   y[t,n] = sum_g s[n,g] sum_{k in g} c[n,k] x[t,k]
 //
-// At up to 16 tokens every weight byte is used by few products, so HBM bounds it, and next to it the instructions that make fp16 of
-// 4-bit codes: a word of 8 takes 5 on the ALU and 4 on the fp16 pipe, and mma.sync gets in their way (together 73 cycles a block and SM
-// partition, where HBM takes 98).  So the 12 product warps of an SM stay clear of one another: each keeps a ring of its own in shared
+// At up to 16 tokens every weight byte is used by few products, so HBM bounds it, and next to it the instructions that make 16-bit
+// values of 4-bit codes: a word of 8 takes 5 on the ALU and 4 on the fp16 pipe (to bf16 7 and 4), and mma.sync gets in their way (fp16:
+// together 73 cycles a block and SM partition, where HBM takes 98).  So the 12 product warps of an SM stay clear of one another: each keeps a ring of its own in shared
 // memory full with bulk copies and waits for nobody else, x stays in its registers, and the sums that it shares with others go to
 // warps that do nothing but add.  The weights are the handle's, written by load alone, so the first copies start before the launch that
 // makes x has ended.
@@ -12,12 +12,13 @@
 // mma.sync, x of 8 or 2 x 8 tokens is B.  A CTA has a range of tiles, so the SMs end together to within 8 rows.  Columns beyond what
 // the registers of one CTA hold (48 blocks at 8 tokens, 24 at 16) are split over a cluster, whose CTAs send their sums to the first one.
 //
-// Measured: 8192 x 6144 with groups of 128 for one token 8.4 us, of which 3.3 are launch and prologue; from 20000 to 40000 rows 11.0 us more, 5.7
-// TB/s (a copy reaches 6.79).  100000 x 6144 for 16 tokens 78 us, 4.1 TB/s: there the instructions bound it.
+// Measured, groups of 128, bf16: 8192 x 6144 for one token 8.4 us, of which 3.3 are launch and prologue; from 20000 to 40000 rows 11.8 us
+// more, 5.4 TB/s (fp16 10.6, 6.0 TB/s; a copy reaches 6.79).  100000 x 6144 for 16 tokens 79 us (fp16 73), 4.0 TB/s: there the
+// instructions bound it.
 //
-// x: bf16 becomes fp16 times a power of two for each token and warp, which puts its largest value there in 2^14..2^15 (what is below
-// 2^-39 of that is lost, beyond fp32's share of the sum).  A code becomes fp16 exactly, a group's sum is fp32, its scale and that
-// power multiply it in fp32.
+// A code becomes a value of x's type exactly, so products are exact whatever the sizes of x; a group's sum is fp32, and its scale
+// multiplies it in fp32.  (bf16 x as fp16 times a power of two for each token and warp, which saves two shifts a word, lost what was 2^39 below the
+// largest value: 100000 rows 55.8 us for one token instead of 60.4, 78.1 for 16 instead of 79.0, 8192 rows 8.7 and 13.1 instead of 8.4 and 12.7.)
 #include <algorithm>
 #include <new>
 
@@ -49,26 +50,38 @@ constexpr int kLaunchTokens = 8 * 65535;  // of one launch: a grid's y goes up t
 __host__ __device__ constexpr int step_tiles(int mt) { return 2 * mt; }    // of a warp
 __host__ __device__ constexpr int sum_buffers(int mt) { return mt == 1 ? 4 : 2; }
 
-// Masks and the exponent of 1024, in registers of their own (as immediates, one of two would be moved to a register each time).
+// Masks and exponents, in registers of their own (as immediates, one of two would be moved to a register each time).
+template <class T>
 struct Bits {
   uint32_t lo, hi, exp;
   __device__ __forceinline__ Bits() {
     asm volatile("mov.b32 %0, 0x000F000F;" : "=r"(lo));
     asm volatile("mov.b32 %0, 0x00F000F0;" : "=r"(hi));
-    asm volatile("mov.b32 %0, 0x64006400;" : "=r"(exp));
+    if constexpr (T::kExp == Fp16::kExp) asm volatile("mov.b32 %0, 0x64006400;" : "=r"(exp));
+    else asm volatile("mov.b32 %0, 0x43004300;" : "=r"(exp));
   }
 };
-// 8 codes of a word as four fp16 pairs of neighbours.  Under the exponent of 1024 a nibble in bits 0-3 is 1024 + u, one in bits 4-7 is
-// 1024 + 16 u, so a word takes one shift; u - 8 is exact.
-__device__ __forceinline__ void unpack(const Bits& k, uint32_t w, uint32_t (&v)[4]) {
+// 8 codes of a word as four pairs of neighbours, exactly.  fp16: under the exponent of 1024 a nibble in bits 0-3 is 1024 + u, one in
+// bits 4-7 is 1024 + 16 u, so a word takes one shift; bf16 has 7 bits under the exponent of 128, so a word takes three.
+template <class T>
+__device__ __forceinline__ void unpack(const Bits<T>& k, uint32_t w, uint32_t (&v)[4]) {
+  if constexpr (T::kExp == Fp16::kExp) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t u = i ? w >> 8 : w;
-    uint32_t lo, hi;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(lo) : "r"(u), "r"(k.lo), "r"(k.exp));  // u & mask | exp
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(hi) : "r"(u), "r"(k.hi), "r"(k.exp));
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(v[2 * i]) : "r"(lo), "r"(0x64086408u));                          // 1032
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(v[2 * i + 1]) : "r"(hi), "r"(0x2C002C00u), "r"(0xD480D480u));  // / 16 - 72
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t u = i ? w >> 8 : w;
+      uint32_t lo, hi;
+      asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(lo) : "r"(u), "r"(k.lo), "r"(k.exp));  // u & mask | exp
+      asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(hi) : "r"(u), "r"(k.hi), "r"(k.exp));
+      asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(v[2 * i]) : "r"(lo), "r"(0x64086408u));                          // 1032
+      asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(v[2 * i + 1]) : "r"(hi), "r"(0x2C002C00u), "r"(0xD480D480u));  // / 16 - 72
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t u;
+      asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(u) : "r"(w >> (4 * i)), "r"(k.lo), "r"(k.exp));
+      asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(v[i]) : "r"(u), "r"(0x43084308u));  // 136
+    }
   }
 }
 
@@ -184,7 +197,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearParams 
     griddep_wait();
     // B fragments: x[b][2j + e][m] are columns 4e..4e+3 of word j for token 8m + lane / 4
     uint32_t x[NB][8][MT][2];
-    float back[MT][2];  // 1 / the power of two, for tokens 8m + 2 (lane % 4) + 0, 1
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       const int t = m * 8 + (lane >> 2);
@@ -199,31 +211,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearParams 
           x[b][2 * j][m][0] = v.x, x[b][2 * j][m][1] = v.y;
           x[b][2 * j + 1][m][0] = v.z, x[b][2 * j + 1][m][1] = v.w;
         }
-      back[m][0] = back[m][1] = 1.f;
-      if constexpr (T::kExp != Fp16::kExp) {
-        uint32_t top = 0;  // as 16-bit magnitudes, two at a time
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) top = __vmaxu2(top, x[b][k][m][e] & 0x7FFF7FFFu);
-        top = __vmaxu2(top, __shfl_xor_sync(FULL, top, 1));
-        top = __vmaxu2(top, __shfl_xor_sync(FULL, top, 2));
-        const int exp = (int)(max(top & 0xFFFFu, top >> 16) >> 7) - 127, up = min(120, 14 - exp);
-        const float mul = __uint_as_float((uint32_t)(up + 127) << 23), inv = __uint_as_float((uint32_t)(127 - up) << 23);
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) x[b][k][m][e] = Fp16::pack(T::lo(x[b][k][m][e]) * mul, T::hi(x[b][k][m][e]) * mul);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) back[m][e] = __shfl_sync(FULL, inv, ((lane & 3) * 2 + e) * 4);
-      }
     }
 
-    const Bits bits;
+    const Bits<T> bits;
     const uint32_t sum_at = smem_addr(sums) + ((sub * TP * p.kw + ki) * OUT + lane * 2) * 4;
     int s = 0, buf = 0, done = 0;
     uint32_t phase = 0, sum_phase = 1;
@@ -240,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearParams 
         // two tiles are the upper and lower rows of the products (those behind t1 are not there: what they give is not read)
 #pragma unroll
         for (int h = 0; h < MT; ++h) {
-          float tot[MT][4] = {};  // rows lane / 4 of the first tile [0, 1] and of the second, tokens as in back
+          float tot[MT][4] = {};  // rows lane / 4 of the first tile [0, 1] and of the second, tokens 8m + 2 (lane % 4) + 0, 1
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
             const uint32_t at0 = at + (2 * h * NB + b) * BLK, at1 = at0 + NB * BLK;
@@ -257,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearParams 
                 for (int e = 0; e < 2; ++e) {
                   const uint32_t f[4] = {u[2 * e], v[2 * e], u[2 * e + 1], v[2 * e + 1]};
 #pragma unroll
-                  for (int m = 0; m < MT; ++m) mma16816<Fp16>(acc[m], f, x[b][2 * j + e][m][0], x[b][2 * j + e][m][1]);
+                  for (int m = 0; m < MT; ++m) mma16816<T>(acc[m], f, x[b][2 * j + e][m][0], x[b][2 * j + e][m][1]);
                 }
               }
               const uint32_t sc = kBlockCodes + (lane >> 2) * 2 * GPB + q * 2;
@@ -271,8 +261,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearParams 
           }
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
-            sts64(dst + m * 256, tot[m][0] * back[m][0], tot[m][1] * back[m][1]);
-            sts64(dst + m * 256 + p.kw * OUT * 4, tot[m][2] * back[m][0], tot[m][3] * back[m][1]);
+            sts64(dst + m * 256, tot[m][0], tot[m][1]);
+            sts64(dst + m * 256 + p.kw * OUT * 4, tot[m][2], tot[m][3]);
           }
           dst += 2 * p.kw * OUT * 4;
         }

@@ -13,8 +13,8 @@
 // two took as long (100000 rows, 32 tokens: 109 us for 108), so it is the products: about 100 cycles for each 16 columns, whose A comes from tensor
 // memory, however few tokens there are.
 // So 16 tokens are better off with linear.cu's kernel, and groups of 32 or 64, whose D would not all fit, at any number.  us, here / there, groups of 128:
-//   8192 x 6144    16 tokens 20.1 / 12.9   24 19.5 / 24.9   64 21.6 / 49.7   128 42.4 / 98.9
-//   100000 x 6144  16 tokens 109 / 78      24 108 / 156     64 118 / 309     128 235 / 617
+//   8192 x 6144    16 tokens 20.1 / 12.7   24 19.5 / 23.4   64 21.5 / 47.8   128 42.2 / 95.2
+//   100000 x 6144  16 tokens 109 / 79      24 107 / 156     64 118 / 313     128 235 / 626
 // A start at another column for each CTA, against all asking for the same x at once, changed nothing.
 #include "attn_tc.cuh"
 #include "coli_linear.h"
