@@ -45,7 +45,7 @@ def lib():
 
 def quantize(w, group=128, dtype=torch.bfloat16, stream=None):
     """w float32 [rows, cols] on the current device -> codes uint8 [rows, cols/2], scales of dtype [rows, cols/group], in memory
-    of the current stream.  coli_linear_quantize"""
+    of `stream` (the current one by default), for others to read once they have waited for it.  coli_linear_quantize"""
     if w.dtype is not torch.float32 or w.dim() != 2 or not w.is_contiguous() or not w.is_cuda or \
             w.device.index != torch.cuda.current_device():
         raise ValueError("w: contiguous float32 [rows, cols] on the current device")
@@ -54,10 +54,15 @@ def quantize(w, group=128, dtype=torch.bfloat16, stream=None):
     if group not in (32, 64, 128) or w.shape[1] % group or w.shape[1] == 0:
         raise ValueError("groups of 32, 64 or 128 columns divide the columns")
     rows, cols = w.shape
-    packed = torch.empty((rows, cols // 2), dtype=torch.uint8, device=w.device)
-    scales = torch.empty((rows, cols // group), dtype=dtype, device=w.device)
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):  # a handle; 0 and 1 are the default stream's
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) > 1 else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):  # None: nothing changes
+        packed = torch.empty((rows, cols // 2), dtype=torch.uint8, device=w.device)
+        scales = torch.empty((rows, cols // group), dtype=dtype, device=w.device)
     coli._check(lib().coli_linear_quantize(w.data_ptr(), rows, cols, group, DTYPES[dtype], packed.data_ptr(), scales.data_ptr(),
                                            coli._stream(stream)), "coli_linear_quantize")
+    if stream is not None:  # kept from reuse there until the current stream is done with them
+        packed.record_stream(torch.cuda.current_stream()), scales.record_stream(torch.cuda.current_stream())
     return packed, scales
 
 

@@ -44,3 +44,30 @@ def test_groups_of_different_sizes(rows, cols, group, tokens):
     x[:, group:2 * group] *= 2.0 ** 45
     check(lin.forward(x), x, expanded(packed, scales), group, BF)
     assert lin.status() == 0
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_quantize_on_another_stream(handle):
+    """its outputs' memory is not what the current stream still has work queued on, nor is it given to their stream again while
+    the current one reads it"""
+    w = torch.randn((512, 512), device="cuda")
+    want, side = linear.quantize(w, 64, HF), torch.cuda.Stream()
+    assert all(torch.equal(a, b) for a, b in zip(linear.quantize(w, 64, HF, stream=0), want))
+    torch.cuda.synchronize()
+    old = [torch.empty_like(t) for t in want]
+    at = [t.data_ptr() for t in old]
+    torch.cuda._sleep(200_000_000)
+    for t in old:
+        t.fill_(5)
+    del old, t  # free for the current stream's next tensors, and the fills are yet to come
+    got = linear.quantize(w, 64, HF, stream=side.cuda_stream if handle else side)
+    assert not {t.data_ptr() for t in got} & set(at)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    torch.cuda._sleep(200_000_000)
+    copy = [t.clone() for t in got]
+    del got
+    with torch.cuda.stream(side):
+        other = [torch.empty_like(t).fill_(9) for t in want]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(copy, want)) and all((t == 9).all() for t in other)
