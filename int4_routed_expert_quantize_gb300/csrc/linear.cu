@@ -9,7 +9,7 @@
 // makes x has ended.
 //
 // A warp has NB blocks of every tile that it takes, the same ones each time, 2 or 4 tiles a step: two tiles' weights are the A operand of
-// mma.sync, x of 8 or 2 x 8 tokens is B.  A CTA has a range of tiles, so the SMs end together to within 8 rows.  Columns beyond what
+// mma.sync, x of 8 or 2 x 8 tokens is B.  A CTA has a range of tiles, so the CTAs end together to within 8 rows.  Columns beyond what
 // the registers of one CTA hold (48 blocks at 8 tokens, 24 at 16) are split over a cluster, whose CTAs send their sums to the first one.
 //
 // Measured, groups of 128, bf16: 8192 x 6144 for one token 8.4 us, of which 3.3 are launch and prologue; from 20000 to 40000 rows 11.8 us
@@ -27,9 +27,19 @@
 
 using namespace coli;
 
+namespace {
+
+struct Room {
+  int num_sms = 0;
+  int clusters[2] = {};  // that run at once, of calls of up to 8 and up to 16 tokens; 0: not asked yet
+};
+
+}  // namespace
+
 struct coli_linear {
   coli_linear_config cfg{};
-  int device = 0, num_sms = 0, tiles = 0, blocks = 0;  // of 8 rows; of 128 columns
+  int device = 0, tiles = 0, blocks = 0;  // of 8 rows; of 128 columns
+  Room room;
   bool loaded = false;
   uint8_t* store = nullptr;
   int32_t* status = nullptr;
@@ -425,16 +435,22 @@ int check_device(int device) {
   return dev == device ? COLI_OK : COLI_ESTATE;
 }
 
+// ask: nothing is launched; the clusters that run at once go there
 template <class T, int G, int MT>
-cudaError_t launch(LinearParams p, int num_sms, cudaStream_t stream) {
+cudaError_t launch(LinearParams p, const Room& room, Room* ask, cudaStream_t stream) {
   constexpr int NB = 4 / MT, BLK = block_bytes(G), TP = step_tiles(MT);
   // the cluster: as few CTAs as hold x in registers
   int parts = (p.blocks + kProduct * NB - 1) / (kProduct * NB);
   p.part = (p.blocks + parts - 1) / parts;
   parts = (p.blocks + p.part - 1) / p.part;
+  // A range of tiles for each cluster that runs at once.  A cluster's CTAs, one an SM, sit in one of the GPU's processor clusters of up to
+  // 20 SMs, so that 152 SMs do not hold 152 / parts of them (of 3 46, of 6 23, of 8 15); one that waits for another to end takes as long
+  // again.  us with ranges for 152 / parts clusters / for those that fit: 16 tokens of 8192 x 8192 27.8 / 17.8, x 12288 34.2 / 19.2,
+  // x 24576 59.8 / 38.0, of 40000 x 8192 95 / 59; one of 40000 x 16384 144 / 87.
+  const int fit = room.clusters[MT - 1] ? room.clusters[MT - 1] : room.num_sms / parts;
   // The warps: as many of a tile's blocks each as keeps most of them busy (fewer warps a tile are fewer sums to add), several
   // steps' tiles at once where a tile takes few warps, while every cluster still gets some.
-  const int clusters = std::min(num_sms / parts, p.tiles), most = (p.tiles + clusters - 1) / clusters;
+  const int clusters = std::min(fit, p.tiles), most = (p.tiles + clusters - 1) / clusters;
   int best = -1, blocks = 1;
   for (int nb = 1; nb <= NB; ++nb) {
     const int kw = (p.part + nb - 1) / nb;
@@ -460,12 +476,13 @@ cudaError_t launch(LinearParams p, int num_sms, cudaStream_t stream) {
   attr[1].val.clusterDim.x = parts, attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = parts > 1 ? 2 : 1;
-  if constexpr (MT == 1) {
-    if (blocks == 4) return cudaLaunchKernelEx(&cfg, linear_kernel<T, G, 1, 4>, p);
-    if (blocks == 3) return cudaLaunchKernelEx(&cfg, linear_kernel<T, G, 1, 3>, p);
-  }
-  return blocks == 2 ? cudaLaunchKernelEx(&cfg, linear_kernel<T, G, MT, 2>, p)
-                     : cudaLaunchKernelEx(&cfg, linear_kernel<T, G, MT, 1>, p);
+  void (*kernel)(LinearParams) = blocks == 2 ? linear_kernel<T, G, MT, 2> : linear_kernel<T, G, MT, 1>;
+  if constexpr (MT == 1) kernel = blocks == 4 ? linear_kernel<T, G, 1, 4> : blocks == 3 ? linear_kernel<T, G, 1, 3> : kernel;
+  if (!ask) return cudaLaunchKernelEx(&cfg, kernel, p);
+  int n = room.num_sms;
+  const cudaError_t e = parts > 1 ? cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) : cudaSuccess;
+  ask->clusters[MT - 1] = std::max(1, std::min(n, room.num_sms / parts));
+  return e;
 }
 
 template <class T, int G, int MT, int NB>
@@ -474,16 +491,35 @@ cudaError_t configure() {
 }
 
 template <class T, int G>
-cudaError_t launch_tokens(const LinearParams& p, bool few, int num_sms, cudaStream_t stream) {
+cudaError_t launch_tokens(const LinearParams& p, bool few, const Room& room, Room* ask, cudaStream_t stream) {
   // (x of 16 tokens and more columns than a cluster holds: 8 tokens at a time)
-  return few || p.blocks > kMaxParts * kProduct * 2 ? launch<T, G, 1>(p, num_sms, stream)
-                                                                 : launch<T, G, 2>(p, num_sms, stream);
+  return few || p.blocks > kMaxParts * kProduct * 2 ? launch<T, G, 1>(p, room, ask, stream) : launch<T, G, 2>(p, room, ask, stream);
 }
 template <class T>
-cudaError_t launch_group(const LinearParams& p, int group, bool few, int num_sms, cudaStream_t stream) {
-  return group == 128  ? launch_tokens<T, 128>(p, few, num_sms, stream)
-         : group == 64 ? launch_tokens<T, 64>(p, few, num_sms, stream)
-                       : launch_tokens<T, 32>(p, few, num_sms, stream);
+cudaError_t launch_group(const LinearParams& p, int group, bool few, const Room& room, Room* ask, cudaStream_t stream) {
+  return group == 128  ? launch_tokens<T, 128>(p, few, room, ask, stream)
+         : group == 64 ? launch_tokens<T, 64>(p, few, room, ask, stream)
+                       : launch_tokens<T, 32>(p, few, room, ask, stream);
+}
+cudaError_t launch_type(const LinearParams& p, const coli_linear_config& c, bool few, const Room& room, Room* ask, cudaStream_t stream) {
+  return c.dtype == COLI_ATTN_BF16 ? launch_group<Bf16>(p, c.group, few, room, ask, stream)
+                                   : launch_group<Fp16>(p, c.group, few, room, ask, stream);
+}
+
+LinearParams params(const coli_linear* h) {
+  LinearParams p = {};
+  p.store = h->store, p.status = h->status;
+  p.rows = h->cfg.rows, p.cols = h->cfg.cols, p.tiles = h->tiles, p.blocks = h->blocks;
+  return p;
+}
+
+// how many clusters of the handle's shape run at once
+cudaError_t ask_room(coli_linear* h) {
+  LinearParams p = params(h);
+  p.n_tokens = 8;
+  const Room room = h->room;
+  const cudaError_t e = launch_type(p, h->cfg, true, room, &h->room, nullptr);
+  return e == cudaSuccess ? launch_type(p, h->cfg, false, room, &h->room, nullptr) : e;
 }
 
 cudaError_t configure_device() {
@@ -528,8 +564,8 @@ extern "C" int coli_linear_create(const coli_linear_config* cfg, coli_linear** o
   h->tiles = (c.rows + 7) / 8, h->blocks = (c.cols + 127) / 128;
   int rc = COLI_OK;
   if (cudaGetDevice(&h->device) != cudaSuccess ||
-      cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess ||
-      configure_device() != cudaSuccess || configure_linear_many() != cudaSuccess)
+      cudaDeviceGetAttribute(&h->room.num_sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess ||
+      configure_device() != cudaSuccess || configure_linear_many() != cudaSuccess || ask_room(h) != cudaSuccess)
     rc = COLI_ECUDA;
   if (!rc) {
     const size_t size = (size_t)h->tiles * h->blocks * block_bytes(c.group);  // a multiple of 16
@@ -585,19 +621,16 @@ extern "C" int coli_linear_forward(const coli_linear* h, const void* x, int64_t 
     return COLI_EINVAL;
   const int rc = check_device(h->device);
   if (rc) return rc;
-  LinearParams p = {};
-  p.store = h->store, p.x_stride = x_stride, p.y_stride = y_stride;
-  p.rows = c.rows, p.cols = c.cols, p.tiles = h->tiles, p.blocks = h->blocks;
-  p.status = h->status;
+  LinearParams p = params(h);
+  p.x_stride = x_stride, p.y_stride = y_stride;
   cudaError_t e = cudaSuccess;
   for (int at = 0; at < n_tokens && e == cudaSuccess; at += kLaunchTokens) {
     p.x = static_cast<const uint16_t*>(x) + at * x_stride, p.y = static_cast<uint16_t*>(y) + at * y_stride;
     p.n_tokens = std::min(n_tokens - at, kLaunchTokens);
     if (n_tokens > 16 && c.group == 128)  // both sides' times: linear_many.cu
-      e = launch_linear_many(p, c.dtype, h->num_sms, (cudaStream_t)stream);
+      e = launch_linear_many(p, c.dtype, h->room.num_sms, (cudaStream_t)stream);
     else
-      e = c.dtype == COLI_ATTN_BF16 ? launch_group<Bf16>(p, c.group, n_tokens <= 8, h->num_sms, (cudaStream_t)stream)
-                                    : launch_group<Fp16>(p, c.group, n_tokens <= 8, h->num_sms, (cudaStream_t)stream);
+      e = launch_type(p, c, n_tokens <= 8, h->room, nullptr, (cudaStream_t)stream);
   }
   return e == cudaSuccess ? COLI_OK : COLI_ECUDA;
 }

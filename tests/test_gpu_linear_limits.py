@@ -17,6 +17,23 @@ def _cuda():
     torch.cuda.set_device(0)
 
 
+def microseconds(rows, cols, tokens, handles=6, calls=60):
+    """a call among others, with weights that are not in the L2"""
+    lins = [linear.Int4Linear(*weights(rows, cols, 128, BF, i), max_tokens=tokens) for i in range(handles)]
+    x = torch.randn((tokens, cols), device="cuda").to(BF)
+    y = torch.empty((tokens, rows), dtype=BF, device="cuda")
+    times = []
+    for _ in range(6):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        for i in range(calls):
+            lins[i % handles].forward(x, out=y)
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b) / calls * 1e3)
+    return min(times[1:])
+
+
 @pytest.mark.parametrize("tokens", [1, 8, 12, 16, 20, 40])
 @pytest.mark.parametrize("rows,cols,group", [(33, 384, 128), (40, 640, 64), (9, 1184, 32), (200, 6144, 128), (24, 16384, 64)])
 def test_outlier_at_codes_of_zero(rows, cols, group, tokens):
@@ -44,6 +61,12 @@ def test_groups_of_different_sizes(rows, cols, group, tokens):
     x[:, group:2 * group] *= 2.0 ** 45
     check(lin.forward(x), x, expanded(packed, scales), group, BF)
     assert lin.status() == 0
+
+
+def test_clusters_run_at_once():
+    """columns that take clusters of three CTAs cost their bytes, 1.33 times those of two, and not a second round of clusters (2.2
+    times; 1.4 without one)"""
+    assert microseconds(8192, 8192, 16) < 1.8 * microseconds(8192, 6144, 16)
 
 
 @pytest.mark.parametrize("handle", [False, True])
