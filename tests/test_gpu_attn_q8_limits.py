@@ -149,3 +149,25 @@ def test_every_code_is_exact(new, dt, kind):
     # equal weights: their fp16 roundings and the sum's cancel to within 2^-11 + 2^-20
     assert ((out.double() - m[:, None]).abs() <= (u + 2.0 ** -11 + 2.0 ** -20) * m[:, None].abs()).all()
     assert s.eng.status() == 0
+
+
+@pytest.mark.parametrize("kind", [I8, E4])
+@pytest.mark.parametrize("news", [[1, 1], [1, 70]])
+@pytest.mark.parametrize("bad", [-1, 10 ** 6])
+def test_a_page_out_of_range_reads_as_zeros(bad, news, kind):
+    """a spare page of zeros, which is in no table, stands in for it in the reference"""
+    s = Setup(news, [100, 200], 8, 2, 64, 32, BF, kind)
+    spare = (set(range(s.kc.shape[0])) - {int(x) for x in s.table.flatten() if x >= 0}).pop()
+    s.kc.view(torch.uint8)[spare], s.vc.view(torch.uint8)[spare], s.ks[spare], s.vs[spare] = 0, 0, 0, 0
+    whole = s.reference()
+    for b, page in ((0, 1), (1, 0), (1, 3)):
+        keep = int(s.table[b, page])
+        s.table[b, page] = bad
+        out, lse = call(s)
+        assert s.eng.status() == -1 and s.eng.status() == 0
+        s.table[b, page] = spare
+        ref = s.reference()
+        s.check(out, lse, ref)
+        other = slice(s.start[1 - b], s.start[2 - b])  # the other sequence's rows are those of before
+        assert torch.equal(ref[0][other], whole[0][other])
+        s.table[b, page] = keep
