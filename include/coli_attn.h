@@ -29,8 +29,9 @@
  * values of one token (rotated, in fp32), append stores scale = m / top and code = top * x / m rounded to the nearest, ties to
  * even: top = 127 for int8, 448 for e4m3.  A head that holds an infinity or NaN is stored as scale NaN and codes 0, so it
  * reads back as NaN; m = 0 is scale 0.  window computes with code * scale: the codes go into the products as they are (exact),
- * scores are multiplied by the key's scale in fp32, weights by the value's scale (relative to the largest one that the row has
- * seen, to within 8) before they are rounded to fp16 for their product with the codes.  A row that sees an infinite or NaN scale gets NaN.
+ * scores are multiplied by the key's scale in fp32, weights by the value's scale before they are rounded to fp16 for their product with
+ * the codes, in units in which the row's largest such product so far is 1 to 2^11 (values' scales of 0, and of 2^-80 to 2^100;
+ * beyond, weights lose bits).  A row that sees an infinite or NaN scale gets NaN.
  * e4m3's codes 0x7F and 0xFF, which append never stores, count as +480 and -480.
  *
  * Conventions are those of coli_moe.h: every call returns COLI_OK or a negative status; device

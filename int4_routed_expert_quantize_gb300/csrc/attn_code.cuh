@@ -61,6 +61,12 @@ struct Code<COLI_ATTN_CODE_E4M3> {
 // A finite scale as it is, any other as NaN: the sign of a score would make an infinite one's weight 0.
 __device__ __forceinline__ float spoil(float scale) { return fmaf(scale, 0.f, scale); }
 
+// log2 |value scale|; not below -80, so that weights of values of (next to) 0 keep their sum in fp32's range
+__device__ __forceinline__ float scale_log(float scale) {
+  const float l = __log2f(fabsf(scale));
+  return l < -80.f ? -80.f : l;  // NaN stays
+}
+
 // One warp fills the stage of a KT-key tile: the boxes that hold keys some row of the block sees, lane i box i: the keys' codes
 // to `keys`, the values' to `vals`, their scales to scales[0..KT-1] and scales[KT..2KT-1].  A page whose id is out of range
 // reads as zeros, scales included, and is reported.

@@ -4,26 +4,26 @@
 // tile's keys for 16 rows each, the list of all units' tiles is cut into equal stretches.
 //
 // The codes are widened on their way from shared memory to mma.sync, which is exact: keys to the queries' type, values to fp16, the
-// weights' type.  Weights: 2^(s_j - m) vs_j / g, where m follows the row's maximum to within 2^8 and g is the largest |vs| that the
-// row has seen, so that they do not run out of fp16's range, and what a row does not see has no part in it; they are rounded to fp16
-// once.  m and g rarely grow, and the accumulators are rescaled only then.
+// weights' type.  Weights: 2^(s_j - m) vs_j, where m follows the row's largest s_j + log2 |vs_j| to within 2^8, so that they do not run
+// out of fp16's range, and neither what a row does not see nor a large value without weight has a part in it; they are rounded to fp16
+// once.  m rarely grows, and the accumulators are rescaled only then.
 //
 // A lane's codes of a key are contiguous in shared memory (the order of the products' inner dimension is free as long as the
 // queries follow it), and a 16-bit transposing load of the values brings two columns' codes of a key in one half, so
 // both operands take one widening of a word for four codes: to fp16 5 instructions (int8) or 7 (e4m3), to bf16 8 or 9.
 //
 // Measured, with the combine kernel: 64 sequences' next tokens, 6 query heads a key head, 8 key heads of 128, windows of 4096 keys: 556 MB
-// in bf16 with int8 118.6 us, 4.7 TB/s, with e4m3 125.6, in fp16 110.6 and 121.7; the copies alone take 97 (pages of 8 KB a head in random
-// order).  Keys as fp16 for bf16 queries too took 112 (and 0.5 us more for one token), which holds only queries whose values are within
+// in bf16 with int8 117.3 us, 4.7 TB/s, with e4m3 122.2, in fp16 105.9 and 121.0; the copies alone take 97 (pages of 8 KB a head in random
+// order).  Keys as fp16 for bf16 queries too took 6 us less (and 0.5 us more for one token), which holds only queries whose values are within
 // 2^31 of one another.  Beside 111 of an earlier form: three CTAs an SM (128 registers) 112, 32 keys a warp of every other tile 110 and
 // 11.4 instead of 10.1 for one token, the queries' fragments in registers 141.
-#include <float.h>
-
 #include "attn_code.cuh"
 
 namespace coli {
 
 namespace {
+
+constexpr float kSlack = 8.f;  // of a row's m
 
 template <int D, int RG>
 struct QSplitCfg {
@@ -43,7 +43,6 @@ struct QSplitCfg {
       stages * 2 * tile_bytes + scale_bytes + merge_bytes + 2 * stages * 8 + (int)sizeof(UnitRing) + 24;
 };
 
-constexpr float kNoScale = 0x1p-100f, kNoScaleLog = -100.f;  // g before the first key
 
 // 16-byte chunk `ch` of row `row` of a code tile, as the tensor copies swizzle it: rows of 128 bytes by row % 8, of 64
 // bytes by row / 2 % 4
@@ -68,17 +67,15 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // What a thread keeps of its two rows (lane / 4 and 8 more).
 template <int D>
 struct Rows {
-  float rs;           // score of a product of codes and q, times log2(e)
-  float slack;        // 8 in units of rs, finite: -inf + inf would never let the first keys in
   float o[D / 8][4];  // columns 16 c + 4 (lane % 4) + 0, 2 in o[2c], 1, 3 in o[2c + 1]
-  float ref[2], g[2], lg[2], sum[2];  // ref in units of rs; lg = log2(g); o and sum are in units of 2^(ref rs) g
+  float m[2], sum[2];  // o and sum are in units of 2^m
 };
 
-// 16 rows at positions pos x kw keys of one tile for one warp; q: its rows' fragments, ks: the keys' codes (the values' D * 64 bytes
+// 16 rows at positions pos x kw keys of one tile for one warp; rs: score of a product of codes and q, times log2(e); q: its rows' fragments, ks: the keys' codes (the values' D * 64 bytes
 // further), all shared-memory addresses.  Step k of the fragments: of the D / 4 values from (lane % 4) D / 4 on, values 4k and 4k + 2,
 // 4k + 1 and 4k + 3
 template <class T, int CODE, int D, int RG, bool Masked>
-__device__ __forceinline__ void tile_step(const AttnParams& p, uint32_t q, uint32_t ks, const float* scales, int key0,
+__device__ __forceinline__ void tile_step(const AttnParams& p, float rs, uint32_t q, uint32_t ks, const float* scales, int key0,
                                           const int (&pos)[2], Rows<D>& r, int lane) {
   using C = QSplitCfg<D, RG>;
   constexpr int NT = C::kw / 8;
@@ -115,50 +112,48 @@ __device__ __forceinline__ void tile_step(const AttnParams& p, uint32_t q, uint3
       for (int i = 0; i < 4; ++i)
         if (sees(p, pos[i >> 1], key0 + n * 8 + c2 + (i & 1))) see |= 1u << (4 * n + i);
   }
-  float vs[NT][2], m[2] = {-INFINITY, -INFINITY}, gm[2] = {0.f, 0.f};
+  float vs[NT][2], m[2] = {-INFINITY, -INFINITY};
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    float2 k2 = *reinterpret_cast<const float2*>(scales + kloc + n * 8 + c2);
-    k2.x = spoil(k2.x), k2.y = spoil(k2.y);
+    const float2 k2 = *reinterpret_cast<const float2*>(scales + kloc + n * 8 + c2);
     const float2 v2 = *reinterpret_cast<const float2*>(scales + kSplitKeys + kloc + n * 8 + c2);
     vs[n][0] = v2.x, vs[n][1] = v2.y;
+    const float k[2] = {spoil(k2.x) * rs, spoil(k2.y) * rs}, lv[2] = {scale_log(v2.x), scale_log(v2.y)};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      s[n][i] *= i & 1 ? k2.y : k2.x;
-      const bool in = !Masked || (see >> (4 * n + i) & 1);
-      if (!in) s[n][i] = -INFINITY;
-      m[i >> 1] = fmaxf(m[i >> 1], s[n][i]);
-      if (in) gm[i >> 1] = max_nan(gm[i >> 1], fabsf(vs[n][i & 1]));
+      s[n][i] *= k[i & 1];
+      if (Masked && !(see >> (4 * n + i) & 1)) s[n][i] = -INFINITY;
+      else m[i >> 1] = max_nan(m[i >> 1], s[n][i] + lv[i & 1]);
     }
   }
-  // (a NaN among the values' scales is above any g)
-  const bool grow = m[0] > r.ref[0] + r.slack || m[1] > r.ref[1] + r.slack || !(gm[0] <= r.g[0]) || !(gm[1] <= r.g[1]);
-  if (__any_sync(FULL, grow)) {
+  // (a NaN is above any m)
+  if (__any_sync(FULL, !(m[0] <= r.m[0] + kSlack) || !(m[1] <= r.m[1] + kSlack))) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      float a = fmaxf(m[i], r.ref[i]), b = max_nan(gm[i], r.g[i]);
-      a = fmaxf(a, __shfl_xor_sync(FULL, a, 1)), b = max_nan(b, __shfl_xor_sync(FULL, b, 1));
-      a = fmaxf(a, __shfl_xor_sync(FULL, a, 2)), b = max_nan(b, __shfl_xor_sync(FULL, b, 2));
+      float a = max_nan(m[i], r.m[i]);
+      a = max_nan(a, __shfl_xor_sync(FULL, a, 1));
+      a = max_nan(a, __shfl_xor_sync(FULL, a, 2));
       // A row moves when its own keys ask for it, whatever the others of the warp do: rows without a token see slots that nobody has
       // asked for, and a row's roundings must not depend on those.
-      if (!(a > r.ref[i] + r.slack || !(b <= r.g[i]))) continue;
-      if (!(b < INFINITY)) b = INFINITY;
-      const float fix = a == -INFINITY ? 1.f : ex2((r.ref[i] - a) * r.rs) * (r.g[i] / b);  // ref = -inf: 0, and o, sum are 0
-      r.ref[i] = a, r.g[i] = b, r.lg[i] = log2f(b);
-      // (with an infinite g all weights are 0 or NaN, and a part whose sum is 0, or whose weight is, would be left out of the row)
-      r.sum[i] = b == INFINITY ? NAN : r.sum[i] * fix;
+      if (a <= r.m[i] + kSlack) continue;
+      if (!(a < INFINITY)) {  // a scale or score that is not finite
+        r.sum[i] = NAN;
+        continue;
+      }
+      const float fix = ex2(r.m[i] - a);  // m = -inf: 0, and o, sum are 0
+      r.m[i] = a, r.sum[i] *= fix;
 #pragma unroll
       for (int d = 0; d < D / 8; ++d) r.o[d][2 * i] *= fix, r.o[d][2 * i + 1] *= fix;
     }
   }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const float base = r.ref[i] == -INFINITY ? 0.f : fmaf(-r.ref[i], r.rs, -r.lg[i]);
+    const float base = r.m[i] == -INFINITY ? 0.f : r.m[i];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const float e = ex2(fmaf(s[n][2 * i + k], r.rs, base));
+        const float e = ex2(s[n][2 * i + k] - base);
         r.sum[i] += e;  // this thread's share of the row; joined at the end
         float w = e * vs[n][k];
         if (Masked && !(see >> (4 * n + 2 * i + k) & 1)) w = 0.f;  // (its scale may be NaN)
@@ -185,7 +180,7 @@ __device__ __forceinline__ void tile_step(const AttnParams& p, uint32_t q, uint3
   }
 }
 
-// Buffer of a warp: H 8-column groups of its 16 rows in fragment order, then the rows' units (lg is ref rs + lg by then) and sums.
+// Buffer of a warp: H 8-column groups of its 16 rows in fragment order, then the rows' units and sums.
 template <int D, int H>
 __device__ __forceinline__ void hand_over(float* merge, int buffer, const Rows<D>& r, int first, int lane) {
   float* base = merge + buffer * (8 * D + 32);
@@ -195,8 +190,8 @@ __device__ __forceinline__ void hand_over(float* merge, int buffer, const Rows<D
     if ((d / H) * H == first) buf[(d % H) * 32 + lane] = make_float4(r.o[d][0], r.o[d][1], r.o[d][2], r.o[d][3]);
   if ((lane & 3) == 0) {
     float2* ml = reinterpret_cast<float2*>(base + 8 * D);
-    ml[lane >> 2] = make_float2(r.lg[0], r.sum[0]);
-    ml[(lane >> 2) + 8] = make_float2(r.lg[1], r.sum[1]);
+    ml[lane >> 2] = make_float2(r.m[0], r.sum[0]);
+    ml[(lane >> 2) + 8] = make_float2(r.m[1], r.sum[1]);
   }
 }
 template <int D, int H>
@@ -208,10 +203,10 @@ __device__ __forceinline__ void take_over(const float* merge, int buffer, Rows<D
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const float2 other = ml[(lane >> 2) + i * 8];
-    const float m = fmaxf(r.lg[i], other.x), at = m == -INFINITY ? 0.f : m;
-    fa[i] = ex2(r.lg[i] - at);
+    const float m = fmaxf(r.m[i], other.x), at = m == -INFINITY ? 0.f : m;
+    fa[i] = ex2(r.m[i] - at);
     fb[i] = ex2(other.x - at);
-    r.lg[i] = m;
+    r.m[i] = m;
     r.sum[i] = r.sum[i] * fa[i] + other.y * fb[i];
   }
 #pragma unroll
@@ -317,8 +312,7 @@ __global__ void __launch_bounds__(QSplitCfg<D, RG>::threads, QSplitCfg<D, RG>::c
     int pos[2], tok[2];
     bool live[2];
     Rows<D> r;
-    r.rs = p.scale_log2 * Code<CODE>::unit;
-    r.slack = fminf(8.f / r.rs, FLT_MAX);
+    const float rs = p.scale_log2 * Code<CODE>::unit;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int row = row0 + (lane >> 2) + i * 8;
@@ -345,7 +339,7 @@ __global__ void __launch_bounds__(QSplitCfg<D, RG>::threads, QSplitCfg<D, RG>::c
         at[0] = __byte_perm(x[2 * k], x[2 * k + 1], 0x5410);
         at[2] = __byte_perm(x[2 * k], x[2 * k + 1], 0x7632);
       }
-      r.ref[i] = -INFINITY, r.sum[i] = 0.f, r.g[i] = kNoScale, r.lg[i] = kNoScaleLog;
+      r.m[i] = -INFINITY, r.sum[i] = 0.f;
     }
     if (!meet()) return;  // all fragments are there
     const uint32_t q_at = smem_addr(merge) + rg * (D / 16) * 512;
@@ -366,9 +360,9 @@ __global__ void __launch_bounds__(QSplitCfg<D, RG>::threads, QSplitCfg<D, RG>::c
         const float* sc = scales + sgi * 2 * kSplitKeys;
         const int key0 = u.tile(i) * kSplitKeys + kg * C::kw;
         if (all_see(p, w0, w1, key0, key0 + C::kw - 1))
-          tile_step<T, CODE, D, RG, false>(p, q_at, ks, sc, key0, pos, r, lane);
+          tile_step<T, CODE, D, RG, false>(p, rs, q_at, ks, sc, key0, pos, r, lane);
         else
-          tile_step<T, CODE, D, RG, true>(p, q_at, ks, sc, key0, pos, r, lane);
+          tile_step<T, CODE, D, RG, true>(p, rs, q_at, ks, sc, key0, pos, r, lane);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(empty + sgi);
@@ -377,7 +371,6 @@ __global__ void __launch_bounds__(QSplitCfg<D, RG>::threads, QSplitCfg<D, RG>::c
     for (int i = 0; i < 2; ++i) {
       r.sum[i] += __shfl_xor_sync(FULL, r.sum[i], 1);
       r.sum[i] += __shfl_xor_sync(FULL, r.sum[i], 2);
-      r.lg[i] = fmaf(r.ref[i], r.rs, r.lg[i]);  // -inf stays -inf
     }
     // Join the KG warps that share these rows.  Each step halves the columns a warp keeps: it hands the other
     // half to its partner and takes its own half's counterpart, so the last step leaves every warp
@@ -406,7 +399,7 @@ __global__ void __launch_bounds__(QSplitCfg<D, RG>::threads, QSplitCfg<D, RG>::c
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int row = row0 + (lane >> 2) + i * 8;
-      const float m2 = r.lg[i], unit = Code<CODE>::unit;
+      const float m2 = r.m[i], unit = Code<CODE>::unit;
       const int hq = u.head * p.group + row - tok[i] * p.group;
       if (whole && !live[i]) continue;
       if (whole) {

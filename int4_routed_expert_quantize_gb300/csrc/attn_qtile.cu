@@ -9,13 +9,13 @@
 //   warp 12          issues every product; warp 13 every copy
 //
 // The codes are exact in the products: keys in the queries' type, values in fp16.  A score is multiplied by its key's scale in fp32; a
-// weight is 2^(s - m) vs / g, with g the largest |vs| that the row has seen, to within 8, so that it is below 2^11 and rounds to fp16 well.  1 / g
-// is part of the exponent (the row's sum and output are in the same unit, which cancels), m and g move rarely, and the output in
-// tensor memory is rescaled only then.  So a tile's scores become exponents in one step, t = acc ks - (m + log2 g), and a tile in which some
-// t is too large is the exception that moves m and g.  What a row does not see has weight 0; codes are always finite, and values' scales that are not
-// become 0 and a bit that spoils the sums of the rows that see them, so nothing is computed again here.
+// weight is 2^(s - m) vs, with m the row's largest s + log2 |vs|, to within 11, so that it is at most 2^11 and rounds to fp16 well.
+// m moves rarely, and the output in tensor memory is rescaled only then.  So a tile's scores become exponents in one step, t = acc ks - m,
+// and a tile whose largest t and largest |vs| could make too large a weight is the exception in which the row looks for its largest t + log2 |vs|.
+// What a row does not see has weight 0; codes are always finite, and values' scales that are not become 0 and a bit that spoils the
+// sums of the rows that see them, so nothing is computed again here.
 //
-// Measured, with the combine kernel: 8192 tokens, window 4096, 48 query and 8 key heads of 128, int8: 831 us (0.75 PFLOP/s; 450 over a 16-bit cache).  A
+// Measured, with the combine kernel: 8192 tokens, window 4096, 48 query and 8 key heads of 128, int8: 839 us (0.74 PFLOP/s; 450 over a 16-bit cache), e4m3 769.  A
 // round of both row tiles takes 6300 cycles, the products of it 2050: they wait for weights, whose softmax takes 4000.  Two threads a row took 930,
 // a second pass over tensor memory instead of 128 registers 1047, one pass over 64 keys and another where m moves 828, four rows a thread 860.
 //
@@ -31,12 +31,12 @@ namespace coli {
 namespace {
 
 constexpr int kThreadsQTile = 16 * 32;
-constexpr float kNoScale = 0x1p-100f, kNoScaleLog = -100.f;  // g before the first key
-constexpr float kSlack = 8.f;  // |vs| / g that weights have room for: they stay below 2^11
+constexpr float kRoom = 11.f;  // log2 of the largest weight
 
 struct TileScales {
   float keys[kTileKeys], values[kTileKeys];
-  float top[4];     // of 32 keys each: the largest |value scale|
+  float logs[kTileKeys];  // scale_log of the values'
+  float top[4];     // of 32 keys each: the largest of these
   uint32_t bad[4];  // and which of them were not finite
 };
 
@@ -356,14 +356,13 @@ __global__ void __launch_bounds__(kThreadsQTile, 1)
           if (!(i & 1)) {  // both scales have come with the keys
             scales[slot].keys[row] = spoil(scales[slot].keys[row]) * rs;
             float* value = scales[slot].values + row;
-            float top = fabsf(*value);
-            const bool bad = !(top < INFINITY);
-            if (bad) *value = top = 0.f;
-            top = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(top)));
+            float v = fabsf(*value);
+            const bool bad = !(v < INFINITY);
+            if (bad) *value = v = 0.f;
+            scales[slot].logs[row] = scale_log(v);
+            const float top = scale_log(__uint_as_float(__reduce_max_sync(FULL, __float_as_uint(v))));
             const uint32_t which = __ballot_sync(FULL, bad);
-            if (lane == 0) {
-              scales[slot].top[warp - 8] = top, scales[slot].bad[warp - 8] = which;
-            }
+            if (lane == 0) scales[slot].top[warp - 8] = top, scales[slot].bad[warp - 8] = which;
             __syncwarp();
             if (lane == 0) mbar_arrive(sc_full + slot);
             if (++slot == NSC) slot = 0;
@@ -400,8 +399,8 @@ __global__ void __launch_bounds__(kThreadsQTile, 1)
       }
       const bool whole = u.flags & kWhole;
       const int pa = u.p0 + s * half_tokens, pb = pa + nt - 1, pos = pa + tok;  // the row tile's positions, the row's
-      // -(m + log2 g); the t from which the row needs another m: 8 - log2 g, or -inf before its first key
-      float off = 0.f, limit = -INFINITY, g = kNoScale, sum0 = 0.f, sum1 = 0.f;
+      // -m; the t + log2 |vs| from which the row needs another m: kRoom, or -inf before its first key
+      float off = 0.f, limit = -INFINITY, sum0 = 0.f, sum1 = 0.f;
       bool ok = true;
 #pragma unroll 1
       for (int i = u.i0; i < u.i1; ++i) {
@@ -422,22 +421,16 @@ __global__ void __launch_bounds__(kThreadsQTile, 1)
         float m0 = -INFINITY, m1 = m0, m2 = m0, m3 = m0;
         const bool masked = !all_see(p, pa, pb, j0, j0 + kTileKeys - 1);
         const int hi = pos - j0, lo = pos - p.window - j0, sk = p.sinks - j0;
-        // What the values' scales ask of the row: the tile's largest |vs|, a bit for each that is not finite.  Which of them the row sees
-        // counts only where they ask for something.
+        // the tile's largest log2 |vs|, and whether the row sees a value's scale that is not finite
         const float4 tops = *reinterpret_cast<const float4*>(sc.top);
         const uint4 bads = *reinterpret_cast<const uint4*>(sc.bad);
-        float gm = fmaxf(fmaxf(tops.x, tops.y), fmaxf(tops.z, tops.w));
+        const float lv = fmaxf(fmaxf(tops.x, tops.y), fmaxf(tops.z, tops.w));
         bool spoilt = (bads.x | bads.y | bads.z | bads.w) != 0;
-        if (masked && (gm > kSlack * g || spoilt)) {
-          gm = 0.f, spoilt = false;
+        if (masked && spoilt) {
+          spoilt = false;
 #pragma unroll 1
-          for (int c = 0; c < 128; c += 32) {
-            const uint32_t see = low_bits(hi + 1 - c) & (~low_bits(lo + 1 - c) | low_bits(sk - c));
-            spoilt |= (sc.bad[c >> 5] & see) != 0;
-#pragma unroll 4
-            for (int k = 0; k < 32; ++k)
-              if (see >> k & 1) gm = fmaxf(gm, fabsf(vs[c + k]));
-          }
+          for (int c = 0; c < 128; c += 32)
+            spoilt |= (sc.bad[c >> 5] & low_bits(hi + 1 - c) & (~low_bits(lo + 1 - c) | low_bits(sk - c))) != 0;
         }
 #pragma unroll
         for (int c = 0; c < 128; c += 32) {
@@ -466,20 +459,23 @@ __global__ void __launch_bounds__(kThreadsQTile, 1)
         }
         const float top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
         if (spoilt) sum0 = NAN;
-        const bool grow = top > limit || gm > kSlack * g;
+        const bool grow = top + lv > limit;
         if (__any_sync(FULL, grow)) {
-          const bool begun = limit != -INFINITY;
+          float u0 = -INFINITY, u1 = u0;  // the largest t + log2 |vs|
+#pragma unroll
+          for (int c = 0; c < 128; c += 4) {
+            float4 l = *reinterpret_cast<const float4*>(sc.logs + c);
+            add2_rn(x[c], x[c + 1], l.x, l.y);
+            add2_rn(x[c + 2], x[c + 3], l.z, l.w);
+            u0 = max3(u0, l.x, l.y);
+            u1 = max3(u1, l.z, l.w);
+          }
           float fix = 1.f, by = 0.f;  // by: added to the row's t
-          if (grow) {
-            const float to = gm > kSlack * g ? gm : g, lg = begun ? 8.f - limit : kNoScaleLog;
-            g = to;
-            if (top > limit || begun) {
-              const float up = !begun || top + lg > 8.f ? top + (begun ? lg : 0.f) : 0.f, now = log2f(to);  // m moves by `up`
-              by = begun ? lg - now - up : -up - now;
-              if (begun) fix = ex2(by);
-              off += by, limit = 8.f - now;
-              sum0 *= fix, sum1 *= fix;
-            }
+          if (fmaxf(u0, u1) > limit) {
+            by = -fmaxf(u0, u1);
+            if (limit == kRoom) fix = ex2(by);
+            off += by, limit = kRoom;
+            sum0 *= fix, sum1 *= fix;
           }
 #pragma unroll
           for (int c = 0; c < 128; c += 2) add2_rn(by, by, x[c], x[c + 1]);

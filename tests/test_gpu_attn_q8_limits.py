@@ -171,3 +171,27 @@ def test_a_page_out_of_range_reads_as_zeros(bad, news, kind):
         other = slice(s.start[1 - b], s.start[2 - b])  # the other sequence's rows are those of before
         assert torch.equal(ref[0][other], whole[0][other])
         s.table[b, page] = keep
+
+
+@pytest.mark.parametrize("kind", [I8, E4])
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("new", [1, 5, 40])
+@pytest.mark.parametrize("far", [20, 60])
+def test_values_of_no_weight_cost_no_bits(new, far, dt, kind):
+    """values 2^far times the others', at keys whose scores are 1000 below: what is lost of a weight is relative to the largest product of a
+    weight and its scale, so the third term of the bound has that in the place of the largest scale"""
+    s = Setup([new], [500], 4, 2, 64, 16, dt, kind)
+    s.q = s.q.abs() + 1
+    for j in (3, 200, 401, 455):  # the last ones in the tiles that only some of 40 rows see whole
+        pg, sl = place(s, 0, j)
+        s.kc.view(torch.uint8)[pg, :, sl] = torch.full((64,), -100.0 if kind is I8 else -448.0, device="cuda").to(kind).view(torch.uint8)
+        s.ks[pg, :, sl] = 2.0
+        s.vs[pg, :, sl] = 2.0 ** far
+    out, lse = call(s)
+    o, bound, ref_lse = s.reference()
+    for j in (3, 200, 401, 455):
+        pg, sl = place(s, 0, j)
+        s.vs[pg, :, sl] = 0.0
+    o2, bound2, _ = s.reference()
+    assert torch.equal(o, o2)  # no weight, in 64 bits too
+    s.check(out, lse, (o, bound2, ref_lse))
