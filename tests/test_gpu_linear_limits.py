@@ -94,3 +94,15 @@ def test_quantize_on_another_stream(handle):
         other = [torch.empty_like(t).fill_(9) for t in want]
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(copy, want)) and all((t == 9).all() for t in other)
+
+
+@pytest.mark.parametrize("rest", [1, 17, 40])
+def test_a_short_last_launch(rest):
+    """more tokens than one grid takes, with groups of 128: the last launch has few"""
+    packed, scales = weights(19, 256, 128, BF)
+    first = 8 * 65535
+    lin = linear.Int4Linear(packed, scales, max_tokens=1000000)
+    x = torch.randn((first + rest, 256), device="cuda").to(BF)
+    y = lin.forward(x)
+    check(y, x, expanded(packed, scales), 128, BF)
+    assert torch.equal(lin.forward(x[-17:]), y[-17:]) and lin.status() == 0
