@@ -13,7 +13,7 @@
 // both operands take one widening of a word for four codes: to fp16 5 instructions (int8) or 7 (e4m3), to bf16 8 or 9.
 //
 // Measured, with the combine kernel: 64 sequences' next tokens, 6 query heads a key head, 8 key heads of 128, windows of 4096 keys: 556 MB
-// in bf16 with int8 117.3 us, 4.7 TB/s, with e4m3 122.2, in fp16 105.9 and 121.0; the copies alone take 97 (pages of 8 KB a head in random
+// in bf16 with int8 117 us, 4.8 TB/s, with e4m3 122.2, in fp16 105.9 and 121.0; the copies alone take 97 (pages of 8 KB a head in random
 // order).  Keys as fp16 for bf16 queries too took 6 us less (and 0.5 us more for one token), which holds only queries whose values are within
 // 2^31 of one another.  Beside 111 of an earlier form: three CTAs an SM (128 registers) 112, 32 keys a warp of every other tile 110 and
 // 11.4 instead of 10.1 for one token, the queries' fragments in registers 141.

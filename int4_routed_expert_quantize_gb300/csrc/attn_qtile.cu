@@ -15,8 +15,8 @@
 // What a row does not see has weight 0; codes are always finite, and values' scales that are not become 0 and a bit that spoils the
 // sums of the rows that see them, so nothing is computed again here.
 //
-// Measured, with the combine kernel: 8192 tokens, window 4096, 48 query and 8 key heads of 128, int8: 839 us (0.74 PFLOP/s; 450 over a 16-bit cache), e4m3 769.  A
-// round of both row tiles takes 6300 cycles, the products of it 2050: they wait for weights, whose softmax takes 4000.  Two threads a row took 930,
+// Measured, with the combine kernel: 8192 tokens, window 4096, 48 query and 8 key heads of 128, int8: 838 us (0.74 PFLOP/s; 450 over a 16-bit cache), e4m3 769.  A
+// round of both row tiles takes 6300 cycles, the products of it 2050: they wait for weights, whose softmax takes 4000.  Beside 831 of an earlier form: two threads a row 930,
 // a second pass over tensor memory instead of 128 registers 1047, one pass over 64 keys and another where m moves 828, four rows a thread 860.
 //
 // The softmax loop is long straight code and shares the instruction cache with the other roles', so what only masked tiles need is

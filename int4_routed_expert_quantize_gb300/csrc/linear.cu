@@ -12,13 +12,14 @@
 // mma.sync, x of 8 or 2 x 8 tokens is B.  A CTA has a range of tiles, so the CTAs end together to within 8 rows.  Columns beyond what
 // the registers of one CTA hold (48 blocks at 8 tokens, 24 at 16) are split over a cluster, whose CTAs send their sums to the first one.
 //
-// Measured, groups of 128, bf16: 8192 x 6144 for one token 8.4 us, of which 3.3 are launch and prologue; from 20000 to 40000 rows 11.8 us
-// more, 5.4 TB/s (fp16 10.6, 6.0 TB/s; a copy reaches 6.79).  100000 x 6144 for 16 tokens 79 us (fp16 73), 4.0 TB/s: there the
+// Measured, groups of 128, bf16: 8192 x 6144 for one token 8.0 us, of which 3.3 are launch and prologue; from 20000 to 40000 rows 11.8 us
+// more, 5.4 TB/s (fp16 10.6, 6.0 TB/s; a copy reaches 6.79).  100000 x 6144 for 16 tokens 78.6 us (fp16 73), 4.1 TB/s: there the
 // instructions bound it.
 //
 // A code becomes a value of x's type exactly, so products are exact whatever the sizes of x; a group's sum is fp32, and its scale
 // multiplies it in fp32.  (bf16 x as fp16 times a power of two for each token and warp, which saves two shifts a word, lost what was 2^39 below the
-// largest value: 100000 rows 55.8 us for one token instead of 60.4, 78.1 for 16 instead of 79.0, 8192 rows 8.7 and 13.1 instead of 8.4 and 12.7.)
+// largest value: back to back, 100000 rows 55.8 us for one token instead of 60.4, 78.1 for 16
+// instead of 79.0, 8192 rows 8.7 and 13.1 instead of 8.4 and 12.7.)
 #include <algorithm>
 #include <new>
 

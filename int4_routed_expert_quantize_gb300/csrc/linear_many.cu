@@ -9,9 +9,9 @@
 //   warps 0-3, 4-7   codes to A, D to sums: even and odd blocks
 //   warp 8           issues every product; warp 9 copies weights, 4 blocks of every tile a stage; warp 10 copies x, a block at a time
 //
-// The weights are read once for 64 tokens.  A block takes 800 to 900 cycles, in which HBM could bring two and a half.  Four warpgroups in place of
-// two took as long (100000 rows, 32 tokens: 109 us for 108), so it is the products: about 100 cycles for each 16 columns, whose A comes from tensor
-// memory, however few tokens there are.
+// The weights are read once for 64 tokens.  A block takes 800 to 900 cycles, in which HBM could bring two and a half, however few tokens there
+// are.  Four warpgroups in place of two took as long (100000 rows, 32 tokens: 109 us for 108), and nothing is near its limit (64 tokens: tensor pipe
+// 32 %, issue slots 53 %, L2 18 %, DRAM 26 %), so what is left is the chain of eight products of a block, each of which waits for the one before it.
 // So 16 tokens are better off with linear.cu's kernel, and groups of 32 or 64, whose D would not all fit, at any number.  us, here / there, groups of 128:
 //   8192 x 6144    16 tokens 20.1 / 12.7   24 19.5 / 23.4   64 21.5 / 47.8   128 42.2 / 95.2
 //   100000 x 6144  16 tokens 109 / 79      24 107 / 156     64 118 / 313     128 235 / 626
